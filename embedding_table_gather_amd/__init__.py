@@ -12,6 +12,10 @@ fallback: if the library is missing, every call raises.
     logits = t.logits_raw(residual)               # raw logits mode, [B, vocab]
     rows = t.embed_gather_wire(ids, WIRE_I8)      # ADR-0009 wire rows (f16 or i8)
     ids, scores = t.logits_topk_wire(rows, WIRE_I8, k=10)
+    ids, probs = t.sample(residual, uniform, temperature=0.8, top_p=0.95)   # next tokens
+    q = t.quantize_i8()                           # int8 rows, a scale each: an I8Table
+    logits = q.logits_raw(residual)               # int8 product, f32 [B, vocab]
+    ids, probs = sample(logits, uniform, top_k=50, min_p=0.05)
 """
 from __future__ import annotations
 
@@ -67,6 +71,12 @@ SIGNATURES = {
     "etg_step_cache_stats": (_I32, [_VP, ctypes.POINTER(_I64), ctypes.POINTER(_I64)]),
     "etg_step_gather": (_I32, [_VP, _VP, _I64, _F, _VP]),
     "etg_step_logits": (_I32, [_VP, _I64, _VP, _VP]),
+    "etg_quantize_i8": (_I32, [_VP, _I32, _I64, _I64, _I64, _VP, _I64, _VP, _I64, _VP]),
+    "etg_matmul_i8_workspace": (_I64, [_I64, _I64, _I64]),
+    "etg_matmul_i8": (_I32, [_VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _I64, _I64, _I64, _VP, _I32, _I64, _VP,
+                             ctypes.c_size_t, _VP]),
+    "etg_sample_workspace": (_I64, [_I64, _I64]),
+    "etg_sample": (_I32, [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
     "etg_last_error": (ctypes.c_char_p, []),
 }
 
@@ -365,6 +375,230 @@ class Table:
             _check(lib().etg_logits_raw(self._h, _ptr(R), B, _ptr(out), _ptr(workspace), workspace.numel(),
                                         int(path), _stream_ptr(self.device)))
         return out
+
+    def sample(self, residual: torch.Tensor, uniform: torch.Tensor, path: int = PATH_AUTO, **kw):
+        """The next token of each residual row: ``sample`` of its raw logits (temperature,
+        top_k, top_p, min_p, allowed as there)."""
+        return sample(self.logits_raw(residual, path=path), uniform, **kw)
+
+    def quantize_i8(self) -> "I8Table":
+        """The table's rows as an int8 lm_head (f32, bf16 and f16 tables)."""
+        if self.dtype not in _TORCH_FLOATS:
+            raise ValueError("only f32, bf16 and f16 tables can be quantised to int8 rows")
+        rows = self.rows.view(-1).view(torch.uint8).view(_TORCH_FLOATS[self.dtype]).view(self.vocab, self.hidden)
+        return I8Table(*quantize_i8(rows))
+
+
+_FLOATS = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+_TORCH_FLOATS = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
+
+
+def _float_dtype(dtype) -> torch.dtype:
+    """A torch dtype from F32 / BF16 / F16 or the torch dtype itself."""
+    dtype = _TORCH_FLOATS.get(dtype, dtype)
+    if dtype not in _FLOATS:
+        raise ValueError(f"{dtype} is not float32, bfloat16 or float16")
+    return dtype
+
+
+def _matrix(t: torch.Tensor, what: str, device: torch.device | None = None) -> torch.Tensor:
+    """t as a 2-D device tensor whose rows are contiguous (any row stride that does not
+    overlap rows)."""
+    if t.dim() != 2 or not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{what} must be a 2-D tensor on the {'same' if device is not None else 'GPU'} device")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return t
+
+
+def _row_stride(t: torch.Tensor, what: str) -> int:
+    s = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if s < t.shape[1]:
+        raise ValueError(f"{what} rows overlap (stride {s}, {t.shape[1]} values)")
+    return s
+
+
+def _scales(t: torch.Tensor, n: int, what: str, device: torch.device) -> int:
+    """Checks a vector of n f32 scales; returns its stride in floats."""
+    if t.dtype != torch.float32 or t.device != device or t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{what} must be a float32 tensor of {n} values on the operands' device")
+    s = t.stride(0) if n > 1 else 1
+    if s < 1:
+        raise ValueError(f"{what} must have a positive stride")
+    return s
+
+
+def quantize_i8(x: torch.Tensor, codes: torch.Tensor | None = None, scale: torch.Tensor | None = None):
+    """(int8 codes [rows, cols], f32 scales [rows]) of the rows of a float32, bfloat16 or
+    float16 matrix: scale = max|x| / 127, codes = round(x / scale) (ADR-0009's i8 wire
+    definition).  A row with a NaN or an infinity gets scale NaN.  ``codes`` and ``scale``
+    may be given, with any row stride."""
+    if x.dtype not in _FLOATS:
+        raise ValueError("x must be a float32, bfloat16 or float16 tensor")
+    _matrix(x, "x")
+    rows, cols = x.shape
+    if codes is None:
+        codes = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+    elif codes.dtype != torch.int8 or codes.shape != x.shape:
+        raise ValueError("codes must be an int8 tensor of x's shape")
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _matrix(codes, "codes", x.device)
+    with torch.cuda.device(x.device):
+        _check(lib().etg_quantize_i8(x.data_ptr(), _FLOATS[x.dtype], rows, cols, _row_stride(x, "x"),
+                                     codes.data_ptr(), _row_stride(codes, "codes"), scale.data_ptr(),
+                                     _scales(scale, rows, "scale", x.device), _stream_ptr(x.device)))
+    return codes, scale
+
+
+def matmul_i8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+              out_dtype=torch.float32, out: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """out [m, n] = (a @ w.T) * a_scale[:, None] * w_scale[None, :] for int8 a [m, k] and
+    w [n, k] (rows of any stride; k <= 65536): exact int32 sums, scaled in f32, rounded
+    once to ``out_dtype`` (float32, bfloat16, float16, or F32 / BF16 / F16)."""
+    if a.dtype != torch.int8 or w.dtype != torch.int8:
+        raise ValueError("a and w must be int8 tensors")
+    _matrix(a, "a")
+    _matrix(w, "w", a.device)
+    m, k = a.shape
+    n = w.shape[0]
+    if w.shape[1] != k:
+        raise ValueError(f"a has {k} columns, w {w.shape[1]}")
+    if out is None:
+        out = torch.empty((m, n), dtype=_float_dtype(out_dtype), device=a.device)
+    elif out.dtype not in _FLOATS or out.shape != (m, n):
+        raise ValueError("out must be a float32, bfloat16 or float16 [m, n] tensor")
+    _matrix(out, "out", a.device)
+    sa, sw = _scales(a_scale, m, "a_scale", a.device), _scales(w_scale, n, "w_scale", a.device)
+    L = lib()
+    if workspace is None:
+        need = int(L.etg_matmul_i8_workspace(m, n, k))
+        if need < 0:
+            _check(need)
+        workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
+    with torch.cuda.device(a.device):
+        _check(L.etg_matmul_i8(a.data_ptr(), _row_stride(a, "a"), a_scale.data_ptr(), sa, w.data_ptr(),
+                               _row_stride(w, "w"), w_scale.data_ptr(), sw, m, n, k, out.data_ptr(),
+                               _FLOATS[out.dtype], max(_row_stride(out, "out"), 1), workspace.data_ptr(),
+                               workspace.numel(), _stream_ptr(a.device)))
+    return out
+
+
+class _Sampling(ctypes.Structure):
+    """etg_sampling of include/etg.h."""
+    _fields_ = [("temperature", _F), ("top_k", _I32), ("top_p", _F), ("min_p", _F), ("d_temperature", _VP),
+                ("d_top_k", _VP), ("d_top_p", _VP), ("d_min_p", _VP), ("d_allowed", _VP), ("allowed_stride", _I64)]
+
+
+def _setting(v, off, dtype: torch.dtype, rows: int, device: torch.device, what: str):
+    """(scalar, device pointer or None) of a sampling setting."""
+    if not isinstance(v, torch.Tensor):
+        return v, None
+    if v.dtype != dtype or v.device != device or v.shape != (rows,) or not v.is_contiguous():
+        raise ValueError(f"{what} must be a number or a contiguous {dtype} tensor of {rows} values on the logits' device")
+    return off, v.data_ptr()
+
+
+def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+           allowed: torch.Tensor | None = None, out_ids: torch.Tensor | None = None,
+           out_probs: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """One token per row of logits (float32, bfloat16 or float16 [B, vocab]): (ids int32
+    [B], probabilities f32 [B] they were drawn with), from random numbers ``uniform`` (f32
+    [B] in [0, 1)).
+
+    temperature (0: greedy), top_k (0: off), top_p (1: off) and min_p (0: off) are numbers
+    or device tensors with one value per row (float32; top_k int32).  ``allowed`` is a bit
+    mask, int32 [ceil(vocab / 32)] or [B, ceil(vocab / 32)], bit v % 32 of word v / 32 set
+    where token v is allowed.  NaN and -inf logits are never drawn.  A row with nothing to
+    draw, or with a setting or random number out of range, has id -1 and probability 0.
+    """
+    if logits.dtype not in _FLOATS:
+        raise ValueError("logits must be a float32, bfloat16 or float16 tensor")
+    _matrix(logits, "logits")
+    rows, vocab = logits.shape
+    dev = logits.device
+    if uniform.dtype != torch.float32 or uniform.device != dev or uniform.shape != (rows,) \
+            or not uniform.is_contiguous():
+        raise ValueError(f"uniform must be a contiguous float32 tensor of {rows} values on the logits' device")
+    T, d_T = _setting(temperature, 1.0, torch.float32, rows, dev, "temperature")
+    k, d_k = _setting(top_k, 0, torch.int32, rows, dev, "top_k")
+    p, d_p = _setting(top_p, 1.0, torch.float32, rows, dev, "top_p")
+    mp, d_mp = _setting(min_p, 0.0, torch.float32, rows, dev, "min_p")
+    d_allowed, a_stride = None, 0
+    if allowed is not None:
+        words = (vocab + 31) // 32
+        if allowed.dtype != torch.int32 or allowed.device != dev or allowed.dim() not in (1, 2) \
+                or allowed.shape[-1] != words or (words > 1 and allowed.stride(-1) != 1) \
+                or (allowed.dim() == 2 and allowed.shape[0] != rows):
+            raise ValueError(f"allowed must be an int32 [{words}] or [{rows}, {words}] tensor with contiguous rows on "
+                             "the logits' device")
+        d_allowed = allowed.data_ptr()
+        if allowed.dim() == 2 and rows > 1:
+            a_stride = allowed.stride(0)  # 0: an expanded row, one for all
+    outs = []
+    for o, dtype in ((out_ids, torch.int32), (out_probs, torch.float32)):
+        if o is None:
+            o = torch.empty(rows, dtype=dtype, device=dev)
+        elif o.dtype != dtype or o.device != dev or o.shape != (rows,) or not o.is_contiguous():
+            raise ValueError(f"out_ids / out_probs must be contiguous int32 / float32 tensors of {rows} values")
+        outs.append(o)
+    L = lib()
+    if workspace is None:
+        need = int(L.etg_sample_workspace(rows, vocab))
+        if need < 0:
+            _check(need)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    how = _Sampling(T, k, p, mp, d_T, d_k, d_p, d_mp, d_allowed, a_stride)
+    with torch.cuda.device(dev):
+        _check(L.etg_sample(logits.data_ptr(), _FLOATS[logits.dtype], rows, vocab, _row_stride(logits, "logits"),
+                            ctypes.addressof(how), uniform.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(),
+                            workspace.data_ptr(), workspace.numel(), _stream_ptr(dev)))
+    return outs[0], outs[1]
+
+
+class I8Table:
+    """A V x hidden lm_head as int8 rows with one f32 scale each (half the bytes of a bf16
+    one): logits come from an int8 product with residual rows quantised the same way.
+
+    ``codes`` is an int8 [V, hidden] device tensor (rows of any stride), ``scale`` float32
+    [V]: Table.quantize_i8() or quantize_i8(rows) make them.  Both are borrowed.
+    """
+
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor):
+        if codes.dtype != torch.int8:
+            raise ValueError("codes must be an int8 tensor")
+        _matrix(codes, "codes")
+        _row_stride(codes, "codes")
+        _scales(scale, codes.shape[0], "scale", codes.device)
+        self.codes, self.scale = codes, scale
+        self.vocab, self.hidden = codes.shape
+        self.device = codes.device
+
+    def logits_raw(self, residual: torch.Tensor, out_dtype=torch.float32,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+        """Logits [B, vocab] of float32, bfloat16 or float16 residual rows [B, hidden],
+        each row quantised to int8 first."""
+        a, a_scale = quantize_i8(residual)
+        return matmul_i8(a, a_scale, self.codes, self.scale, out_dtype=out_dtype, out=out)
+
+    def logits_raw_wire(self, residual: torch.Tensor, out_dtype=torch.float32,
+                        out: torch.Tensor | None = None) -> torch.Tensor:
+        """Logits of residual rows in the WIRE_I8 format (a contiguous device buffer of
+        whole wire rows), whose codes are multiplied as they are."""
+        rb = wire_row_bytes(WIRE_I8, self.hidden)
+        nbytes = residual.numel() * residual.element_size()
+        if residual.device != self.device or not residual.is_contiguous() or nbytes % rb:
+            raise ValueError("residual must be a contiguous device buffer of whole wire rows")
+        if rb % 4 or residual.data_ptr() % 4:
+            raise ValueError("wire rows must be 4-byte aligned (hidden a multiple of 4)")
+        rows = residual.view(-1).view(torch.int8).view(-1, rb)
+        return matmul_i8(rows[:, 8:], residual.view(-1).view(torch.float32).view(-1, rb // 4)[:, 0], self.codes,
+                         self.scale, out_dtype=out_dtype, out=out)
+
+    def sample(self, residual: torch.Tensor, uniform: torch.Tensor, **kw):
+        """The next token of each residual row: ``sample`` of its logits (same settings)."""
+        return sample(self.logits_raw(residual), uniform, **kw)
 
 
 class StepCache:

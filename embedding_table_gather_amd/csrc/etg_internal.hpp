@@ -183,6 +183,49 @@ hipError_t launch_rank(const TableDesc& t, const LogitsPlan& p, const void* R, u
                        const LogitsExtras& x, int32_t* ids, float* scores, hipStream_t stream, hipEvent_t ev0,
                        hipEvent_t ev1);
 
+// Quantisation of rows to int8 codes with one scale each (quant.hip); x_stride in bytes.
+hipError_t launch_quantize_i8(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t x_stride,
+                              int8_t* codes, int64_t code_stride, float* scale, int64_t scale_stride,
+                              hipStream_t stream);
+
+// One etg_matmul_i8 call (imatmul.hip): strides of codes in bytes, of scales in
+// floats, of the output in values.
+struct MatmulI8 {
+  const int8_t* a;
+  int64_t a_stride;
+  const float* a_scale;
+  int64_t a_scale_stride;
+  const int8_t* w;
+  int64_t w_stride;
+  const float* w_scale;
+  int64_t w_scale_stride;
+  int64_t m, n, k;
+  void* out;
+  int32_t out_dtype;
+  int64_t out_stride;
+};
+size_t matmul_i8_workspace(int64_t m, int64_t n, int64_t k);
+hipError_t launch_matmul_i8(const MatmulI8& p, void* ws, hipStream_t stream);
+
+// One etg_sample call (sample.hip): strides in values (logits) and words (allowed);
+// a null array takes the scalar for every row.
+struct Sample {
+  const void* logits;
+  int32_t dtype;
+  int64_t rows, vocab, stride;
+  const float* uniform;
+  float temperature, top_p, min_p;
+  int32_t top_k;
+  const float *d_temperature, *d_top_p, *d_min_p;
+  const int32_t* d_top_k;
+  const uint32_t* allowed;
+  int64_t allowed_stride;
+  int32_t* ids;
+  float* probs;
+};
+size_t sample_workspace(int64_t rows, int64_t vocab);
+hipError_t launch_sample(const Sample& p, void* ws, hipStream_t stream);
+
 }  // namespace etg
 
 // The opaque handle of etg.h: host metadata of a table in device memory.

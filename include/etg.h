@@ -406,6 +406,106 @@ int32_t etg_hbm_write_probe(void* d_dst, int64_t bytes, uint32_t value, void* st
 int32_t etg_logits_topk_noalloc(const etg_table* lm_head, const float* d_residual, int64_t batch,
                                 int32_t k, int32_t* d_topk_ids, float* d_topk_scores, void* stream);
 
+/*
+ * int8 lm_head: rows as int8 codes with one f32 scale each.  ADR-0009's i8 residual
+ * wire carries one scale per position; here the codes of both sides are multiplied as
+ * int8, with a scale per token and one per vocabulary row (channel).
+ *
+ * etg_quantize_i8 encodes the rows of a matrix, ETG_WIRE_I8's definition on any
+ * f32, bf16 or f16 input:
+ *   scale[r] = max_c |x[r][c]| / 127,  codes[r][c] = round-half-even(x[r][c] / scale[r]),
+ * both quotients rounded to f32, codes clamped to [-127, 127].  A row with scale 0 has
+ * codes 0.  A row that holds a NaN or an infinity has scale NaN and codes 0.
+ *   d_x           [rows] rows of cols values of `dtype` (ETG_F32, ETG_BF16, ETG_F16),
+ *                 x_stride values apart; aligned to the value
+ *   d_codes       int8, rows code_stride bytes apart, any alignment
+ *   d_scale       f32, scale_stride floats apart
+ *   rows          0 <= rows <= 2^31 - 1; 0 enqueues nothing;  1 <= cols <= 65536
+ * Strides are at least cols (1 for scales) and at most 2^40.  Bytes between rows are
+ * left as they were.  Bit-exact to the definition.
+ * Errors: EDTYPE, ESHAPE (sizes, strides), EINVAL (null), EALIGN.
+ */
+int32_t etg_quantize_i8(const void* d_x, int32_t dtype, int64_t rows, int64_t cols, int64_t x_stride,
+                        int8_t* d_codes, int64_t code_stride, float* d_scale, int64_t scale_stride, void* stream);
+
+/*
+ * Product of int8 rows:
+ *   out[i][j] = T( f32(sum_c a[i][c] * w[j][c]) * a_scale[i] * w_scale[j] )
+ * with the sum exact (int32), its conversion and the two multiplications (left to
+ * right) rounded to f32, and one rounding to the output type T (f16 past 65504:
+ * infinity).  Codes may be any int8, -128 included.
+ *   d_a, d_w       rows a_stride / w_stride bytes apart, any alignment (16-byte
+ *                  aligned rows are faster); ETG_WIRE_I8 rows are read in place with
+ *                  d_a = rows + 8, d_a_scale = rows, a_stride = hidden + 8 and
+ *                  a_scale_stride = (hidden + 8) / 4
+ *   d_a_scale, d_w_scale  f32, their strides in floats
+ *   m, n, k        0 <= m <= 65536, 0 <= n <= 2^31 - 1 (0 enqueues nothing),
+ *                  1 <= k <= 65536
+ *   d_out          `out_dtype` (ETG_F32, ETG_BF16, ETG_F16) [m][n], rows out_stride
+ *                  values apart, aligned to the value; values between rows are left
+ *                  as they were
+ *   d_workspace    at least etg_matmul_i8_workspace() bytes, 256-byte aligned (may be
+ *                  NULL where that is 0)
+ * Results are bitwise repeatable and depend on no other row.
+ * Errors: EDTYPE, ESHAPE (sizes, strides), EINVAL (null), EALIGN, EWORKSPACE.
+ */
+int64_t etg_matmul_i8_workspace(int64_t m, int64_t n, int64_t k);
+int32_t etg_matmul_i8(const int8_t* d_a, int64_t a_stride, const float* d_a_scale, int64_t a_scale_stride,
+                      const int8_t* d_w, int64_t w_stride, const float* d_w_scale, int64_t w_scale_stride, int64_t m,
+                      int64_t n, int64_t k, void* d_out, int32_t out_dtype, int64_t out_stride, void* d_workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * Sampling (what ADR-0008 "POST /v1/logits" leaves to the caller of its raw logits
+ * mode): one token per row of logits with temperature, top-k, top-p and min-p, from
+ * given random numbers.  The settings are one value for all rows, or a device array
+ * with one per row where the pointer is not NULL.
+ */
+typedef struct {
+  float temperature;            /* finite, >= 0; 0: greedy (the first token of the order)  */
+  int32_t top_k;                /* >= 0; 0: off                                            */
+  float top_p;                  /* in (0, 1]; 1: off                                       */
+  float min_p;                  /* in [0, 1]; 0: off                                       */
+  const float* d_temperature;   /* f32 [batch] or NULL                                     */
+  const int32_t* d_top_k;       /* int32 [batch] or NULL                                   */
+  const float* d_top_p;         /* f32 [batch] or NULL                                     */
+  const float* d_min_p;         /* f32 [batch] or NULL                                     */
+  const uint32_t* d_allowed;    /* NULL (all tokens) or a bit mask, ceil(vocab / 32) words
+                                   a row: token v is allowed where bit v % 32 of word
+                                   v / 32 is set                                           */
+  int64_t allowed_stride;       /* words between the mask's rows; 0: one row for all       */
+} etg_sampling;
+
+/*
+ * A row's candidates are its allowed tokens whose logit is neither NaN nor -inf.  With
+ * M the largest of their logits and T the temperature, candidate v weighs
+ * w_v = exp((l_v - M) / T) in 64 bits, 1 where l_v == M.  Candidates are ordered by
+ * logit descending, equal ones (-0 and +0 are equal) by id ascending, and are kept where
+ *   top-k  they are among the first k,
+ *   top-p  the mass before them is less than top_p times the mass of the first k,
+ *   min-p  w_v >= min_p.
+ *   ids[b]    the first kept token in id order whose running sum of kept weights exceeds
+ *             uniform[b] times their total
+ *   probs[b]  its weight over that total: the probability that it was drawn with
+ * A row without candidates, or with a setting or random number outside its range
+ * (uniform: [0, 1)), has id -1 and probability 0.
+ *   d_logits     `dtype` (ETG_F32, ETG_BF16, ETG_F16) [batch][vocab], rows logits_stride
+ *                values apart, aligned to the value; may be rewritten once the call's
+ *                work has run
+ *   d_uniform    f32 [batch]
+ *   batch        0 <= batch <= 65536 (0 enqueues nothing);  1 <= vocab <= 2^20
+ *   d_workspace  at least etg_sample_workspace() bytes, 256-byte aligned (may be NULL
+ *                where that is 0)
+ * Weights are added in 64-bit fixed point (rounded to 2^-45 of the largest one at vocab
+ * 2^18, coarser by one bit per doubling), so results do not depend on timing: they
+ * repeat bitwise, and tokens of equal logits weigh the same.
+ * Errors: EDTYPE, ESHAPE, ERANGE (a scalar setting), EINVAL (null), EALIGN, EWORKSPACE.
+ */
+int64_t etg_sample_workspace(int64_t batch, int64_t vocab);
+int32_t etg_sample(const void* d_logits, int32_t dtype, int64_t batch, int64_t vocab, int64_t logits_stride,
+                   const etg_sampling* how, const float* d_uniform, int32_t* d_ids, float* d_probs,
+                   void* d_workspace, size_t workspace_bytes, void* stream);
+
 /* Message of the calling thread's last failed call ("" if none). */
 const char* etg_last_error(void);
 
