@@ -27,7 +27,7 @@ namespace etg {
 // and 2^-24 at the largest vocabulary, 2^20.
 //
 // Kernels:
-//  1. sample_chunk_kernel streams the logits once, a workgroup per 4,096 tokens: the
+//  1. sample_chunk_kernel streams the logits once, a wave per 2,048 tokens: the
 //     maximum of every small group of tokens and of the chunk and, for rows whose
 //     filters need it, the chunk's mass.
 //  2. sample_row_kernel, a workgroup per row.  A row without filters picks a chunk by
@@ -70,13 +70,13 @@ __device__ __forceinline__ SampleRow sample_row(const Sample& s, int64_t row) {
 static constexpr int kSampleThreads = 1024;
 static constexpr int kSampleWaves = kSampleThreads / 64;
 static constexpr int kSampleBins = 1024;         // one per thread
-static constexpr int kChunk = 4096;              // tokens of a chunk
+static constexpr int kChunk = 2048;              // tokens of a chunk (a wave's)
 static constexpr int kChunkThreads = 256;
 static constexpr int kSlice = 32768;             // tokens of a histogram slice
 static constexpr int kMaxSlices = (1 << 20) / kSlice;
 static constexpr int kList = 2048;               // tokens sorted in LDS by the row kernel
 static constexpr int kHeavyList = 8192;          // tokens of one bin in the heavy kernel
-static constexpr int kMaxGroups = 4096;          // groups per row up to 2^18 tokens
+static constexpr int kMaxGroups = 4096;          // groups per row
 static constexpr int64_t kHeavySlots = 512;      // rows of one call with histograms
 
 // Workspace of a call, from its sizes alone.
@@ -89,9 +89,9 @@ static SampleWs sample_ws(int64_t rows, int64_t vocab, int32_t dtype) {
   SampleWs w;
   w.chunks = (int)cdiv(vocab, kChunk);
   w.slices = (int)cdiv(vocab, kSlice);
-  // groups of one 16-byte load (4 or 8 tokens) to 64 tokens, at most kMaxGroups up to 2^18
+  // groups of one 16-byte load (4 or 8 tokens) or more (256 at 2^20 tokens)
   w.group_log2 = dtype == DT_F32 ? 2 : 3;
-  while (w.group_log2 < 6 && cdiv(vocab, 1ll << w.group_log2) > kMaxGroups) w.group_log2++;
+  while (cdiv(vocab, 1ll << w.group_log2) > kMaxGroups) w.group_log2++;
   w.groups = (int)cdiv(vocab, 1ll << w.group_log2);
   w.slots = (int)std::min(rows, kHeavySlots);
   size_t at = 0;
@@ -115,7 +115,7 @@ struct SamplePtrs {
   float* gmax;       // [rows][groups] largest candidate logit, -inf for none
   float* cmax;       // [rows][chunks]
   uint64_t* csum;    // [rows][chunks] mass relative to the chunk's own maximum
-  int32_t* flag;     // [rows] -1: done, else the histogram slot
+  int32_t* flag;     // [rows] -1: done, else the histogram slot, or -2 for none
   uint32_t* nheavy;  // slots taken
   uint32_t* hcount;  // [slots][slices][bins]
   uint64_t* hmass;
@@ -156,9 +156,11 @@ struct SampleWeight {
   __device__ __forceinline__ double weight(float l) const {
     return (double)l == M ? 1.0 : scaled_exp2(power(l), 0);
   }
-  // rint(weight * 2^shift): at most 2^45, so adding 2^52 leaves it in the low bits
+  // rint(weight * 2^shift): at most 2^45, so adding 2^52 leaves it in the low bits.  0 for
+  // -inf and NaN (the maximum of NaN and a number is the number).
   __device__ __forceinline__ uint64_t fixed(float l) const {
-    const double x = ((double)l == M ? ldexp(1.0, shift) : scaled_exp2(power(l), shift)) + 4503599627370496.0;
+    const double y = (double)l == M ? 0.0 : power(l);
+    const double x = scaled_exp2(y, shift) + 4503599627370496.0;
     return (uint64_t)__double_as_longlong(x) & 0xfffffffffffffull;
   }
 };
@@ -198,10 +200,10 @@ struct SampleSource {
     const bool live = l > -__builtin_inff() && (allowed == nullptr || ((allowed[v >> 5] >> (v & 31)) & 1u));
     return live ? l : -__builtin_inff();
   }
-  // tokens [v, v + N) (v a multiple of N, N = 4 or 8 by type), -inf past the vocabulary:
-  // one 16-byte load at any alignment of the value
+  // tokens [v, v + N) (v a multiple of N, N = 4 or 8 by type), -inf past the vocabulary and
+  // where barred: one 16-byte load at any alignment of the value.  A NaN logit is left as it is.
   static constexpr int N = DT == DT_F32 ? 4 : 8;
-  __device__ __forceinline__ void load(int v, float (&l)[N]) const {
+  __device__ __forceinline__ void load_raw(int v, float (&l)[N]) const {
     if (v + N <= V) {
       u32x4 w;
       __builtin_memcpy(&w, base + (size_t)v * (16 / N), 16);
@@ -211,26 +213,42 @@ struct SampleSource {
         else if constexpr (DT == DT_BF16) l[j] = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
         else l[j] = f16_bits_to_f32(j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu);
       }
-      const uint32_t ok = allowed ? allowed[v >> 5] >> (v & 31) : 0xffffffffu;
+      if (allowed != nullptr) {
+        const uint32_t ok = allowed[v >> 5] >> (v & 31);
 #pragma unroll
-      for (int j = 0; j < N; j++)
-        if (!(l[j] > -__builtin_inff()) || !((ok >> j) & 1u)) l[j] = -__builtin_inff();
+        for (int j = 0; j < N; j++)
+          if (!((ok >> j) & 1u)) l[j] = -__builtin_inff();
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < N; j++) l[j] = v + j < V ? logit(v + j) : -__builtin_inff();
     }
+  }
+  __device__ __forceinline__ void load(int v, float (&l)[N]) const {
+    load_raw(v, l);
+#pragma unroll
+    for (int j = 0; j < N; j++) l[j] = l[j] > -__builtin_inff() ? l[j] : -__builtin_inff();
   }
 };
 
 // Order key of a logit, 0 for -inf (every candidate's is larger).
 __device__ __forceinline__ uint32_t sample_key(float l) { return l > -__builtin_inff() ? score_ord(l) : 0u; }
 
-// Bin of a logit: logarithmic in its distance to the largest one, 64 bins per octave
-// from 2^-8 to 2^8 (nearer ones in bin 0, farther ones in the last).  It never falls
-// as the logit falls.
+// What bounds and bins go by: the f32 distance of a logit to the row's largest one, as
+// bits (which order as it does).  It never falls as the logit falls.
+__device__ __forceinline__ uint32_t sample_dist(float l, float top) {
+  return l == top ? 0u : __float_as_uint(top - l) & 0x7fffffffu;
+}
+
+// Bin of a logit: logarithmic in the distance, 128 bins per octave from 2^-3 to 2^5
+// (nearer ones in bin 0, farther ones in the last).
+static constexpr int kBinShift = 16, kBinBase = 124 << 7;
 __device__ __forceinline__ int sample_bin(float l, float top) {
-  const uint32_t d = l == top ? 0u : __float_as_uint(top - l) & 0x7fffffffu;
-  return min(max((int)(d >> 17) - (119 << 6), 0), kSampleBins - 1);
+  return min(max((int)(sample_dist(l, top) >> kBinShift) - kBinBase, 0), kSampleBins - 1);
+}
+// Distances below this are those of bins up to b.
+__device__ __forceinline__ uint32_t sample_bin_limit(int b) {
+  return b >= kSampleBins - 1 ? 0xffffffffu : (uint32_t)(b + 1 + kBinBase) << kBinShift;
 }
 
 // The smallest key whose bin is at most b.
@@ -257,13 +275,13 @@ __device__ __forceinline__ uint32_t sample_minp_key(const SampleWeight& w, float
 }
 
 // ---------------------------------------------------------------------------
-// Workgroup primitives (1,024 threads); every one begins and ends with the shared
-// scratch free to reuse.
+// Workgroup primitives (NW waves); every one begins and ends with the shared scratch
+// free to reuse.
 // ---------------------------------------------------------------------------
+template <int NW>
 struct SampleScratch {
-  uint64_t part[kSampleWaves];
+  uint64_t part[NW];
   uint64_t value[2];
-  uint32_t index[2];
 };
 
 __device__ __forceinline__ uint64_t wave_scan_u64(uint64_t v) {  // inclusive
@@ -277,7 +295,8 @@ __device__ __forceinline__ uint64_t wave_scan_u64(uint64_t v) {  // inclusive
 }
 
 // Inclusive prefix sum over the threads; *total receives the sum.
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* total, SampleScratch& sc) {
+template <int NW>
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* total, SampleScratch<NW>& sc) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   v = wave_scan_u64(v);
   __syncthreads();
@@ -285,9 +304,10 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* total, Samp
   __syncthreads();
   uint64_t before = 0, all = 0;
 #pragma unroll
-  for (int i = 0; i < kSampleWaves; i++) {
-    if (i < wv) before += sc.part[i];
-    all += sc.part[i];
+  for (int i = 0; i < NW; i++) {
+    const uint64_t p = sc.part[i];
+    if (i < wv) before += p;
+    all += p;
   }
   *total = all;
   __syncthreads();
@@ -295,8 +315,9 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* total, Samp
 }
 
 // The first thread with `hit`, and the two values it holds, to every thread; -1 for none.
+template <int NW>
 __device__ __forceinline__ int block_first(bool hit, uint64_t a, uint64_t b, uint64_t* oa, uint64_t* ob,
-                                           SampleScratch& sc) {
+                                           SampleScratch<NW>& sc) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const uint64_t m = __ballot(hit);
   __syncthreads();
@@ -304,7 +325,7 @@ __device__ __forceinline__ int block_first(bool hit, uint64_t a, uint64_t b, uin
   __syncthreads();
   int first = -1;
 #pragma unroll
-  for (int i = kSampleWaves - 1; i >= 0; i--)
+  for (int i = NW - 1; i >= 0; i--)
     if (sc.part[i] != 0) first = 64 * i + __ffsll((unsigned long long)sc.part[i]) - 1;
   if ((int)threadIdx.x == first) {
     sc.value[0] = a;
@@ -319,17 +340,22 @@ __device__ __forceinline__ int block_first(bool hit, uint64_t a, uint64_t b, uin
   return first;
 }
 
-// The token of [lo, hi) (lo a multiple of 4) in which the running mass first exceeds
-// target; weigh(v) is a token's mass.  The range's mass exceeds target.
-template <typename F>
-__device__ __forceinline__ int block_pick(int lo, int hi, uint64_t target, F weigh, SampleScratch& sc) {
-  int last = lo;
-  for (int at = lo; at < hi; at += 4 * kSampleThreads) {
-    const int v = at + 4 * (int)threadIdx.x;
-    uint64_t w[4], sum = 0;
+// The token of [lo, hi) (lo a multiple of 8) in which the running mass first exceeds
+// target, which the range's mass exceeds; weigh(l, v) is the mass of token v with logit l.
+template <int NW, int DT, typename F>
+__device__ __forceinline__ int block_pick(const SampleSource<DT>& src, int lo, int hi, uint64_t target, F weigh,
+                                          SampleScratch<NW>& sc) {
+  constexpr int N = SampleSource<DT>::N;
+  for (int at = lo; at < hi; at += N * 64 * NW) {
+    const int v = at + N * (int)threadIdx.x;
+    float l[N];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      w[j] = v + j < hi ? weigh(v + j) : 0;
+    for (int j = 0; j < N; j++) l[j] = -__builtin_inff();
+    if (v < hi) src.load(v, l);
+    uint64_t w[N], sum = 0;
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      w[j] = l[j] > -__builtin_inff() && v + j < hi ? weigh(l[j], v + j) : 0;
       sum += w[j];
     }
     uint64_t total;
@@ -338,7 +364,7 @@ __device__ __forceinline__ int block_pick(int lo, int hi, uint64_t target, F wei
       uint64_t run = upto - sum;
       int id = v;
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
+      for (int j = 0; j < N; j++) {
         if (run <= target) id = v + j;  // the last token that begins at or below the target
         run += w[j];
       }
@@ -347,15 +373,14 @@ __device__ __forceinline__ int block_pick(int lo, int hi, uint64_t target, F wei
       return (int)got;
     }
     target -= total;
-    last = at;
   }
-  return last;  // not reached
+  return lo;  // not reached
 }
 
 // ---------------------------------------------------------------------------
 // 1. Chunks
 // ---------------------------------------------------------------------------
-// Max over the 2^steps-lane groups of a 16-lane row (DPP), to every lane of the group.
+// Max over groups of 2^steps lanes (DPP within 16-lane rows), to every lane of the group.
 __device__ __forceinline__ float group_max(float m, int steps) {
   auto dpp = [&](auto ctrl) {
     return fmaxf(m, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(m), decltype(ctrl)::value, 0xf, 0xf,
@@ -365,57 +390,54 @@ __device__ __forceinline__ float group_max(float m, int steps) {
   if (steps > 1) m = dpp(std::integral_constant<int, 0x4e>{});   // quad_perm 2,3,0,1
   if (steps > 2) m = dpp(std::integral_constant<int, 0x141>{});  // row_half_mirror
   if (steps > 3) m = dpp(std::integral_constant<int, 0x140>{});  // row_mirror
+  if (steps > 4) m = fmaxf(m, __shfl_xor(m, 16, 64));
+  if (steps > 5) m = fmaxf(m, __shfl_xor(m, 32, 64));
   return m;
 }
 
-// Bound by the logits' bytes (one 16-byte load per 4 or 8 tokens) where no mass is
-// needed, else by about 30 f64 operations per token.
+// A wave per chunk, no workgroup synchronisation: bound by the logits' bytes (8 or 4
+// 16-byte loads in flight per lane) where no mass is needed, else by about 25 f64
+// operations per token.
 template <int DT>
 __global__ void __launch_bounds__(kChunkThreads) sample_chunk_kernel(Sample s, SamplePtrs ws) {
   using Src = SampleSource<DT>;
-  constexpr int N = Src::N, NV = kChunk / (kChunkThreads * N);
-  __shared__ float pmax[kChunkThreads / 64];
-  __shared__ uint64_t psum[kChunkThreads / 64];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, c = blockIdx.x;
+  constexpr int N = Src::N, NV = kChunk / (64 * N);
+  const int lane = threadIdx.x & 63;
+  const uint32_t unit = blockIdx.x * (kChunkThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (unit == 0 && lane == 0) *ws.nheavy = 0;
+  const int64_t row = unit / (uint32_t)ws.chunks;  // units: at most 2^16 rows of 2^9 chunks
+  const int c = (int)(unit % (uint32_t)ws.chunks);
+  if (row >= s.rows) return;  // whole wave, no barrier
   const int steps = ws.group_log2 - (DT == DT_F32 ? 2 : 3);
-  if (c == 0 && blockIdx.y == 0 && tid == 0) *ws.nheavy = 0;
-  for (int64_t row = blockIdx.y; row < s.rows; row += gridDim.y) {
-    const Src src(s, row);
-    float l[NV][N];
+  const Src src(s, row);
+  float l[NV][N];
 #pragma unroll
-    for (int j = 0; j < NV; j++) src.load(c * kChunk + (j * kChunkThreads + tid) * N, l[j]);
-    float m = -__builtin_inff();
+  for (int j = 0; j < NV; j++) src.load_raw(c * kChunk + (j * 64 + lane) * N, l[j]);
+  const SampleRow r = sample_row(s, row);
+  float m = -__builtin_inff();
 #pragma unroll
-    for (int j = 0; j < NV; j++) {
-      float g = l[j][0];
+  for (int j = 0; j < NV; j++) {
+    float g = -__builtin_inff();
 #pragma unroll
-      for (int e = 1; e < N; e++) g = fmaxf(g, l[j][e]);
-      g = group_max(g, steps);
-      const int v = c * kChunk + (j * kChunkThreads + tid) * N;
-      if ((lane & ((1 << steps) - 1)) == 0 && v < src.V) ws.gmax[row * ws.groups + (v >> ws.group_log2)] = g;
-      m = fmaxf(m, g);
-    }
-    m = wave_max_f32(m);
-    __syncthreads();
-    if (lane == 0) pmax[wv] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(pmax[0], pmax[1]), fmaxf(pmax[2], pmax[3]));
-    if (tid == 0) ws.cmax[row * ws.chunks + c] = m;
-    const SampleRow r = sample_row(s, row);
-    if (r.k != 0 || !(r.p < 1.f || r.minp == 0.f) || !r.ok) continue;  // no filter of this row needs the mass
-    uint64_t sum = 0;
-    if (m > -__builtin_inff()) {
-      const SampleWeight w(m, r.T, ws.shift);
-#pragma unroll
-      for (int j = 0; j < NV; j++)
-#pragma unroll
-        for (int e = 0; e < N; e++) sum += l[j][e] > -__builtin_inff() ? w.fixed(l[j][e]) : 0;
-    }
-    sum = wave_scan_u64(sum);
-    if (lane == 63) psum[wv] = sum;
-    __syncthreads();
-    if (tid == 0) ws.csum[row * ws.chunks + c] = psum[0] + psum[1] + psum[2] + psum[3];
+    for (int e = 0; e < N; e++) g = fmaxf(g, l[j][e]);  // passes over NaN
+    g = group_max(g, steps);
+    const int v = c * kChunk + (j * 64 + lane) * N;
+    if ((lane & ((1 << steps) - 1)) == 0 && v < src.V) ws.gmax[row * ws.groups + (v >> ws.group_log2)] = g;
+    m = fmaxf(m, g);
   }
+  m = wave_max_f32(m);
+  if (lane == 0) ws.cmax[unit] = m;
+  if (r.k != 0 || !(r.p < 1.f || r.minp == 0.f) || !r.ok) return;  // no filter of this row needs the mass
+  uint64_t sum = 0;
+  if (m > -__builtin_inff()) {
+    const SampleWeight w(m, r.T, ws.shift);
+#pragma unroll
+    for (int j = 0; j < NV; j++)
+#pragma unroll
+      for (int e = 0; e < N; e++) sum += w.fixed(l[j][e]);
+  }
+  sum = wave_scan_u64(sum);
+  if (lane == 63) ws.csum[unit] = sum;
 }
 
 // ---------------------------------------------------------------------------
@@ -432,16 +454,66 @@ struct SampleHist {
   uint64_t mass[kSampleBins];
 };
 
+// f(key, id) for every candidate of a row, the vocabulary dealt to the threads, four
+// loads in flight each (one workgroup reads a whole row: latency is what it waits for).
+template <int NT, int DT, typename F>
+__device__ __forceinline__ void sample_each(const SampleSource<DT>& src, F f) {
+  constexpr int N = SampleSource<DT>::N, U = 32 / N;
+  for (int at = 0; at < src.V; at += NT * N * U) {
+    float l[U][N];
+#pragma unroll
+    for (int u = 0; u < U; u++) src.load(at + (u * NT + (int)threadIdx.x) * N, l[u]);
+#pragma unroll
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int j = 0; j < N; j++)
+        if (l[u][j] > -__builtin_inff()) f(score_ord(l[u][j]), (uint32_t)(at + (u * NT + (int)threadIdx.x) * N + j));
+  }
+}
+
+// Tokens of one row between two keys: in an LDS list where they fit, else the row itself.
+template <int NT, int DT>
+struct SampleRange {
+  const SampleSource<DT>& src;
+  uint64_t* list;  // key << 32 | id, in no order
+  uint32_t* size;
+  int n = -1;      // entries of the list; -1: the row
+  __device__ __forceinline__ SampleRange(const SampleSource<DT>& s_, uint64_t* l_, uint32_t* n_)
+      : src(s_), list(l_), size(n_) {}
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    if (n >= 0) {
+      for (int i = threadIdx.x; i < n; i += NT) f((uint32_t)(list[i] >> 32), (uint32_t)list[i]);
+    } else {
+      sample_each<NT>(src, f);
+    }
+  }
+  // lists the row's `count` candidates with keys in [klo, khi] if they fit
+  __device__ __forceinline__ void gather(uint32_t klo, uint32_t khi, uint64_t count) {
+    n = -1;
+    if (count > kHeavyList) return;
+    if (threadIdx.x == 0) *size = 0;
+    __syncthreads();
+    sample_each<NT>(src, [&](uint32_t key, uint32_t id) {
+      if (key >= klo && key <= khi) list[atomicAdd(size, 1u)] = ((uint64_t)key << 32) | id;
+    });
+    __syncthreads();
+    n = (int)*size;
+    __syncthreads();
+  }
+};
+
 // Narrows *cut to the element at which the prefix of its kept elements first holds
 // `count` of them (by_count) or `mass`; returns the prefix's mass.  That element's key
-// lies in [klo, khi]; before_count and before_mass are those of the keys above khi.
-// each(f) calls f(key, id) for every element with a key in [klo, khi] at least, each by
-// one thread.  1,024 bins per round, then the same on the ids of the last key.
-template <typename E>
-__device__ __forceinline__ uint64_t sample_find(E each, const SampleWeight& w, int V, SampleCut* cut, uint32_t klo,
-                                                uint32_t khi, bool by_count, uint64_t count, uint64_t mass,
-                                                uint64_t before_count, uint64_t before_mass, SampleHist& h,
-                                                SampleScratch& sc) {
+// lies in [klo, khi], whose tokens `range` holds; before_count and before_mass are those
+// of the keys above khi.  1,024 bins per round (a bin per thread), then the same on the
+// ids of the last key.
+template <int DT>
+__device__ __forceinline__ uint64_t sample_find(SampleRange<kSampleThreads, DT>& range, const SampleWeight& w,
+                                                SampleCut* cut, uint32_t klo, uint32_t khi, bool by_count,
+                                                uint64_t count, uint64_t mass, uint64_t before_count,
+                                                uint64_t before_mass, SampleHist& h,
+                                                SampleScratch<kSampleWaves>& sc) {
   const int tid = threadIdx.x;
   const SampleCut old = *cut;
   while (klo < khi) {
@@ -449,7 +521,7 @@ __device__ __forceinline__ uint64_t sample_find(E each, const SampleWeight& w, i
     h.count[tid] = 0;
     h.mass[tid] = 0;
     __syncthreads();
-    each([&](uint32_t key, uint32_t id) {
+    range.each([&](uint32_t key, uint32_t id) {
       if (key >= klo && key <= khi && old.keeps(key, id)) {
         const int b = (int)((key - klo) >> sh);
         atomicAdd(&h.count[b], 1u);
@@ -463,22 +535,26 @@ __device__ __forceinline__ uint64_t sample_find(E each, const SampleWeight& w, i
     // the first bin from the top that reaches the target, else the last that holds any
     int t = block_first(c != 0 && (by_count ? ic >= count : im >= mass), ic - c, im - m, &bc, &bm, sc);
     if (t < 0) t = block_first(c != 0 && ic == before_count + tc, ic - c, im - m, &bc, &bm, sc);
+    const int bin = kSampleBins - 1 - t;
+    const uint32_t in_bin = h.count[bin];
     before_count = bc;
     before_mass = bm;
-    klo += (uint32_t)(kSampleBins - 1 - t) << sh;
+    klo += (uint32_t)bin << sh;
     khi = min(khi, klo + ((1u << sh) - 1));
     __syncthreads();
+    // elements that an earlier cut leaves out are not counted: only without one is the list's size known
+    if (range.n < 0 && old.key == 1 && sh > 0) range.gather(klo, khi, in_bin);
   }
   const uint64_t wk = w.fixed(ord_score(klo));
   uint64_t ties = by_count ? count - before_count : wk != 0 ? (mass - before_mass + wk - 1) / wk : ~0ull >> 1;
   // the id of the last of `ties` elements with the key
-  uint32_t ilo = 0, ihi = (uint32_t)V - 1;
+  uint32_t ilo = 0, ihi = (uint32_t)range.src.V - 1;
   uint64_t passed = 0;
   do {
     const int sh = max(0, 22 - __clz((int)(ihi - ilo)));
     h.count[tid] = 0;
     __syncthreads();
-    each([&](uint32_t key, uint32_t id) {
+    range.each([&](uint32_t key, uint32_t id) {
       if (key == klo && id >= ilo && id <= ihi && old.keeps(key, id)) atomicAdd(&h.count[(id - ilo) >> sh], 1u);
     });
     __syncthreads();
@@ -497,19 +573,6 @@ __device__ __forceinline__ uint64_t sample_find(E each, const SampleWeight& w, i
   return before_mass + ties * wk;
 }
 
-// f(key, id) for every candidate of a row, the vocabulary dealt to the threads.
-template <int DT, typename F>
-__device__ __forceinline__ void sample_each(const SampleSource<DT>& src, F f) {
-  constexpr int N = SampleSource<DT>::N;
-  for (int v = (int)threadIdx.x * N; v < src.V; v += kSampleThreads * N) {
-    float l[N];
-    src.load(v, l);
-#pragma unroll
-    for (int j = 0; j < N; j++)
-      if (l[j] > -__builtin_inff()) f(score_ord(l[j]), (uint32_t)(v + j));
-  }
-}
-
 __device__ __forceinline__ void sample_store(const Sample& s, int64_t row, int id, double w, uint64_t total, int shift) {
   if (threadIdx.x == 0) {
     s.ids[row] = id;
@@ -517,74 +580,54 @@ __device__ __forceinline__ void sample_store(const Sample& s, int64_t row, int i
   }
 }
 
-// A row by nothing but passes over its logits: for rows past the histogram slots and
-// for lists that do not fit.
-template <int DT>
-__device__ __attribute__((noinline)) void sample_by_passes(const Sample& s, int64_t row, float top, int shift,
-                                                           SampleHist& h, SampleScratch& sc) {
-  const SampleSource<DT> src(s, row);
-  const SampleRow r = sample_row(s, row);
-  const SampleWeight w(top, r.T, shift);
-  auto each = [&](auto f) { sample_each<DT>(src, f); };
-  SampleCut cut;
-  auto kept_mass = [&]() {
-    uint64_t m = 0, total;
-    each([&](uint32_t key, uint32_t id) { m += cut.keeps(key, id) ? w.fixed(ord_score(key)) : 0; });
-    block_scan(m, &total, sc);
-    return total;
-  };
-  const uint32_t top_key = score_ord(top);
-  uint64_t mass = 0;
-  if (r.k > 0) mass = sample_find(each, w, src.V, &cut, 1u, top_key, true, (uint64_t)r.k, 0, 0, 0, h, sc);
-  if (r.p < 1.f) {
-    if (r.k == 0) mass = kept_mass();
-    sample_find(each, w, src.V, &cut, 1u, top_key, false, 0, scaled_ceil(r.p, mass), 0, 0, h, sc);
-  }
-  if (r.minp > 0.f) {
-    const uint32_t key = sample_minp_key(w, top, r.minp);
-    if (key > cut.key) cut.key = key, cut.id = 0xffffffffu;
-  }
-  const uint64_t total = kept_mass();
-  const int id = block_pick(0, src.V, scaled_floor(r.u, total), [&](int v) {
-    const float l = src.logit(v);
-    const uint32_t key = sample_key(l);
-    return key != 0 && cut.keeps(key, (uint32_t)v) ? w.fixed(l) : 0ull;
-  }, sc);
-  sample_store(s, row, id, w.weight(src.logit(id)), total, shift);
-}
-
 // ---------------------------------------------------------------------------
 // 2. Rows
 // ---------------------------------------------------------------------------
+static constexpr int kRowThreads = 512;
+static constexpr int kRowWaves = kRowThreads / 64;
+
 struct SampleRowShared {
-  SampleScratch sc;
-  SampleHist h;
-  uint64_t list[kList];    // the tokens at or above the bound in id order: key << 32 | ~id
-  uint64_t sorted[kList];  // the same in the row's order
-  uint32_t groups[kList];  // groups that reach the bound, in order
-  uint32_t wave_count[kSampleWaves];
+  SampleScratch<kRowWaves> sc;
+  uint64_t list[kList];  // the tokens at or above the bound in id order: key << 32 | ~id
+  union {
+    struct {
+      SampleHist h;
+      uint32_t groups[kList];  // groups that reach the bound, in order
+    };
+    struct {
+      uint64_t sorted[kList];  // the list in the row's order
+      uint64_t mass[kList];
+    };
+  };
+  uint32_t wave_count[kRowWaves];
 };
 
+// A row is a chain of short dependent steps: 512 threads, as more waves synchronise
+// more slowly and fewer read a long list's groups more slowly.
 template <int DT>
-__global__ void __launch_bounds__(kSampleThreads) sample_row_kernel(Sample s, SamplePtrs ws, int heavy) {
+__global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, SamplePtrs ws) {
   __shared__ SampleRowShared sh;
-  SampleScratch& sc = sh.sc;
+  SampleScratch<kRowWaves>& sc = sh.sc;
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const SampleSource<DT> src(s, row);
   const SampleRow r = sample_row(s, row);
   const int V = src.V;
-  if (tid == 0 && heavy) ws.flag[row] = -1;
+  if (tid == 0) ws.flag[row] = -1;
 
-  // the row's largest logit and, where the chunks have masses, their sum
-  float cm = -__builtin_inff();
-  if (tid < ws.chunks) cm = ws.cmax[row * ws.chunks + tid];
-  float top = wave_max_f32(cm);
+  // the row's largest logit
+  const float* cmax = ws.cmax + row * ws.chunks;
+  float top = -__builtin_inff();
+  for (int c = tid; c < ws.chunks; c += kRowThreads) top = fmaxf(top, cmax[c]);
+  top = wave_max_f32(top);
   if (lane == 0) sc.part[wv] = __float_as_uint(top);
+  for (int i = tid; i < kSampleBins; i += kRowThreads) {
+    sh.h.count[i] = 0;
+    sh.h.mass[i] = 0;
+  }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSampleWaves; i++) top = fmaxf(top, __uint_as_float((uint32_t)sc.part[i]));
-  __syncthreads();
+  for (int i = 0; i < kRowWaves; i++) top = fmaxf(top, __uint_as_float((uint32_t)sc.part[i]));
   if (!(top > -__builtin_inff()) || !r.ok) {  // whole workgroup
     if (tid == 0) {
       s.ids[row] = -1;
@@ -593,193 +636,251 @@ __global__ void __launch_bounds__(kSampleThreads) sample_row_kernel(Sample s, Sa
     return;
   }
   const SampleWeight w(top, r.T, ws.shift);
-  uint64_t total = 0;
+  uint64_t total = 0, unused, unused2;
   if (r.k == 0 && (r.p < 1.f || r.minp == 0.f)) {
     // chunk masses to the row's maximum: a chunk at it keeps its integer sum
+    const uint64_t* csum = ws.csum + row * ws.chunks;
+    const int per = (ws.chunks + kRowThreads - 1) / kRowThreads, c0 = tid * per, c1 = min(c0 + per, ws.chunks);
+    auto chunk_mass = [&](int c) -> uint64_t {
+      const float m = cmax[c];
+      if (!(m > -__builtin_inff())) return 0;
+      return m == top ? csum[c] : (uint64_t)rint((double)csum[c] * w.weight(m));
+    };
     uint64_t z = 0;
-    if (cm > -__builtin_inff()) {
-      z = ws.csum[row * ws.chunks + tid];
-      if (cm != top) z = (uint64_t)rint((double)z * w.weight(cm));
-    }
+    for (int c = c0; c < c1; c++) z += chunk_mass(c);
     const uint64_t upto = block_scan(z, &total, sc);
     if (r.p == 1.f) {  // no filter: the chunk, then the token by weights relative to the chunk's maximum
       const uint64_t target = scaled_floor(r.u, total);
-      uint64_t left, cbits;
-      const int c = block_first(upto > target, target - (upto - z), (uint64_t)__float_as_uint(cm), &left, &cbits, sc);
-      const float m = __uint_as_float((uint32_t)cbits);
+      uint64_t left = target - (upto - z), mine = (uint64_t)c0, chunk;
+      if (upto > target && upto - z <= target)
+        for (int c = c0; c < c1; c++) {
+          const uint64_t x = chunk_mass(c);
+          mine = (uint64_t)c;
+          if (x > left) break;
+          left -= x;
+        }
+      block_first(upto > target, left, mine, &left, &chunk, sc);
+      const int c = (int)chunk;
+      const float m = cmax[c];
+      if (m != top) left = min((uint64_t)((double)left / w.weight(m)), csum[c] - 1);
       const SampleWeight wc(m, r.T, ws.shift);
-      if (m != top) {
-        const uint64_t all = ws.csum[row * ws.chunks + c];
-        left = min((uint64_t)((double)left / w.weight(m)), all - 1);
-      }
-      const int id = block_pick(c * kChunk, min(V, (c + 1) * kChunk), left, [&](int v) {
-        const float l = src.logit(v);
-        return l > -__builtin_inff() ? wc.fixed(l) : 0ull;
-      }, sc);
+      const int id = block_pick(src, c * kChunk, min(V, (c + 1) * kChunk), left,
+                                [&](float l, int) { return wc.fixed(l); }, sc);
       sample_store(s, row, id, w.weight(src.logit(id)), total, ws.shift);
       return;
     }
   }
 
-  // A key that every kept token (for top-p after top-k: every one of the first k)
-  // reaches; 0: none found.
-  const float* gmax = ws.gmax + row * ws.groups;
-  uint32_t bound = 0;
+  // Tokens nearer to the largest logit than `limit` are gathered: among them is every
+  // kept token (for top-p after top-k: every one of the first k); 0: no bound found.
+  uint32_t limit = 0;
+  constexpr int G = kMaxGroups / kRowThreads;  // consecutive groups of a thread, kept in registers
+  float gm[G];
+#pragma unroll
+  for (int q = 0; q < G; q++) {
+    const int g = G * tid + q;
+    gm[q] = g < ws.groups ? ws.gmax[row * ws.groups + g] : -__builtin_inff();
+  }
   const uint64_t p_mass = r.p < 1.f && r.k == 0 ? scaled_ceil(r.p, total) : 0;
   if (r.k > 0 || p_mass > 0) {
-    sh.h.count[tid] = 0;
-    sh.h.mass[tid] = 0;
-    __syncthreads();
-    for (int g = tid; g < ws.groups; g += kSampleThreads) {
-      const float m = gmax[g];
-      if (m > -__builtin_inff()) {
-        const int b = sample_bin(m, top);
-        atomicAdd(&sh.h.count[b], 1u);
-        if (p_mass > 0) atomicAdd((unsigned long long*)&sh.h.mass[b], (unsigned long long)w.fixed(m));
-      }
-    }
-    __syncthreads();
-    uint64_t all, unused1, unused2;
-    const uint64_t upto = block_scan(r.k > 0 ? (uint64_t)sh.h.count[tid] : sh.h.mass[tid], &all, sc);
-    const int b = block_first(upto >= (r.k > 0 ? (uint64_t)r.k : p_mass), 0, 0, &unused1, &unused2, sc);
-    if (b >= 0) bound = sample_bin_floor(b, top);
-  }
-  uint32_t minp_key = 1;
-  if (r.minp > 0.f) {
-    minp_key = sample_minp_key(w, top, r.minp);
-    // top-p after top-k needs the mass of all of the first k
-    if (!(r.k > 0 && r.p < 1.f)) bound = max(bound, minp_key);
-  }
-  if (bound == 0 && V <= kList) bound = 1;
-
-  // the groups that reach the bound, then their tokens that do, both in id order
-  int n = -1;
-  if (bound != 0) {
-    const int per = (ws.groups + kSampleThreads - 1) / kSampleThreads;
-    const int g0 = tid * per, g1 = min(g0 + per, ws.groups);
-    uint32_t mine = 0;
-    for (int g = g0; g < g1; g++) mine += sample_key(gmax[g]) >= bound;
-    uint64_t ng;
-    uint32_t at = (uint32_t)block_scan(mine, &ng, sc) - mine;
-    if (ng <= kList) {
-      for (int g = g0; g < g1; g++)
-        if (sample_key(gmax[g]) >= bound) sh.groups[at++] = (uint32_t)g;
-      __syncthreads();
-      const int items = (int)ng << ws.group_log2;
-      const int seg = ((items + kSampleThreads - 1) / kSampleThreads) * 64;  // per wave, whole wave steps
-      const int i0 = wv * seg, i1 = min(i0 + seg, items);
-      auto key_at = [&](int i, int* v) {
-        *v = (int)(sh.groups[i >> ws.group_log2] << ws.group_log2) + (i & ((1 << ws.group_log2) - 1));
-        return *v < V ? sample_key(src.logit(*v)) : 0u;
-      };
-      uint32_t hits = 0;
-      for (int i = i0; i < i1; i += 64) {
-        int v;
-        const bool hit = i + lane < i1 && key_at(i + lane, &v) >= bound;
-        hits += (uint32_t)__popcll(__ballot(hit));
-      }
-      if (lane == 0) sh.wave_count[wv] = hits;
-      __syncthreads();
-      uint32_t base = 0, sum = 0;
 #pragma unroll
-      for (int i = 0; i < kSampleWaves; i++) {
-        if (i < wv) base += sh.wave_count[i];
-        sum += sh.wave_count[i];
+    for (int q = 0; q < G; q++)
+      if (gm[q] > -__builtin_inff()) {
+        const int b = sample_bin(gm[q], top);
+        atomicAdd(&sh.h.count[b], 1u);
+        if (p_mass > 0) atomicAdd((unsigned long long*)&sh.h.mass[b], (unsigned long long)w.fixed(gm[q]));
       }
-      if (sum <= kList) {
-        n = (int)sum;
-        for (int i = i0; i < i1; i += 64) {
-          int v = 0;
-          const uint32_t key = i + lane < i1 ? key_at(i + lane, &v) : 0u;
-          const uint64_t m = __ballot(key >= bound);
-          if (key >= bound) {
-            const uint64_t x = ((uint64_t)key << 32) | (uint32_t)~(uint32_t)v;
-            const uint32_t to = base + (uint32_t)__popcll(m & ((1ull << lane) - 1));
-            sh.list[to] = x;
-            sh.sorted[to] = x;
-          }
-          base += (uint32_t)__popcll(m);
+    __syncthreads();
+    constexpr int Q = kSampleBins / kRowThreads;
+    uint64_t x[Q], sum = 0, all, bin;
+#pragma unroll
+    for (int q = 0; q < Q; q++) {
+      x[q] = r.k > 0 ? (uint64_t)sh.h.count[Q * tid + q] : sh.h.mass[Q * tid + q];
+      sum += x[q];
+    }
+    const uint64_t goal = r.k > 0 ? (uint64_t)r.k : p_mass, upto = block_scan(sum, &all, sc);
+    uint64_t run = upto;
+    int mine = Q * tid;
+#pragma unroll
+    for (int q = Q - 1; q >= 0; q--) {
+      if (run >= goal) mine = Q * tid + q;  // the first bin that reaches the goal
+      run -= x[q];
+    }
+    if (block_first(upto >= goal, (uint64_t)mine, 0, &bin, &unused, sc) >= 0) limit = sample_bin_limit((int)bin);
+  }
+  if (r.minp > 0.f && !(r.k > 0 && r.p < 1.f)) {  // top-p after top-k needs the mass of all of the first k
+    // w >= minp means a distance of at most -T ln(minp); 2^-16 of it and 1e-14 T cover
+    // the rounding of this product, of the distances and of the weights
+    const float most = r.T * (-logf(r.minp) * (1.f + 1.52587890625e-5f) + 1e-14f) + 1.17549435e-38f;
+    const uint32_t lim = most < __builtin_inff() ? __float_as_uint(most) + 1 : 0xffffffffu;
+    limit = limit == 0 ? lim : min(limit, lim);
+  }
+  if (limit == 0 && V <= kList) limit = 0xffffffffu;
+
+  // the groups within the limit, then their tokens that are, both in id order
+  int n = -1;
+  if (limit != 0) {
+    auto near = [&](float l) { return l > -__builtin_inff() && sample_dist(l, top) < limit; };
+    uint32_t mine = 0;
+#pragma unroll
+    for (int q = 0; q < G; q++) mine += near(gm[q]);
+    uint64_t ng;
+    uint32_t at = (uint32_t)block_scan((uint64_t)mine, &ng, sc) - mine;
+    if (ng <= kList) {
+#pragma unroll
+      for (int q = 0; q < G; q++)
+        if (near(gm[q])) sh.groups[at++] = (uint32_t)(G * tid + q);
+      __syncthreads();
+      // rounds of U loads per lane, a wave's loads consecutive
+      constexpr int N = SampleSource<DT>::N, U = 16 / N;
+      const int items = (int)ng << ws.group_log2;
+      uint32_t base = 0;
+      n = 0;
+      for (int r0 = 0; r0 < items && n >= 0; r0 += kRowThreads * N * U) {
+        float l[U][N];
+        int v[U];
+        uint32_t hits = 0;
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+          const int i = r0 + ((wv * U + u) * 64 + lane) * N;
+          v[u] = V;
+          if (i < items)
+            v[u] = (int)(sh.groups[i >> ws.group_log2] << ws.group_log2) + (i & ((1 << ws.group_log2) - 1));
+          src.load(v[u], l[u]);
         }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+#pragma unroll
+          for (int j = 0; j < N; j++) hits += near(l[u][j]);
+        // places in (wave, u, lane, j) order
+        uint32_t wave_hits = hits;
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) wave_hits += __shfl_xor(wave_hits, off, 64);
+        if (lane == 0) sh.wave_count[wv] = wave_hits;
+        __syncthreads();
+        uint32_t to = base, sum = 0;
+#pragma unroll
+        for (int i = 0; i < kRowWaves; i++) {
+          const uint32_t x = sh.wave_count[i];
+          if (i < wv) to += x;
+          sum += x;
+        }
+        if (base + sum > kList) {
+          n = -1;  // whole workgroup
+        } else if (wave_hits != 0) {
+#pragma unroll
+          for (int u = 0; u < U; u++) {
+            uint32_t c = 0;
+#pragma unroll
+            for (int j = 0; j < N; j++) c += near(l[u][j]);
+            if (__ballot(c != 0) == 0) continue;
+            uint32_t upto = c;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+              const uint32_t o = __shfl_up(upto, off, 64);
+              if (lane >= off) upto += o;
+            }
+            uint32_t place = to + upto - c;
+#pragma unroll
+            for (int j = 0; j < N; j++)
+              if (near(l[u][j]))
+                sh.list[place++] = ((uint64_t)score_ord(l[u][j]) << 32) | (uint32_t)~(uint32_t)(v[u] + j);
+            to += __builtin_amdgcn_readlane(upto, 63);
+          }
+        }
+        base += sum;
+        if (n >= 0) n = (int)base;
+        __syncthreads();
       }
     }
   }
-  if (n < 0) {  // too many tokens for the list
-    if (heavy) {
-      if (tid == 0) sc.index[0] = atomicAdd(ws.nheavy, 1u);
-      __syncthreads();
-      const uint32_t slot = sc.index[0];
-      if (slot < (uint32_t)ws.slots) {
-        if (tid == 0) ws.flag[row] = (int32_t)slot;
-        return;
-      }
+  if (n < 0) {  // too many tokens for the list: a heavy row, -2 past the histogram slots
+    if (tid == 0) {
+      const uint32_t slot = atomicAdd(ws.nheavy, 1u);
+      ws.flag[row] = slot < (uint32_t)ws.slots ? (int32_t)slot : -2;
     }
-    __syncthreads();
-    sample_by_passes<DT>(s, row, top, ws.shift, sh.h, sc);
     return;
   }
-
-  // sort descending (bitonic, empty entries 0 last)
-  int size = 64;
-  while (size < n) size <<= 1;
-  for (int i = n + tid; i < size; i += kSampleThreads) {
-    sh.sorted[i] = 0;
-    sh.list[i] = 0;
-  }
   __syncthreads();
-  for (int len = 2; len <= size; len <<= 1) {
-    for (int step = len >> 1; step > 0; step >>= 1) {
-      for (int i = tid; i < size / 2; i += kSampleThreads) {
-        const int a = 2 * step * (i / step) + i % step, b = a + step;
-        const uint64_t x = sh.sorted[a], y = sh.sorted[b];
-        if ((x < y) == ((a & len) == 0)) {
-          sh.sorted[a] = y;
-          sh.sorted[b] = x;
+
+  // sort descending: by counting for short lists, else bitonic with empty entries 0 last
+  int size = kRowThreads;
+  while (size < n) size <<= 1;
+  if (size == kRowThreads) {
+    const uint64_t x = tid < n ? sh.list[tid] : 0;
+    int rank = 0;
+    for (int i = 0; i < n; i++) rank += sh.list[i] > x;
+    if (tid < n) sh.sorted[rank] = x;
+    __syncthreads();
+  } else {
+    for (int i = tid; i < size; i += kRowThreads) sh.sorted[i] = i < n ? sh.list[i] : 0;
+    __syncthreads();
+    for (int len = 2; len <= size; len <<= 1) {
+      for (int step = len >> 1; step > 0; step >>= 1) {
+        for (int i = tid; i < size / 2; i += kRowThreads) {
+          const int a = 2 * step * (i / step) + i % step, b = a + step;
+          const uint64_t x = sh.sorted[a], y = sh.sorted[b];
+          if ((x < y) == ((a & len) == 0)) {
+            sh.sorted[a] = y;
+            sh.sorted[b] = x;
+          }
         }
+        __syncthreads();
       }
-      __syncthreads();
     }
   }
 
-  // prefix masses in the row's order, two tokens per thread; the number kept
-  static_assert(kList == 2 * kSampleThreads, "two tokens per thread");
-  const uint64_t x0 = sh.sorted[min(2 * tid, size - 1)], x1 = sh.sorted[min(2 * tid + 1, size - 1)];
-  const bool have0 = 2 * tid < n, have1 = 2 * tid + 1 < n;
-  const float l0 = ord_score((uint32_t)(x0 >> 32)), l1 = ord_score((uint32_t)(x1 >> 32));
-  const uint64_t m0 = have0 ? w.fixed(l0) : 0, m1 = have1 ? w.fixed(l1) : 0;
-  uint64_t all;
-  const uint64_t upto1 = block_scan(m0 + m1, &all, sc), upto0 = upto1 - m1;
-  uint64_t n_keep = (uint64_t)n, unused;
-  if (r.k > 0) n_keep = min(n_keep, (uint64_t)r.k);
+  // prefix masses in the row's order, `per` tokens per thread; the number kept
+  const int per = size / kRowThreads, e0 = tid * per, e1 = min(e0 + per, n);
+  auto logit_of = [](uint64_t x) { return ord_score((uint32_t)(x >> 32)); };
+  uint64_t sum = 0, reach = 0, all;
+  for (int e = e0; e < e1; e++) {
+    const uint64_t m = w.fixed(logit_of(sh.sorted[e]));
+    sh.mass[e] = m;
+    sum += m;
+    if (r.minp > 0.f) reach += w.weight(logit_of(sh.sorted[e])) >= (double)r.minp;
+  }
+  const uint64_t upto = block_scan(sum, &all, sc);
+  int n_keep = n;
+  if (r.k > 0) n_keep = min(n_keep, r.k);
   uint64_t goal = p_mass;
   if (r.p < 1.f && r.k > 0) {  // mass of the first k
-    uint64_t mass = 0;
-    const uint64_t last = n_keep - 1;
-    block_first((uint64_t)tid == last / 2, last & 1 ? upto1 : upto0, 0, &mass, &unused, sc);
+    uint64_t run = upto - sum, mass = 0;
+    for (int e = e0; e < min(e1, n_keep); e++) run += sh.mass[e];
+    block_first(e0 <= n_keep - 1 && n_keep - 1 < e0 + per, run, 0, &mass, &unused, sc);
     goal = scaled_ceil(r.p, mass);
   }
   if (goal > 0) {
-    uint64_t len = 0;
-    const bool in0 = have0 && upto0 >= goal, in1 = have1 && upto1 >= goal;
-    if (block_first(in0 || in1, (uint64_t)(2 * tid + (in0 ? 1 : 2)), 0, &len, &unused, sc) >= 0)
-      n_keep = min(n_keep, len);
+    uint64_t run = upto - sum, len = 0;
+    int mine = e0;
+    while (mine < e1 && run < goal) run += sh.mass[mine++];
+    if (block_first(upto >= goal && e0 < e1, (uint64_t)mine, 0, &len, &unused, sc) >= 0) n_keep = min(n_keep, (int)len);
   }
   if (r.minp > 0.f) {
-    uint64_t reach;
-    block_scan((uint64_t)(have0 && (uint32_t)(x0 >> 32) >= minp_key) + (have1 && (uint32_t)(x1 >> 32) >= minp_key), &reach,
-               sc);
-    n_keep = min(n_keep, reach);
+    uint64_t reached;
+    block_scan(reach, &reached, sc);
+    n_keep = min(n_keep, (int)reached);
   }
   const uint64_t last = sh.sorted[n_keep - 1];
 
   // the pick, in id order
-  const uint64_t y0 = sh.list[min(2 * tid, size - 1)], y1 = sh.list[min(2 * tid + 1, size - 1)];
-  const uint64_t k0 = have0 && y0 >= last ? w.fixed(ord_score((uint32_t)(y0 >> 32))) : 0;
-  const uint64_t k1 = have1 && y1 >= last ? w.fixed(ord_score((uint32_t)(y1 >> 32))) : 0;
-  const uint64_t sum1 = block_scan(k0 + k1, &total, sc);
+  sum = 0;
+  for (int e = e0; e < e1; e++) {
+    const uint64_t x = sh.list[e];
+    sum += x >= last ? w.fixed(logit_of(x)) : 0;
+  }
+  const uint64_t to = block_scan(sum, &total, sc);
   const uint64_t target = scaled_floor(r.u, total);
-  uint64_t got = 0;
-  block_first(sum1 > target, sum1 - k1 > target ? y0 : y1, 0, &got, &unused, sc);
-  sample_store(s, row, (int)~(uint32_t)got, w.weight(ord_score((uint32_t)(got >> 32))), total, ws.shift);
+  uint64_t run = to - sum, mine = 0, got = 0;
+  if (to > target && run <= target)
+    for (int e = e0; e < e1; e++) {
+      const uint64_t x = sh.list[e];
+      mine = x;
+      run += x >= last ? w.fixed(logit_of(x)) : 0;
+      if (run > target) break;
+    }
+  block_first(to > target, mine, 0, &got, &unused2, sc);
+  sample_store(s, row, (int)~(uint32_t)got, w.weight(logit_of(got)), total, ws.shift);
 }
 
 // ---------------------------------------------------------------------------
@@ -792,7 +893,7 @@ __device__ __forceinline__ float sample_top(const SamplePtrs& ws, int64_t row) {
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kSampleThreads) sample_hist_kernel(Sample s, SamplePtrs ws) {
+__global__ void __launch_bounds__(kSampleThreads, 4) sample_hist_kernel(Sample s, SamplePtrs ws) {
   constexpr int N = SampleSource<DT>::N;
   __shared__ SampleHist h;
   const int tid = threadIdx.x, c = blockIdx.x;
@@ -806,17 +907,20 @@ __global__ void __launch_bounds__(kSampleThreads) sample_hist_kernel(Sample s, S
     h.count[tid] = 0;
     h.mass[tid] = 0;
     __syncthreads();
-    const int end = min(src.V, (c + 1) * kSlice);
-    for (int v = c * kSlice + tid * N; v < end; v += kSampleThreads * N) {
-      float l[N];
-      src.load(v, l);
+    constexpr int U = 16 / N;
+    for (int at = c * kSlice; at < min(src.V, (c + 1) * kSlice); at += kSampleThreads * N * U) {
+      float l[U][N];
 #pragma unroll
-      for (int j = 0; j < N; j++)
-        if (l[j] > -__builtin_inff()) {
-          const int b = sample_bin(l[j], top);
-          atomicAdd(&h.count[b], 1u);
-          atomicAdd((unsigned long long*)&h.mass[b], (unsigned long long)w.fixed(l[j]));
-        }
+      for (int u = 0; u < U; u++) src.load(at + (u * kSampleThreads + tid) * N, l[u]);
+#pragma unroll
+      for (int u = 0; u < U; u++)
+#pragma unroll
+        for (int j = 0; j < N; j++)
+          if (l[u][j] > -__builtin_inff()) {
+            const int b = sample_bin(l[u][j], top);
+            atomicAdd(&h.count[b], 1u);
+            atomicAdd((unsigned long long*)&h.mass[b], (unsigned long long)w.fixed(l[u][j]));
+          }
     }
     __syncthreads();
     const size_t at = ((size_t)slot * ws.slices + c) * kSampleBins + tid;
@@ -827,7 +931,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_hist_kernel(Sample s, S
 }
 
 struct SampleHeavyShared {
-  SampleScratch sc;
+  SampleScratch<kSampleWaves> sc;
   SampleHist h;
   uint64_t list[kHeavyList];
   uint64_t slice[kMaxSlices];
@@ -835,102 +939,107 @@ struct SampleHeavyShared {
 };
 
 template <int DT>
-__global__ void __launch_bounds__(kSampleThreads) sample_heavy_kernel(Sample s, SamplePtrs ws) {
+__global__ void __launch_bounds__(kSampleThreads, 4) sample_heavy_kernel(Sample s, SamplePtrs ws) {
   __shared__ SampleHeavyShared sh;
-  SampleScratch& sc = sh.sc;
+  SampleScratch<kSampleWaves>& sc = sh.sc;
   const int64_t row = blockIdx.x;
   const int slot = ws.flag[row];
-  if (slot < 0) return;  // whole workgroup
+  if (slot == -1) return;  // whole workgroup
+  const bool hist = slot >= 0;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const SampleSource<DT> src(s, row);
   const SampleRow r = sample_row(s, row);
   const float top = sample_top(ws, row);
+  const uint32_t top_key = score_ord(top);
   const SampleWeight w(top, r.T, ws.shift);
-  const uint32_t* hcount = ws.hcount + (size_t)slot * ws.slices * kSampleBins;
-  const uint64_t* hmass = ws.hmass + (size_t)slot * ws.slices * kSampleBins;
+  const uint32_t* hcount = ws.hcount + (size_t)(hist ? slot : 0) * ws.slices * kSampleBins;
+  const uint64_t* hmass = ws.hmass + (size_t)(hist ? slot : 0) * ws.slices * kSampleBins;
 
   // the row's histogram, bin 0 (the largest logits) first
-  uint64_t c = 0, m = 0, tc, tm;
-  for (int i = 0; i < ws.slices; i++) {
-    c += hcount[i * kSampleBins + tid];
-    m += hmass[i * kSampleBins + tid];
+  uint64_t c = 0, m = 0, tc = 0, tm = 0, ic = 0, im = 0;
+  if (hist) {
+    for (int i = 0; i < ws.slices; i++) {
+      c += hcount[i * kSampleBins + tid];
+      m += hmass[i * kSampleBins + tid];
+    }
+    ic = block_scan(c, &tc, sc);
+    im = block_scan(m, &tm, sc);
   }
-  const uint64_t ic = block_scan(c, &tc, sc), im = block_scan(m, &tm, sc);
 
-  // f over the tokens of one bin: from the list if they fit there, else by a pass over the row
+  // the tokens of one bin
+  SampleRange<kSampleThreads, DT> range(src, sh.list, &sh.n);
   int listed = -1;
-  uint32_t klo = 1, khi = 0;
-  int n = -1;
+  uint32_t klo = 1, khi = top_key;
   auto bin_open = [&](int b) {
     if (listed == b) return;
     listed = b;
     klo = sample_bin_floor(b, top);
-    khi = b == 0 ? score_ord(top) : sample_bin_floor(b - 1, top) - 1;
+    khi = b == 0 ? top_key : sample_bin_floor(b - 1, top) - 1;
     uint64_t in_bin, unused;
     block_first(tid == b, c, 0, &in_bin, &unused, sc);
-    n = -1;
-    if (in_bin > kHeavyList) return;
-    if (tid == 0) sh.n = 0;
-    __syncthreads();
-    sample_each<DT>(src, [&](uint32_t key, uint32_t id) {
-      if (key >= klo && key <= khi) sh.list[atomicAdd(&sh.n, 1u)] = ((uint64_t)key << 32) | id;
-    });
-    __syncthreads();
-    n = (int)sh.n;
-  };
-  auto each = [&](auto f) {
-    if (n >= 0) {
-      for (int i = tid; i < n; i += kSampleThreads) f((uint32_t)(sh.list[i] >> 32), (uint32_t)sh.list[i]);
-    } else {
-      sample_each<DT>(src, f);
-    }
+    range.gather(klo, khi, in_bin);
   };
   SampleCut cut;
-  uint64_t mass = tm, bc, bm;
-  if (r.k > 0) {
-    const int b = block_first(ic >= (uint64_t)r.k, ic - c, im - m, &bc, &bm, sc);
-    if (b >= 0) {  // else there are fewer candidates than k
-      bin_open(b);
-      mass = sample_find(each, w, src.V, &cut, klo, khi, true, (uint64_t)r.k, 0, bc, bm, sh.h, sc);
-    }
+  auto kept = [&](float l, int v) {
+    const uint32_t key = score_ord(l);
+    return cut.keeps(key, (uint32_t)v) ? w.fixed(l) : 0ull;
+  };
+  auto kept_mass = [&]() {  // by a pass over the row
+    uint64_t z = 0, all;
+    sample_each<kSampleThreads>(src, [&](uint32_t key, uint32_t id) { z += kept(ord_score(key), (int)id); });
+    block_scan(z, &all, sc);
+    return all;
+  };
+  uint64_t mass = tm, bc = 0, bm = 0;
+  if (r.k > 0 && (!hist || tc >= (uint64_t)r.k)) {  // else there are fewer candidates than k
+    if (hist) bin_open(block_first(ic >= (uint64_t)r.k, ic - c, im - m, &bc, &bm, sc));
+    const bool whole = range.n >= 0;
+    mass = sample_find(range, w, &cut, klo, khi, true, (uint64_t)r.k, 0, bc, bm, sh.h, sc);
+    if (!whole) listed = -1, range.n = -1;  // the search may have listed a part of the range
+  } else if (!hist && r.p < 1.f) {
+    mass = kept_mass();
   }
   if (r.p < 1.f) {
     const uint64_t goal = scaled_ceil(r.p, mass);
-    const int b = block_first(im >= goal, ic - c, im - m, &bc, &bm, sc);
-    bin_open(b);
-    sample_find(each, w, src.V, &cut, klo, khi, false, 0, goal, bc, bm, sh.h, sc);
+    if (hist) bin_open(block_first(im >= goal, ic - c, im - m, &bc, &bm, sc));
+    const bool whole = range.n >= 0;
+    sample_find(range, w, &cut, klo, khi, false, 0, goal, bc, bm, sh.h, sc);
+    if (!whole) listed = -1, range.n = -1;
   }
   if (r.minp > 0.f) {
     const uint32_t key = sample_minp_key(w, top, r.minp);
     if (key > cut.key) cut.key = key, cut.id = 0xffffffffu;
   }
-
-  // the kept mass of each slice: whole bins above the cut's, the kept tokens of that one
-  const int b = sample_bin(ord_score(cut.key), top);
-  bin_open(b);
-  if (tid < ws.slices) sh.slice[tid] = 0;
-  __syncthreads();
-  for (int i = wv; i < ws.slices; i += kSampleWaves) {
-    uint64_t z = 0;
-    for (int j = lane; j < b; j += 64) z += hmass[i * kSampleBins + j];
-    z = wave_scan_u64(z);
-    if (lane == 63) atomicAdd((unsigned long long*)&sh.slice[i], (unsigned long long)z);
-  }
-  each([&](uint32_t key, uint32_t id) {
-    if (key >= klo && key <= khi && cut.keeps(key, id))
-      atomicAdd((unsigned long long*)&sh.slice[id / kSlice], (unsigned long long)w.fixed(ord_score(key)));
-  });
-  __syncthreads();
+  int first = 0, end = src.V;
   uint64_t total, left, unused;
-  const uint64_t z = tid < ws.slices ? sh.slice[tid] : 0;
-  const uint64_t upto = block_scan(z, &total, sc);
-  const uint64_t target = scaled_floor(r.u, total);
-  const int i = block_first(upto > target, target - (upto - z), 0, &left, &unused, sc);
-  const int id = block_pick(i * kSlice, min(src.V, (i + 1) * kSlice), left, [&](int v) {
-    const float l = src.logit(v);
-    const uint32_t key = sample_key(l);
-    return key != 0 && cut.keeps(key, (uint32_t)v) ? w.fixed(l) : 0ull;
-  }, sc);
+  if (hist) {
+    // the kept mass of each slice: whole bins above the cut's, the kept tokens of that one
+    const int b = sample_bin(ord_score(cut.key), top);
+    bin_open(b);
+    if (tid < ws.slices) sh.slice[tid] = 0;
+    __syncthreads();
+    for (int i = wv; i < ws.slices; i += kSampleWaves) {
+      uint64_t z = 0;
+      for (int j = lane; j < b; j += 64) z += hmass[i * kSampleBins + j];
+      z = wave_scan_u64(z);
+      if (lane == 63) atomicAdd((unsigned long long*)&sh.slice[i], (unsigned long long)z);
+    }
+    range.each([&](uint32_t key, uint32_t id) {
+      if (key >= klo && key <= khi && cut.keeps(key, id))
+        atomicAdd((unsigned long long*)&sh.slice[id / kSlice], (unsigned long long)w.fixed(ord_score(key)));
+    });
+    __syncthreads();
+    const uint64_t z = tid < ws.slices ? sh.slice[tid] : 0;
+    const uint64_t upto = block_scan(z, &total, sc);
+    left = scaled_floor(r.u, total);
+    const int i = block_first(upto > left, left - (upto - z), 0, &left, &unused, sc);
+    first = i * kSlice;
+    end = min(src.V, first + kSlice);
+  } else {
+    total = kept_mass();
+    left = scaled_floor(r.u, total);
+  }
+  const int id = block_pick(src, first, end, left, kept, sc);
   sample_store(s, row, id, w.weight(src.logit(id)), total, ws.shift);
 }
 
@@ -941,15 +1050,16 @@ size_t sample_workspace(int64_t rows, int64_t vocab) {
 }
 
 template <int DT>
-static hipError_t launch_sample_dt(const Sample& s, const SamplePtrs& ws, bool heavy, hipStream_t stream) {
-  const unsigned y = (unsigned)std::min<int64_t>(s.rows, 32768);
-  hipLaunchKernelGGL((sample_chunk_kernel<DT>), dim3((unsigned)ws.chunks, y), dim3(kChunkThreads), 0, stream, s, ws);
-  hipLaunchKernelGGL((sample_row_kernel<DT>), dim3((unsigned)s.rows), dim3(kSampleThreads), 0, stream, s, ws,
-                     (int)heavy);
-  if (heavy) {
-    hipLaunchKernelGGL((sample_hist_kernel<DT>), dim3((unsigned)ws.slices, y), dim3(kSampleThreads), 0, stream, s, ws);
+static hipError_t launch_sample_dt(const Sample& s, const SamplePtrs& ws, bool filtered, bool flat, hipStream_t stream) {
+  const int64_t units = s.rows * ws.chunks;
+  hipLaunchKernelGGL((sample_chunk_kernel<DT>), dim3((unsigned)cdiv(units, kChunkThreads / 64)), dim3(kChunkThreads), 0,
+                     stream, s, ws);
+  hipLaunchKernelGGL((sample_row_kernel<DT>), dim3((unsigned)s.rows), dim3(kRowThreads), 0, stream, s, ws);
+  if (flat)
+    hipLaunchKernelGGL((sample_hist_kernel<DT>), dim3((unsigned)ws.slices, (unsigned)std::min<int64_t>(s.rows, 32768)),
+                       dim3(kSampleThreads), 0, stream, s, ws);
+  if (filtered)
     hipLaunchKernelGGL((sample_heavy_kernel<DT>), dim3((unsigned)s.rows), dim3(kSampleThreads), 0, stream, s, ws);
-  }
   return hipGetLastError();
 }
 
@@ -972,16 +1082,17 @@ hipError_t launch_sample(const Sample& s, void* space, hipStream_t stream) {
   int bits = 0;
   while ((1ll << bits) < s.vocab) bits++;
   p.shift = std::min(45, 63 - bits);
-  // Rows whose settings may keep more than the list holds: the histogram kernels are
-  // launched for them.  With one small k for all rows only ties can overflow the list,
-  // which the row kernel then sorts out by itself.
+  // Rows that keep more than the list holds are left to the heavy kernel, with the
+  // histograms where their settings may ask for it: with one small k for all rows only
+  // ties overflow the list, and the heavy kernel does without (no slots).
   const bool small_k = s.d_top_k == nullptr && s.top_k > 0 && s.top_k <= kList / 2;
-  const bool no_filter = s.d_top_k == nullptr && s.top_k == 0 && s.d_top_p == nullptr && s.top_p == 1.f &&
-                         s.d_min_p == nullptr && s.min_p == 0.f;
-  const bool heavy = s.vocab > kList && !small_k && !no_filter;
-  if (s.dtype == DT_F32) return launch_sample_dt<DT_F32>(s, p, heavy, stream);
-  if (s.dtype == DT_BF16) return launch_sample_dt<DT_BF16>(s, p, heavy, stream);
-  return launch_sample_dt<DT_F16>(s, p, heavy, stream);
+  const bool no_filter = s.temperature > 0.f && s.d_temperature == nullptr && s.d_top_k == nullptr && s.top_k == 0 &&
+                         s.d_top_p == nullptr && s.top_p == 1.f && s.d_min_p == nullptr && s.min_p == 0.f;
+  const bool filtered = s.vocab > kList && !no_filter, flat = filtered && !small_k;
+  if (!flat) p.slots = 0;
+  if (s.dtype == DT_F32) return launch_sample_dt<DT_F32>(s, p, filtered, flat, stream);
+  if (s.dtype == DT_BF16) return launch_sample_dt<DT_BF16>(s, p, filtered, flat, stream);
+  return launch_sample_dt<DT_F16>(s, p, filtered, flat, stream);
 }
 
 }  // namespace etg
