@@ -3,6 +3,8 @@
 // The sum is exact: |sum| <= 65536 * 128 * 128 = 2^30 fits the int32 accumulators.
 // Its conversion to f32 and the two multiplications round to nearest (relative
 // error at most 3 * 2^-24), the store in T once more.
+#include <algorithm>
+
 #include "etg_device.hpp"
 #include "etg_internal.hpp"
 
@@ -64,19 +66,294 @@ __global__ void __launch_bounds__(256) matmul_i8_kernel(
   }
 }
 
-size_t matmul_i8_workspace(int64_t, int64_t, int64_t) { return 0; }
+// ---------------------------------------------------------------------------
+// Streaming kernels: few a rows, bound by reading w once.
+//
+// The a rows are the B operand of v_mfma_i32_16x16x64_i8, kept as an image in the order
+// in which the lanes read it: 1 KiB per K step of 64 and tile of 16 a rows, lane l's 16
+// bytes at 16 l (a row 16 t + l % 16, bytes of K slot 4 step + l / 16).  K slot j stands
+// for the 16 bytes at k = min(16 j, K - 16): where K is no multiple of 16 the last slot
+// overlaps the one before, and the image holds zeros for the bytes that are covered
+// twice and for slots and rows past the end.  So w rows of any length are read by
+// 16-byte loads that stay inside the row.
+// ---------------------------------------------------------------------------
+// The image's 16 bytes for a row `row` (nullptr: past the end) and slot j.
+__device__ __forceinline__ i32x4 image_slot(const int8_t* row, int j, int K) {
+  i32x4 v = {0, 0, 0, 0};
+  if (row == nullptr || 16 * j >= K) return v;
+  const int k = min(16 * j, K - 16), twice = 16 * j - k;  // bytes of the slot before
+  __builtin_memcpy(&v, row + k, 16);
+  if (twice != 0) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int cut = min(max(twice - 4 * i, 0), 4);
+      v[i] = cut == 4 ? 0 : (int)((uint32_t)v[i] & (0xffffffffu << (8 * cut)));
+    }
+  }
+  return v;
+}
 
-hipError_t launch_matmul_i8(const MatmulI8& p, void*, hipStream_t stream) {
-  const dim3 grid((unsigned)cdiv(p.n, 64), (unsigned)cdiv(p.m, 16));
-#define ETG_MATMUL(DT)                                                                                             \
-  hipLaunchKernelGGL((matmul_i8_kernel<DT>), grid, dim3(256), 0, stream, p.a, p.a_stride, p.a_scale,               \
-                     p.a_scale_stride, p.w, p.w_stride, p.w_scale, p.w_scale_stride, p.m, p.n, (int)p.k, p.out,    \
-                     p.out_stride)
-  if (p.out_dtype == DT_F32) ETG_MATMUL(DT_F32);
-  else if (p.out_dtype == DT_BF16) ETG_MATMUL(DT_BF16);
-  else ETG_MATMUL(DT_F16);
-#undef ETG_MATMUL
+// Stores of one 16 x 16 tile: lane l has w rows n0 .. n0 + 3 of a row m (values acc).
+template <int DT>
+__device__ __forceinline__ void store_tile4(void* out, int64_t out_stride, int64_t m, int64_t n0, int64_t N, i32x4 acc,
+                                            float s, const float (&w4)[4], bool vec) {
+  float x[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) x[i] = (float)acc[i] * s * w4[i];
+  const int64_t at = m * out_stride + n0;
+  if (vec && n0 + 4 <= N) {  // rows of the output start at multiples of four values
+    if constexpr (DT == DT_F32) {
+      *(f32x4*)((float*)out + at) = f32x4{x[0], x[1], x[2], x[3]};
+    } else {
+      typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
+      u16x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        if constexpr (DT == DT_BF16) {
+          v[i] = __builtin_bit_cast(unsigned short, (__bf16)x[i]);
+        } else {
+          asm volatile("" : "+v"(x[i]));  // as in store_out
+          v[i] = __builtin_bit_cast(unsigned short, (_Float16)x[i]);
+        }
+      }
+      *(u16x4*)((uint16_t*)out + at) = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      if (n0 + i < N) store_out<DT>(out, at + i, x[i]);
+  }
+}
+
+// Up to 16 a rows: the whole image in LDS, a persistent grid, each wave a contiguous
+// run of 16-row w tiles.  A lane loads 16 bytes of w row l % 16 at slot 4 step + l / 16;
+// four steps (256 bytes a row) are in flight while the four before are multiplied, across
+// tiles too.
+template <int DT>
+__global__ void __launch_bounds__(1024) stream_i8_kernel(MatmulI8 p, int64_t ntiles, int steps, int vec) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  i32x4* img = (i32x4*)smem;  // [steps][64]
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nw = blockDim.x >> 6, K = (int)p.k;
+  const int64_t wave = (int64_t)blockIdx.x * nw + wv, waves = (int64_t)gridDim.x * nw;
+  const int64_t t0 = wave * ntiles / waves, t1 = (wave + 1) * ntiles / waves;
+
+  i32x4 cur[4], nxt[4];
+  auto row_of = [&](int64_t t) { return p.w + min(t * 16 + (lane & 15), p.n - 1) * p.w_stride; };
+  auto load = [&](const int8_t* row, int step, i32x4 (&v)[4]) {
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      const i32x4* at = (const i32x4*)(row + min(64 * (step + q) + 16 * (lane >> 4), K - 16));
+      typedef i32x4 i32x4u __attribute__((aligned(1)));
+      v[q] = __builtin_nontemporal_load((const i32x4u*)at);
+    }
+  };
+  const int8_t* row = row_of(t0 < t1 ? t0 : 0);
+  if (t0 < t1) load(row, 0, cur);
+  for (int i = threadIdx.x; i < steps * 64; i += blockDim.x) {
+    const int m = i & 15;
+    img[i] = image_slot(m < p.m ? p.a + m * p.a_stride : nullptr, 4 * (i >> 6) + ((i >> 4) & 3), K);
+  }
+  __syncthreads();
+  const int m = lane & 15;
+  const float s = m < p.m ? p.a_scale[m * p.a_scale_stride] : 0.f;
+  for (int64_t t = t0; t < t1; t++) {
+    const int8_t* next_row = row_of(t + 1 < t1 ? t + 1 : t);
+    i32x4 acc = {0, 0, 0, 0};
+    for (int st = 0; st < steps; st += 4) {  // steps is a multiple of 4
+      if (st + 4 < steps) load(row, st + 4, nxt);
+      else load(next_row, 0, nxt);
+#pragma unroll
+      for (int q = 0; q < 4; q++)
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(cur[q], img[(st + q) * 64 + lane], acc, 0, 0, 0);
+#pragma unroll
+      for (int q = 0; q < 4; q++) cur[q] = nxt[q];
+    }
+    row = next_row;
+    if (m < p.m) {
+      const int64_t n = t * 16 + 4 * (lane >> 4);
+      float w4[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) w4[i] = p.w_scale[min(n + i, p.n - 1) * p.w_scale_stride];
+      store_tile4<DT>(p.out, p.out_stride, m, n, p.n, acc, s, w4, vec);
+    }
+  }
+}
+
+// Image of all a rows for the wide kernel: [pass][step][tile of the pass][64 lanes].
+__global__ void __launch_bounds__(256) wide_i8_image_kernel(MatmulI8 p, int nt, int steps, i32x4* __restrict__ img,
+                                                            int64_t total) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  const int lane = (int)(i & 63);
+  const int64_t r = i >> 6;
+  const int t = (int)(r % nt), step = (int)(r / nt % steps);
+  const int64_t m = (r / nt / steps * nt + t) * 16 + (lane & 15);
+  img[i] = image_slot(m < p.m ? p.a + m * p.a_stride : nullptr, 4 * step + (lane >> 4), (int)p.k);
+}
+
+// Passes of up to 16 NT a rows: 8 waves x MT tiles of 16 w rows per workgroup.  The image
+// passes through three LDS buffers of four K steps each, copied by global_load_lds two
+// chunks ahead; the w rows are loaded one chunk ahead into registers.  One barrier per
+// chunk.
+static constexpr int kWideWaves = 8;
+static constexpr int kWideSteps = 4;
+
+template <int DT, int NT, int MT>
+__global__ void __launch_bounds__(64 * kWideWaves, 4) wide_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
+                                                                     int chunks, int vec) {
+  constexpr int CHUNK = kWideSteps * NT * 1024, DMA = CHUNK / 1024 / kWideWaves;
+  static_assert(DMA * kWideWaves * 1024 == CHUNK, "whole DMA instructions per wave");
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [3][CHUNK]
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int K = (int)p.k;
+  const int64_t n0 = ((int64_t)blockIdx.x * kWideWaves + wv) * MT * 16;
+  const unsigned char* src = img + (size_t)blockIdx.y * chunks * CHUNK;
+  auto copy = [&](int c) {
+    unsigned char* dst = smem + c % 3 * CHUNK;
+#pragma unroll
+    for (int d = 0; d < DMA; d++) {
+      const int at = (wv * DMA + d) * 1024;
+      __builtin_amdgcn_global_load_lds((const void*)(src + (size_t)c * CHUNK + at + lane * 16),
+                                       (__attribute__((address_space(3))) void*)(dst + at), 16, 0, 0);
+    }
+  };
+  const int8_t* row[MT];
+#pragma unroll
+  for (int t = 0; t < MT; t++) row[t] = p.w + min(n0 + 16 * t + (lane & 15), p.n - 1) * p.w_stride;
+  i32x4 cur[kWideSteps][MT], nxt[kWideSteps][MT];
+  auto load = [&](int c, i32x4 (&v)[kWideSteps][MT]) {
+#pragma unroll
+    for (int q = 0; q < kWideSteps; q++) {
+      const int off = min(64 * (kWideSteps * c + q) + 16 * (lane >> 4), K - 16);
+#pragma unroll
+      for (int t = 0; t < MT; t++) {
+        typedef i32x4 i32x4u __attribute__((aligned(1)));
+        v[q][t] = __builtin_nontemporal_load((const i32x4u*)(row[t] + off));
+      }
+    }
+  };
+  i32x4 acc[MT][NT];
+#pragma unroll
+  for (int t = 0; t < MT; t++)
+#pragma unroll
+    for (int j = 0; j < NT; j++) acc[t][j] = i32x4{0, 0, 0, 0};
+  copy(0);
+  if (chunks > 1) copy(1);
+  load(0, cur);
+  for (int c = 0; c < chunks; c++) {
+    // vmcnt(0) lgkmcnt(0): the w loads of chunk c and the copy before them, which are all that is in
+    // flight, and the reads of the buffer that the copy below refills
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    asm volatile("s_barrier" ::: "memory");
+    if (c + 2 < chunks) copy(c + 2);
+    if (c + 1 < chunks) load(c + 1, nxt);
+    const i32x4* b = (const i32x4*)(smem + c % 3 * CHUNK);
+#pragma unroll
+    for (int q = 0; q < kWideSteps; q++)
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        const i32x4 f = b[(q * NT + j) * 64 + lane];
+#pragma unroll
+        for (int t = 0; t < MT; t++) acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cur[q][t], f, acc[t][j], 0, 0, 0);
+      }
+#pragma unroll
+    for (int q = 0; q < kWideSteps; q++)
+#pragma unroll
+      for (int t = 0; t < MT; t++) cur[q][t] = nxt[q][t];
+  }
+#pragma unroll
+  for (int t = 0; t < MT; t++) {
+    const int64_t n = n0 + 16 * t + 4 * (lane >> 4);
+    float w4[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) w4[i] = p.w_scale[min(n + i, p.n - 1) * p.w_scale_stride];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      const int64_t m = ((int64_t)blockIdx.y * NT + j) * 16 + (lane & 15);
+      if (m < p.m) store_tile4<DT>(p.out, p.out_stride, m, n, p.n, acc[t][j], p.a_scale[m * p.a_scale_stride], w4, vec);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Dispatch
+// ---------------------------------------------------------------------------
+enum { I8_SIMPLE, I8_STREAM, I8_WIDE };
+struct I8Plan {
+  int kind, nt, steps;  // steps of 64, a multiple of 4
+  int64_t passes;
+  size_t img_bytes;
+};
+
+static I8Plan i8_plan(int64_t m, int64_t n, int64_t k) {
+  I8Plan p = {};
+  p.steps = (int)cdiv(k, 256) * 4;
+  if (k < 16 || n > ((int64_t)1 << 30)) {
+    p.kind = I8_SIMPLE;
+  } else if (m <= 16 && (size_t)p.steps * 1024 <= kMaxLds) {
+    p.kind = I8_STREAM;
+  } else {
+    p.kind = I8_WIDE;
+    p.nt = m <= 32 ? 2 : m <= 64 ? 4 : 8;
+    p.passes = cdiv(m, 16 * p.nt);
+    p.img_bytes = (size_t)p.passes * p.nt * p.steps * 1024;
+  }
+  return p;
+}
+
+size_t matmul_i8_workspace(int64_t m, int64_t n, int64_t k) {
+  if (m == 0 || n == 0) return 0;
+  return i8_plan(m, n, k).img_bytes;
+}
+
+template <int DT, int NT, int MT>
+static hipError_t launch_wide_i8(const MatmulI8& p, const I8Plan& pl, const void* img, int vec, hipStream_t stream) {
+  const size_t lds = (size_t)3 * kWideSteps * NT * 1024;
+  hipError_t e = set_dynamic_lds((const void*)wide_i8_kernel<DT, NT, MT>, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((wide_i8_kernel<DT, NT, MT>), dim3((unsigned)cdiv(p.n, kWideWaves * MT * 16), (unsigned)pl.passes),
+                     dim3(64 * kWideWaves), lds, stream, p, (const unsigned char*)img, pl.steps / kWideSteps, vec);
   return hipGetLastError();
+}
+
+template <int DT>
+static hipError_t launch_matmul_dt(const MatmulI8& p, void* ws, hipStream_t stream) {
+  const I8Plan pl = i8_plan(p.m, p.n, p.k);
+  // four-value stores of an output whose rows all start at a multiple of four values
+  const int vec = (uintptr_t)p.out % (DT == DT_F32 ? 16 : 8) == 0 && p.out_stride % 4 == 0;
+  if (pl.kind == I8_SIMPLE) {
+    hipLaunchKernelGGL((matmul_i8_kernel<DT>), dim3((unsigned)cdiv(p.n, 64), (unsigned)cdiv(p.m, 16)), dim3(256), 0,
+                       stream, p.a, p.a_stride, p.a_scale, p.a_scale_stride, p.w, p.w_stride, p.w_scale,
+                       p.w_scale_stride, p.m, p.n, (int)p.k, p.out, p.out_stride);
+    return hipGetLastError();
+  }
+  if (pl.kind == I8_STREAM) {
+    const size_t lds = (size_t)pl.steps * 1024;
+    hipError_t e = set_dynamic_lds((const void*)stream_i8_kernel<DT>, lds);
+    if (e != hipSuccess) return e;
+    const int64_t ntiles = cdiv(p.n, 16);
+    // one 16-wave workgroup per CU, or small ones where there are fewer tiles than waves
+    const int nw = ntiles >= 16 * kTargetBlocks ? 16 : 4;
+    const int64_t blocks = std::min<int64_t>(cdiv(ntiles, nw), nw == 16 ? kTargetBlocks : 4 * kTargetBlocks);
+    hipLaunchKernelGGL((stream_i8_kernel<DT>), dim3((unsigned)blocks), dim3(64 * nw), lds, stream, p, ntiles, pl.steps,
+                       vec);
+    return hipGetLastError();
+  }
+  const int64_t total = (int64_t)(pl.img_bytes / 16);
+  hipLaunchKernelGGL(wide_i8_image_kernel, dim3((unsigned)cdiv(total, 256)), dim3(256), 0, stream, p, pl.nt, pl.steps,
+                     (i32x4*)ws, total);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (pl.nt == 2) return launch_wide_i8<DT, 2, 2>(p, pl, ws, vec, stream);
+  if (pl.nt == 4) return launch_wide_i8<DT, 4, 2>(p, pl, ws, vec, stream);
+  return launch_wide_i8<DT, 8, 2>(p, pl, ws, vec, stream);
+}
+
+hipError_t launch_matmul_i8(const MatmulI8& p, void* ws, hipStream_t stream) {
+  if (p.out_dtype == DT_F32) return launch_matmul_dt<DT_F32>(p, ws, stream);
+  if (p.out_dtype == DT_BF16) return launch_matmul_dt<DT_BF16>(p, ws, stream);
+  return launch_matmul_dt<DT_F16>(p, ws, stream);
 }
 
 }  // namespace etg
