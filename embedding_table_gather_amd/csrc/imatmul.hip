@@ -125,112 +125,169 @@ __device__ __forceinline__ void store_tile4(void* out, int64_t out_stride, int64
   }
 }
 
-// Up to 16 a rows: the whole image in LDS, a persistent grid, each wave a contiguous
-// run of 16-row w tiles.  A lane loads 16 bytes of w row l % 16 at slot 4 step + l / 16;
-// four steps (256 bytes a row) are in flight while the four before are multiplied, across
-// tiles too.
-template <int DT>
+typedef i32x4 i32x4u __attribute__((aligned(1)));
+
+// Up to 8 IMG a rows: the whole image in LDS, a persistent grid, each wave a contiguous
+// run of tiles of 8 w rows.
+//
+// One load instruction reads 8 rows x 128 bytes (full lines): lane l row l % 8, slot l / 8
+// of the step.  As the A operand of the MFMA that is w row m % 8 at slots 2 g + m / 8 in A
+// row m and lane group g; the image's column n holds a row n % 8 at the same slots
+// 2 g + n / 8, so the sum for (w row r, a row b) is D[r][b] + D[r + 8][b + 8] and the other
+// half of D is unused: the matrix cores idle anyway (16 rows: a second image).
+//
+// Two groups of four steps (8 KiB a wave) are always in flight, in two register sets used
+// in turn, across tiles too; a tile's scales are loaded with its groups.
+static constexpr int kStreamSteps = 4;  // steps of 128 bytes per group
+
+template <int DT, int IMG>
 __global__ void __launch_bounds__(1024) stream_i8_kernel(MatmulI8 p, int64_t ntiles, int steps, int vec) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  i32x4* img = (i32x4*)smem;  // [steps][64]
+  i32x4* img = (i32x4*)smem;  // [steps][IMG][64]
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nw = blockDim.x >> 6, K = (int)p.k;
   const int64_t wave = (int64_t)blockIdx.x * nw + wv, waves = (int64_t)gridDim.x * nw;
   const int64_t t0 = wave * ntiles / waves, t1 = (wave + 1) * ntiles / waves;
 
-  i32x4 cur[4], nxt[4];
-  auto row_of = [&](int64_t t) { return p.w + min(t * 16 + (lane & 15), p.n - 1) * p.w_stride; };
-  auto load = [&](const int8_t* row, int step, i32x4 (&v)[4]) {
+  struct Set {
+    i32x4 v[kStreamSteps];
+    float scale;  // of w row lane % 8
+  } set[2];
+  // The group that is loaded next.  Every call loads (past the last tile that one again):
+  // with a fixed number of loads the wait for one set leaves the other's in flight.
+  int64_t lt = t0;
+  int ls = 0;
+  auto load = [&](Set& x) {
+    const int64_t r = min(max(min(lt, t1 - 1), (int64_t)0) * 8 + (lane & 7), p.n - 1);
+    const int8_t* row = p.w + r * p.w_stride;
+    x.scale = p.w_scale[r * p.w_scale_stride];
 #pragma unroll
-    for (int q = 0; q < 4; q++) {
-      const i32x4* at = (const i32x4*)(row + min(64 * (step + q) + 16 * (lane >> 4), K - 16));
-      typedef i32x4 i32x4u __attribute__((aligned(1)));
-      v[q] = __builtin_nontemporal_load((const i32x4u*)at);
-    }
+    for (int q = 0; q < kStreamSteps; q++)
+      x.v[q] = __builtin_nontemporal_load((const i32x4u*)(row + min(128 * (ls + q) + 16 * (lane >> 3), K - 16)));
+    ls += kStreamSteps;
+    if (ls >= steps) ls = 0, lt++;
   };
-  const int8_t* row = row_of(t0 < t1 ? t0 : 0);
-  if (t0 < t1) load(row, 0, cur);
-  for (int i = threadIdx.x; i < steps * 64; i += blockDim.x) {
-    const int m = i & 15;
-    img[i] = image_slot(m < p.m ? p.a + m * p.a_stride : nullptr, 4 * (i >> 6) + ((i >> 4) & 3), K);
+  load(set[0]);
+  load(set[1]);
+  for (int i = threadIdx.x; i < steps * IMG * 64; i += blockDim.x) {
+    const int l = i & 63, im = IMG == 1 ? 0 : (i >> 6) & 1, st = (i >> 6) / IMG;
+    const int m = 8 * im + (l & 7);
+    img[i] = image_slot(m < p.m ? p.a + m * p.a_stride : nullptr, 8 * st + 2 * (l >> 4) + ((l >> 3) & 1), K);
   }
   __syncthreads();
-  const int m = lane & 15;
-  const float s = m < p.m ? p.a_scale[m * p.a_scale_stride] : 0.f;
-  for (int64_t t = t0; t < t1; t++) {
-    const int8_t* next_row = row_of(t + 1 < t1 ? t + 1 : t);
-    i32x4 acc = {0, 0, 0, 0};
-    for (int st = 0; st < steps; st += 4) {  // steps is a multiple of 4
-      if (st + 4 < steps) load(row, st + 4, nxt);
-      else load(next_row, 0, nxt);
+  const int b = lane & 7;
+  const bool holder = (lane & 40) == 0;  // lanes with the first half of a useful sum
+  float s[IMG];
 #pragma unroll
-      for (int q = 0; q < 4; q++)
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(cur[q], img[(st + q) * 64 + lane], acc, 0, 0, 0);
+  for (int im = 0; im < IMG; im++) s[im] = 8 * im + b < p.m ? p.a_scale[(8 * im + b) * p.a_scale_stride] : 0.f;
+  i32x4 acc[IMG];
 #pragma unroll
-      for (int q = 0; q < 4; q++) cur[q] = nxt[q];
+  for (int im = 0; im < IMG; im++) acc[im] = i32x4{0, 0, 0, 0};
+  int64_t t = t0;
+  int st = 0;
+  auto compute = [&](const Set& x) {
+#pragma unroll
+    for (int q = 0; q < kStreamSteps; q++)
+#pragma unroll
+      for (int im = 0; im < IMG; im++)
+        acc[im] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x.v[q], img[((st + q) * IMG + im) * 64 + lane], acc[im], 0, 0, 0);
+    st += kStreamSteps;
+    if (st < steps || t >= t1) return;
+    // holder lane l: w rows 4 (l / 16) + i of the tile, a row 8 im + l % 8
+    const int64_t n = t * 8 + 4 * (lane >> 4);
+    float w4[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) w4[i] = __shfl(x.scale, 4 * ((lane >> 4) & 1) + i, 64);
+#pragma unroll
+    for (int im = 0; im < IMG; im++) {
+      i32x4 sum;
+#pragma unroll
+      for (int i = 0; i < 4; i++) sum[i] = acc[im][i] + __shfl(acc[im][i], (lane + 40) & 63, 64);
+      if (holder && 8 * im + b < p.m) store_tile4<DT>(p.out, p.out_stride, 8 * im + b, n, p.n, sum, s[im], w4, vec);
+      acc[im] = i32x4{0, 0, 0, 0};
     }
-    row = next_row;
-    if (m < p.m) {
-      const int64_t n = t * 16 + 4 * (lane >> 4);
-      float w4[4];
-#pragma unroll
-      for (int i = 0; i < 4; i++) w4[i] = p.w_scale[min(n + i, p.n - 1) * p.w_scale_stride];
-      store_tile4<DT>(p.out, p.out_stride, m, n, p.n, acc, s, w4, vec);
-    }
+    st = 0;
+    t++;
+  };
+  const int64_t groups = (t1 - t0) * (steps / kStreamSteps);
+  for (int64_t g = 0; g < groups; g += 2) {  // an odd number: the last half has no tile to store
+    compute(set[0]);
+    load(set[0]);
+    compute(set[1]);
+    load(set[1]);
   }
 }
 
-// Image of all a rows for the wide kernel: [pass][step][tile of the pass][64 lanes].
+// Image of all a rows for the wide kernel: [pass][step of 128][tile of the pass][even, odd
+// slots][64 lanes], lane l's 16 bytes being a row l % 16 at slot 8 step + 2 (l / 16) + odd.
 __global__ void __launch_bounds__(256) wide_i8_image_kernel(MatmulI8 p, int nt, int steps, i32x4* __restrict__ img,
-                                                            int64_t total) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+                                                            uint32_t total) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
   if (i >= total) return;
-  const int lane = (int)(i & 63);
-  const int64_t r = i >> 6;
+  const int lane = (int)(i & 63), odd = (int)(i >> 6) & 1;
+  const uint32_t r = i >> 7;
   const int t = (int)(r % nt), step = (int)(r / nt % steps);
-  const int64_t m = (r / nt / steps * nt + t) * 16 + (lane & 15);
-  img[i] = image_slot(m < p.m ? p.a + m * p.a_stride : nullptr, 4 * step + (lane >> 4), (int)p.k);
+  const int64_t m = (int64_t)(r / nt / steps * nt + t) * 16 + (lane & 15);
+  img[i] = image_slot(m < p.m ? p.a + m * p.a_stride : nullptr, 8 * step + 2 * (lane >> 4) + odd, (int)p.k);
 }
 
-// Passes of up to 16 NT a rows: 8 waves x MT tiles of 16 w rows per workgroup.  The image
-// passes through three LDS buffers of four K steps each, copied by global_load_lds two
-// chunks ahead; the w rows are loaded one chunk ahead into registers.  One barrier per
-// chunk.
+// Passes of up to 16 NT a rows: 8 waves x MT tiles of 16 w rows per workgroup.  A load reads
+// 8 w rows x 128 bytes as in the stream kernel (X: rows 0 - 7 of a tile, Y: rows 8 - 15); two
+// DPP moves per register swap the odd half of X with the even half of Y, which leaves the
+// 16-row A operands of the even and of the odd slots.  The image
+// passes through three LDS buffers of one K step each, copied by global_load_lds two
+// chunks ahead; the w rows are loaded up to two chunks ahead into two register sets used in
+// turn.  One barrier per chunk.
 static constexpr int kWideWaves = 8;
-static constexpr int kWideSteps = 4;
+static constexpr int kWideSteps = 1;  // of 128 bytes, per chunk
+
+// 1 KiB from memory to LDS: lane l's 16 bytes at src to lds + 16 l.  In assembly because the
+// compiler would wait for every such copy before any LDS read; wide_barrier waits for the one
+// that is due.  No register is written.
+__device__ __forceinline__ void lds_copy_1k(const void* src, uint32_t lds) {
+  uint32_t m0;  // the LDS base register, left as it was
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b32 m0, %0"
+               : "=&s"(m0)
+               : "v"(src), "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "memory");
+}
+
+// vmcnt(N) lgkmcnt(0), then a workgroup barrier that no memory access crosses.
+template <int N>
+__device__ __forceinline__ void wide_barrier() {
+  static_assert(N >= 0 && N < 64, "vmcnt field");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
+  asm volatile("s_barrier" ::: "memory");
+}
 
 template <int DT, int NT, int MT>
-__global__ void __launch_bounds__(64 * kWideWaves, 4) wide_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
+__global__ void __launch_bounds__(64 * kWideWaves, NT < 8 ? 4 : 2) wide_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
                                                                      int chunks, int vec) {
-  constexpr int CHUNK = kWideSteps * NT * 1024, DMA = CHUNK / 1024 / kWideWaves;
-  static_assert(DMA * kWideWaves * 1024 == CHUNK, "whole DMA instructions per wave");
+  constexpr int CHUNK = kWideSteps * NT * 2048, DMA = (CHUNK / 1024 + kWideWaves - 1) / kWideWaves;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [3][CHUNK]
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int K = (int)p.k;
   const int64_t n0 = ((int64_t)blockIdx.x * kWideWaves + wv) * MT * 16;
   const unsigned char* src = img + (size_t)blockIdx.y * chunks * CHUNK;
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem;
   auto copy = [&](int c) {
-    unsigned char* dst = smem + c % 3 * CHUNK;
 #pragma unroll
     for (int d = 0; d < DMA; d++) {
       const int at = (wv * DMA + d) * 1024;
-      __builtin_amdgcn_global_load_lds((const void*)(src + (size_t)c * CHUNK + at + lane * 16),
-                                       (__attribute__((address_space(3))) void*)(dst + at), 16, 0, 0);
+      if (at < CHUNK) lds_copy_1k(src + (size_t)c * CHUNK + at + lane * 16, lds + c % 3 * CHUNK + at);  // uniform
     }
   };
-  const int8_t* row[MT];
+  const int8_t* row[2 * MT];  // X and Y rows of each tile
 #pragma unroll
-  for (int t = 0; t < MT; t++) row[t] = p.w + min(n0 + 16 * t + (lane & 15), p.n - 1) * p.w_stride;
-  i32x4 cur[kWideSteps][MT], nxt[kWideSteps][MT];
-  auto load = [&](int c, i32x4 (&v)[kWideSteps][MT]) {
+  for (int t = 0; t < 2 * MT; t++) row[t] = p.w + min(n0 + 8 * t + (lane & 7), p.n - 1) * p.w_stride;
+  // w rows of the chunk that is multiplied and of the next, in turn
+  i32x4 set[2][kWideSteps][2 * MT];
+  auto load = [&](int c, i32x4 (&v)[kWideSteps][2 * MT]) {
 #pragma unroll
     for (int q = 0; q < kWideSteps; q++) {
-      const int off = min(64 * (kWideSteps * c + q) + 16 * (lane >> 4), K - 16);
+      const int off = min(128 * (kWideSteps * c + q) + 16 * (lane >> 3), K - 16);
 #pragma unroll
-      for (int t = 0; t < MT; t++) {
-        typedef i32x4 i32x4u __attribute__((aligned(1)));
-        v[q][t] = __builtin_nontemporal_load((const i32x4u*)(row[t] + off));
-      }
+      for (int t = 0; t < 2 * MT; t++) v[q][t] = __builtin_nontemporal_load((const i32x4u*)(row[t] + off));
     }
   };
   i32x4 acc[MT][NT];
@@ -238,30 +295,44 @@ __global__ void __launch_bounds__(64 * kWideWaves, 4) wide_i8_kernel(MatmulI8 p,
   for (int t = 0; t < MT; t++)
 #pragma unroll
     for (int j = 0; j < NT; j++) acc[t][j] = i32x4{0, 0, 0, 0};
-  copy(0);
-  if (chunks > 1) copy(1);
-  load(0, cur);
-  for (int c = 0; c < chunks; c++) {
-    // vmcnt(0) lgkmcnt(0): the w loads of chunk c and the copy before them, which are all that is in
-    // flight, and the reads of the buffer that the copy below refills
-    __builtin_amdgcn_s_waitcnt(0x0070);
-    asm volatile("s_barrier" ::: "memory");
-    if (c + 2 < chunks) copy(c + 2);
-    if (c + 1 < chunks) load(c + 1, nxt);
+  auto chunk = [&](int c, i32x4 (&v)[kWideSteps][2 * MT]) {
+    // chunk c and its w rows have landed (loads complete in order; the w rows of chunk c + 1 stay
+    // in flight), and this wave has read the buffer that the copy below refills
+    wide_barrier<kWideSteps * 2 * MT>();
+    if (c + 2 < chunks) copy(c + 2);  // uniform
     const i32x4* b = (const i32x4*)(smem + c % 3 * CHUNK);
 #pragma unroll
-    for (int q = 0; q < kWideSteps; q++)
+    for (int q = 0; q < kWideSteps; q++) {
+      i32x4 even[MT], odd[MT];
+#pragma unroll
+      for (int t = 0; t < MT; t++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const int x = v[q][2 * t][e], y = v[q][2 * t + 1][e];
+          even[t][e] = __builtin_amdgcn_update_dpp(x, y, 0x118, 0xf, 0xc, false);  // row_shr:8 into lanes 8 - 15
+          odd[t][e] = __builtin_amdgcn_update_dpp(y, x, 0x108, 0xf, 0x3, false);   // row_shl:8 into lanes 0 - 7
+        }
 #pragma unroll
       for (int j = 0; j < NT; j++) {
-        const i32x4 f = b[(q * NT + j) * 64 + lane];
+        const i32x4 f0 = b[(q * NT + j) * 128 + lane], f1 = b[(q * NT + j) * 128 + 64 + lane];
 #pragma unroll
-        for (int t = 0; t < MT; t++) acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(cur[q][t], f, acc[t][j], 0, 0, 0);
+        for (int t = 0; t < MT; t++) {
+          acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(even[t], f0, acc[t][j], 0, 0, 0);
+          acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(odd[t], f1, acc[t][j], 0, 0, 0);
+        }
       }
-#pragma unroll
-    for (int q = 0; q < kWideSteps; q++)
-#pragma unroll
-      for (int t = 0; t < MT; t++) cur[q][t] = nxt[q][t];
+    }
+    load(min(c + 2, chunks - 1), v);  // always the same number of loads in flight
+  };
+  copy(0);
+  load(0, set[0]);
+  copy(1);
+  load(1, set[1]);
+  for (int c = 0; c < chunks; c += 2) {  // an even number
+    chunk(c, set[0]);
+    chunk(c + 1, set[1]);
   }
+  wide_barrier<0>();  // the last (repeated) loads
 #pragma unroll
   for (int t = 0; t < MT; t++) {
     const int64_t n = n0 + 16 * t + 4 * (lane >> 4);
@@ -281,23 +352,24 @@ __global__ void __launch_bounds__(64 * kWideWaves, 4) wide_i8_kernel(MatmulI8 p,
 // ---------------------------------------------------------------------------
 enum { I8_SIMPLE, I8_STREAM, I8_WIDE };
 struct I8Plan {
-  int kind, nt, steps;  // steps of 64, a multiple of 4
+  int kind, nt, steps;  // wide: K steps of 128, a multiple of 2 (an even number of chunks)
   int64_t passes;
   size_t img_bytes;
 };
 
 static I8Plan i8_plan(int64_t m, int64_t n, int64_t k) {
   I8Plan p = {};
-  p.steps = (int)cdiv(k, 256) * 4;
+  p.steps = (int)cdiv(k, 256 * kWideSteps) * 2 * kWideSteps;
   if (k < 16 || n > ((int64_t)1 << 30)) {
     p.kind = I8_SIMPLE;
-  } else if (m <= 16 && (size_t)p.steps * 1024 <= kMaxLds) {
+  } else if (m <= 16 && (size_t)cdiv(k, 512) * 4 * (m <= 8 ? 1024 : 2048) <= kMaxLds) {
     p.kind = I8_STREAM;
+    p.steps = (int)cdiv(k, 128 * kStreamSteps) * kStreamSteps;  // steps of 128
   } else {
     p.kind = I8_WIDE;
     p.nt = m <= 32 ? 2 : m <= 64 ? 4 : 8;
     p.passes = cdiv(m, 16 * p.nt);
-    p.img_bytes = (size_t)p.passes * p.nt * p.steps * 1024;
+    p.img_bytes = (size_t)p.passes * p.nt * p.steps * 2048;
   }
   return p;
 }
@@ -307,9 +379,23 @@ size_t matmul_i8_workspace(int64_t m, int64_t n, int64_t k) {
   return i8_plan(m, n, k).img_bytes;
 }
 
+template <int DT, int IMG>
+static hipError_t launch_stream_i8(const MatmulI8& p, const I8Plan& pl, int vec, hipStream_t stream) {
+  const size_t lds = (size_t)pl.steps * IMG * 1024;
+  hipError_t e = set_dynamic_lds((const void*)stream_i8_kernel<DT, IMG>, lds);
+  if (e != hipSuccess) return e;
+  const int64_t ntiles = cdiv(p.n, 8);
+  // one 16-wave workgroup per CU, or small ones where there are fewer tiles than waves
+  const int nw = ntiles >= 16 * kTargetBlocks ? 16 : 4;
+  const int64_t blocks = std::min<int64_t>(cdiv(ntiles, nw), nw == 16 ? kTargetBlocks : 4 * kTargetBlocks);
+  hipLaunchKernelGGL((stream_i8_kernel<DT, IMG>), dim3((unsigned)blocks), dim3(64 * nw), lds, stream, p, ntiles, pl.steps,
+                     vec);
+  return hipGetLastError();
+}
+
 template <int DT, int NT, int MT>
 static hipError_t launch_wide_i8(const MatmulI8& p, const I8Plan& pl, const void* img, int vec, hipStream_t stream) {
-  const size_t lds = (size_t)3 * kWideSteps * NT * 1024;
+  const size_t lds = (size_t)3 * kWideSteps * NT * 2048;
   hipError_t e = set_dynamic_lds((const void*)wide_i8_kernel<DT, NT, MT>, lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((wide_i8_kernel<DT, NT, MT>), dim3((unsigned)cdiv(p.n, kWideWaves * MT * 16), (unsigned)pl.passes),
@@ -328,19 +414,9 @@ static hipError_t launch_matmul_dt(const MatmulI8& p, void* ws, hipStream_t stre
                        p.w_scale_stride, p.m, p.n, (int)p.k, p.out, p.out_stride);
     return hipGetLastError();
   }
-  if (pl.kind == I8_STREAM) {
-    const size_t lds = (size_t)pl.steps * 1024;
-    hipError_t e = set_dynamic_lds((const void*)stream_i8_kernel<DT>, lds);
-    if (e != hipSuccess) return e;
-    const int64_t ntiles = cdiv(p.n, 16);
-    // one 16-wave workgroup per CU, or small ones where there are fewer tiles than waves
-    const int nw = ntiles >= 16 * kTargetBlocks ? 16 : 4;
-    const int64_t blocks = std::min<int64_t>(cdiv(ntiles, nw), nw == 16 ? kTargetBlocks : 4 * kTargetBlocks);
-    hipLaunchKernelGGL((stream_i8_kernel<DT>), dim3((unsigned)blocks), dim3(64 * nw), lds, stream, p, ntiles, pl.steps,
-                       vec);
-    return hipGetLastError();
-  }
-  const int64_t total = (int64_t)(pl.img_bytes / 16);
+  if (pl.kind == I8_STREAM)
+    return p.m <= 8 ? launch_stream_i8<DT, 1>(p, pl, vec, stream) : launch_stream_i8<DT, 2>(p, pl, vec, stream);
+  const uint32_t total = (uint32_t)(pl.img_bytes / 16);  // at most 65536 x 65792 bytes
   hipLaunchKernelGGL(wide_i8_image_kernel, dim3((unsigned)cdiv(total, 256)), dim3(256), 0, stream, p, pl.nt, pl.steps,
                      (i32x4*)ws, total);
   hipError_t e = hipGetLastError();
