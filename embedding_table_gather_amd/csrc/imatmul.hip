@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(256) wide_i8_image_kernel(MatmulI8 p, int nt, 
 // chunks ahead; the w rows are loaded up to two chunks ahead into two register sets used in
 // turn.  One barrier per chunk.
 static constexpr int kWideWaves = 8;
+static constexpr int kWideSets = 3;   // register sets of w rows: chunks loaded ahead, and the one multiplied
 static constexpr int kWideSteps = 1;  // of 128 bytes, per chunk
 
 // 1 KiB from memory to LDS: lane l's 16 bytes at src to lds + 16 l.  In assembly because the
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(64 * kWideWaves, NT < 8 ? 4 : 2) wide_i8_kerne
 #pragma unroll
   for (int t = 0; t < 2 * MT; t++) row[t] = p.w + min(n0 + 8 * t + (lane & 7), p.n - 1) * p.w_stride;
   // w rows of the chunk that is multiplied and of the next, in turn
-  i32x4 set[2][kWideSteps][2 * MT];
+  i32x4 set[kWideSets][kWideSteps][2 * MT];
   auto load = [&](int c, i32x4 (&v)[kWideSteps][2 * MT]) {
 #pragma unroll
     for (int q = 0; q < kWideSteps; q++) {
@@ -296,9 +297,11 @@ __global__ void __launch_bounds__(64 * kWideWaves, NT < 8 ? 4 : 2) wide_i8_kerne
 #pragma unroll
     for (int j = 0; j < NT; j++) acc[t][j] = i32x4{0, 0, 0, 0};
   auto chunk = [&](int c, i32x4 (&v)[kWideSteps][2 * MT]) {
-    // chunk c and its w rows have landed (loads complete in order; the w rows of chunk c + 1 stay
-    // in flight), and this wave has read the buffer that the copy below refills
-    wide_barrier<kWideSteps * 2 * MT>();
+    // Chunk c and its w rows have landed, and this wave has read the buffer that the copy below
+    // refills.  Loads complete in order, and at least the w rows of two chunks were loaded after
+    // the copy of chunk c, which was started two chunks ago: they stay in flight.
+    static_assert(kWideSets == 3, "the wait below");
+    wide_barrier<2 * kWideSteps * 2 * MT>();
     if (c + 2 < chunks) copy(c + 2);  // uniform
     const i32x4* b = (const i32x4*)(smem + c % 3 * CHUNK);
 #pragma unroll
@@ -322,15 +325,16 @@ __global__ void __launch_bounds__(64 * kWideWaves, NT < 8 ? 4 : 2) wide_i8_kerne
         }
       }
     }
-    load(min(c + 2, chunks - 1), v);  // always the same number of loads in flight
+    load(min(c + kWideSets, chunks - 1), v);  // always the same number of loads in flight
   };
   copy(0);
-  load(0, set[0]);
   copy(1);
-  load(1, set[1]);
-  for (int c = 0; c < chunks; c += 2) {  // an even number
+#pragma unroll
+  for (int i = 0; i < kWideSets; i++) load(min(i, chunks - 1), set[i]);
+  for (int c = 0; c < chunks; c += kWideSets) {  // a multiple of kWideSets
     chunk(c, set[0]);
     chunk(c + 1, set[1]);
+    chunk(c + 2, set[2]);
   }
   wide_barrier<0>();  // the last (repeated) loads
 #pragma unroll
@@ -352,14 +356,14 @@ __global__ void __launch_bounds__(64 * kWideWaves, NT < 8 ? 4 : 2) wide_i8_kerne
 // ---------------------------------------------------------------------------
 enum { I8_SIMPLE, I8_STREAM, I8_WIDE };
 struct I8Plan {
-  int kind, nt, steps;  // wide: K steps of 128, a multiple of 2 (an even number of chunks)
+  int kind, nt, steps;  // wide: K steps of 128, a multiple of the register sets
   int64_t passes;
   size_t img_bytes;
 };
 
 static I8Plan i8_plan(int64_t m, int64_t n, int64_t k) {
   I8Plan p = {};
-  p.steps = (int)cdiv(k, 256 * kWideSteps) * 2 * kWideSteps;
+  p.steps = (int)cdiv(k, 128 * kWideSteps * kWideSets) * kWideSets * kWideSteps;
   if (k < 16 || n > ((int64_t)1 << 30)) {
     p.kind = I8_SIMPLE;
   } else if (m <= 16 && (size_t)cdiv(k, 512) * 4 * (m <= 8 ? 1024 : 2048) <= kMaxLds) {
