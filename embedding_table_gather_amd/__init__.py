@@ -75,6 +75,9 @@ SIGNATURES = {
     "etg_matmul_i8_workspace": (_I64, [_I64, _I64, _I64]),
     "etg_matmul_i8": (_I32, [_VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _I64, _I64, _I64, _VP, _I32, _I64, _VP,
                              ctypes.c_size_t, _VP]),
+    "etg_logits_i8_workspace": (_I64, [_I64, _I64, _I64]),
+    "etg_logits_i8": (_I32, [_VP, _I64, _VP, _I64, _I64, _I64, _VP, _I32, _I64, _I64, _VP, _I32, _I64, _VP,
+                             ctypes.c_size_t, _VP]),
     "etg_sample_workspace": (_I64, [_I64, _I64]),
     "etg_sample": (_I32, [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
     "etg_last_error": (ctypes.c_char_p, []),
@@ -395,32 +398,43 @@ _TORCH_FLOATS = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
 
 def _float_dtype(dtype) -> torch.dtype:
     """A torch dtype from F32 / BF16 / F16 or the torch dtype itself."""
-    dtype = _TORCH_FLOATS.get(dtype, dtype)
     if dtype not in _FLOATS:
-        raise ValueError(f"{dtype} is not float32, bfloat16 or float16")
+        dtype = _TORCH_FLOATS.get(dtype)
+        if dtype is None:
+            raise ValueError("a dtype is float32, bfloat16 or float16 (F32, BF16 or F16)")
     return dtype
 
 
-def _matrix(t: torch.Tensor, what: str, device: torch.device | None = None) -> torch.Tensor:
-    """t as a 2-D device tensor whose rows are contiguous (any row stride that does not
-    overlap rows)."""
+def _call(fn, device: torch.device, *args) -> None:
+    """fn(*args, current stream of the device), with the device current; raises on an error."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status != 0:
+        _check(status)
+
+
+def _rows(t: torch.Tensor, what: str, device: torch.device | None = None) -> int:
+    """The row stride of a 2-D device tensor whose rows are contiguous and do not overlap."""
     if t.dim() != 2 or not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{what} must be a 2-D tensor on the {'same' if device is not None else 'GPU'} device")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    n, cols = t.shape
+    stride, inner = t.stride()
+    if cols > 1 and inner != 1:
         raise ValueError(f"{what} must have contiguous rows")
-    return t
-
-
-def _row_stride(t: torch.Tensor, what: str) -> int:
-    s = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    if s < t.shape[1]:
-        raise ValueError(f"{what} rows overlap (stride {s}, {t.shape[1]} values)")
-    return s
+    if n <= 1:
+        return cols
+    if stride < cols:
+        raise ValueError(f"{what} rows overlap (stride {stride}, {cols} values)")
+    return stride
 
 
 def _scales(t: torch.Tensor, n: int, what: str, device: torch.device) -> int:
     """Checks a vector of n f32 scales; returns its stride in floats."""
-    if t.dtype != torch.float32 or t.device != device or t.dim() != 1 or t.shape[0] != n:
+    if t.dtype != torch.float32 or t.device != device or t.shape != (n,):
         raise ValueError(f"{what} must be a float32 tensor of {n} values on the operands' device")
     s = t.stride(0) if n > 1 else 1
     if s < 1:
@@ -428,27 +442,46 @@ def _scales(t: torch.Tensor, n: int, what: str, device: torch.device) -> int:
     return s
 
 
+def _workspace_for(need: int, device: torch.device) -> torch.Tensor:
+    """A workspace of one call: fresh, as calls on other streams and captured graphs keep
+    their own (the caching allocator makes that cheap)."""
+    if need < 0:
+        _check(need)
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
 def quantize_i8(x: torch.Tensor, codes: torch.Tensor | None = None, scale: torch.Tensor | None = None):
     """(int8 codes [rows, cols], f32 scales [rows]) of the rows of a float32, bfloat16 or
     float16 matrix: scale = max|x| / 127, codes = round(x / scale) (ADR-0009's i8 wire
     definition).  A row with a NaN or an infinity gets scale NaN.  ``codes`` and ``scale``
     may be given, with any row stride."""
-    if x.dtype not in _FLOATS:
+    dtype = _FLOATS.get(x.dtype)
+    if dtype is None:
         raise ValueError("x must be a float32, bfloat16 or float16 tensor")
-    _matrix(x, "x")
+    xs = _rows(x, "x")
     rows, cols = x.shape
+    dev = x.device
     if codes is None:
-        codes = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+        codes, qs = torch.empty((rows, cols), dtype=torch.int8, device=dev), cols
     elif codes.dtype != torch.int8 or codes.shape != x.shape:
         raise ValueError("codes must be an int8 tensor of x's shape")
+    else:
+        qs = _rows(codes, "codes", dev)
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _matrix(codes, "codes", x.device)
-    with torch.cuda.device(x.device):
-        _check(lib().etg_quantize_i8(x.data_ptr(), _FLOATS[x.dtype], rows, cols, _row_stride(x, "x"),
-                                     codes.data_ptr(), _row_stride(codes, "codes"), scale.data_ptr(),
-                                     _scales(scale, rows, "scale", x.device), _stream_ptr(x.device)))
+        scale, ss = torch.empty(rows, dtype=torch.float32, device=dev), 1
+    else:
+        ss = _scales(scale, rows, "scale", dev)
+    _call(lib().etg_quantize_i8, dev, x.data_ptr(), dtype, rows, cols, xs, codes.data_ptr(), qs, scale.data_ptr(), ss)
     return codes, scale
+
+
+def _out(out: torch.Tensor | None, out_dtype, m: int, n: int, device: torch.device):
+    """(output [m, n], its row stride): the given one checked, or a new one."""
+    if out is None:
+        return torch.empty((m, n), dtype=_float_dtype(out_dtype), device=device), max(n, 1)
+    if out.dtype not in _FLOATS or out.shape != (m, n):
+        raise ValueError("out must be a float32, bfloat16 or float16 tensor of the result's shape")
+    return out, max(_rows(out, "out", device), 1)
 
 
 def matmul_i8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -459,29 +492,20 @@ def matmul_i8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     once to ``out_dtype`` (float32, bfloat16, float16, or F32 / BF16 / F16)."""
     if a.dtype != torch.int8 or w.dtype != torch.int8:
         raise ValueError("a and w must be int8 tensors")
-    _matrix(a, "a")
-    _matrix(w, "w", a.device)
+    dev = a.device
+    a_stride, w_stride = _rows(a, "a"), _rows(w, "w", dev)
     m, k = a.shape
     n = w.shape[0]
     if w.shape[1] != k:
         raise ValueError(f"a has {k} columns, w {w.shape[1]}")
-    if out is None:
-        out = torch.empty((m, n), dtype=_float_dtype(out_dtype), device=a.device)
-    elif out.dtype not in _FLOATS or out.shape != (m, n):
-        raise ValueError("out must be a float32, bfloat16 or float16 [m, n] tensor")
-    _matrix(out, "out", a.device)
-    sa, sw = _scales(a_scale, m, "a_scale", a.device), _scales(w_scale, n, "w_scale", a.device)
+    sa, sw = _scales(a_scale, m, "a_scale", dev), _scales(w_scale, n, "w_scale", dev)
+    out, out_stride = _out(out, out_dtype, m, n, dev)
     L = lib()
     if workspace is None:
-        need = int(L.etg_matmul_i8_workspace(m, n, k))
-        if need < 0:
-            _check(need)
-        workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
-    with torch.cuda.device(a.device):
-        _check(L.etg_matmul_i8(a.data_ptr(), _row_stride(a, "a"), a_scale.data_ptr(), sa, w.data_ptr(),
-                               _row_stride(w, "w"), w_scale.data_ptr(), sw, m, n, k, out.data_ptr(),
-                               _FLOATS[out.dtype], max(_row_stride(out, "out"), 1), workspace.data_ptr(),
-                               workspace.numel(), _stream_ptr(a.device)))
+        workspace = _workspace_for(L.etg_matmul_i8_workspace(m, n, k), dev)
+    _call(L.etg_matmul_i8, dev, a.data_ptr(), a_stride, a_scale.data_ptr(), sa, w.data_ptr(), w_stride,
+          w_scale.data_ptr(), sw, m, n, k, out.data_ptr(), _FLOATS[out.dtype], out_stride, workspace.data_ptr(),
+          workspace.numel())
     return out
 
 
@@ -513,9 +537,10 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0
     where token v is allowed.  NaN and -inf logits are never drawn.  A row with nothing to
     draw, or with a setting or random number out of range, has id -1 and probability 0.
     """
-    if logits.dtype not in _FLOATS:
+    dtype = _FLOATS.get(logits.dtype)
+    if dtype is None:
         raise ValueError("logits must be a float32, bfloat16 or float16 tensor")
-    _matrix(logits, "logits")
+    stride = _rows(logits, "logits")
     rows, vocab = logits.shape
     dev = logits.device
     if uniform.dtype != torch.float32 or uniform.device != dev or uniform.shape != (rows,) \
@@ -536,25 +561,23 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0
         d_allowed = allowed.data_ptr()
         if allowed.dim() == 2 and rows > 1:
             a_stride = allowed.stride(0)  # 0: an expanded row, one for all
-    outs = []
-    for o, dtype in ((out_ids, torch.int32), (out_probs, torch.float32)):
-        if o is None:
-            o = torch.empty(rows, dtype=dtype, device=dev)
-        elif o.dtype != dtype or o.device != dev or o.shape != (rows,) or not o.is_contiguous():
-            raise ValueError(f"out_ids / out_probs must be contiguous int32 / float32 tensors of {rows} values")
-        outs.append(o)
+    if out_ids is None:
+        out_ids = torch.empty(rows, dtype=torch.int32, device=dev)
+    elif out_ids.dtype != torch.int32 or out_ids.device != dev or out_ids.shape != (rows,) \
+            or not out_ids.is_contiguous():
+        raise ValueError(f"out_ids must be a contiguous int32 tensor of {rows} values on the logits' device")
+    if out_probs is None:
+        out_probs = torch.empty(rows, dtype=torch.float32, device=dev)
+    elif out_probs.dtype != torch.float32 or out_probs.device != dev or out_probs.shape != (rows,) \
+            or not out_probs.is_contiguous():
+        raise ValueError(f"out_probs must be a contiguous float32 tensor of {rows} values on the logits' device")
     L = lib()
     if workspace is None:
-        need = int(L.etg_sample_workspace(rows, vocab))
-        if need < 0:
-            _check(need)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _workspace_for(L.etg_sample_workspace(rows, vocab), dev)
     how = _Sampling(T, k, p, mp, d_T, d_k, d_p, d_mp, d_allowed, a_stride)
-    with torch.cuda.device(dev):
-        _check(L.etg_sample(logits.data_ptr(), _FLOATS[logits.dtype], rows, vocab, _row_stride(logits, "logits"),
-                            ctypes.addressof(how), uniform.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(),
-                            workspace.data_ptr(), workspace.numel(), _stream_ptr(dev)))
-    return outs[0], outs[1]
+    _call(L.etg_sample, dev, logits.data_ptr(), dtype, rows, vocab, stride, ctypes.addressof(how), uniform.data_ptr(),
+          out_ids.data_ptr(), out_probs.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out_ids, out_probs
 
 
 class I8Table:
@@ -568,19 +591,31 @@ class I8Table:
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor):
         if codes.dtype != torch.int8:
             raise ValueError("codes must be an int8 tensor")
-        _matrix(codes, "codes")
-        _row_stride(codes, "codes")
-        _scales(scale, codes.shape[0], "scale", codes.device)
+        self._stride = _rows(codes, "codes")
         self.codes, self.scale = codes, scale
         self.vocab, self.hidden = codes.shape
         self.device = codes.device
+        self._scale_stride = _scales(scale, self.vocab, "scale", self.device)
 
-    def logits_raw(self, residual: torch.Tensor, out_dtype=torch.float32,
-                   out: torch.Tensor | None = None) -> torch.Tensor:
+    def logits_raw(self, residual: torch.Tensor, out_dtype=torch.float32, out: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
         """Logits [B, vocab] of float32, bfloat16 or float16 residual rows [B, hidden],
         each row quantised to int8 first."""
-        a, a_scale = quantize_i8(residual)
-        return matmul_i8(a, a_scale, self.codes, self.scale, out_dtype=out_dtype, out=out)
+        dtype, dev = _FLOATS.get(residual.dtype), self.device
+        if dtype is None:
+            raise ValueError("residual must be a float32, bfloat16 or float16 tensor")
+        stride = _rows(residual, "residual", dev)
+        B, hidden = residual.shape
+        if hidden != self.hidden:
+            raise ValueError(f"residual has {hidden} columns, the table {self.hidden}")
+        out, out_stride = _out(out, out_dtype, B, self.vocab, dev)
+        L = lib()
+        if workspace is None:
+            workspace = _workspace_for(L.etg_logits_i8_workspace(B, self.vocab, hidden), dev)
+        _call(L.etg_logits_i8, dev, self.codes.data_ptr(), self._stride, self.scale.data_ptr(), self._scale_stride,
+              self.vocab, hidden, residual.data_ptr(), dtype, stride, B, out.data_ptr(), _FLOATS[out.dtype], out_stride,
+              workspace.data_ptr(), workspace.numel())
+        return out
 
     def logits_raw_wire(self, residual: torch.Tensor, out_dtype=torch.float32,
                         out: torch.Tensor | None = None) -> torch.Tensor:

@@ -36,6 +36,28 @@ int32_t check_matmul_shape(int64_t m, int64_t n, int64_t k) {
   return ETG_OK;
 }
 
+// Every argument of a product but its workspace; with m or n 0 the pointers are not looked at.
+int32_t check_matmul(const int8_t* d_a, int64_t a_stride, const float* d_a_scale, int64_t a_scale_stride,
+                     const int8_t* d_w, int64_t w_stride, const float* d_w_scale, int64_t w_scale_stride, int64_t m,
+                     int64_t n, int64_t k, const void* d_out, int32_t out_dtype, int64_t out_stride) {
+  const size_t esize = float_bytes(out_dtype);
+  if (esize == 0) return etg::set_error(ETG_EDTYPE, "output dtype %d is not f32, bf16 or f16", out_dtype);
+  int32_t st = check_matmul_shape(m, n, k);
+  if (st == ETG_OK) st = check_stride("a", a_stride, k);
+  if (st == ETG_OK) st = check_stride("w", w_stride, k);
+  if (st == ETG_OK) st = check_stride("a scale", a_scale_stride, 1);
+  if (st == ETG_OK) st = check_stride("w scale", w_scale_stride, 1);
+  if (st == ETG_OK) st = check_stride("output", out_stride, n > 1 ? n : 1);
+  if (st != ETG_OK) return st;
+  if (m == 0 || n == 0) return ETG_OK;
+  if (d_a == nullptr || d_a_scale == nullptr || d_w == nullptr || d_w_scale == nullptr || d_out == nullptr)
+    return etg::set_error(ETG_EINVAL, "an operand, scale or output pointer is NULL");
+  if (!aligned(d_a_scale, 4) || !aligned(d_w_scale, 4))
+    return etg::set_error(ETG_EALIGN, "a scale pointer is not 4-byte aligned");
+  if (!aligned(d_out, esize)) return etg::set_error(ETG_EALIGN, "output pointer is not %zu-byte aligned", esize);
+  return ETG_OK;
+}
+
 int32_t check_sample_shape(int64_t batch, int64_t vocab) {
   if (batch < 0 || batch > kMaxTokens)
     return etg::set_error(ETG_ESHAPE, "batch %lld outside [0, %lld]", (long long)batch, (long long)kMaxTokens);
@@ -80,21 +102,10 @@ int32_t etg_matmul_i8(const int8_t* d_a, int64_t a_stride, const float* d_a_scal
                       const int8_t* d_w, int64_t w_stride, const float* d_w_scale, int64_t w_scale_stride, int64_t m,
                       int64_t n, int64_t k, void* d_out, int32_t out_dtype, int64_t out_stride, void* d_workspace,
                       size_t workspace_bytes, void* stream) {
-  const size_t esize = float_bytes(out_dtype);
-  if (esize == 0) return etg::set_error(ETG_EDTYPE, "output dtype %d is not f32, bf16 or f16", out_dtype);
-  int32_t st = check_matmul_shape(m, n, k);
-  if (st == ETG_OK) st = check_stride("a", a_stride, k);
-  if (st == ETG_OK) st = check_stride("w", w_stride, k);
-  if (st == ETG_OK) st = check_stride("a scale", a_scale_stride, 1);
-  if (st == ETG_OK) st = check_stride("w scale", w_scale_stride, 1);
-  if (st == ETG_OK) st = check_stride("output", out_stride, n > 1 ? n : 1);
-  if (st != ETG_OK) return st;
-  if (m == 0 || n == 0) return ETG_OK;
-  if (d_a == nullptr || d_a_scale == nullptr || d_w == nullptr || d_w_scale == nullptr || d_out == nullptr)
-    return etg::set_error(ETG_EINVAL, "an operand, scale or output pointer is NULL");
-  if (!aligned(d_a_scale, 4) || !aligned(d_w_scale, 4))
-    return etg::set_error(ETG_EALIGN, "a scale pointer is not 4-byte aligned");
-  if (!aligned(d_out, esize)) return etg::set_error(ETG_EALIGN, "output pointer is not %zu-byte aligned", esize);
+  const int32_t st =
+      check_matmul(d_a, a_stride, d_a_scale, a_scale_stride, d_w, w_stride, d_w_scale, w_scale_stride, m, n, k, d_out,
+                   out_dtype, out_stride);
+  if (st != ETG_OK || m == 0 || n == 0) return st;
   const size_t need = etg::matmul_i8_workspace(m, n, k);
   if (need != 0) {
     if (d_workspace == nullptr) return etg::set_error(ETG_EINVAL, "workspace pointer is NULL");
@@ -107,6 +118,61 @@ int32_t etg_matmul_i8(const int8_t* d_a, int64_t a_stride, const float* d_a_scal
   const hipError_t e = etg::launch_matmul_i8(p, d_workspace, (hipStream_t)stream);
   if (e != hipSuccess) return etg::set_error(ETG_EHIP, "int8 product launch failed: %s", hipGetErrorString(e));
   return ETG_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Workspace of etg_logits_i8: the residual rows' codes (rows 16-byte aligned), their
+// scales, then the product's own workspace.
+struct LogitsI8Ws {
+  int64_t code_stride;
+  size_t scale_offset, product_offset, bytes;
+};
+LogitsI8Ws logits_i8_ws(int64_t batch, int64_t vocab, int64_t hidden) {
+  LogitsI8Ws w;
+  w.code_stride = (int64_t)etg::align_up((size_t)hidden, 16);
+  w.scale_offset = etg::align_up((size_t)(batch * w.code_stride), 256);
+  w.product_offset = etg::align_up(w.scale_offset + (size_t)batch * 4, 256);
+  w.bytes = w.product_offset + etg::matmul_i8_workspace(batch, vocab, hidden);
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t etg_logits_i8_workspace(int64_t batch, int64_t vocab, int64_t hidden) {
+  const int32_t st = check_matmul_shape(batch, vocab, hidden);
+  return st != ETG_OK ? st : (int64_t)logits_i8_ws(batch, vocab, hidden).bytes;
+}
+
+int32_t etg_logits_i8(const int8_t* d_codes, int64_t code_stride, const float* d_scale, int64_t scale_stride,
+                      int64_t vocab, int64_t hidden, const void* d_residual, int32_t dtype, int64_t residual_stride,
+                      int64_t batch, void* d_out, int32_t out_dtype, int64_t out_stride, void* d_workspace,
+                      size_t workspace_bytes, void* stream) {
+  int32_t st = check_matmul_shape(batch, vocab, hidden);
+  if (st != ETG_OK) return st;
+  const LogitsI8Ws w = logits_i8_ws(batch, vocab, hidden);
+  if (batch > 0 && vocab > 0) {
+    if (d_workspace == nullptr) return etg::set_error(ETG_EINVAL, "workspace pointer is NULL");
+    if (!aligned(d_workspace, 256)) return etg::set_error(ETG_EALIGN, "workspace pointer is not 256-byte aligned");
+    if (workspace_bytes < w.bytes)
+      return etg::set_error(ETG_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, w.bytes);
+  }
+  uint8_t* ws = (uint8_t*)d_workspace;
+  int8_t* a = (int8_t*)ws;
+  float* a_scale = (float*)(ws + w.scale_offset);
+  // the product's own checks, before anything is enqueued
+  st = check_matmul(a, w.code_stride, a_scale, 1, d_codes, code_stride, d_scale, scale_stride, batch, vocab, hidden,
+                    d_out, out_dtype, out_stride);
+  if (st != ETG_OK) return st;
+  if (batch == 0 || vocab == 0) return ETG_OK;
+  st = etg_quantize_i8(d_residual, dtype, batch, hidden, residual_stride, a, w.code_stride, a_scale, 1, stream);
+  if (st != ETG_OK) return st;
+  return etg_matmul_i8(a, w.code_stride, a_scale, 1, d_codes, code_stride, d_scale, scale_stride, batch, vocab, hidden,
+                       d_out, out_dtype, out_stride, ws + w.product_offset, w.bytes - w.product_offset, stream);
 }
 
 int64_t etg_sample_workspace(int64_t batch, int64_t vocab) {

@@ -456,6 +456,22 @@ int32_t etg_matmul_i8(const int8_t* d_a, int64_t a_stride, const float* d_a_scal
                       size_t workspace_bytes, void* stream);
 
 /*
+ * Raw logits on an int8 lm_head (codes [vocab][hidden] with a scale per row, as
+ * etg_quantize_i8 makes them from a table's rows): the residual rows are quantised the
+ * same way and multiplied, etg_quantize_i8 then etg_matmul_i8 in one call.
+ *   d_residual   `dtype` (ETG_F32, ETG_BF16, ETG_F16) [batch][hidden], rows
+ *                residual_stride values apart
+ *   d_out        `out_dtype` [batch][vocab], rows out_stride values apart
+ *   d_workspace  at least etg_logits_i8_workspace() bytes, 256-byte aligned
+ * The other arguments, limits and errors are those of the two calls.
+ */
+int64_t etg_logits_i8_workspace(int64_t batch, int64_t vocab, int64_t hidden);
+int32_t etg_logits_i8(const int8_t* d_codes, int64_t code_stride, const float* d_scale, int64_t scale_stride,
+                      int64_t vocab, int64_t hidden, const void* d_residual, int32_t dtype, int64_t residual_stride,
+                      int64_t batch, void* d_out, int32_t out_dtype, int64_t out_stride, void* d_workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
  * Sampling (what ADR-0008 "POST /v1/logits" leaves to the caller of its raw logits
  * mode): one token per row of logits with temperature, top-k, top-p and min-p, from
  * given random numbers.  The settings are one value for all rows, or a device array

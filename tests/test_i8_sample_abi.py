@@ -67,6 +67,28 @@ def test_matmul_errors(L):
     assert L.etg_matmul_i8_workspace(65537, 1, 1) == -3 and L.etg_matmul_i8_workspace(1, 1, 0) == -3
 
 
+def test_logits_i8_errors(L):
+    f = L.etg_logits_i8
+
+    def call(w=_p(), ws=64, sw=_p(), sws=1, vocab=100, hidden=64, r=_p(), dt=etg.F32, rs=64, batch=4, out=_p(),
+             odt=etg.F32, os_=100, work=_p(), nbytes=1 << 40):
+        return f(w, ws, sw, sws, vocab, hidden, r, dt, rs, batch, out, odt, os_, work, nbytes, None)
+    assert call(batch=-1) == -3 and call(batch=65537) == -3 and call(vocab=-1) == -3 and call(hidden=0) == -3
+    assert call(dt=etg.Q8_0) == -2 and "dtype" in _err(L)
+    assert call(odt=7) == -2 and "output dtype" in _err(L)
+    assert call(ws=63) == -3 and "w stride" in _err(L)
+    assert call(rs=63) == -3 and "input stride" in _err(L)
+    assert call(os_=99) == -3 and call(sws=0) == -3
+    for name in ("w", "sw", "r", "out", "work"):
+        assert call(**{name: None}) == -1, name
+    assert call(r=_p(2)) == -4 and call(sw=_p(2)) == -4 and call(out=_p(2)) == -4 and call(work=_p(16)) == -4
+    need = L.etg_logits_i8_workspace(4, 100, 64)
+    assert need > L.etg_matmul_i8_workspace(4, 100, 64)
+    assert call(nbytes=need - 1) == -6 and "workspace" in _err(L)
+    assert call(batch=0, r=None, out=None, work=None) == 0 and call(vocab=0, w=None, out=None, work=None) == 0
+    assert L.etg_logits_i8_workspace(65537, 1, 1) == -3
+
+
 def _how(T=1.0, k=0, p=1.0, mp=0.0, dT=None, dk=None, dp=None, dmp=None, allowed=None, stride=0):
     return etg._Sampling(T, k, p, mp, dT, dk, dp, dmp, allowed, stride)
 
