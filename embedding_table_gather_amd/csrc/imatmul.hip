@@ -218,29 +218,33 @@ __global__ void __launch_bounds__(1024) stream_i8_kernel(MatmulI8 p, int64_t nti
   }
 }
 
-// Image of all a rows for the wide kernel: [pass][step of 128][tile of the pass][even, odd
-// slots][64 lanes], lane l's 16 bytes being a row l % 16 at slot 8 step + 2 (l / 16) + odd.
-__global__ void __launch_bounds__(256) wide_i8_image_kernel(MatmulI8 p, int nt, int steps, i32x4* __restrict__ img,
-                                                            uint32_t total) {
+// Image of all a rows, lane l's 16 bytes being a row l % 16 of its tile:
+//  wide kernel  [pass][step of 128][tile of the pass][even, odd][64 lanes], slot 8 step + 2 (l / 16) + odd
+//  tile kernel  [pass][step of 128][half][tile of the pass][64 lanes], slot 8 step + 4 half + l / 16
+__global__ void __launch_bounds__(256) i8_image_kernel(MatmulI8 p, int nt, int steps, int wide,
+                                                       i32x4* __restrict__ img, uint32_t total) {
   const uint32_t i = blockIdx.x * 256 + threadIdx.x;
   if (i >= total) return;
-  const int lane = (int)(i & 63), odd = (int)(i >> 6) & 1;
-  const uint32_t r = i >> 7;
-  const int t = (int)(r % nt), step = (int)(r / nt % steps);
-  const int64_t m = (int64_t)(r / nt / steps * nt + t) * 16 + (lane & 15);
-  img[i] = image_slot(m < p.m ? p.a + m * p.a_stride : nullptr, 8 * step + 2 * (lane >> 4) + odd, (int)p.k);
+  const int lane = (int)(i & 63);
+  const uint32_t frag = i >> 6, r = frag / (2 * nt);
+  const int f = (int)(frag % (2 * nt)), step = (int)(r % steps);
+  const int t = wide ? f >> 1 : f % nt, part = wide ? f & 1 : f / nt;
+  const int64_t m = (int64_t)(r / steps * nt + t) * 16 + (lane & 15);
+  const int slot = 8 * step + (wide ? 2 * (lane >> 4) + part : 4 * part + (lane >> 4));
+  img[i] = image_slot(m < p.m ? p.a + m * p.a_stride : nullptr, slot, (int)p.k);
 }
 
-// Passes of up to 16 NT a rows: 8 waves x MT tiles of 16 w rows per workgroup.  A load reads
+// Passes of up to 16 NT a rows: WAVES x MT tiles of 16 w rows per workgroup.  A load reads
 // 8 w rows x 128 bytes as in the stream kernel (X: rows 0 - 7 of a tile, Y: rows 8 - 15); two
 // DPP moves per register swap the odd half of X with the even half of Y, which leaves the
 // 16-row A operands of the even and of the odd slots.  The image
 // passes through three LDS buffers of one K step each, copied by global_load_lds two
 // chunks ahead; the w rows are loaded up to two chunks ahead into two register sets used in
 // turn.  One barrier per chunk.
-static constexpr int kWideWaves = 8;
-static constexpr int kWideSets = 3;   // register sets of w rows: chunks loaded ahead, and the one multiplied
-static constexpr int kWideSteps = 1;  // of 128 bytes, per chunk
+//
+// Template: NT tiles of 16 a rows and MT of 16 w rows per wave, WAVES per workgroup, SETS
+// register sets of w rows (the chunk multiplied and those loaded ahead), MINW waves per
+// SIMD.
 
 // 1 KiB from memory to LDS: lane l's 16 bytes at src to lds + 16 l.  In assembly because the
 // compiler would wait for every such copy before any LDS read; wide_barrier waits for the one
@@ -261,15 +265,19 @@ __device__ __forceinline__ void wide_barrier() {
   asm volatile("s_barrier" ::: "memory");
 }
 
-template <int DT, int NT, int MT>
-__global__ void __launch_bounds__(64 * kWideWaves, NT < 8 ? 4 : 2) wide_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
-                                                                     int chunks, int vec) {
-  constexpr int CHUNK = kWideSteps * NT * 2048, DMA = (CHUNK / 1024 + kWideWaves - 1) / kWideWaves;
+template <int DT, int NT, int MT, int WAVES, int SETS, int MINW>
+__global__ void __launch_bounds__(64 * WAVES, MINW) wide_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
+                                                                   int chunks, int passes, int nblk, int vec) {
+  constexpr int CHUNK = NT * 2048, DMA = (CHUNK / 1024 + WAVES - 1) / WAVES;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [3][CHUNK]
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int K = (int)p.k;
-  const int64_t n0 = ((int64_t)blockIdx.x * kWideWaves + wv) * MT * 16;
-  const unsigned char* src = img + (size_t)blockIdx.y * chunks * CHUNK;
+  // Workgroup ids {x, x + 8, ...} run on XCD x: the passes of one block of w rows follow each
+  // other there, and find its rows in that XCD's L2.
+  const int id = blockIdx.x, pass = id / 8 % passes, blk = id % 8 + 8 * (id / 8 / passes);
+  if (blk >= nblk) return;  // whole workgroup
+  const int64_t n0 = ((int64_t)blk * WAVES + wv) * MT * 16;
+  const unsigned char* src = img + (size_t)pass * chunks * CHUNK;
   const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem;
   auto copy = [&](int c) {
 #pragma unroll
@@ -282,59 +290,51 @@ __global__ void __launch_bounds__(64 * kWideWaves, NT < 8 ? 4 : 2) wide_i8_kerne
 #pragma unroll
   for (int t = 0; t < 2 * MT; t++) row[t] = p.w + min(n0 + 8 * t + (lane & 7), p.n - 1) * p.w_stride;
   // w rows of the chunk that is multiplied and of the next, in turn
-  i32x4 set[kWideSets][kWideSteps][2 * MT];
-  auto load = [&](int c, i32x4 (&v)[kWideSteps][2 * MT]) {
+  i32x4 set[SETS][2 * MT];
+  auto load = [&](int c, i32x4 (&v)[2 * MT]) {
+    const int off = min(128 * c + 16 * (lane >> 3), K - 16);
 #pragma unroll
-    for (int q = 0; q < kWideSteps; q++) {
-      const int off = min(128 * (kWideSteps * c + q) + 16 * (lane >> 3), K - 16);
-#pragma unroll
-      for (int t = 0; t < 2 * MT; t++) v[q][t] = __builtin_nontemporal_load((const i32x4u*)(row[t] + off));
-    }
+    for (int t = 0; t < 2 * MT; t++) v[t] = __builtin_nontemporal_load((const i32x4u*)(row[t] + off));
   };
   i32x4 acc[MT][NT];
 #pragma unroll
   for (int t = 0; t < MT; t++)
 #pragma unroll
     for (int j = 0; j < NT; j++) acc[t][j] = i32x4{0, 0, 0, 0};
-  auto chunk = [&](int c, i32x4 (&v)[kWideSteps][2 * MT]) {
+  auto chunk = [&](int c, i32x4 (&v)[2 * MT]) {
     // Chunk c and its w rows have landed, and this wave has read the buffer that the copy below
-    // refills.  Loads complete in order, and at least the w rows of two chunks were loaded after
-    // the copy of chunk c, which was started two chunks ago: they stay in flight.
-    static_assert(kWideSets == 3, "the wait below");
-    wide_barrier<2 * kWideSteps * 2 * MT>();
+    // refills.  Loads complete in order: the w rows of the SETS - 1 chunks after c stay in flight,
+    // all loaded after the copy of chunk c, which was started two chunks ago.
+    static_assert(SETS == 2 || SETS == 3, "the wait below");
+    wide_barrier<(SETS - 1) * 2 * MT>();
     if (c + 2 < chunks) copy(c + 2);  // uniform
     const i32x4* b = (const i32x4*)(smem + c % 3 * CHUNK);
+    i32x4 even[MT], odd[MT];
 #pragma unroll
-    for (int q = 0; q < kWideSteps; q++) {
-      i32x4 even[MT], odd[MT];
+    for (int t = 0; t < MT; t++)
 #pragma unroll
-      for (int t = 0; t < MT; t++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const int x = v[q][2 * t][e], y = v[q][2 * t + 1][e];
-          even[t][e] = __builtin_amdgcn_update_dpp(x, y, 0x118, 0xf, 0xc, false);  // row_shr:8 into lanes 8 - 15
-          odd[t][e] = __builtin_amdgcn_update_dpp(y, x, 0x108, 0xf, 0x3, false);   // row_shl:8 into lanes 0 - 7
-        }
-#pragma unroll
-      for (int j = 0; j < NT; j++) {
-        const i32x4 f0 = b[(q * NT + j) * 128 + lane], f1 = b[(q * NT + j) * 128 + 64 + lane];
-#pragma unroll
-        for (int t = 0; t < MT; t++) {
-          acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(even[t], f0, acc[t][j], 0, 0, 0);
-          acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(odd[t], f1, acc[t][j], 0, 0, 0);
-        }
+      for (int e = 0; e < 4; e++) {
+        const int x = v[2 * t][e], y = v[2 * t + 1][e];
+        even[t][e] = __builtin_amdgcn_update_dpp(x, y, 0x118, 0xf, 0xc, false);  // row_shr:8 into lanes 8 - 15
+        odd[t][e] = __builtin_amdgcn_update_dpp(y, x, 0x108, 0xf, 0x3, false);   // row_shl:8 into lanes 0 - 7
       }
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      const i32x4 f0 = b[j * 128 + lane], f1 = b[j * 128 + 64 + lane];
+#pragma unroll
+      for (int t = 0; t < MT; t++) acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(even[t], f0, acc[t][j], 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < MT; t++) acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(odd[t], f1, acc[t][j], 0, 0, 0);
     }
-    load(min(c + kWideSets, chunks - 1), v);  // always the same number of loads in flight
+    load(min(c + SETS, chunks - 1), v);  // always the same number of loads in flight
   };
   copy(0);
   copy(1);
 #pragma unroll
-  for (int i = 0; i < kWideSets; i++) load(min(i, chunks - 1), set[i]);
-  for (int c = 0; c < chunks; c += kWideSets) {  // a multiple of kWideSets
-    chunk(c, set[0]);
-    chunk(c + 1, set[1]);
-    chunk(c + 2, set[2]);
+  for (int i = 0; i < SETS; i++) load(min(i, chunks - 1), set[i]);
+  for (int c = 0; c < chunks; c += SETS) {  // a multiple of SETS
+#pragma unroll
+    for (int i = 0; i < SETS; i++) chunk(c + i, set[i]);
   }
   wide_barrier<0>();  // the last (repeated) loads
 #pragma unroll
@@ -345,7 +345,108 @@ __global__ void __launch_bounds__(64 * kWideWaves, NT < 8 ? 4 : 2) wide_i8_kerne
     for (int i = 0; i < 4; i++) w4[i] = p.w_scale[min(n + i, p.n - 1) * p.w_scale_stride];
 #pragma unroll
     for (int j = 0; j < NT; j++) {
-      const int64_t m = ((int64_t)blockIdx.y * NT + j) * 16 + (lane & 15);
+      const int64_t m = ((int64_t)pass * NT + j) * 16 + (lane & 15);
+      if (m < p.m) store_tile4<DT>(p.out, p.out_stride, m, n, p.n, acc[t][j], p.a_scale[m * p.a_scale_stride], w4, vec);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tile kernel: many a rows, bound by the matrix cores.
+//
+// 8 waves x 64 w rows by 128 a rows per workgroup: a wave holds 4 x 8 tiles of 16 x 16
+// (128 accumulator registers), so one 1 KiB fragment of the image read from LDS serves
+// four MFMAs (64 B / clock per CU of LDS reads at the full MFMA rate), and its own w rows
+// come straight from memory into the A operand (lane l: row l % 16, 16 bytes at
+// 16 (l / 16) of each half step), two steps ahead.
+// ---------------------------------------------------------------------------
+static constexpr int kTileWaves = 8, kTileMT = 4, kTileNT = 8;
+
+// acc += a b, in assembly so that the accumulators stay where they are: with 128 of them the
+// compiler rotates them through other registers, and copies and spills what no longer fits.
+// A product's accumulator is used again 32 MFMAs later, and read otherwise only after
+// mfma_settle.
+__device__ __forceinline__ void mfma_in_place(i32x4& acc, const i32x4& a, const i32x4& b) {
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+
+template <int DT>
+__global__ void __launch_bounds__(64 * kTileWaves, 2) tile_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
+                                                                     int chunks, int passes, int nblk, int vec) {
+  constexpr int MT = kTileMT, NT = kTileNT, CHUNK = NT * 2048, DMA = CHUNK / 1024 / kTileWaves, F = 2 * NT;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [3][CHUNK]
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int K = (int)p.k;
+  // passes of one block of w rows follow each other on one XCD, as in the wide kernel
+  const int id = blockIdx.x, pass = id / 8 % passes, blk = id % 8 + 8 * (id / 8 / passes);
+  if (blk >= nblk) return;  // whole workgroup
+  const int64_t n0 = ((int64_t)blk * kTileWaves + wv) * MT * 16;
+  const unsigned char* src = img + (size_t)pass * chunks * CHUNK;
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem;
+  auto copy = [&](int c) {
+#pragma unroll
+    for (int d = 0; d < DMA; d++) {
+      const int at = (wv * DMA + d) * 1024;
+      lds_copy_1k(src + (size_t)c * CHUNK + at + lane * 16, lds + c % 3 * CHUNK + at);
+    }
+  };
+  const int8_t* row[MT];
+#pragma unroll
+  for (int t = 0; t < MT; t++) row[t] = p.w + min(n0 + 16 * t + (lane & 15), p.n - 1) * p.w_stride;
+  i32x4 set[2][2][MT];
+  auto load = [&](int c, i32x4 (&v)[2][MT]) {
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+      const int off = min(128 * c + 64 * q + 16 * (lane >> 4), K - 16);
+#pragma unroll
+      for (int t = 0; t < MT; t++) v[q][t] = *(const i32x4u*)(row[t] + off);
+    }
+  };
+  i32x4 acc[MT][NT];
+#pragma unroll
+  for (int t = 0; t < MT; t++)
+#pragma unroll
+    for (int j = 0; j < NT; j++) acc[t][j] = i32x4{0, 0, 0, 0};
+  auto chunk = [&](int c, i32x4 (&v)[2][MT]) {
+    wide_barrier<2 * MT>();  // as in the wide kernel
+    if (c + 2 < chunks) copy(c + 2);
+    const i32x4* b = (const i32x4*)(smem + c % 3 * CHUNK) + lane;
+    i32x4 f[3];  // fragments read two ahead of their MFMAs
+    f[0] = b[0];
+    f[1] = b[64];
+#pragma unroll
+    for (int i = 0; i < F; i++) {
+      if (i + 2 < F) f[(i + 2) % 3] = b[(i + 2) * 64];
+#pragma unroll
+      for (int t = 0; t < MT; t++) mfma_in_place(acc[t][i % NT], v[i / NT][t], f[i % 3]);
+    }
+    load(min(c + 2, chunks - 1), v);
+  };
+  copy(0);
+  copy(1);
+  load(0, set[0]);
+  load(1, set[1]);
+  mfma_settle();
+  for (int c = 0; c < chunks; c += 2) {  // an even number
+    chunk(c, set[0]);
+    chunk(c + 1, set[1]);
+  }
+  wide_barrier<0>();  // the last (repeated) loads
+  mfma_settle();
+#pragma unroll
+  for (int t = 0; t < MT; t++)
+#pragma unroll
+    for (int j = 0; j < NT; j++) asm volatile("" : "+a"(acc[t][j]));  // read after the wait
+#pragma unroll
+  for (int t = 0; t < MT; t++) {
+    const int64_t n = n0 + 16 * t + 4 * (lane >> 4);
+    float w4[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) w4[i] = p.w_scale[min(n + i, p.n - 1) * p.w_scale_stride];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      const int64_t m = ((int64_t)pass * NT + j) * 16 + (lane & 15);
       if (m < p.m) store_tile4<DT>(p.out, p.out_stride, m, n, p.n, acc[t][j], p.a_scale[m * p.a_scale_stride], w4, vec);
     }
   }
@@ -354,23 +455,23 @@ __global__ void __launch_bounds__(64 * kWideWaves, NT < 8 ? 4 : 2) wide_i8_kerne
 // ---------------------------------------------------------------------------
 // Dispatch
 // ---------------------------------------------------------------------------
-enum { I8_SIMPLE, I8_STREAM, I8_WIDE };
+enum { I8_SIMPLE, I8_STREAM, I8_WIDE, I8_TILE };
 struct I8Plan {
-  int kind, nt, steps;  // wide: K steps of 128, a multiple of the register sets
+  int kind, nt, steps;  // wide: K steps of 128, a multiple of any number of sets
   int64_t passes;
   size_t img_bytes;
 };
 
 static I8Plan i8_plan(int64_t m, int64_t n, int64_t k) {
   I8Plan p = {};
-  p.steps = (int)cdiv(k, 128 * kWideSteps * kWideSets) * kWideSets * kWideSteps;
+  p.steps = (int)cdiv(k, 128 * 6) * 6;
   if (k < 16 || n > ((int64_t)1 << 30)) {
     p.kind = I8_SIMPLE;
   } else if (m <= 16 && (size_t)cdiv(k, 512) * 4 * (m <= 8 ? 1024 : 2048) <= kMaxLds) {
     p.kind = I8_STREAM;
     p.steps = (int)cdiv(k, 128 * kStreamSteps) * kStreamSteps;  // steps of 128
   } else {
-    p.kind = I8_WIDE;
+    p.kind = m <= 128 ? I8_WIDE : I8_TILE;
     p.nt = m <= 32 ? 2 : m <= 64 ? 4 : 8;
     p.passes = cdiv(m, 16 * p.nt);
     p.img_bytes = (size_t)p.passes * p.nt * p.steps * 2048;
@@ -397,13 +498,15 @@ static hipError_t launch_stream_i8(const MatmulI8& p, const I8Plan& pl, int vec,
   return hipGetLastError();
 }
 
-template <int DT, int NT, int MT>
+template <int DT, int NT, int MT, int WAVES, int SETS, int MINW>
 static hipError_t launch_wide_i8(const MatmulI8& p, const I8Plan& pl, const void* img, int vec, hipStream_t stream) {
-  const size_t lds = (size_t)3 * kWideSteps * NT * 2048;
-  hipError_t e = set_dynamic_lds((const void*)wide_i8_kernel<DT, NT, MT>, lds);
+  auto kernel = wide_i8_kernel<DT, NT, MT, WAVES, SETS, MINW>;
+  const size_t lds = (size_t)3 * NT * 2048;
+  hipError_t e = set_dynamic_lds((const void*)kernel, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((wide_i8_kernel<DT, NT, MT>), dim3((unsigned)cdiv(p.n, kWideWaves * MT * 16), (unsigned)pl.passes),
-                     dim3(64 * kWideWaves), lds, stream, p, (const unsigned char*)img, pl.steps / kWideSteps, vec);
+  const int64_t nblk = cdiv(p.n, WAVES * MT * 16);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(align_up((size_t)nblk, 8) * pl.passes)), dim3(64 * WAVES), lds, stream, p,
+                     (const unsigned char*)img, pl.steps, (int)pl.passes, (int)nblk, vec);
   return hipGetLastError();
 }
 
@@ -421,13 +524,23 @@ static hipError_t launch_matmul_dt(const MatmulI8& p, void* ws, hipStream_t stre
   if (pl.kind == I8_STREAM)
     return p.m <= 8 ? launch_stream_i8<DT, 1>(p, pl, vec, stream) : launch_stream_i8<DT, 2>(p, pl, vec, stream);
   const uint32_t total = (uint32_t)(pl.img_bytes / 16);  // at most 65536 x 65792 bytes
-  hipLaunchKernelGGL(wide_i8_image_kernel, dim3((unsigned)cdiv(total, 256)), dim3(256), 0, stream, p, pl.nt, pl.steps,
-                     (i32x4*)ws, total);
+  hipLaunchKernelGGL(i8_image_kernel, dim3((unsigned)cdiv(total, 256)), dim3(256), 0, stream, p, pl.nt, pl.steps,
+                     (int)(pl.kind == I8_WIDE), (i32x4*)ws, total);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (pl.nt == 2) return launch_wide_i8<DT, 2, 2>(p, pl, ws, vec, stream);
-  if (pl.nt == 4) return launch_wide_i8<DT, 4, 2>(p, pl, ws, vec, stream);
-  return launch_wide_i8<DT, 8, 2>(p, pl, ws, vec, stream);
+  if (pl.kind == I8_TILE) {
+    const size_t lds = (size_t)3 * kTileNT * 2048;
+    e = set_dynamic_lds((const void*)tile_i8_kernel<DT>, lds);
+    if (e != hipSuccess) return e;
+    const int64_t nblk = cdiv(p.n, kTileWaves * kTileMT * 16);
+    hipLaunchKernelGGL((tile_i8_kernel<DT>), dim3((unsigned)(align_up((size_t)nblk, 8) * pl.passes)),
+                       dim3(64 * kTileWaves), lds, stream, p, (const unsigned char*)ws, pl.steps, (int)pl.passes, (int)nblk,
+                       vec);
+    return hipGetLastError();
+  }
+  if (pl.nt == 2) return launch_wide_i8<DT, 2, 2, 8, 3, 4>(p, pl, ws, vec, stream);
+  if (pl.nt == 4) return launch_wide_i8<DT, 4, 2, 8, 3, 4>(p, pl, ws, vec, stream);
+  return launch_wide_i8<DT, 8, 2, 8, 3, 2>(p, pl, ws, vec, stream);
 }
 
 hipError_t launch_matmul_i8(const MatmulI8& p, void* ws, hipStream_t stream) {
