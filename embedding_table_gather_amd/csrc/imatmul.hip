@@ -67,17 +67,30 @@ __global__ void __launch_bounds__(256) matmul_i8_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Streaming kernels: few a rows, bound by reading w once.
+// Operands of v_mfma_i32_16x16x64_i8: lane l of the A operand holds 16 bytes of row l % 16,
+// of the B operand of column l % 16, both of K group l / 16; result register i is row
+// 4 (l / 16) + i of column l % 16.  Here w rows are A rows and a rows are B columns, and a
+// K step of 256 bytes is four MFMAs: MFMA i takes slot 4 g + i of the step for K group g.
 //
-// The a rows are the B operand of v_mfma_i32_16x16x64_i8, kept as an image in the order
-// in which the lanes read it: 1 KiB per K step of 64 and tile of 16 a rows, lane l's 16
-// bytes at 16 l (a row 16 t + l % 16, bytes of K slot 4 step + l / 16).  K slot j stands
-// for the 16 bytes at k = min(16 j, K - 16): where K is no multiple of 16 the last slot
-// overlaps the one before, and the image holds zeros for the bytes that are covered
-// twice and for slots and rows past the end.  So w rows of any length are read by
-// 16-byte loads that stay inside the row.
+// K slot j stands for the 16 bytes at k = min(16 j, K - 16): where K is no multiple of 16 the
+// last slot overlaps the one before, and the a rows' image below holds zeros for the bytes
+// that are covered twice and for slots and rows past the end.  So w rows of any length are
+// read by 16-byte loads that stay inside the row.
+//
+// The a rows are kept as an image in fragment order, 1 KiB per (step, i, tile of 16 a rows)
+// with lane l's 16 bytes at 16 l: reads of it are free of LDS bank conflicts.
+//
+// w rows go straight from memory to registers, in four loads per 16 rows and step: lane l of
+// load q reads slot 4 (l / 16) + l % 4 of row 4 (l / 4 % 4) + q, so the four lanes of a quad
+// read 64 contiguous bytes and an instruction four rows of 256.  (With lane l at row l % 16
+// every lane of a quad is in another line, and the address unit takes four times as long: it
+// was what bound the kernels, at 16 bytes a clock per CU.)  A 4 x 4 transposition over the
+// quad's lanes and the four loads, two DPP selects per register, then leaves row l % 16 and
+// slot 4 (l / 16) + i in register set i.
 // ---------------------------------------------------------------------------
-// The image's 16 bytes for a row `row` (nullptr: past the end) and slot j.
+typedef i32x4 i32x4u __attribute__((aligned(1)));
+
+// The image's 16 bytes for a row (nullptr: past the end) and slot j.
 __device__ __forceinline__ i32x4 image_slot(const int8_t* row, int j, int K) {
   i32x4 v = {0, 0, 0, 0};
   if (row == nullptr || 16 * j >= K) return v;
@@ -91,6 +104,29 @@ __device__ __forceinline__ i32x4 image_slot(const int8_t* row, int j, int K) {
     }
   }
   return v;
+}
+
+// Row of the tile that a lane's load q reads, and the slot of the step.
+__device__ __forceinline__ int load_row(int lane, int q) { return 4 * ((lane >> 2) & 3) + q; }
+__device__ __forceinline__ int load_slot(int lane) { return 4 * (lane >> 4) + (lane & 3); }
+
+// v[i] of lane (quad, j) <- v[j] of lane (quad, i).
+__device__ __forceinline__ void quad_transpose(i32x4 (&v)[4], int lane) {
+  const bool b0 = lane & 1, b1 = lane & 2;
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    int r[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {  // exchange bit 0 of the lane and of the register
+      const int o = __builtin_amdgcn_mov_dpp(v[i ^ 1][e], 0xb1, 0xf, 0xf, true);  // quad_perm 1,0,3,2
+      r[i] = b0 == (bool)(i & 1) ? v[i][e] : o;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {  // bit 1
+      const int o = __builtin_amdgcn_mov_dpp(r[i ^ 2], 0x4e, 0xf, 0xf, true);  // quad_perm 2,3,0,1
+      v[i][e] = b1 == (bool)(i & 2) ? r[i] : o;
+    }
+  }
 }
 
 // Stores of one 16 x 16 tile: lane l has w rows n0 .. n0 + 3 of a row m (values acc).
@@ -125,331 +161,285 @@ __device__ __forceinline__ void store_tile4(void* out, int64_t out_stride, int64
   }
 }
 
-typedef i32x4 i32x4u __attribute__((aligned(1)));
-
-// Up to 8 IMG a rows: the whole image in LDS, a persistent grid, each wave a contiguous
-// run of tiles of 8 w rows.
-//
-// One load instruction reads 8 rows x 128 bytes (full lines): lane l row l % 8, slot l / 8
-// of the step.  As the A operand of the MFMA that is w row m % 8 at slots 2 g + m / 8 in A
-// row m and lane group g; the image's column n holds a row n % 8 at the same slots
-// 2 g + n / 8, so the sum for (w row r, a row b) is D[r][b] + D[r + 8][b + 8] and the other
-// half of D is unused: the matrix cores idle anyway (16 rows: a second image).
-//
-// Two groups of four steps (8 KiB a wave) are always in flight, in two register sets used
-// in turn, across tiles too; a tile's scales are loaded with its groups.
-static constexpr int kStreamSteps = 4;  // steps of 128 bytes per group
-
-template <int DT, int IMG>
+// ---------------------------------------------------------------------------
+// Up to 16 a rows, bound by reading w once: the whole image in LDS, a persistent grid, each
+// wave a contiguous run of tiles of 16 w rows.  Two steps (8 KiB a wave) are always in
+// flight, in two register sets used in turn, across tiles too; a tile's scales are loaded
+// with its steps.
+// ---------------------------------------------------------------------------
+template <int DT>
 __global__ void __launch_bounds__(1024) stream_i8_kernel(MatmulI8 p, int64_t ntiles, int steps, int vec) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  i32x4* img = (i32x4*)smem;  // [steps][IMG][64]
+  i32x4* img = (i32x4*)smem;  // [steps][4][64]
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nw = blockDim.x >> 6, K = (int)p.k;
   const int64_t wave = (int64_t)blockIdx.x * nw + wv, waves = (int64_t)gridDim.x * nw;
   const int64_t t0 = wave * ntiles / waves, t1 = (wave + 1) * ntiles / waves;
 
   struct Set {
-    i32x4 v[kStreamSteps];
-    float scale;  // of w row lane % 8
+    i32x4 v[4];
+    float scale;  // of w row lane % 16
   } set[2];
-  // The group that is loaded next.  Every call loads (past the last tile that one again):
+  // The step that is loaded next.  Every call loads (past the last tile that one again):
   // with a fixed number of loads the wait for one set leaves the other's in flight.
   int64_t lt = t0;
   int ls = 0;
   auto load = [&](Set& x) {
-    const int64_t r = min(max(min(lt, t1 - 1), (int64_t)0) * 8 + (lane & 7), p.n - 1);
-    const int8_t* row = p.w + r * p.w_stride;
-    x.scale = p.w_scale[r * p.w_scale_stride];
+    const int64_t t = max(min(lt, t1 - 1), (int64_t)0) * 16;
+    x.scale = p.w_scale[min(t + (lane & 15), p.n - 1) * p.w_scale_stride];
+    const int off = min(256 * ls + 16 * load_slot(lane), K - 16);
 #pragma unroll
-    for (int q = 0; q < kStreamSteps; q++)
-      x.v[q] = __builtin_nontemporal_load((const i32x4u*)(row + min(128 * (ls + q) + 16 * (lane >> 3), K - 16)));
-    ls += kStreamSteps;
-    if (ls >= steps) ls = 0, lt++;
+    for (int q = 0; q < 4; q++)
+      x.v[q] = __builtin_nontemporal_load(
+          (const i32x4u*)(p.w + min(t + load_row(lane, q), p.n - 1) * p.w_stride + off));
+    if (++ls == steps) ls = 0, lt++;
   };
   load(set[0]);
   load(set[1]);
-  for (int i = threadIdx.x; i < steps * IMG * 64; i += blockDim.x) {
-    const int l = i & 63, im = IMG == 1 ? 0 : (i >> 6) & 1, st = (i >> 6) / IMG;
-    const int m = 8 * im + (l & 7);
-    img[i] = image_slot(m < p.m ? p.a + m * p.a_stride : nullptr, 8 * st + 2 * (l >> 4) + ((l >> 3) & 1), K);
+  for (int i = threadIdx.x; i < steps * 256; i += blockDim.x) {
+    const int m = i & 15;
+    img[i] = image_slot(m < p.m ? p.a + m * p.a_stride : nullptr, 16 * (i >> 8) + 4 * ((i >> 4) & 3) + ((i >> 6) & 3), K);
   }
   __syncthreads();
-  const int b = lane & 7;
-  const bool holder = (lane & 40) == 0;  // lanes with the first half of a useful sum
-  float s[IMG];
-#pragma unroll
-  for (int im = 0; im < IMG; im++) s[im] = 8 * im + b < p.m ? p.a_scale[(8 * im + b) * p.a_scale_stride] : 0.f;
-  i32x4 acc[IMG];
-#pragma unroll
-  for (int im = 0; im < IMG; im++) acc[im] = i32x4{0, 0, 0, 0};
+  const int m = lane & 15;
+  const float s = m < p.m ? p.a_scale[m * p.a_scale_stride] : 0.f;
+  i32x4 acc = {0, 0, 0, 0};
   int64_t t = t0;
   int st = 0;
-  auto compute = [&](const Set& x) {
+  auto compute = [&](Set& x) {
+    quad_transpose(x.v, lane);
 #pragma unroll
-    for (int q = 0; q < kStreamSteps; q++)
-#pragma unroll
-      for (int im = 0; im < IMG; im++)
-        acc[im] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x.v[q], img[((st + q) * IMG + im) * 64 + lane], acc[im], 0, 0, 0);
-    st += kStreamSteps;
-    if (st < steps || t >= t1) return;
-    // holder lane l: w rows 4 (l / 16) + i of the tile, a row 8 im + l % 8
-    const int64_t n = t * 8 + 4 * (lane >> 4);
+    for (int i = 0; i < 4; i++)
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(x.v[i], img[(st * 4 + i) * 64 + lane], acc, 0, 0, 0);
+    if (++st < steps || t >= t1) return;
     float w4[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) w4[i] = __shfl(x.scale, 4 * ((lane >> 4) & 1) + i, 64);
-#pragma unroll
-    for (int im = 0; im < IMG; im++) {
-      i32x4 sum;
-#pragma unroll
-      for (int i = 0; i < 4; i++) sum[i] = acc[im][i] + __shfl(acc[im][i], (lane + 40) & 63, 64);
-      if (holder && 8 * im + b < p.m) store_tile4<DT>(p.out, p.out_stride, 8 * im + b, n, p.n, sum, s[im], w4, vec);
-      acc[im] = i32x4{0, 0, 0, 0};
-    }
+    for (int i = 0; i < 4; i++) w4[i] = __shfl(x.scale, 4 * (lane >> 4) + i, 64);
+    if (m < p.m) store_tile4<DT>(p.out, p.out_stride, m, t * 16 + 4 * (lane >> 4), p.n, acc, s, w4, vec);
+    acc = i32x4{0, 0, 0, 0};
     st = 0;
     t++;
   };
-  const int64_t groups = (t1 - t0) * (steps / kStreamSteps);
-  for (int64_t g = 0; g < groups; g += 2) {  // an odd number: the last half has no tile to store
+  const int64_t total = (t1 - t0) * steps;
+  for (int64_t g = 0; g < total; g += 2) {  // an odd number: the last half has no tile to store
     compute(set[0]);
     load(set[0]);
+    if (st == steps) st = 0;
     compute(set[1]);
     load(set[1]);
   }
 }
 
-// Image of all a rows, lane l's 16 bytes being a row l % 16 of its tile:
-//  wide kernel  [pass][step of 128][tile of the pass][even, odd][64 lanes], slot 8 step + 2 (l / 16) + odd
-//  tile kernel  [pass][step of 128][half][tile of the pass][64 lanes], slot 8 step + 4 half + l / 16
-__global__ void __launch_bounds__(256) i8_image_kernel(MatmulI8 p, int nt, int steps, int wide,
-                                                       i32x4* __restrict__ img, uint32_t total) {
-  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= total) return;
-  const int lane = (int)(i & 63);
-  const uint32_t frag = i >> 6, r = frag / (2 * nt);
-  const int f = (int)(frag % (2 * nt)), step = (int)(r % steps);
-  const int t = wide ? f >> 1 : f % nt, part = wide ? f & 1 : f / nt;
+// Image of all a rows for the kernels below: [pass][step][i][tile of the pass][64 lanes].
+__global__ void __launch_bounds__(256) i8_image_kernel(MatmulI8 p, int nt, int steps, i32x4* __restrict__ img,
+                                                       uint32_t total) {
+  const uint32_t x = blockIdx.x * 256 + threadIdx.x;
+  if (x >= total) return;
+  const int lane = (int)(x & 63);
+  const uint32_t frag = x >> 6, r = frag / (4 * nt);
+  const int t = (int)(frag % nt), i = (int)(frag / nt & 3), step = (int)(r % steps);
   const int64_t m = (int64_t)(r / steps * nt + t) * 16 + (lane & 15);
-  const int slot = 8 * step + (wide ? 2 * (lane >> 4) + part : 4 * part + (lane >> 4));
-  img[i] = image_slot(m < p.m ? p.a + m * p.a_stride : nullptr, slot, (int)p.k);
+  img[x] = image_slot(m < p.m ? p.a + m * p.a_stride : nullptr, 16 * step + 4 * (lane >> 4) + i, (int)p.k);
 }
 
-// Passes of up to 16 NT a rows: WAVES x MT tiles of 16 w rows per workgroup.  A load reads
-// 8 w rows x 128 bytes as in the stream kernel (X: rows 0 - 7 of a tile, Y: rows 8 - 15); two
-// DPP moves per register swap the odd half of X with the even half of Y, which leaves the
-// 16-row A operands of the even and of the odd slots.  The image
-// passes through three LDS buffers of one K step each, copied by global_load_lds two
-// chunks ahead; the w rows are loaded up to two chunks ahead into two register sets used in
-// turn.  One barrier per chunk.
-//
-// Template: NT tiles of 16 a rows and MT of 16 w rows per wave, WAVES per workgroup, SETS
-// register sets of w rows (the chunk multiplied and those loaded ahead), MINW waves per
-// SIMD.
-
-// 1 KiB from memory to LDS: lane l's 16 bytes at src to lds + 16 l.  In assembly because the
-// compiler would wait for every such copy before any LDS read; wide_barrier waits for the one
-// that is due.  No register is written.
-__device__ __forceinline__ void lds_copy_1k(const void* src, uint32_t lds) {
+// 1 KiB from memory to LDS: lane l's 16 bytes at src + offset (16 l) to lds + 16 l.  In
+// assembly because the compiler would wait for every such copy before any LDS read;
+// load_barrier waits for the one that is due.  No register is written.
+__device__ __forceinline__ void lds_copy_1k(const void* src, uint32_t offset, uint32_t lds) {
   uint32_t m0;  // the LDS base register, left as it was
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b32 m0, %0"
+  const uint64_t base = ((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)src >> 32)) << 32) |
+                        (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(uint64_t)src);
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
                : "=&s"(m0)
-               : "v"(src), "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "v"(offset), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
                : "memory");
 }
 
 // vmcnt(N) lgkmcnt(0), then a workgroup barrier that no memory access crosses.
 template <int N>
-__device__ __forceinline__ void wide_barrier() {
+__device__ __forceinline__ void load_barrier() {
   static_assert(N >= 0 && N < 64, "vmcnt field");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
   asm volatile("s_barrier" ::: "memory");
 }
 
-template <int DT, int NT, int MT, int WAVES, int SETS, int MINW>
-__global__ void __launch_bounds__(64 * WAVES, MINW) wide_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
-                                                                   int chunks, int passes, int nblk, int vec) {
-  constexpr int CHUNK = NT * 2048, DMA = (CHUNK / 1024 + WAVES - 1) / WAVES;
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [3][CHUNK]
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int K = (int)p.k;
-  // Workgroup ids {x, x + 8, ...} run on XCD x: the passes of one block of w rows follow each
-  // other there, and find its rows in that XCD's L2.
-  const int id = blockIdx.x, pass = id / 8 % passes, blk = id % 8 + 8 * (id / 8 / passes);
-  if (blk >= nblk) return;  // whole workgroup
-  const int64_t n0 = ((int64_t)blk * WAVES + wv) * MT * 16;
-  const unsigned char* src = img + (size_t)pass * chunks * CHUNK;
-  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem;
-  auto copy = [&](int c) {
+// What the two kernels below share: the place of a workgroup, its w rows and its part of the
+// image.  Workgroup ids {x, x + 8, ...} run on XCD x: the passes of one block of w rows
+// follow each other there, and find its rows in that XCD's L2.
+template <int NT, int MT, int WAVES>
+struct I8Block {
+  static constexpr int CHUNK = NT * 4096, DMA = (CHUNK / 1024 + WAVES - 1) / WAVES;
+  int lane, wv, pass, blk, K;
+  int64_t n0;
+  const unsigned char* src;
+  const int8_t* row[MT][4];
+  __device__ __forceinline__ I8Block(const MatmulI8& p, const unsigned char* img, int steps, int passes) {
+    lane = threadIdx.x & 63;
+    wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int id = blockIdx.x;
+    pass = id / 8 % passes;
+    blk = id % 8 + 8 * (id / 8 / passes);
+    K = (int)p.k;
+    n0 = ((int64_t)blk * WAVES + wv) * MT * 16;
+    src = img + (size_t)pass * steps * CHUNK;
+#pragma unroll
+    for (int t = 0; t < MT; t++)
+#pragma unroll
+      for (int q = 0; q < 4; q++) row[t][q] = p.w + min(n0 + 16 * t + load_row(lane, q), p.n - 1) * p.w_stride;
+  }
+  // this wave's part of the image of step c to the buffer at lds
+  __device__ __forceinline__ void copy(int c, uint32_t lds) const {
 #pragma unroll
     for (int d = 0; d < DMA; d++) {
       const int at = (wv * DMA + d) * 1024;
-      if (at < CHUNK) lds_copy_1k(src + (size_t)c * CHUNK + at + lane * 16, lds + c % 3 * CHUNK + at);  // uniform
+      if (CHUNK % (1024 * WAVES) == 0 || at < CHUNK)  // uniform
+        lds_copy_1k(src + (size_t)c * CHUNK + at, (uint32_t)lane * 16, lds + at);
     }
-  };
-  const int8_t* row[2 * MT];  // X and Y rows of each tile
+  }
+  template <bool ONCE>
+  __device__ __forceinline__ void load(int c, i32x4 (&v)[MT][4]) const {
+    const int off = min(256 * c + 16 * load_slot(lane), K - 16);
 #pragma unroll
-  for (int t = 0; t < 2 * MT; t++) row[t] = p.w + min(n0 + 8 * t + (lane & 7), p.n - 1) * p.w_stride;
-  // w rows of the chunk that is multiplied and of the next, in turn
-  i32x4 set[SETS][2 * MT];
-  auto load = [&](int c, i32x4 (&v)[2 * MT]) {
-    const int off = min(128 * c + 16 * (lane >> 3), K - 16);
+    for (int t = 0; t < MT; t++)
 #pragma unroll
-    for (int t = 0; t < 2 * MT; t++) v[t] = __builtin_nontemporal_load((const i32x4u*)(row[t] + off));
-  };
-  i32x4 acc[MT][NT];
+      for (int q = 0; q < 4; q++) {
+        if constexpr (ONCE) v[t][q] = __builtin_nontemporal_load((const i32x4u*)(row[t][q] + off));
+        else v[t][q] = *(const i32x4u*)(row[t][q] + off);
+      }
+  }
+  template <int DT>
+  __device__ __forceinline__ void store(const MatmulI8& p, const i32x4 (&acc)[MT][NT], int vec) const {
+#pragma unroll
+    for (int t = 0; t < MT; t++) {
+      const int64_t n = n0 + 16 * t + 4 * (lane >> 4);
+      float w4[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) w4[i] = p.w_scale[min(n + i, p.n - 1) * p.w_scale_stride];
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        const int64_t m = ((int64_t)pass * NT + j) * 16 + (lane & 15);
+        if (m < p.m) store_tile4<DT>(p.out, p.out_stride, m, n, p.n, acc[t][j], p.a_scale[m * p.a_scale_stride], w4, vec);
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Passes of up to 16 NT a rows, bound by reading w: WAVES x MT tiles of 16 w rows per
+// workgroup.  The image passes through three LDS buffers of one step each, copied by
+// global_load_lds two steps ahead; the w rows are loaded up to two steps ahead into two
+// register sets used in turn.  One barrier per step.
+// ---------------------------------------------------------------------------
+template <int DT, int NT, int MT, int WAVES, int MINW>
+__global__ void __launch_bounds__(64 * WAVES, MINW) wide_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
+                                                                   int steps, int passes, int nblk, int vec) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [3][CHUNK]
+  using B = I8Block<NT, MT, WAVES>;
+  const B blk(p, img, steps, passes);
+  if (blk.blk >= nblk) return;  // whole workgroup
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem;
+  i32x4 set[2][MT][4], acc[MT][NT];
 #pragma unroll
   for (int t = 0; t < MT; t++)
 #pragma unroll
     for (int j = 0; j < NT; j++) acc[t][j] = i32x4{0, 0, 0, 0};
-  auto chunk = [&](int c, i32x4 (&v)[2 * MT]) {
-    // Chunk c and its w rows have landed, and this wave has read the buffer that the copy below
-    // refills.  Loads complete in order: the w rows of the SETS - 1 chunks after c stay in flight,
-    // all loaded after the copy of chunk c, which was started two chunks ago.
-    static_assert(SETS == 2 || SETS == 3, "the wait below");
-    wide_barrier<(SETS - 1) * 2 * MT>();
-    if (c + 2 < chunks) copy(c + 2);  // uniform
-    const i32x4* b = (const i32x4*)(smem + c % 3 * CHUNK);
-    i32x4 even[MT], odd[MT];
+  auto step = [&](int c, i32x4 (&v)[MT][4]) {
+    // Step c's image and w rows have landed, and this wave has read the buffer that the copy
+    // below refills.  Loads complete in order: the w rows of step c + 1 stay in flight.
+    load_barrier<4 * MT>();
+    if (c + 2 < steps) blk.copy(c + 2, lds + (c + 2) % 3 * B::CHUNK);  // uniform
+    const i32x4* b = (const i32x4*)(smem + c % 3 * B::CHUNK) + blk.lane;
 #pragma unroll
-    for (int t = 0; t < MT; t++)
+    for (int t = 0; t < MT; t++) quad_transpose(v[t], blk.lane);
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        const int x = v[2 * t][e], y = v[2 * t + 1][e];
-        even[t][e] = __builtin_amdgcn_update_dpp(x, y, 0x118, 0xf, 0xc, false);  // row_shr:8 into lanes 8 - 15
-        odd[t][e] = __builtin_amdgcn_update_dpp(y, x, 0x108, 0xf, 0x3, false);   // row_shl:8 into lanes 0 - 7
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        const i32x4 f = b[(i * NT + j) * 64];
+#pragma unroll
+        for (int t = 0; t < MT; t++) acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[t][i], f, acc[t][j], 0, 0, 0);
       }
-#pragma unroll
-    for (int j = 0; j < NT; j++) {
-      const i32x4 f0 = b[j * 128 + lane], f1 = b[j * 128 + 64 + lane];
-#pragma unroll
-      for (int t = 0; t < MT; t++) acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(even[t], f0, acc[t][j], 0, 0, 0);
-#pragma unroll
-      for (int t = 0; t < MT; t++) acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(odd[t], f1, acc[t][j], 0, 0, 0);
-    }
-    load(min(c + SETS, chunks - 1), v);  // always the same number of loads in flight
+    blk.template load<true>(min(c + 2, steps - 1), v);  // always the same number of loads in flight
   };
-  copy(0);
-  copy(1);
-#pragma unroll
-  for (int i = 0; i < SETS; i++) load(min(i, chunks - 1), set[i]);
-  for (int c = 0; c < chunks; c += SETS) {  // a multiple of SETS
-#pragma unroll
-    for (int i = 0; i < SETS; i++) chunk(c + i, set[i]);
+  blk.copy(0, lds);
+  blk.copy(1, lds + B::CHUNK);
+  blk.template load<true>(0, set[0]);
+  blk.template load<true>(1, set[1]);
+  for (int c = 0; c < steps; c += 2) {  // an even number
+    step(c, set[0]);
+    step(c + 1, set[1]);
   }
-  wide_barrier<0>();  // the last (repeated) loads
-#pragma unroll
-  for (int t = 0; t < MT; t++) {
-    const int64_t n = n0 + 16 * t + 4 * (lane >> 4);
-    float w4[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) w4[i] = p.w_scale[min(n + i, p.n - 1) * p.w_scale_stride];
-#pragma unroll
-    for (int j = 0; j < NT; j++) {
-      const int64_t m = ((int64_t)pass * NT + j) * 16 + (lane & 15);
-      if (m < p.m) store_tile4<DT>(p.out, p.out_stride, m, n, p.n, acc[t][j], p.a_scale[m * p.a_scale_stride], w4, vec);
-    }
-  }
+  load_barrier<0>();  // the last (repeated) loads
+  blk.template store<DT>(p, acc, vec);
 }
 
 // ---------------------------------------------------------------------------
-// Tile kernel: many a rows, bound by the matrix cores.
-//
-// 8 waves x 64 w rows by 128 a rows per workgroup: a wave holds 4 x 8 tiles of 16 x 16
-// (128 accumulator registers), so one 1 KiB fragment of the image read from LDS serves
-// four MFMAs (64 B / clock per CU of LDS reads at the full MFMA rate), and its own w rows
-// come straight from memory into the A operand (lane l: row l % 16, 16 bytes at
-// 16 (l / 16) of each half step), two steps ahead.
+// Passes of 256 a rows, bound by the matrix cores: 4 waves x 64 w rows per workgroup.  A wave
+// holds 4 x 16 tiles of 16 x 16 in 256 accumulator registers (one wave per SIMD), so a 1 KiB
+// fragment of the image read from LDS serves four MFMAs: 64 B a clock per CU of LDS reads at
+// the full MFMA rate.  The image passes through two LDS buffers of one step, each refilled
+// one step ahead.  The next step's w rows are transposed between the MFMAs of this one.
 // ---------------------------------------------------------------------------
-static constexpr int kTileWaves = 8, kTileMT = 4, kTileNT = 8;
+static constexpr int kTileWaves = 4, kTileMT = 4, kTileNT = 16;
 
-// acc += a b, in assembly so that the accumulators stay where they are: with 128 of them the
-// compiler rotates them through other registers, and copies and spills what no longer fits.
-// A product's accumulator is used again 32 MFMAs later, and read otherwise only after
-// mfma_settle.
+// acc += a b, in assembly so that the accumulators stay where they are: the compiler rotates
+// them through other registers, and copies and spills what no longer fits.  An accumulator is
+// used again 64 MFMAs later, and read otherwise only after mfma_settle.
 __device__ __forceinline__ void mfma_in_place(i32x4& acc, const i32x4& a, const i32x4& b) {
   asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
 __device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 template <int DT>
-__global__ void __launch_bounds__(64 * kTileWaves, 2) tile_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
-                                                                     int chunks, int passes, int nblk, int vec) {
-  constexpr int MT = kTileMT, NT = kTileNT, CHUNK = NT * 2048, DMA = CHUNK / 1024 / kTileWaves, F = 2 * NT;
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [3][CHUNK]
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int K = (int)p.k;
-  // passes of one block of w rows follow each other on one XCD, as in the wide kernel
-  const int id = blockIdx.x, pass = id / 8 % passes, blk = id % 8 + 8 * (id / 8 / passes);
-  if (blk >= nblk) return;  // whole workgroup
-  const int64_t n0 = ((int64_t)blk * kTileWaves + wv) * MT * 16;
-  const unsigned char* src = img + (size_t)pass * chunks * CHUNK;
+__global__ void __launch_bounds__(64 * kTileWaves, 1) tile_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
+                                                                     int steps, int passes, int nblk, int vec) {
+  constexpr int MT = kTileMT, NT = kTileNT, F = 4 * NT, AHEAD = 2;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [2][CHUNK]
+  using B = I8Block<NT, MT, kTileWaves>;
+  const B blk(p, img, steps, passes);
+  if (blk.blk >= nblk) return;  // whole workgroup
   const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem;
-  auto copy = [&](int c) {
-#pragma unroll
-    for (int d = 0; d < DMA; d++) {
-      const int at = (wv * DMA + d) * 1024;
-      lds_copy_1k(src + (size_t)c * CHUNK + at + lane * 16, lds + c % 3 * CHUNK + at);
-    }
-  };
-  const int8_t* row[MT];
-#pragma unroll
-  for (int t = 0; t < MT; t++) row[t] = p.w + min(n0 + 16 * t + (lane & 15), p.n - 1) * p.w_stride;
-  i32x4 set[2][2][MT];
-  auto load = [&](int c, i32x4 (&v)[2][MT]) {
-#pragma unroll
-    for (int q = 0; q < 2; q++) {
-      const int off = min(128 * c + 64 * q + 16 * (lane >> 4), K - 16);
-#pragma unroll
-      for (int t = 0; t < MT; t++) v[q][t] = *(const i32x4u*)(row[t] + off);
-    }
-  };
-  i32x4 acc[MT][NT];
+  i32x4 set[2][MT][4], acc[MT][NT];
 #pragma unroll
   for (int t = 0; t < MT; t++)
 #pragma unroll
     for (int j = 0; j < NT; j++) acc[t][j] = i32x4{0, 0, 0, 0};
-  auto chunk = [&](int c, i32x4 (&v)[2][MT]) {
-    wide_barrier<2 * MT>();  // as in the wide kernel
-    if (c + 2 < chunks) copy(c + 2);
-    const i32x4* b = (const i32x4*)(smem + c % 3 * CHUNK) + lane;
-    i32x4 f[3];  // fragments read two ahead of their MFMAs
-    f[0] = b[0];
-    f[1] = b[64];
+  auto step = [&](int c, i32x4 (&v)[MT][4], i32x4 (&next)[MT][4]) {
+    // Step c's image has landed and every wave has read step c - 1's buffer, which the copy
+    // below refills; the w rows of step c + 1, loaded after that image's copy, stay in flight.
+    load_barrier<4 * MT>();
+    if (c + 1 < steps) blk.copy(c + 1, lds + (c + 1) % 2 * B::CHUNK);  // uniform
+    const i32x4* b = (const i32x4*)(smem + c % 2 * B::CHUNK) + blk.lane;
+    i32x4 f[AHEAD + 1];  // fragments read ahead of their MFMAs
 #pragma unroll
-    for (int i = 0; i < F; i++) {
-      if (i + 2 < F) f[(i + 2) % 3] = b[(i + 2) * 64];
+    for (int x = 0; x < AHEAD; x++) f[x] = b[x * 64];
 #pragma unroll
-      for (int t = 0; t < MT; t++) mfma_in_place(acc[t][i % NT], v[i / NT][t], f[i % 3]);
+    for (int x = 0; x < F; x++) {
+      if (x + AHEAD < F) f[(x + AHEAD) % (AHEAD + 1)] = b[(x + AHEAD) * 64];
+#pragma unroll
+      for (int t = 0; t < MT; t++) mfma_in_place(acc[t][x % NT], v[t][x / NT], f[x % (AHEAD + 1)]);
+      if (x >= 44 && x % 4 == 0 && (x - 44) / 4 < MT) quad_transpose(next[(x - 44) / 4], blk.lane);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    load(min(c + 2, chunks - 1), v);
+    blk.template load<false>(min(c + 2, steps - 1), v);
   };
-  copy(0);
-  copy(1);
-  load(0, set[0]);
-  load(1, set[1]);
+  blk.copy(0, lds);
+  blk.template load<false>(0, set[0]);
+  blk.template load<false>(1, set[1]);
+#pragma unroll
+  for (int t = 0; t < MT; t++) quad_transpose(set[0][t], blk.lane);
   mfma_settle();
-  for (int c = 0; c < chunks; c += 2) {  // an even number
-    chunk(c, set[0]);
-    chunk(c + 1, set[1]);
+  for (int c = 0; c < steps; c += 2) {  // an even number
+    step(c, set[0], set[1]);
+    step(c + 1, set[1], set[0]);
   }
-  wide_barrier<0>();  // the last (repeated) loads
+  load_barrier<0>();  // the last (repeated) loads
   mfma_settle();
 #pragma unroll
   for (int t = 0; t < MT; t++)
 #pragma unroll
     for (int j = 0; j < NT; j++) asm volatile("" : "+a"(acc[t][j]));  // read after the wait
-#pragma unroll
-  for (int t = 0; t < MT; t++) {
-    const int64_t n = n0 + 16 * t + 4 * (lane >> 4);
-    float w4[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) w4[i] = p.w_scale[min(n + i, p.n - 1) * p.w_scale_stride];
-#pragma unroll
-    for (int j = 0; j < NT; j++) {
-      const int64_t m = ((int64_t)pass * NT + j) * 16 + (lane & 15);
-      if (m < p.m) store_tile4<DT>(p.out, p.out_stride, m, n, p.n, acc[t][j], p.a_scale[m * p.a_scale_stride], w4, vec);
-    }
-  }
+  blk.template store<DT>(p, acc, vec);
 }
 
 // ---------------------------------------------------------------------------
@@ -457,24 +447,24 @@ __global__ void __launch_bounds__(64 * kTileWaves, 2) tile_i8_kernel(MatmulI8 p,
 // ---------------------------------------------------------------------------
 enum { I8_SIMPLE, I8_STREAM, I8_WIDE, I8_TILE };
 struct I8Plan {
-  int kind, nt, steps;  // wide: K steps of 128, a multiple of any number of sets
+  int kind, nt, steps;  // steps of 256 (wide, tile: an even number)
   int64_t passes;
   size_t img_bytes;
 };
 
 static I8Plan i8_plan(int64_t m, int64_t n, int64_t k) {
   I8Plan p = {};
-  p.steps = (int)cdiv(k, 128 * 6) * 6;
-  if (k < 16 || n > ((int64_t)1 << 30)) {
+  p.steps = (int)cdiv(k, 256);
+  if (k < 16) {
     p.kind = I8_SIMPLE;
-  } else if (m <= 16 && (size_t)cdiv(k, 512) * 4 * (m <= 8 ? 1024 : 2048) <= kMaxLds) {
+  } else if (m <= 16 && (size_t)p.steps * 4096 <= kMaxLds) {
     p.kind = I8_STREAM;
-    p.steps = (int)cdiv(k, 128 * kStreamSteps) * kStreamSteps;  // steps of 128
   } else {
     p.kind = m <= 128 ? I8_WIDE : I8_TILE;
-    p.nt = m <= 32 ? 2 : m <= 64 ? 4 : 8;
+    p.nt = m <= 32 ? 2 : m <= 64 ? 4 : m <= 128 ? 8 : kTileNT;
+    p.steps = (p.steps + 1) / 2 * 2;
     p.passes = cdiv(m, 16 * p.nt);
-    p.img_bytes = (size_t)p.passes * p.nt * p.steps * 2048;
+    p.img_bytes = (size_t)p.passes * p.nt * p.steps * 4096;
   }
   return p;
 }
@@ -484,30 +474,22 @@ size_t matmul_i8_workspace(int64_t m, int64_t n, int64_t k) {
   return i8_plan(m, n, k).img_bytes;
 }
 
-template <int DT, int IMG>
-static hipError_t launch_stream_i8(const MatmulI8& p, const I8Plan& pl, int vec, hipStream_t stream) {
-  const size_t lds = (size_t)pl.steps * IMG * 1024;
-  hipError_t e = set_dynamic_lds((const void*)stream_i8_kernel<DT, IMG>, lds);
+// blocks of rows_per_block w rows, all passes of each on one XCD
+template <typename K>
+static hipError_t launch_blocks(K kernel, int threads, size_t lds, int rows_per_block, const MatmulI8& p,
+                                const I8Plan& pl, const void* img, int vec, hipStream_t stream) {
+  hipError_t e = set_dynamic_lds((const void*)kernel, lds);
   if (e != hipSuccess) return e;
-  const int64_t ntiles = cdiv(p.n, 8);
-  // one 16-wave workgroup per CU, or small ones where there are fewer tiles than waves
-  const int nw = ntiles >= 16 * kTargetBlocks ? 16 : 4;
-  const int64_t blocks = std::min<int64_t>(cdiv(ntiles, nw), nw == 16 ? kTargetBlocks : 4 * kTargetBlocks);
-  hipLaunchKernelGGL((stream_i8_kernel<DT, IMG>), dim3((unsigned)blocks), dim3(64 * nw), lds, stream, p, ntiles, pl.steps,
-                     vec);
+  const int64_t nblk = cdiv(p.n, rows_per_block);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(align_up((size_t)nblk, 8) * pl.passes)), dim3(threads), lds, stream, p,
+                     (const unsigned char*)img, pl.steps, (int)pl.passes, (int)nblk, vec);
   return hipGetLastError();
 }
 
-template <int DT, int NT, int MT, int WAVES, int SETS, int MINW>
+template <int DT, int NT, int MT, int WAVES, int MINW>
 static hipError_t launch_wide_i8(const MatmulI8& p, const I8Plan& pl, const void* img, int vec, hipStream_t stream) {
-  auto kernel = wide_i8_kernel<DT, NT, MT, WAVES, SETS, MINW>;
-  const size_t lds = (size_t)3 * NT * 2048;
-  hipError_t e = set_dynamic_lds((const void*)kernel, lds);
-  if (e != hipSuccess) return e;
-  const int64_t nblk = cdiv(p.n, WAVES * MT * 16);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(align_up((size_t)nblk, 8) * pl.passes)), dim3(64 * WAVES), lds, stream, p,
-                     (const unsigned char*)img, pl.steps, (int)pl.passes, (int)nblk, vec);
-  return hipGetLastError();
+  return launch_blocks(wide_i8_kernel<DT, NT, MT, WAVES, MINW>, 64 * WAVES, (size_t)3 * NT * 4096, WAVES * MT * 16, p, pl,
+                       img, vec, stream);
 }
 
 template <int DT>
@@ -521,26 +503,29 @@ static hipError_t launch_matmul_dt(const MatmulI8& p, void* ws, hipStream_t stre
                        p.w_scale_stride, p.m, p.n, (int)p.k, p.out, p.out_stride);
     return hipGetLastError();
   }
-  if (pl.kind == I8_STREAM)
-    return p.m <= 8 ? launch_stream_i8<DT, 1>(p, pl, vec, stream) : launch_stream_i8<DT, 2>(p, pl, vec, stream);
-  const uint32_t total = (uint32_t)(pl.img_bytes / 16);  // at most 65536 x 65792 bytes
-  hipLaunchKernelGGL(i8_image_kernel, dim3((unsigned)cdiv(total, 256)), dim3(256), 0, stream, p, pl.nt, pl.steps,
-                     (int)(pl.kind == I8_WIDE), (i32x4*)ws, total);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (pl.kind == I8_TILE) {
-    const size_t lds = (size_t)3 * kTileNT * 2048;
-    e = set_dynamic_lds((const void*)tile_i8_kernel<DT>, lds);
+  if (pl.kind == I8_STREAM) {
+    const size_t lds = (size_t)pl.steps * 4096;
+    hipError_t e = set_dynamic_lds((const void*)stream_i8_kernel<DT>, lds);
     if (e != hipSuccess) return e;
-    const int64_t nblk = cdiv(p.n, kTileWaves * kTileMT * 16);
-    hipLaunchKernelGGL((tile_i8_kernel<DT>), dim3((unsigned)(align_up((size_t)nblk, 8) * pl.passes)),
-                       dim3(64 * kTileWaves), lds, stream, p, (const unsigned char*)ws, pl.steps, (int)pl.passes, (int)nblk,
+    const int64_t ntiles = cdiv(p.n, 16);
+    // one 16-wave workgroup per CU, or small ones where there are fewer tiles than waves
+    const int nw = ntiles >= 16 * kTargetBlocks ? 16 : 4;
+    const int64_t blocks = std::min<int64_t>(cdiv(ntiles, nw), nw == 16 ? kTargetBlocks : 4 * kTargetBlocks);
+    hipLaunchKernelGGL((stream_i8_kernel<DT>), dim3((unsigned)blocks), dim3(64 * nw), lds, stream, p, ntiles, pl.steps,
                        vec);
     return hipGetLastError();
   }
-  if (pl.nt == 2) return launch_wide_i8<DT, 2, 2, 8, 3, 4>(p, pl, ws, vec, stream);
-  if (pl.nt == 4) return launch_wide_i8<DT, 4, 2, 8, 3, 4>(p, pl, ws, vec, stream);
-  return launch_wide_i8<DT, 8, 2, 8, 3, 2>(p, pl, ws, vec, stream);
+  const uint32_t total = (uint32_t)(pl.img_bytes / 16);  // at most 65536 x 66048 bytes
+  hipLaunchKernelGGL(i8_image_kernel, dim3((unsigned)cdiv(total, 256)), dim3(256), 0, stream, p, pl.nt, pl.steps,
+                     (i32x4*)ws, total);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (pl.kind == I8_TILE)
+    return launch_blocks(tile_i8_kernel<DT>, 64 * kTileWaves, (size_t)2 * kTileNT * 4096, kTileWaves * kTileMT * 16, p, pl,
+                         ws, vec, stream);
+  if (pl.nt == 2) return launch_wide_i8<DT, 2, 1, 16, 4>(p, pl, ws, vec, stream);
+  if (pl.nt == 4) return launch_wide_i8<DT, 4, 1, 16, 4>(p, pl, ws, vec, stream);
+  return launch_wide_i8<DT, 8, 2, 8, 2>(p, pl, ws, vec, stream);
 }
 
 hipError_t launch_matmul_i8(const MatmulI8& p, void* ws, hipStream_t stream) {
