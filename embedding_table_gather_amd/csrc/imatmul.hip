@@ -307,19 +307,25 @@ struct I8Block {
         else v[t][q] = *(const i32x4u*)(row[t][q] + off);
       }
   }
+  // Every scale is loaded before the first store: a load after it would wait for it.
   template <int DT>
   __device__ __forceinline__ void store(const MatmulI8& p, const i32x4 (&acc)[MT][NT], int vec) const {
+    float w4[MT][4], s[NT];
 #pragma unroll
-    for (int t = 0; t < MT; t++) {
-      const int64_t n = n0 + 16 * t + 4 * (lane >> 4);
-      float w4[4];
+    for (int t = 0; t < MT; t++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) w4[i] = p.w_scale[min(n + i, p.n - 1) * p.w_scale_stride];
+      for (int i = 0; i < 4; i++)
+        w4[t][i] = p.w_scale[min(n0 + 16 * t + 4 * (lane >> 4) + i, p.n - 1) * p.w_scale_stride];
 #pragma unroll
-      for (int j = 0; j < NT; j++) {
-        const int64_t m = ((int64_t)pass * NT + j) * 16 + (lane & 15);
-        if (m < p.m) store_tile4<DT>(p.out, p.out_stride, m, n, p.n, acc[t][j], p.a_scale[m * p.a_scale_stride], w4, vec);
-      }
+    for (int j = 0; j < NT; j++)
+      s[j] = p.a_scale[min(((int64_t)pass * NT + j) * 16 + (lane & 15), p.m - 1) * p.a_scale_stride];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+      const int64_t m = ((int64_t)pass * NT + j) * 16 + (lane & 15);
+      if (m >= p.m) continue;
+#pragma unroll
+      for (int t = 0; t < MT; t++)
+        store_tile4<DT>(p.out, p.out_stride, m, n0 + 16 * t + 4 * (lane >> 4), p.n, acc[t][j], s[j], w4[t], vec);
     }
   }
 };
@@ -406,9 +412,10 @@ __global__ void __launch_bounds__(64 * kTileWaves, 1) tile_i8_kernel(MatmulI8 p,
     for (int j = 0; j < NT; j++) acc[t][j] = i32x4{0, 0, 0, 0};
   auto step = [&](int c, i32x4 (&v)[MT][4], i32x4 (&next)[MT][4]) {
     // Step c's image has landed and every wave has read step c - 1's buffer, which the copy
-    // below refills; the w rows of step c + 1, loaded after that image's copy, stay in flight.
-    load_barrier<4 * MT>();
+    // below refills.
+    load_barrier<0>();
     if (c + 1 < steps) blk.copy(c + 1, lds + (c + 1) % 2 * B::CHUNK);  // uniform
+    blk.template load<false>(min(c + 1, steps - 1), next);
     const i32x4* b = (const i32x4*)(smem + c % 2 * B::CHUNK) + blk.lane;
     i32x4 f[AHEAD + 1];  // fragments read ahead of their MFMAs
 #pragma unroll
@@ -421,11 +428,9 @@ __global__ void __launch_bounds__(64 * kTileWaves, 1) tile_i8_kernel(MatmulI8 p,
       if (x >= 44 && x % 4 == 0 && (x - 44) / 4 < MT) quad_transpose(next[(x - 44) / 4], blk.lane);
       __builtin_amdgcn_sched_barrier(0);
     }
-    blk.template load<false>(min(c + 2, steps - 1), v);
   };
   blk.copy(0, lds);
   blk.template load<false>(0, set[0]);
-  blk.template load<false>(1, set[1]);
 #pragma unroll
   for (int t = 0; t < MT; t++) quad_transpose(set[0][t], blk.lane);
   mfma_settle();
