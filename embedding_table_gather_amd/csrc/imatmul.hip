@@ -242,16 +242,14 @@ __global__ void __launch_bounds__(256) i8_image_kernel(MatmulI8 p, int nt, int s
   img[x] = image_slot(m < p.m ? p.a + m * p.a_stride : nullptr, 16 * step + 4 * (lane >> 4) + i, (int)p.k);
 }
 
-// 1 KiB from memory to LDS: lane l's 16 bytes at src + offset (16 l) to lds + 16 l.  In
+// 1 KiB from memory to LDS: lane l's 16 bytes at src + offset (16 l) to lds + 16 l (src and lds uniform).  In
 // assembly because the compiler would wait for every such copy before any LDS read;
 // load_barrier waits for the one that is due.  No register is written.
 __device__ __forceinline__ void lds_copy_1k(const void* src, uint32_t offset, uint32_t lds) {
   uint32_t m0;  // the LDS base register, left as it was
-  const uint64_t base = ((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)src >> 32)) << 32) |
-                        (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(uint64_t)src);
   asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
                : "=&s"(m0)
-               : "v"(offset), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
+               : "v"(offset), "s"(src), "s"(lds)
                : "memory");
 }
 
@@ -272,40 +270,54 @@ struct I8Block {
   int lane, wv, pass, blk, K;
   int64_t n0;
   const unsigned char* src;
-  const int8_t* row[MT][4];
+  const int8_t* base;   // w row n0 of the block
+  uint32_t row[MT][4];  // offsets of the lane's rows from it (at most 256 rows of 2^22 bytes)
   __device__ __forceinline__ I8Block(const MatmulI8& p, const unsigned char* img, int steps, int passes) {
     lane = threadIdx.x & 63;
     wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int id = blockIdx.x;
-    pass = id / 8 % passes;
-    blk = id % 8 + 8 * (id / 8 / passes);
+    // uniform, but divided in vector registers
+    const int group = __builtin_amdgcn_readfirstlane(id / 8 / passes);
+    pass = id / 8 - group * passes;
+    blk = id % 8 + 8 * group;
     K = (int)p.k;
-    n0 = ((int64_t)blk * WAVES + wv) * MT * 16;
+    const int64_t b0 = (int64_t)blk * WAVES * MT * 16;
+    n0 = b0 + wv * MT * 16;
+    base = p.w + b0 * p.w_stride;
     src = img + (size_t)pass * steps * CHUNK;
 #pragma unroll
     for (int t = 0; t < MT; t++)
 #pragma unroll
-      for (int q = 0; q < 4; q++) row[t][q] = p.w + min(n0 + 16 * t + load_row(lane, q), p.n - 1) * p.w_stride;
+      for (int q = 0; q < 4; q++)
+        row[t][q] = (uint32_t)max(min(n0 + 16 * t + load_row(lane, q), p.n - 1) - b0, (int64_t)0) * (uint32_t)p.w_stride;
   }
-  // this wave's part of the image of step c to the buffer at lds
+  // this wave's part of the image of step c to the buffer at lds, and its d-th KiB
+  __device__ __forceinline__ void copy_part(int c, uint32_t lds, int d) const {
+    const int at = (wv * DMA + d) * 1024;
+    if (CHUNK % (1024 * WAVES) == 0 || at < CHUNK)  // uniform
+      lds_copy_1k(src + (size_t)c * CHUNK + at, (uint32_t)lane * 16, lds + at);
+  }
   __device__ __forceinline__ void copy(int c, uint32_t lds) const {
 #pragma unroll
-    for (int d = 0; d < DMA; d++) {
-      const int at = (wv * DMA + d) * 1024;
-      if (CHUNK % (1024 * WAVES) == 0 || at < CHUNK)  // uniform
-        lds_copy_1k(src + (size_t)c * CHUNK + at, (uint32_t)lane * 16, lds + at);
-    }
+    for (int d = 0; d < DMA; d++) copy_part(c, lds, d);
+  }
+  // w rows of step c; ONCE: no other pass reads them
+  __device__ __forceinline__ uint32_t load_offset(int c) const {
+    return (uint32_t)min(256 * c + 16 * load_slot(lane), K - 16);
+  }
+  template <bool ONCE>
+  __device__ __forceinline__ i32x4 load_part(uint32_t off, int t, int q) const {
+    const i32x4u* at = (const i32x4u*)(base + (row[t][q] + off));
+    if constexpr (ONCE) return __builtin_nontemporal_load(at);
+    return *at;
   }
   template <bool ONCE>
   __device__ __forceinline__ void load(int c, i32x4 (&v)[MT][4]) const {
-    const int off = min(256 * c + 16 * load_slot(lane), K - 16);
+    const uint32_t off = load_offset(c);
 #pragma unroll
     for (int t = 0; t < MT; t++)
 #pragma unroll
-      for (int q = 0; q < 4; q++) {
-        if constexpr (ONCE) v[t][q] = __builtin_nontemporal_load((const i32x4u*)(row[t][q] + off));
-        else v[t][q] = *(const i32x4u*)(row[t][q] + off);
-      }
+      for (int q = 0; q < 4; q++) v[t][q] = load_part<ONCE>(off, t, q);
   }
   // Every scale is loaded before the first store: a load after it would wait for it.
   template <int DT>
@@ -384,7 +396,9 @@ __global__ void __launch_bounds__(64 * WAVES, MINW) wide_i8_kernel(MatmulI8 p, c
 // holds 4 x 16 tiles of 16 x 16 in 256 accumulator registers (one wave per SIMD), so a 1 KiB
 // fragment of the image read from LDS serves four MFMAs: 64 B a clock per CU of LDS reads at
 // the full MFMA rate.  The image passes through two LDS buffers of one step, each refilled
-// one step ahead.  The next step's w rows are transposed between the MFMAs of this one.
+// one step ahead.  The next step's copies and w loads are issued one at a time between the
+// MFMAs of this one (32 in a row would hold up the wave, whose MFMAs wait behind them), and its
+// w rows are transposed there too.
 // ---------------------------------------------------------------------------
 static constexpr int kTileWaves = 4, kTileMT = 4, kTileNT = 16;
 
@@ -400,6 +414,7 @@ template <int DT>
 __global__ void __launch_bounds__(64 * kTileWaves, 1) tile_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
                                                                      int steps, int passes, int nblk, int vec) {
   constexpr int MT = kTileMT, NT = kTileNT, F = 4 * NT, AHEAD = 2;
+  static_assert(F == 64 && MT == 4 && NT * 4 == 16 * kTileWaves, "the schedule of a step below");
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [2][CHUNK]
   using B = I8Block<NT, MT, kTileWaves>;
   const B blk(p, img, steps, passes);
@@ -414,8 +429,8 @@ __global__ void __launch_bounds__(64 * kTileWaves, 1) tile_i8_kernel(MatmulI8 p,
     // Step c's image has landed and every wave has read step c - 1's buffer, which the copy
     // below refills.
     load_barrier<0>();
-    if (c + 1 < steps) blk.copy(c + 1, lds + (c + 1) % 2 * B::CHUNK);  // uniform
-    blk.template load<false>(min(c + 1, steps - 1), next);
+    const int ahead = min(c + 1, steps - 1);  // the last step's own again: not read
+    const uint32_t off = blk.load_offset(ahead), to = lds + (c + 1) % 2 * B::CHUNK;
     const i32x4* b = (const i32x4*)(smem + c % 2 * B::CHUNK) + blk.lane;
     i32x4 f[AHEAD + 1];  // fragments read ahead of their MFMAs
 #pragma unroll
@@ -425,6 +440,8 @@ __global__ void __launch_bounds__(64 * kTileWaves, 1) tile_i8_kernel(MatmulI8 p,
       if (x + AHEAD < F) f[(x + AHEAD) % (AHEAD + 1)] = b[(x + AHEAD) * 64];
 #pragma unroll
       for (int t = 0; t < MT; t++) mfma_in_place(acc[t][x % NT], v[t][x / NT], f[x % (AHEAD + 1)]);
+      if (x < 32 && x % 2 == 0) blk.copy_part(ahead, to, x / 2);
+      if (x < 32 && x % 2 == 1) next[x / 8][x / 2 % 4] = blk.template load_part<false>(off, x / 8, x / 2 % 4);
       if (x >= 44 && x % 4 == 0 && (x - 44) / 4 < MT) quad_transpose(next[(x - 44) / 4], blk.lane);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -502,7 +519,9 @@ static hipError_t launch_matmul_dt(const MatmulI8& p, void* ws, hipStream_t stre
   const I8Plan pl = i8_plan(p.m, p.n, p.k);
   // four-value stores of an output whose rows all start at a multiple of four values
   const int vec = (uintptr_t)p.out % (DT == DT_F32 ? 16 : 8) == 0 && p.out_stride % 4 == 0;
-  if (pl.kind == I8_SIMPLE) {
+  // the block kernels' row offsets are 32-bit (256 rows and K of at most 2^16 bytes)
+  const bool far = (pl.kind == I8_WIDE || pl.kind == I8_TILE) && p.w_stride > (1 << 22);
+  if (pl.kind == I8_SIMPLE || far) {
     hipLaunchKernelGGL((matmul_i8_kernel<DT>), dim3((unsigned)cdiv(p.n, 64), (unsigned)cdiv(p.m, 16)), dim3(256), 0,
                        stream, p.a, p.a_stride, p.a_scale, p.a_scale_stride, p.w, p.w_stride, p.w_scale,
                        p.w_scale_stride, p.m, p.n, (int)p.k, p.out, p.out_stride);
