@@ -129,30 +129,38 @@ __device__ __forceinline__ void quad_transpose(i32x4 (&v)[4], int lane) {
   }
 }
 
+// Four f32 values rounded to 16-bit ones.
+typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
+template <int DT>
+__device__ __forceinline__ u16x4 round4(float (&x)[4]) {
+  u16x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if constexpr (DT == DT_BF16) {
+      v[i] = __builtin_bit_cast(unsigned short, (__bf16)x[i]);
+    } else {
+      asm volatile("" : "+v"(x[i]));  // as in store_out
+      v[i] = __builtin_bit_cast(unsigned short, (_Float16)x[i]);
+    }
+  }
+  return v;
+}
+
 // Stores of one 16 x 16 tile: lane l has w rows n0 .. n0 + 3 of a row m (values acc).
 template <int DT>
 __device__ __forceinline__ void store_tile4(void* out, int64_t out_stride, int64_t m, int64_t n0, int64_t N, i32x4 acc,
-                                            float s, const float (&w4)[4], bool vec) {
+                                            float s, const float (&w4)[4]) {
   float x[4];
 #pragma unroll
   for (int i = 0; i < 4; i++) x[i] = (float)acc[i] * s * w4[i];
   const int64_t at = m * out_stride + n0;
-  if (vec && n0 + 4 <= N) {  // rows of the output start at multiples of four values
+  if (n0 + 4 <= N) {  // one store at any alignment
     if constexpr (DT == DT_F32) {
-      *(f32x4*)((float*)out + at) = f32x4{x[0], x[1], x[2], x[3]};
+      const f32x4 v = {x[0], x[1], x[2], x[3]};
+      __builtin_memcpy((float*)out + at, &v, 16);
     } else {
-      typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
-      u16x4 v;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        if constexpr (DT == DT_BF16) {
-          v[i] = __builtin_bit_cast(unsigned short, (__bf16)x[i]);
-        } else {
-          asm volatile("" : "+v"(x[i]));  // as in store_out
-          v[i] = __builtin_bit_cast(unsigned short, (_Float16)x[i]);
-        }
-      }
-      *(u16x4*)((uint16_t*)out + at) = v;
+      const u16x4 v = round4<DT>(x);
+      __builtin_memcpy((uint16_t*)out + at, &v, 8);
     }
   } else {
 #pragma unroll
@@ -168,7 +176,7 @@ __device__ __forceinline__ void store_tile4(void* out, int64_t out_stride, int64
 // with its steps.
 // ---------------------------------------------------------------------------
 template <int DT>
-__global__ void __launch_bounds__(1024) stream_i8_kernel(MatmulI8 p, int64_t ntiles, int steps, int vec) {
+__global__ void __launch_bounds__(1024) stream_i8_kernel(MatmulI8 p, int64_t ntiles, int steps) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   i32x4* img = (i32x4*)smem;  // [steps][4][64]
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -215,7 +223,7 @@ __global__ void __launch_bounds__(1024) stream_i8_kernel(MatmulI8 p, int64_t nti
     float w4[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) w4[i] = __shfl(x.scale, 4 * (lane >> 4) + i, 64);
-    if (m < p.m) store_tile4<DT>(p.out, p.out_stride, m, t * 16 + 4 * (lane >> 4), p.n, acc, s, w4, vec);
+    if (m < p.m) store_tile4<DT>(p.out, p.out_stride, m, t * 16 + 4 * (lane >> 4), p.n, acc, s, w4);
     acc = i32x4{0, 0, 0, 0};
     st = 0;
     t++;
@@ -319,25 +327,62 @@ struct I8Block {
 #pragma unroll
       for (int q = 0; q < 4; q++) v[t][q] = load_part<ONCE>(off, t, q);
   }
-  // Every scale is loaded before the first store: a load after it would wait for it.
+  // The output passes through LDS, JT a row tiles at a time, so that a store instruction
+  // writes whole lines of one or two output rows (a tile's own registers hold 16 rows of a
+  // few values).  16-byte stores at any alignment.  Every scale is loaded before the first
+  // store: a load after it would wait for it.
+  static constexpr int ROWS = WAVES * MT * 16;  // w rows of the workgroup
   template <int DT>
-  __device__ __forceinline__ void store(const MatmulI8& p, const i32x4 (&acc)[MT][NT], int vec) const {
+  static constexpr int JT = DT == DT_F32 ? (NT < 4 ? NT : 4) : (NT < 8 ? NT : 8);
+  template <int DT>
+  static constexpr int PITCH = ROWS * (DT == DT_F32 ? 4 : 2) + 16;  // bytes of an LDS row
+  template <int DT>
+  static constexpr size_t STORE_LDS = (size_t)16 * JT<DT> * PITCH<DT>;
+  template <int DT>
+  __device__ __forceinline__ void store(const MatmulI8& p, const i32x4 (&acc)[MT][NT], unsigned char* smem) const {
+    constexpr int ES = DT == DT_F32 ? 4 : 2, VN = 16 / ES, LPR = ROWS / VN;  // values per store, lanes per row
+    static_assert(LPR <= 64 && 64 % LPR == 0, "whole rows per store instruction");
     float w4[MT][4], s[NT];
 #pragma unroll
     for (int t = 0; t < MT; t++)
 #pragma unroll
       for (int i = 0; i < 4; i++)
         w4[t][i] = p.w_scale[min(n0 + 16 * t + 4 * (lane >> 4) + i, p.n - 1) * p.w_scale_stride];
+    const int64_t m0 = (int64_t)pass * NT * 16;
 #pragma unroll
-    for (int j = 0; j < NT; j++)
-      s[j] = p.a_scale[min(((int64_t)pass * NT + j) * 16 + (lane & 15), p.m - 1) * p.a_scale_stride];
+    for (int j = 0; j < NT; j++) s[j] = p.a_scale[min(m0 + 16 * j + (lane & 15), p.m - 1) * p.a_scale_stride];
+    const int64_t b0 = (int64_t)blk * ROWS;
 #pragma unroll
-    for (int j = 0; j < NT; j++) {
-      const int64_t m = ((int64_t)pass * NT + j) * 16 + (lane & 15);
-      if (m >= p.m) continue;
+    for (int j0 = 0; j0 < NT; j0 += JT<DT>) {
+      __syncthreads();
 #pragma unroll
-      for (int t = 0; t < MT; t++)
-        store_tile4<DT>(p.out, p.out_stride, m, n0 + 16 * t + 4 * (lane >> 4), p.n, acc[t][j], s[j], w4[t], vec);
+      for (int j = 0; j < JT<DT>; j++)
+#pragma unroll
+        for (int t = 0; t < MT; t++) {
+          float x[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) x[i] = (float)acc[t][j0 + j][i] * s[j0 + j] * w4[t][i];
+          unsigned char* to = smem + (16 * j + (lane & 15)) * PITCH<DT> + ((wv * MT + t) * 16 + 4 * (lane >> 4)) * ES;
+          if constexpr (DT == DT_F32) *(f32x4*)to = f32x4{x[0], x[1], x[2], x[3]};
+          else *(u16x4*)to = round4<DT>(x);
+        }
+      __syncthreads();
+      const int r0 = wv * (64 / LPR) + lane / LPR, col = lane % LPR * VN;
+      for (int r = r0; r < 16 * JT<DT>; r += WAVES * (64 / LPR)) {
+        const int64_t m = m0 + 16 * j0 + r, n = b0 + col;
+        if (m >= p.m) break;
+        const unsigned char* from = smem + r * PITCH<DT> + col * ES;
+        if (n + VN <= p.n) {
+          const u32x4 v = *(const u32x4*)from;
+          __builtin_memcpy((unsigned char*)p.out + (m * p.out_stride + n) * ES, &v, 16);
+        } else {
+          for (int i = 0; i < VN; i++)
+            if (n + i < p.n) {
+              if constexpr (ES == 4) ((uint32_t*)p.out)[m * p.out_stride + n + i] = ((const uint32_t*)from)[i];
+              else ((uint16_t*)p.out)[m * p.out_stride + n + i] = ((const uint16_t*)from)[i];
+            }
+        }
+      }
     }
   }
 };
@@ -350,7 +395,7 @@ struct I8Block {
 // ---------------------------------------------------------------------------
 template <int DT, int NT, int MT, int WAVES, int MINW>
 __global__ void __launch_bounds__(64 * WAVES, MINW) wide_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
-                                                                   int steps, int passes, int nblk, int vec) {
+                                                                   int steps, int passes, int nblk) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [3][CHUNK]
   using B = I8Block<NT, MT, WAVES>;
   const B blk(p, img, steps, passes);
@@ -388,7 +433,7 @@ __global__ void __launch_bounds__(64 * WAVES, MINW) wide_i8_kernel(MatmulI8 p, c
     step(c + 1, set[1]);
   }
   load_barrier<0>();  // the last (repeated) loads
-  blk.template store<DT>(p, acc, vec);
+  blk.template store<DT>(p, acc, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -412,7 +457,7 @@ __device__ __forceinline__ void mfma_settle() { asm volatile("s_nop 15\n\ts_nop 
 
 template <int DT>
 __global__ void __launch_bounds__(64 * kTileWaves, 1) tile_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
-                                                                     int steps, int passes, int nblk, int vec) {
+                                                                     int steps, int passes, int nblk) {
   constexpr int MT = kTileMT, NT = kTileNT, F = 4 * NT, AHEAD = 2;
   static_assert(F == 64 && MT == 4 && NT * 4 == 16 * kTileWaves, "the schedule of a step below");
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [2][CHUNK]
@@ -461,7 +506,7 @@ __global__ void __launch_bounds__(64 * kTileWaves, 1) tile_i8_kernel(MatmulI8 p,
   for (int t = 0; t < MT; t++)
 #pragma unroll
     for (int j = 0; j < NT; j++) asm volatile("" : "+a"(acc[t][j]));  // read after the wait
-  blk.template store<DT>(p, acc, vec);
+  blk.template store<DT>(p, acc, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -499,26 +544,25 @@ size_t matmul_i8_workspace(int64_t m, int64_t n, int64_t k) {
 // blocks of rows_per_block w rows, all passes of each on one XCD
 template <typename K>
 static hipError_t launch_blocks(K kernel, int threads, size_t lds, int rows_per_block, const MatmulI8& p,
-                                const I8Plan& pl, const void* img, int vec, hipStream_t stream) {
+                                const I8Plan& pl, const void* img, hipStream_t stream) {
   hipError_t e = set_dynamic_lds((const void*)kernel, lds);
   if (e != hipSuccess) return e;
   const int64_t nblk = cdiv(p.n, rows_per_block);
   hipLaunchKernelGGL(kernel, dim3((unsigned)(align_up((size_t)nblk, 8) * pl.passes)), dim3(threads), lds, stream, p,
-                     (const unsigned char*)img, pl.steps, (int)pl.passes, (int)nblk, vec);
+                     (const unsigned char*)img, pl.steps, (int)pl.passes, (int)nblk);
   return hipGetLastError();
 }
 
 template <int DT, int NT, int MT, int WAVES, int MINW>
-static hipError_t launch_wide_i8(const MatmulI8& p, const I8Plan& pl, const void* img, int vec, hipStream_t stream) {
-  return launch_blocks(wide_i8_kernel<DT, NT, MT, WAVES, MINW>, 64 * WAVES, (size_t)3 * NT * 4096, WAVES * MT * 16, p, pl,
-                       img, vec, stream);
+static hipError_t launch_wide_i8(const MatmulI8& p, const I8Plan& pl, const void* img, hipStream_t stream) {
+  using B = I8Block<NT, MT, WAVES>;
+  return launch_blocks(wide_i8_kernel<DT, NT, MT, WAVES, MINW>, 64 * WAVES,
+                       std::max((size_t)3 * B::CHUNK, B::template STORE_LDS<DT>), B::ROWS, p, pl, img, stream);
 }
 
 template <int DT>
 static hipError_t launch_matmul_dt(const MatmulI8& p, void* ws, hipStream_t stream) {
   const I8Plan pl = i8_plan(p.m, p.n, p.k);
-  // four-value stores of an output whose rows all start at a multiple of four values
-  const int vec = (uintptr_t)p.out % (DT == DT_F32 ? 16 : 8) == 0 && p.out_stride % 4 == 0;
   // the block kernels' row offsets are 32-bit (256 rows and K of at most 2^16 bytes)
   const bool far = (pl.kind == I8_WIDE || pl.kind == I8_TILE) && p.w_stride > (1 << 22);
   if (pl.kind == I8_SIMPLE || far) {
@@ -535,8 +579,7 @@ static hipError_t launch_matmul_dt(const MatmulI8& p, void* ws, hipStream_t stre
     // one 16-wave workgroup per CU, or small ones where there are fewer tiles than waves
     const int nw = ntiles >= 16 * kTargetBlocks ? 16 : 4;
     const int64_t blocks = std::min<int64_t>(cdiv(ntiles, nw), nw == 16 ? kTargetBlocks : 4 * kTargetBlocks);
-    hipLaunchKernelGGL((stream_i8_kernel<DT>), dim3((unsigned)blocks), dim3(64 * nw), lds, stream, p, ntiles, pl.steps,
-                       vec);
+    hipLaunchKernelGGL((stream_i8_kernel<DT>), dim3((unsigned)blocks), dim3(64 * nw), lds, stream, p, ntiles, pl.steps);
     return hipGetLastError();
   }
   const uint32_t total = (uint32_t)(pl.img_bytes / 16);  // at most 65536 x 66048 bytes
@@ -544,12 +587,14 @@ static hipError_t launch_matmul_dt(const MatmulI8& p, void* ws, hipStream_t stre
                      (i32x4*)ws, total);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (pl.kind == I8_TILE)
-    return launch_blocks(tile_i8_kernel<DT>, 64 * kTileWaves, (size_t)2 * kTileNT * 4096, kTileWaves * kTileMT * 16, p, pl,
-                         ws, vec, stream);
-  if (pl.nt == 2) return launch_wide_i8<DT, 2, 1, 16, 4>(p, pl, ws, vec, stream);
-  if (pl.nt == 4) return launch_wide_i8<DT, 4, 1, 16, 4>(p, pl, ws, vec, stream);
-  return launch_wide_i8<DT, 8, 2, 8, 2>(p, pl, ws, vec, stream);
+  if (pl.kind == I8_TILE) {
+    using B = I8Block<kTileNT, kTileMT, kTileWaves>;
+    static_assert(B::template STORE_LDS<DT> <= 2 * B::CHUNK, "the image's buffers hold the output tile");
+    return launch_blocks(tile_i8_kernel<DT>, 64 * kTileWaves, (size_t)2 * B::CHUNK, B::ROWS, p, pl, ws, stream);
+  }
+  if (pl.nt == 2) return launch_wide_i8<DT, 2, 1, 16, 4>(p, pl, ws, stream);
+  if (pl.nt == 4) return launch_wide_i8<DT, 4, 1, 16, 4>(p, pl, ws, stream);
+  return launch_wide_i8<DT, 8, 2, 8, 2>(p, pl, ws, stream);
 }
 
 hipError_t launch_matmul_i8(const MatmulI8& p, void* ws, hipStream_t stream) {
