@@ -38,8 +38,8 @@ namespace etg {
 //     than are kept) are sorted in LDS.
 //  3. Rows that keep more than the list holds (flat distributions) go on to
 //     sample_hist_kernel, which counts and weighs every token in 1,024 bins per slice
-//     of 32,768 tokens, and sample_heavy_kernel, which finds the cut's bin, reads the
-//     tokens of that bin and narrows it to the cut.
+//     of 16,384 tokens, sample_gather_kernel, which lists the tokens of the bin that holds
+//     the cut, and sample_heavy_kernel, which narrows the list to the cut.
 
 struct SampleRow {
   float T, p, minp, u;
@@ -72,17 +72,17 @@ static constexpr int kSampleWaves = kSampleThreads / 64;
 static constexpr int kSampleBins = 1024;         // one per thread
 static constexpr int kChunk = 2048;              // tokens of a chunk (a wave's)
 static constexpr int kChunkThreads = 256;
-static constexpr int kSlice = 32768;             // tokens of a histogram slice
+static constexpr int kSlice = 16384;             // tokens of a histogram slice
 static constexpr int kMaxSlices = (1 << 20) / kSlice;
 static constexpr int kList = 2048;               // tokens sorted in LDS by the row kernel
 static constexpr int kHeavyList = 8192;          // tokens of one bin in the heavy kernel
 static constexpr int kMaxGroups = 4096;          // groups per row
-static constexpr int64_t kHeavySlots = 512;      // rows of one call with histograms
+static constexpr size_t kHeavyBytes = 128 << 20;  // most workspace for heavy rows (one slot each)
 
 // Workspace of a call, from its sizes alone.
 struct SampleWs {
   int chunks, slices, group_log2, groups, slots;
-  size_t gmax, cmax, csum, flag, nheavy, hcount, hmass, bytes;
+  size_t gmax, cmax, csum, heavy, nheavy, hcount, hmass, hlist, hlisted, hbin, bytes;
 };
 
 static SampleWs sample_ws(int64_t rows, int64_t vocab, int32_t dtype) {
@@ -93,7 +93,8 @@ static SampleWs sample_ws(int64_t rows, int64_t vocab, int32_t dtype) {
   w.group_log2 = dtype == DT_F32 ? 2 : 3;
   while (cdiv(vocab, 1ll << w.group_log2) > kMaxGroups) w.group_log2++;
   w.groups = (int)cdiv(vocab, 1ll << w.group_log2);
-  w.slots = (int)std::min(rows, kHeavySlots);
+  const size_t slot = (size_t)w.slices * kSampleBins * 12 + kHeavyList * 8;
+  w.slots = (int)std::min<int64_t>(rows, (int64_t)(kHeavyBytes / slot));
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t o = at;
@@ -103,10 +104,13 @@ static SampleWs sample_ws(int64_t rows, int64_t vocab, int32_t dtype) {
   w.gmax = take((size_t)rows * w.groups * 4);
   w.cmax = take((size_t)rows * w.chunks * 4);
   w.csum = take((size_t)rows * w.chunks * 8);
-  w.flag = take((size_t)rows * 4);
+  w.heavy = take((size_t)rows * 4);
   w.nheavy = take(4);
   w.hcount = take((size_t)w.slots * w.slices * kSampleBins * 4);
   w.hmass = take((size_t)w.slots * w.slices * kSampleBins * 8);
+  w.hlist = take((size_t)w.slots * kHeavyList * 8);
+  w.hlisted = take((size_t)w.slots * 4);
+  w.hbin = take((size_t)w.slots * 4);
   w.bytes = at;
   return w;
 }
@@ -115,10 +119,13 @@ struct SamplePtrs {
   float* gmax;       // [rows][groups] largest candidate logit, -inf for none
   float* cmax;       // [rows][chunks]
   uint64_t* csum;    // [rows][chunks] mass relative to the chunk's own maximum
-  int32_t* flag;     // [rows] -1: done, else the histogram slot, or -2 for none
-  uint32_t* nheavy;  // slots taken
+  uint32_t* nheavy;  // how many heavy rows there are
+  int32_t* heavy;    // [rows] which; the first `slots` of them have histograms
   uint32_t* hcount;  // [slots][slices][bins]
   uint64_t* hmass;
+  uint64_t* hlist;    // [slots][kHeavyList] tokens of the bin that holds the cut, key << 32 | id
+  uint32_t* hlisted;  // [slots] how many there are
+  int32_t* hbin;      // [slots] the bin, -1: not listed
   int chunks, slices, group_log2, groups, slots, shift;
 };
 
@@ -294,24 +301,30 @@ __device__ __forceinline__ uint64_t wave_scan_u64(uint64_t v) {  // inclusive
   return v;
 }
 
-// Inclusive prefix sum over the threads; *total receives the sum.
+__device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane) {  // lane uniform
+  return ((uint64_t)__builtin_amdgcn_readlane((uint32_t)(v >> 32), lane) << 32) |
+         (uint32_t)__builtin_amdgcn_readlane((uint32_t)v, lane);
+}
+
+// Inclusive prefix sum over the threads; *total receives the sum.  Every wave sums the
+// waves' parts by itself, a part per lane.
 template <int NW>
 __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* total, SampleScratch<NW>& sc) {
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   v = wave_scan_u64(v);
   __syncthreads();
   if (lane == 63) sc.part[wv] = v;
   __syncthreads();
-  uint64_t before = 0, all = 0;
+  uint64_t p = lane < NW ? sc.part[lane] : 0;
 #pragma unroll
-  for (int i = 0; i < NW; i++) {
-    const uint64_t p = sc.part[i];
-    if (i < wv) before += p;
-    all += p;
+  for (int off = 1; off < NW; off <<= 1) {
+    const uint64_t o = (uint64_t)__shfl_up((unsigned long long)p, off, 64);
+    if (lane >= off) p += o;
   }
-  *total = all;
+  *total = lane_u64(p, NW - 1);
+  if (wv > 0) v += lane_u64(p, wv - 1);
   __syncthreads();
-  return before + v;
+  return v;
 }
 
 // The first thread with `hit`, and the two values it holds, to every thread; -1 for none.
@@ -323,13 +336,16 @@ __device__ __forceinline__ int block_first(bool hit, uint64_t a, uint64_t b, uin
   __syncthreads();
   if (lane == 0) sc.part[wv] = m;
   __syncthreads();
+  const uint64_t p = lane < NW ? sc.part[lane] : 0;
+  const uint64_t waves = __ballot(p != 0);
   int first = -1;
-#pragma unroll
-  for (int i = NW - 1; i >= 0; i--)
-    if (sc.part[i] != 0) first = 64 * i + __ffsll((unsigned long long)sc.part[i]) - 1;
-  if ((int)threadIdx.x == first) {
-    sc.value[0] = a;
-    sc.value[1] = b;
+  if (waves != 0) {
+    const int w = __ffsll((unsigned long long)waves) - 1;
+    first = 64 * w + __ffsll((unsigned long long)lane_u64(p, w)) - 1;
+    if ((int)threadIdx.x == first) {
+      sc.value[0] = a;
+      sc.value[1] = b;
+    }
   }
   __syncthreads();
   if (first >= 0) {
@@ -458,7 +474,7 @@ struct SampleHist {
 // loads in flight each (one workgroup reads a whole row: latency is what it waits for).
 template <int NT, int DT, typename F>
 __device__ __forceinline__ void sample_each(const SampleSource<DT>& src, F f) {
-  constexpr int N = SampleSource<DT>::N, U = 32 / N;
+  constexpr int N = SampleSource<DT>::N, U = 16 / N;
   for (int at = 0; at < src.V; at += NT * N * U) {
     float l[U][N];
 #pragma unroll
@@ -613,7 +629,6 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, Sampl
   const SampleSource<DT> src(s, row);
   const SampleRow r = sample_row(s, row);
   const int V = src.V;
-  if (tid == 0) ws.flag[row] = -1;
 
   // the row's largest logit
   const float* cmax = ws.cmax + row * ws.chunks;
@@ -672,8 +687,8 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, Sampl
   }
 
   // Tokens nearer to the largest logit than `limit` are gathered: among them is every
-  // kept token (for top-p after top-k: every one of the first k); 0: no bound found.
-  uint32_t limit = 0;
+  // kept token (for top-p after top-k: every one of the first k).
+  uint32_t limit = 0xffffffffu;
   constexpr int G = kMaxGroups / kRowThreads;  // consecutive groups of a thread, kept in registers
   float gm[G];
 #pragma unroll
@@ -713,13 +728,12 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, Sampl
     // the rounding of this product, of the distances and of the weights
     const float most = r.T * (-logf(r.minp) * (1.f + 1.52587890625e-5f) + 1e-14f) + 1.17549435e-38f;
     const uint32_t lim = most < __builtin_inff() ? __float_as_uint(most) + 1 : 0xffffffffu;
-    limit = limit == 0 ? lim : min(limit, lim);
+    limit = min(limit, lim);
   }
-  if (limit == 0 && V <= kList) limit = 0xffffffffu;
 
   // the groups within the limit, then their tokens that are, both in id order
   int n = -1;
-  if (limit != 0) {
+  {
     auto near = [&](float l) { return l > -__builtin_inff() && sample_dist(l, top) < limit; };
     uint32_t mine = 0;
 #pragma unroll
@@ -732,7 +746,7 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, Sampl
         if (near(gm[q])) sh.groups[at++] = (uint32_t)(G * tid + q);
       __syncthreads();
       // rounds of U loads per lane, a wave's loads consecutive
-      constexpr int N = SampleSource<DT>::N, U = 16 / N;
+      constexpr int N = SampleSource<DT>::N, U = 32 / N;
       const int items = (int)ng << ws.group_log2;
       uint32_t base = 0;
       n = 0;
@@ -794,10 +808,14 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, Sampl
       }
     }
   }
-  if (n < 0) {  // too many tokens for the list: a heavy row, -2 past the histogram slots
+  if (n < 0) {  // too many tokens for the list: a heavy row
     if (tid == 0) {
-      const uint32_t slot = atomicAdd(ws.nheavy, 1u);
-      ws.flag[row] = slot < (uint32_t)ws.slots ? (int32_t)slot : -2;
+      const uint32_t i = atomicAdd(ws.nheavy, 1u);
+      ws.heavy[i] = (int32_t)row;
+      if (i < (uint32_t)ws.slots) {
+        ws.hlisted[i] = 0;
+        ws.hbin[i] = -1;
+      }
     }
     return;
   }
@@ -818,7 +836,7 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, Sampl
     for (int len = 2; len <= size; len <<= 1) {
       for (int step = len >> 1; step > 0; step >>= 1) {
         for (int i = tid; i < size / 2; i += kRowThreads) {
-          const int a = 2 * step * (i / step) + i % step, b = a + step;
+          const int a = ((i & -step) << 1) | (i & (step - 1)), b = a + step;
           const uint64_t x = sh.sorted[a], y = sh.sorted[b];
           if ((x < y) == ((a & len) == 0)) {
             sh.sorted[a] = y;
@@ -896,37 +914,110 @@ template <int DT>
 __global__ void __launch_bounds__(kSampleThreads, 4) sample_hist_kernel(Sample s, SamplePtrs ws) {
   constexpr int N = SampleSource<DT>::N;
   __shared__ SampleHist h;
-  const int tid = threadIdx.x, c = blockIdx.x;
-  for (int64_t row = blockIdx.y; row < s.rows; row += gridDim.y) {
-    const int slot = ws.flag[row];
-    if (slot < 0) continue;  // whole workgroup
+  const int tid = threadIdx.x, c = blockIdx.x, n = (int)min(*ws.nheavy, (uint32_t)ws.slots);
+  for (int slot = blockIdx.y; slot < n; slot += gridDim.y) {
+    const int64_t row = ws.heavy[slot];
     const SampleSource<DT> src(s, row);
+    constexpr int U = kSlice / (kSampleThreads * N);
+    float l[U][N];
+#pragma unroll
+    for (int u = 0; u < U; u++) src.load(c * kSlice + (u * kSampleThreads + tid) * N, l[u]);
     const SampleRow r = sample_row(s, row);
     const float top = sample_top(ws, row);
     const SampleWeight w(top, r.T, ws.shift);
     h.count[tid] = 0;
     h.mass[tid] = 0;
     __syncthreads();
-    constexpr int U = 16 / N;
-    for (int at = c * kSlice; at < min(src.V, (c + 1) * kSlice); at += kSampleThreads * N * U) {
-      float l[U][N];
 #pragma unroll
-      for (int u = 0; u < U; u++) src.load(at + (u * kSampleThreads + tid) * N, l[u]);
+    for (int u = 0; u < U; u++)
 #pragma unroll
-      for (int u = 0; u < U; u++)
-#pragma unroll
-        for (int j = 0; j < N; j++)
-          if (l[u][j] > -__builtin_inff()) {
-            const int b = sample_bin(l[u][j], top);
-            atomicAdd(&h.count[b], 1u);
-            atomicAdd((unsigned long long*)&h.mass[b], (unsigned long long)w.fixed(l[u][j]));
-          }
-    }
+      for (int j = 0; j < N; j++)
+        if (l[u][j] > -__builtin_inff()) {
+          const int b = sample_bin(l[u][j], top);
+          atomicAdd(&h.count[b], 1u);
+          atomicAdd((unsigned long long*)&h.mass[b], (unsigned long long)w.fixed(l[u][j]));
+        }
     __syncthreads();
     const size_t at = ((size_t)slot * ws.slices + c) * kSampleBins + tid;
     ws.hcount[at] = h.count[tid];
     ws.hmass[at] = h.mass[tid];
     __syncthreads();
+  }
+}
+
+// The row's histogram, one bin per thread (bin 0, the largest logits, first): the bin's
+// count and mass, and their sums up to and including it.
+struct SampleRowHist {
+  uint64_t c, m, tc, tm, ic, im;
+  __device__ __forceinline__ SampleRowHist(const SamplePtrs& ws, int slot, SampleScratch<kSampleWaves>& sc)
+      : c(0), m(0), tc(0), tm(0), ic(0), im(0) {
+    if (slot < 0) return;
+    const size_t at = (size_t)slot * ws.slices * kSampleBins + threadIdx.x;
+#pragma unroll 4
+    for (int i = 0; i < ws.slices; i++) {
+      c += ws.hcount[at + (size_t)i * kSampleBins];
+      m += ws.hmass[at + (size_t)i * kSampleBins];
+    }
+    ic = block_scan(c, &tc, sc);
+    im = block_scan(m, &tm, sc);
+  }
+};
+
+// The bin whose tokens the heavy kernel needs first: the one where the first k end, else
+// where the nucleus ends, or that of min-p's bound if that comes first.
+template <int DT>
+__global__ void __launch_bounds__(kSampleThreads, 4) sample_gather_kernel(Sample s, SamplePtrs ws) {
+  constexpr int N = SampleSource<DT>::N, U = kSlice / (kSampleThreads * N);
+  __shared__ SampleScratch<kSampleWaves> sc;
+  const int tid = threadIdx.x, lane = tid & 63, count = (int)min(*ws.nheavy, (uint32_t)ws.slots);
+  for (int slot = blockIdx.y; slot < count; slot += gridDim.y) {
+    const int64_t row = ws.heavy[slot];
+    const SampleSource<DT> src(s, row);
+    const SampleRow r = sample_row(s, row);
+    const float top = sample_top(ws, row);
+    const SampleRowHist h(ws, slot, sc);
+    uint64_t in_bin = 0, unused;
+    int b = -1;
+    if (r.k > 0 && h.tc >= (uint64_t)r.k) {
+      b = block_first(h.ic >= (uint64_t)r.k, 0, 0, &unused, &unused, sc);
+    } else {
+      if (r.p < 1.f) b = block_first(h.im >= scaled_ceil(r.p, h.tm), 0, 0, &unused, &unused, sc);
+      if (r.minp > 0.f) {
+        const SampleWeight w(top, r.T, ws.shift);
+        const int bm = sample_bin(ord_score(sample_minp_key(w, top, r.minp)), top);
+        b = b < 0 ? bm : min(b, bm);
+      }
+    }
+    if (b < 0) continue;
+    block_first(tid == b, h.c, 0, &in_bin, &unused, sc);
+    if (in_bin > kHeavyList) continue;  // the heavy kernel narrows the bin by passes first
+    if (blockIdx.x == 0 && tid == 0) ws.hbin[slot] = b;
+    float l[U][N];
+#pragma unroll
+    for (int u = 0; u < U; u++) src.load(blockIdx.x * kSlice + (u * kSampleThreads + tid) * N, l[u]);
+    uint32_t n = 0;
+#pragma unroll
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int j = 0; j < N; j++) n += l[u][j] > -__builtin_inff() && sample_bin(l[u][j], top) == b;
+    // places by wave: the order of the list does not matter
+    uint32_t upto = n;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const uint32_t o = __shfl_up(upto, off, 64);
+      if (lane >= off) upto += o;
+    }
+    uint32_t place = 0;
+    if (lane == 63 && upto != 0) place = atomicAdd(&ws.hlisted[slot], upto);
+    place = __builtin_amdgcn_readlane(place, 63) + upto - n;
+    uint64_t* list = ws.hlist + (size_t)slot * kHeavyList;
+#pragma unroll
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int j = 0; j < N; j++)
+        if (l[u][j] > -__builtin_inff() && sample_bin(l[u][j], top) == b)
+          list[place++] = ((uint64_t)score_ord(l[u][j]) << 32) |
+                          (uint32_t)(blockIdx.x * kSlice + (u * kSampleThreads + tid) * N + j);
   }
 }
 
@@ -938,13 +1029,11 @@ struct SampleHeavyShared {
   uint32_t n;
 };
 
+// Heavy row `row`, with the histograms and the list of `slot`, or (slot -1) by passes over it.
 template <int DT>
-__global__ void __launch_bounds__(kSampleThreads, 4) sample_heavy_kernel(Sample s, SamplePtrs ws) {
-  __shared__ SampleHeavyShared sh;
+__device__ __forceinline__ void sample_heavy_row(const Sample& s, const SamplePtrs& ws, int64_t row, int slot,
+                                                 SampleHeavyShared& sh) {
   SampleScratch<kSampleWaves>& sc = sh.sc;
-  const int64_t row = blockIdx.x;
-  const int slot = ws.flag[row];
-  if (slot == -1) return;  // whole workgroup
   const bool hist = slot >= 0;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const SampleSource<DT> src(s, row);
@@ -952,19 +1041,10 @@ __global__ void __launch_bounds__(kSampleThreads, 4) sample_heavy_kernel(Sample 
   const float top = sample_top(ws, row);
   const uint32_t top_key = score_ord(top);
   const SampleWeight w(top, r.T, ws.shift);
-  const uint32_t* hcount = ws.hcount + (size_t)(hist ? slot : 0) * ws.slices * kSampleBins;
   const uint64_t* hmass = ws.hmass + (size_t)(hist ? slot : 0) * ws.slices * kSampleBins;
 
-  // the row's histogram, bin 0 (the largest logits) first
-  uint64_t c = 0, m = 0, tc = 0, tm = 0, ic = 0, im = 0;
-  if (hist) {
-    for (int i = 0; i < ws.slices; i++) {
-      c += hcount[i * kSampleBins + tid];
-      m += hmass[i * kSampleBins + tid];
-    }
-    ic = block_scan(c, &tc, sc);
-    im = block_scan(m, &tm, sc);
-  }
+  const SampleRowHist rh(ws, slot, sc);
+  const uint64_t c = rh.c, m = rh.m, tc = rh.tc, tm = rh.tm, ic = rh.ic, im = rh.im;
 
   // the tokens of one bin
   SampleRange<kSampleThreads, DT> range(src, sh.list, &sh.n);
@@ -977,7 +1057,13 @@ __global__ void __launch_bounds__(kSampleThreads, 4) sample_heavy_kernel(Sample 
     khi = b == 0 ? top_key : sample_bin_floor(b - 1, top) - 1;
     uint64_t in_bin, unused;
     block_first(tid == b, c, 0, &in_bin, &unused, sc);
-    range.gather(klo, khi, in_bin);
+    if (b == ws.hbin[slot]) {  // the gather kernel has listed them
+      range.n = (int)in_bin;
+      for (int i = tid; i < range.n; i += kSampleThreads) sh.list[i] = ws.hlist[(size_t)slot * kHeavyList + i];
+      __syncthreads();
+    } else {
+      range.gather(klo, khi, in_bin);
+    }
   };
   SampleCut cut;
   auto kept = [&](float l, int v) {
@@ -1043,6 +1129,16 @@ __global__ void __launch_bounds__(kSampleThreads, 4) sample_heavy_kernel(Sample 
   sample_store(s, row, id, w.weight(src.logit(id)), total, ws.shift);
 }
 
+template <int DT>
+__global__ void __launch_bounds__(kSampleThreads, 4) sample_heavy_kernel(Sample s, SamplePtrs ws) {
+  __shared__ SampleHeavyShared sh;
+  const int n = (int)*ws.nheavy;
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    sample_heavy_row<DT>(s, ws, ws.heavy[i], i < ws.slots ? i : -1, sh);
+    __syncthreads();
+  }
+}
+
 size_t sample_workspace(int64_t rows, int64_t vocab) {
   if (rows == 0) return 0;
   // 16-bit logits have no more groups than f32 ones
@@ -1055,11 +1151,16 @@ static hipError_t launch_sample_dt(const Sample& s, const SamplePtrs& ws, bool f
   hipLaunchKernelGGL((sample_chunk_kernel<DT>), dim3((unsigned)cdiv(units, kChunkThreads / 64)), dim3(kChunkThreads), 0,
                      stream, s, ws);
   hipLaunchKernelGGL((sample_row_kernel<DT>), dim3((unsigned)s.rows), dim3(kRowThreads), 0, stream, s, ws);
-  if (flat)
-    hipLaunchKernelGGL((sample_hist_kernel<DT>), dim3((unsigned)ws.slices, (unsigned)std::min<int64_t>(s.rows, 32768)),
-                       dim3(kSampleThreads), 0, stream, s, ws);
+  if (flat) {
+    // few workgroups, as there are few heavy rows as a rule and none often (10,240 workgroups that
+    // found nothing to do took 40 us)
+    const dim3 grid((unsigned)ws.slices, (unsigned)std::min<int64_t>(s.rows, cdiv(2 * kTargetBlocks, ws.slices)));
+    hipLaunchKernelGGL((sample_hist_kernel<DT>), grid, dim3(kSampleThreads), 0, stream, s, ws);
+    hipLaunchKernelGGL((sample_gather_kernel<DT>), grid, dim3(kSampleThreads), 0, stream, s, ws);
+  }
   if (filtered)
-    hipLaunchKernelGGL((sample_heavy_kernel<DT>), dim3((unsigned)s.rows), dim3(kSampleThreads), 0, stream, s, ws);
+    hipLaunchKernelGGL((sample_heavy_kernel<DT>), dim3((unsigned)std::min<int64_t>(s.rows, kTargetBlocks)),
+                       dim3(kSampleThreads), 0, stream, s, ws);
   return hipGetLastError();
 }
 
@@ -1070,10 +1171,13 @@ hipError_t launch_sample(const Sample& s, void* space, hipStream_t stream) {
   p.gmax = (float*)(base + w.gmax);
   p.cmax = (float*)(base + w.cmax);
   p.csum = (uint64_t*)(base + w.csum);
-  p.flag = (int32_t*)(base + w.flag);
+  p.heavy = (int32_t*)(base + w.heavy);
   p.nheavy = (uint32_t*)(base + w.nheavy);
   p.hcount = (uint32_t*)(base + w.hcount);
   p.hmass = (uint64_t*)(base + w.hmass);
+  p.hlist = (uint64_t*)(base + w.hlist);
+  p.hlisted = (uint32_t*)(base + w.hlisted);
+  p.hbin = (int32_t*)(base + w.hbin);
   p.chunks = w.chunks;
   p.slices = w.slices;
   p.group_log2 = w.group_log2;
@@ -1085,7 +1189,8 @@ hipError_t launch_sample(const Sample& s, void* space, hipStream_t stream) {
   // Rows that keep more than the list holds are left to the heavy kernel, with the
   // histograms where their settings may ask for it: with one small k for all rows only
   // ties overflow the list, and the heavy kernel does without (no slots).
-  const bool small_k = s.d_top_k == nullptr && s.top_k > 0 && s.top_k <= kList / 2;
+  const bool greedy = s.d_temperature == nullptr && s.temperature == 0.f;
+  const bool small_k = greedy || (s.d_top_k == nullptr && s.top_k > 0 && s.top_k <= kList / 2);
   const bool no_filter = s.temperature > 0.f && s.d_temperature == nullptr && s.d_top_k == nullptr && s.top_k == 0 &&
                          s.d_top_p == nullptr && s.top_p == 1.f && s.d_min_p == nullptr && s.min_p == 0.f;
   const bool filtered = s.vocab > kList && !no_filter, flat = filtered && !small_k;
