@@ -210,25 +210,46 @@ struct SampleSource {
   // tokens [v, v + N) (v a multiple of N, N = 4 or 8 by type), -inf past the vocabulary and
   // where barred: one 16-byte load at any alignment of the value.  A NaN logit is left as it is.
   static constexpr int N = DT == DT_F32 ? 4 : 8;
+  __device__ __forceinline__ u32x4 vec(int v) const {  // v + N <= V
+    u32x4 w;
+    __builtin_memcpy(&w, base + (size_t)v * (16 / N), 16);
+    return w;
+  }
+  __device__ __forceinline__ void unpack(const u32x4& w, int v, float (&l)[N]) const {
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      if constexpr (DT == DT_F32) l[j] = __uint_as_float(w[j]);
+      else if constexpr (DT == DT_BF16) l[j] = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+      else l[j] = f16_bits_to_f32(j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu);
+    }
+    if (allowed != nullptr) {
+      const uint32_t ok = allowed[v >> 5] >> (v & 31);
+#pragma unroll
+      for (int j = 0; j < N; j++)
+        if (!((ok >> j) & 1u)) l[j] = -__builtin_inff();
+    }
+  }
   __device__ __forceinline__ void load_raw(int v, float (&l)[N]) const {
     if (v + N <= V) {
-      u32x4 w;
-      __builtin_memcpy(&w, base + (size_t)v * (16 / N), 16);
-#pragma unroll
-      for (int j = 0; j < N; j++) {
-        if constexpr (DT == DT_F32) l[j] = __uint_as_float(w[j]);
-        else if constexpr (DT == DT_BF16) l[j] = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
-        else l[j] = f16_bits_to_f32(j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu);
-      }
-      if (allowed != nullptr) {
-        const uint32_t ok = allowed[v >> 5] >> (v & 31);
-#pragma unroll
-        for (int j = 0; j < N; j++)
-          if (!((ok >> j) & 1u)) l[j] = -__builtin_inff();
-      }
+      unpack(vec(v), v, l);
     } else {
 #pragma unroll
       for (int j = 0; j < N; j++) l[j] = v + j < V ? logit(v + j) : -__builtin_inff();
+    }
+  }
+  // M vectors STRIDE tokens apart from v, the lane's; `end` bounds the whole workgroup's or
+  // wave's tokens: where all are in the row the loads are issued together.
+  template <int M, int STRIDE>
+  __device__ __forceinline__ void load_many(int v, int end, float (&l)[M][N]) const {
+    if (end <= V) {
+      u32x4 w[M];
+#pragma unroll
+      for (int i = 0; i < M; i++) w[i] = vec(v + i * STRIDE);
+#pragma unroll
+      for (int i = 0; i < M; i++) unpack(w[i], v + i * STRIDE, l[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < M; i++) load_raw(v + i * STRIDE, l[i]);
     }
   }
   __device__ __forceinline__ void load(int v, float (&l)[N]) const {
@@ -258,27 +279,37 @@ __device__ __forceinline__ uint32_t sample_bin_limit(int b) {
   return b >= kSampleBins - 1 ? 0xffffffffu : (uint32_t)(b + 1 + kBinBase) << kBinShift;
 }
 
-// The smallest key whose bin is at most b.
-__device__ __forceinline__ uint32_t sample_bin_floor(int b, float top) {
-  if (b >= kSampleBins - 1) return 1;
-  uint32_t lo = 0, hi = score_ord(top);  // hi's bin is 0
+// The smallest key for which reaches(logit) holds, given that it holds for `hi` and goes on
+// holding as keys grow: every lane tries a key of its own, 6 rounds.
+template <typename F>
+__device__ __forceinline__ uint32_t first_key(uint32_t hi, F reaches) {
+  const uint32_t lane = threadIdx.x & 63;
+  uint32_t lo = 0;  // does not reach it, or is no candidate's key
   while (hi - lo > 1) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (sample_bin(ord_score(mid), top) <= b) hi = mid;  // keys below -inf's decode to NaN: the last bin
-    else lo = mid;
+    const uint32_t step = (hi - lo - 1) / 64 + 1;  // lane i: lo + (i + 1) step, at most hi
+    const uint32_t mine = step <= (hi - lo) / (lane + 1) ? lo + (lane + 1) * step : hi;
+    const uint64_t m = __ballot(reaches(ord_score(mine)));  // hi is among the tried or beyond the last
+    if (m == 0) {
+      lo += 64 * step;
+      continue;
+    }
+    const uint32_t i = (uint32_t)__ffsll((unsigned long long)m) - 1;
+    const uint32_t to = step <= (hi - lo) / (i + 1) ? lo + (i + 1) * step : hi;
+    lo += i * step;
+    hi = to;
   }
   return hi;
 }
 
+// The smallest key whose bin is at most b (keys below -inf's decode to NaN: the last bin).
+__device__ __forceinline__ uint32_t sample_bin_floor(int b, float top) {
+  if (b >= kSampleBins - 1) return 1;
+  return first_key(score_ord(top), [&](float l) { return sample_bin(l, top) <= b; });
+}
+
 // The smallest key whose weight reaches minp (weights do not fall as keys grow).
 __device__ __forceinline__ uint32_t sample_minp_key(const SampleWeight& w, float top, float minp) {
-  uint32_t lo = 0, hi = score_ord(top);  // keys above lo are undecided, hi's weight reaches it
-  while (hi - lo > 1) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (w.weight(ord_score(mid)) >= (double)minp) hi = mid;
-    else lo = mid;
-  }
-  return hi;
+  return first_key(score_ord(top), [&](float l) { return w.weight(l) >= (double)minp; });
 }
 
 // ---------------------------------------------------------------------------
@@ -427,8 +458,7 @@ __global__ void __launch_bounds__(kChunkThreads) sample_chunk_kernel(Sample s, S
   const int steps = ws.group_log2 - (DT == DT_F32 ? 2 : 3);
   const Src src(s, row);
   float l[NV][N];
-#pragma unroll
-  for (int j = 0; j < NV; j++) src.load_raw(c * kChunk + (j * 64 + lane) * N, l[j]);
+  src.template load_many<NV, 64 * N>(c * kChunk + lane * N, (c + 1) * kChunk, l);
   const SampleRow r = sample_row(s, row);
   float m = -__builtin_inff();
 #pragma unroll
@@ -477,8 +507,7 @@ __device__ __forceinline__ void sample_each(const SampleSource<DT>& src, F f) {
   constexpr int N = SampleSource<DT>::N, U = 16 / N;
   for (int at = 0; at < src.V; at += NT * N * U) {
     float l[U][N];
-#pragma unroll
-    for (int u = 0; u < U; u++) src.load(at + (u * NT + (int)threadIdx.x) * N, l[u]);
+    src.template load_many<U, NT * N>(at + (int)threadIdx.x * N, at + NT * N * U, l);
 #pragma unroll
     for (int u = 0; u < U; u++)
 #pragma unroll
@@ -630,6 +659,15 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, Sampl
   const SampleRow r = sample_row(s, row);
   const int V = src.V;
 
+  // loaded before anything waits
+  constexpr int G = kMaxGroups / kRowThreads;  // consecutive groups of a thread, kept in registers
+  float gm[G];
+#pragma unroll
+  for (int q = 0; q < G; q++) {
+    const int g = G * tid + q;
+    gm[q] = g < ws.groups ? ws.gmax[row * ws.groups + g] : -__builtin_inff();
+  }
+
   // the row's largest logit
   const float* cmax = ws.cmax + row * ws.chunks;
   float top = -__builtin_inff();
@@ -689,13 +727,6 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, Sampl
   // Tokens nearer to the largest logit than `limit` are gathered: among them is every
   // kept token (for top-p after top-k: every one of the first k).
   uint32_t limit = 0xffffffffu;
-  constexpr int G = kMaxGroups / kRowThreads;  // consecutive groups of a thread, kept in registers
-  float gm[G];
-#pragma unroll
-  for (int q = 0; q < G; q++) {
-    const int g = G * tid + q;
-    gm[q] = g < ws.groups ? ws.gmax[row * ws.groups + g] : -__builtin_inff();
-  }
   const uint64_t p_mass = r.p < 1.f && r.k == 0 ? scaled_ceil(r.p, total) : 0;
   if (r.k > 0 || p_mass > 0) {
 #pragma unroll
@@ -784,22 +815,19 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, Sampl
         } else if (wave_hits != 0) {
 #pragma unroll
           for (int u = 0; u < U; u++) {
-            uint32_t c = 0;
+            uint32_t place = to, hits_u = 0;
 #pragma unroll
-            for (int j = 0; j < N; j++) c += near(l[u][j]);
-            if (__ballot(c != 0) == 0) continue;
-            uint32_t upto = c;
-#pragma unroll
-            for (int off = 1; off < 64; off <<= 1) {
-              const uint32_t o = __shfl_up(upto, off, 64);
-              if (lane >= off) upto += o;
+            for (int j = 0; j < N; j++) {
+              const uint64_t m = __ballot(near(l[u][j]));
+              place += __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+              hits_u += (uint32_t)__popcll(m);
             }
-            uint32_t place = to + upto - c;
+            if (hits_u == 0) continue;
 #pragma unroll
             for (int j = 0; j < N; j++)
               if (near(l[u][j]))
                 sh.list[place++] = ((uint64_t)score_ord(l[u][j]) << 32) | (uint32_t)~(uint32_t)(v[u] + j);
-            to += __builtin_amdgcn_readlane(upto, 63);
+            to += hits_u;
           }
         }
         base += sum;
@@ -920,8 +948,7 @@ __global__ void __launch_bounds__(kSampleThreads, 4) sample_hist_kernel(Sample s
     const SampleSource<DT> src(s, row);
     constexpr int U = kSlice / (kSampleThreads * N);
     float l[U][N];
-#pragma unroll
-    for (int u = 0; u < U; u++) src.load(c * kSlice + (u * kSampleThreads + tid) * N, l[u]);
+    src.template load_many<U, kSampleThreads * N>(c * kSlice + tid * N, (c + 1) * kSlice, l);
     const SampleRow r = sample_row(s, row);
     const float top = sample_top(ws, row);
     const SampleWeight w(top, r.T, ws.shift);
@@ -993,8 +1020,7 @@ __global__ void __launch_bounds__(kSampleThreads, 4) sample_gather_kernel(Sample
     if (in_bin > kHeavyList) continue;  // the heavy kernel narrows the bin by passes first
     if (blockIdx.x == 0 && tid == 0) ws.hbin[slot] = b;
     float l[U][N];
-#pragma unroll
-    for (int u = 0; u < U; u++) src.load(blockIdx.x * kSlice + (u * kSampleThreads + tid) * N, l[u]);
+    src.template load_many<U, kSampleThreads * N>(blockIdx.x * kSlice + tid * N, (blockIdx.x + 1) * kSlice, l);
     uint32_t n = 0;
 #pragma unroll
     for (int u = 0; u < U; u++)
