@@ -79,10 +79,20 @@ static constexpr int kHeavyList = 8192;          // tokens of one bin in the hea
 static constexpr int kMaxGroups = 4096;          // groups per row
 static constexpr size_t kHeavyBytes = 128 << 20;  // most workspace for heavy rows (one slot each)
 
+// Where the first cut of a heavy row lies.
+struct SampleState {
+  int32_t filter;  // which filter makes it: 0 min-p or none, 1 top-k, 2 top-p
+  int32_t bin;     // the bin that holds it
+  int32_t listed;  // whether the bin's tokens are in the slot's list
+  int32_t pad;
+  uint64_t goal;                        // top-p's mass
+  uint64_t before_count, before_mass;   // of the bins before it
+};
+
 // Workspace of a call, from its sizes alone.
 struct SampleWs {
   int chunks, slices, group_log2, groups, slots;
-  size_t gmax, cmax, csum, heavy, nheavy, hcount, hmass, hlist, hlisted, hbin, bytes;
+  size_t gmax, cmax, csum, heavy, nheavy, hcount, hmass, hlist, hlisted, hstate, bytes;
 };
 
 static SampleWs sample_ws(int64_t rows, int64_t vocab, int32_t dtype) {
@@ -110,7 +120,7 @@ static SampleWs sample_ws(int64_t rows, int64_t vocab, int32_t dtype) {
   w.hmass = take((size_t)w.slots * w.slices * kSampleBins * 8);
   w.hlist = take((size_t)w.slots * kHeavyList * 8);
   w.hlisted = take((size_t)w.slots * 4);
-  w.hbin = take((size_t)w.slots * 4);
+  w.hstate = take((size_t)w.slots * sizeof(SampleState));
   w.bytes = at;
   return w;
 }
@@ -125,7 +135,7 @@ struct SamplePtrs {
   uint64_t* hmass;
   uint64_t* hlist;    // [slots][kHeavyList] tokens of the bin that holds the cut, key << 32 | id
   uint32_t* hlisted;  // [slots] how many there are
-  int32_t* hbin;      // [slots] the bin, -1: not listed
+  SampleState* hstate;  // [slots]
   int chunks, slices, group_log2, groups, slots, shift;
 };
 
@@ -533,17 +543,18 @@ struct SampleRange {
       sample_each<NT>(src, f);
     }
   }
-  // lists the row's `count` candidates with keys in [klo, khi] if they fit
-  __device__ __forceinline__ void gather(uint32_t klo, uint32_t khi, uint64_t count) {
-    n = -1;
-    if (count > kHeavyList) return;
+  // lists the row's candidates with keys in [klo, khi] if they fit
+  __device__ __forceinline__ void gather(uint32_t klo, uint32_t khi) {
     if (threadIdx.x == 0) *size = 0;
     __syncthreads();
     sample_each<NT>(src, [&](uint32_t key, uint32_t id) {
-      if (key >= klo && key <= khi) list[atomicAdd(size, 1u)] = ((uint64_t)key << 32) | id;
+      if (key >= klo && key <= khi) {
+        const uint32_t i = atomicAdd(size, 1u);
+        if (i < kHeavyList) list[i] = ((uint64_t)key << 32) | id;
+      }
     });
     __syncthreads();
-    n = (int)*size;
+    n = *size <= kHeavyList ? (int)*size : -1;
     __syncthreads();
   }
 };
@@ -581,14 +592,12 @@ __device__ __forceinline__ uint64_t sample_find(SampleRange<kSampleThreads, DT>&
     int t = block_first(c != 0 && (by_count ? ic >= count : im >= mass), ic - c, im - m, &bc, &bm, sc);
     if (t < 0) t = block_first(c != 0 && ic == before_count + tc, ic - c, im - m, &bc, &bm, sc);
     const int bin = kSampleBins - 1 - t;
-    const uint32_t in_bin = h.count[bin];
     before_count = bc;
     before_mass = bm;
     klo += (uint32_t)bin << sh;
     khi = min(khi, klo + ((1u << sh) - 1));
     __syncthreads();
-    // elements that an earlier cut leaves out are not counted: only without one is the list's size known
-    if (range.n < 0 && old.key == 1 && sh > 0) range.gather(klo, khi, in_bin);
+    if (range.n < 0 && sh > 0) range.gather(klo, khi);
   }
   const uint64_t wk = w.fixed(ord_score(klo));
   uint64_t ties = by_count ? count - before_count : wk != 0 ? (mass - before_mass + wk - 1) / wk : ~0ull >> 1;
@@ -645,6 +654,7 @@ struct SampleRowShared {
     };
   };
   uint32_t wave_count[kRowWaves];
+  uint32_t bin_end[kSampleBins];
 };
 
 // A row is a chain of short dependent steps: 512 threads, as more waves synchronise
@@ -840,25 +850,66 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, Sampl
     if (tid == 0) {
       const uint32_t i = atomicAdd(ws.nheavy, 1u);
       ws.heavy[i] = (int32_t)row;
-      if (i < (uint32_t)ws.slots) {
-        ws.hlisted[i] = 0;
-        ws.hbin[i] = -1;
-      }
+      if (i < (uint32_t)ws.slots) ws.hlisted[i] = 0;
     }
     return;
   }
   __syncthreads();
 
-  // sort descending: by counting for short lists, else bitonic with empty entries 0 last
+  // Sort descending.  Short lists: a token's place is the number of larger ones.  Longer ones:
+  // by bins first (a scan of their counts), where a token's place in its bin is counted the
+  // same way; where a bin holds many, the whole list bitonically, empty entries 0 last.
   int size = kRowThreads;
   while (size < n) size <<= 1;
-  if (size == kRowThreads) {
+  bool done = size == kRowThreads;
+  if (done) {
     const uint64_t x = tid < n ? sh.list[tid] : 0;
     int rank = 0;
     for (int i = 0; i < n; i++) rank += sh.list[i] > x;
     if (tid < n) sh.sorted[rank] = x;
     __syncthreads();
   } else {
+    constexpr int Q = kSampleBins / kRowThreads, MANY = 64;
+    uint64_t* binned = sh.mass;
+    for (int i = tid; i < kSampleBins; i += kRowThreads) sh.bin_end[i] = 0;
+    __syncthreads();
+    auto bin_of = [&](uint64_t x) { return sample_bin(ord_score((uint32_t)(x >> 32)), top); };
+    for (int i = tid; i < n; i += kRowThreads) atomicAdd(&sh.bin_end[bin_of(sh.list[i])], 1u);
+    __syncthreads();
+    uint32_t count[Q], sum = 0;
+    bool many = false;
+#pragma unroll
+    for (int q = 0; q < Q; q++) {
+      count[q] = sh.bin_end[Q * tid + q];
+      many |= count[q] > MANY;
+      sum += count[q];
+    }
+    uint64_t all;
+    uint32_t start = (uint32_t)block_scan((uint64_t)sum, &all, sc) - sum;
+    if (block_first(many, 0, 0, &unused, &unused2, sc) < 0) {
+#pragma unroll
+      for (int q = 0; q < Q; q++) {  // each bin's start, which the placing turns into its end
+        sh.bin_end[Q * tid + q] = start;
+        start += count[q];
+      }
+      __syncthreads();
+      for (int i = tid; i < n; i += kRowThreads) {
+        const uint64_t x = sh.list[i];
+        binned[atomicAdd(&sh.bin_end[bin_of(x)], 1u)] = x;
+      }
+      __syncthreads();
+      for (int i = tid; i < n; i += kRowThreads) {
+        const uint64_t x = sh.list[i];
+        const int b = bin_of(x), from = b == 0 ? 0 : (int)sh.bin_end[b - 1], to = (int)sh.bin_end[b];
+        int rank = from;
+        for (int j = from; j < to; j++) rank += binned[j] > x;
+        sh.sorted[rank] = x;
+      }
+      __syncthreads();
+      done = true;
+    }
+  }
+  if (!done) {
     for (int i = tid; i < size; i += kRowThreads) sh.sorted[i] = i < n ? sh.list[i] : 0;
     __syncthreads();
     for (int len = 2; len <= size; len <<= 1) {
@@ -990,37 +1041,53 @@ struct SampleRowHist {
   }
 };
 
-// The bin whose tokens the heavy kernel needs first: the one where the first k end, else
-// where the nucleus ends, or that of min-p's bound if that comes first.
-template <int DT>
-__global__ void __launch_bounds__(kSampleThreads, 4) sample_gather_kernel(Sample s, SamplePtrs ws) {
-  constexpr int N = SampleSource<DT>::N, U = kSlice / (kSampleThreads * N);
+// Where the first cut of each heavy row lies: the bin in which the first k end, else that in
+// which the nucleus ends, or that of min-p's bound if it comes first.
+__global__ void __launch_bounds__(kSampleThreads, 4) sample_bin_kernel(Sample s, SamplePtrs ws) {
   __shared__ SampleScratch<kSampleWaves> sc;
-  const int tid = threadIdx.x, lane = tid & 63, count = (int)min(*ws.nheavy, (uint32_t)ws.slots);
-  for (int slot = blockIdx.y; slot < count; slot += gridDim.y) {
+  const int tid = threadIdx.x, count = (int)min(*ws.nheavy, (uint32_t)ws.slots);
+  for (int slot = blockIdx.x; slot < count; slot += gridDim.x) {
     const int64_t row = ws.heavy[slot];
-    const SampleSource<DT> src(s, row);
     const SampleRow r = sample_row(s, row);
     const float top = sample_top(ws, row);
     const SampleRowHist h(ws, slot, sc);
+    SampleState st = {};
+    st.bin = kSampleBins - 1;
     uint64_t in_bin = 0, unused;
-    int b = -1;
-    if (r.k > 0 && h.tc >= (uint64_t)r.k) {
-      b = block_first(h.ic >= (uint64_t)r.k, 0, 0, &unused, &unused, sc);
+    if (r.k > 0 && h.tc >= (uint64_t)r.k) {  // else there are fewer candidates than k
+      st.filter = 1;
+      st.bin = block_first(h.ic >= (uint64_t)r.k, h.ic - h.c, h.im - h.m, &st.before_count, &st.before_mass, sc);
     } else {
-      if (r.p < 1.f) b = block_first(h.im >= scaled_ceil(r.p, h.tm), 0, 0, &unused, &unused, sc);
+      if (r.p < 1.f) {
+        st.filter = 2;
+        st.goal = scaled_ceil(r.p, h.tm);
+        st.bin = block_first(h.im >= st.goal, h.ic - h.c, h.im - h.m, &st.before_count, &st.before_mass, sc);
+      }
       if (r.minp > 0.f) {
         const SampleWeight w(top, r.T, ws.shift);
-        const int bm = sample_bin(ord_score(sample_minp_key(w, top, r.minp)), top);
-        b = b < 0 ? bm : min(b, bm);
+        const int b = sample_bin(ord_score(sample_minp_key(w, top, r.minp)), top);
+        if (b < st.bin) st.filter = 0, st.bin = b;  // the nucleus ends in a later bin
       }
     }
-    if (b < 0) continue;
-    block_first(tid == b, h.c, 0, &in_bin, &unused, sc);
-    if (in_bin > kHeavyList) continue;  // the heavy kernel narrows the bin by passes first
-    if (blockIdx.x == 0 && tid == 0) ws.hbin[slot] = b;
+    block_first(tid == st.bin, h.c, 0, &in_bin, &unused, sc);
+    st.listed = in_bin <= kHeavyList;  // else the heavy kernel narrows the bin by a pass first
+    if (tid == 0) ws.hstate[slot] = st;
+  }
+}
+
+// Lists the tokens of those bins.
+template <int DT>
+__global__ void __launch_bounds__(kSampleThreads) sample_gather_kernel(Sample s, SamplePtrs ws) {
+  constexpr int N = SampleSource<DT>::N, U = kSlice / (kSampleThreads * N);
+  const int tid = threadIdx.x, lane = tid & 63, count = (int)min(*ws.nheavy, (uint32_t)ws.slots);
+  for (int slot = blockIdx.y; slot < count; slot += gridDim.y) {
+    const int64_t row = ws.heavy[slot];
+    const int b = ws.hstate[slot].listed ? ws.hstate[slot].bin : -1;
+    if (b < 0) continue;  // whole workgroup
+    const SampleSource<DT> src(s, row);
     float l[U][N];
     src.template load_many<U, kSampleThreads * N>(blockIdx.x * kSlice + tid * N, (blockIdx.x + 1) * kSlice, l);
+    const float top = sample_top(ws, row);
     uint32_t n = 0;
 #pragma unroll
     for (int u = 0; u < U; u++)
@@ -1069,8 +1136,7 @@ __device__ __forceinline__ void sample_heavy_row(const Sample& s, const SamplePt
   const SampleWeight w(top, r.T, ws.shift);
   const uint64_t* hmass = ws.hmass + (size_t)(hist ? slot : 0) * ws.slices * kSampleBins;
 
-  const SampleRowHist rh(ws, slot, sc);
-  const uint64_t c = rh.c, m = rh.m, tc = rh.tc, tm = rh.tm, ic = rh.ic, im = rh.im;
+  const SampleState st = hist ? ws.hstate[slot] : SampleState{};
 
   // the tokens of one bin
   SampleRange<kSampleThreads, DT> range(src, sh.list, &sh.n);
@@ -1081,14 +1147,12 @@ __device__ __forceinline__ void sample_heavy_row(const Sample& s, const SamplePt
     listed = b;
     klo = sample_bin_floor(b, top);
     khi = b == 0 ? top_key : sample_bin_floor(b - 1, top) - 1;
-    uint64_t in_bin, unused;
-    block_first(tid == b, c, 0, &in_bin, &unused, sc);
-    if (b == ws.hbin[slot]) {  // the gather kernel has listed them
-      range.n = (int)in_bin;
+    if (b == st.bin && st.listed) {  // the gather kernel has listed them
+      range.n = (int)ws.hlisted[slot];
       for (int i = tid; i < range.n; i += kSampleThreads) sh.list[i] = ws.hlist[(size_t)slot * kHeavyList + i];
       __syncthreads();
     } else {
-      range.gather(klo, khi, in_bin);
+      range.gather(klo, khi);
     }
   };
   SampleCut cut;
@@ -1102,21 +1166,32 @@ __device__ __forceinline__ void sample_heavy_row(const Sample& s, const SamplePt
     block_scan(z, &all, sc);
     return all;
   };
-  uint64_t mass = tm, bc = 0, bm = 0;
-  if (r.k > 0 && (!hist || tc >= (uint64_t)r.k)) {  // else there are fewer candidates than k
-    if (hist) bin_open(block_first(ic >= (uint64_t)r.k, ic - c, im - m, &bc, &bm, sc));
+  auto find = [&](bool by_count, uint64_t goal, uint64_t bc, uint64_t bm) {
     const bool whole = range.n >= 0;
-    mass = sample_find(range, w, &cut, klo, khi, true, (uint64_t)r.k, 0, bc, bm, sh.h, sc);
+    const uint64_t mass =
+        sample_find(range, w, &cut, klo, khi, by_count, by_count ? goal : 0, by_count ? 0 : goal, bc, bm, sh.h, sc);
     if (!whole) listed = -1, range.n = -1;  // the search may have listed a part of the range
-  } else if (!hist && r.p < 1.f) {
-    mass = kept_mass();
-  }
-  if (r.p < 1.f) {
-    const uint64_t goal = scaled_ceil(r.p, mass);
-    if (hist) bin_open(block_first(im >= goal, ic - c, im - m, &bc, &bm, sc));
-    const bool whole = range.n >= 0;
-    sample_find(range, w, &cut, klo, khi, false, 0, goal, bc, bm, sh.h, sc);
-    if (!whole) listed = -1, range.n = -1;
+    return mass;
+  };
+  if (hist) {
+    if (st.filter != 0) {
+      bin_open(st.bin);
+      const uint64_t mass =
+          find(st.filter == 1, st.filter == 1 ? (uint64_t)r.k : st.goal, st.before_count, st.before_mass);
+      if (st.filter == 1 && r.p < 1.f) {
+        uint64_t bc, bm;
+        const uint64_t goal = scaled_ceil(r.p, mass);
+        const SampleRowHist h(ws, slot, sc);
+        const int b = block_first(h.im >= goal, h.ic - h.c, h.im - h.m, &bc, &bm, sc);
+        bin_open(b);
+        find(false, goal, bc, bm);
+      }
+    }
+  } else {
+    uint64_t mass = 0;
+    if (r.k > 0) mass = find(true, (uint64_t)r.k, 0, 0);
+    else if (r.p < 1.f) mass = kept_mass();
+    if (r.p < 1.f) find(false, scaled_ceil(r.p, mass), 0, 0);
   }
   if (r.minp > 0.f) {
     const uint32_t key = sample_minp_key(w, top, r.minp);
@@ -1182,6 +1257,8 @@ static hipError_t launch_sample_dt(const Sample& s, const SamplePtrs& ws, bool f
     // found nothing to do took 40 us)
     const dim3 grid((unsigned)ws.slices, (unsigned)std::min<int64_t>(s.rows, cdiv(2 * kTargetBlocks, ws.slices)));
     hipLaunchKernelGGL((sample_hist_kernel<DT>), grid, dim3(kSampleThreads), 0, stream, s, ws);
+    hipLaunchKernelGGL(sample_bin_kernel, dim3((unsigned)std::min<int64_t>(s.rows, kTargetBlocks)), dim3(kSampleThreads), 0,
+                       stream, s, ws);
     hipLaunchKernelGGL((sample_gather_kernel<DT>), grid, dim3(kSampleThreads), 0, stream, s, ws);
   }
   if (filtered)
@@ -1203,7 +1280,7 @@ hipError_t launch_sample(const Sample& s, void* space, hipStream_t stream) {
   p.hmass = (uint64_t*)(base + w.hmass);
   p.hlist = (uint64_t*)(base + w.hlist);
   p.hlisted = (uint32_t*)(base + w.hlisted);
-  p.hbin = (int32_t*)(base + w.hbin);
+  p.hstate = (SampleState*)(base + w.hstate);
   p.chunks = w.chunks;
   p.slices = w.slices;
   p.group_log2 = w.group_log2;
