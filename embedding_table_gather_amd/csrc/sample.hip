@@ -775,7 +775,11 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, Sampl
   // the groups within the limit, then their tokens that are, both in id order
   int n = -1;
   {
-    auto near = [&](float l) { return l > -__builtin_inff() && sample_dist(l, top) < limit; };
+    // the smallest logit within the limit: one comparison per token, which NaN and -inf fail
+    const float least = limit == 0xffffffffu ? -3.40282347e38f : ord_score(first_key(score_ord(top), [&](float l) {
+      return sample_dist(l, top) < limit;
+    }));
+    auto near = [&](float l) { return l >= least; };
     uint32_t mine = 0;
 #pragma unroll
     for (int q = 0; q < G; q++) mine += near(gm[q]);
@@ -795,13 +799,27 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, Sampl
         float l[U][N];
         int v[U];
         uint32_t hits = 0;
+        bool whole = V >= N;
 #pragma unroll
         for (int u = 0; u < U; u++) {
           const int i = r0 + ((wv * U + u) * 64 + lane) * N;
-          v[u] = V;
-          if (i < items)
-            v[u] = (int)(sh.groups[i >> ws.group_log2] << ws.group_log2) + (i & ((1 << ws.group_log2) - 1));
-          src.load(v[u], l[u]);
+          const int g = (int)(sh.groups[min(i, items - 1) >> ws.group_log2] << ws.group_log2);
+          v[u] = i < items ? g + (i & ((1 << ws.group_log2) - 1)) : V;
+          whole = whole && (v[u] == V || v[u] + N <= V);
+        }
+        if (__all(whole)) {  // the loads of all steps together
+          u32x4 w4[U];
+#pragma unroll
+          for (int u = 0; u < U; u++) w4[u] = src.vec(v[u] < V ? v[u] : 0);
+#pragma unroll
+          for (int u = 0; u < U; u++) {
+            src.unpack(w4[u], v[u] < V ? v[u] : 0, l[u]);
+#pragma unroll
+            for (int j = 0; j < N; j++) l[u][j] = v[u] < V ? l[u][j] : -__builtin_inff();
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; u++) src.load(v[u], l[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; u++)
@@ -869,11 +887,21 @@ __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, Sampl
     if (tid < n) sh.sorted[rank] = x;
     __syncthreads();
   } else {
-    constexpr int Q = kSampleBins / kRowThreads, MANY = 64;
+    constexpr int Q = kSampleBins / kRowThreads, MANY = 128;
     uint64_t* binned = sh.mass;
+    float low = top;  // the smallest logit of the list
     for (int i = tid; i < kSampleBins; i += kRowThreads) sh.bin_end[i] = 0;
+    for (int i = tid; i < n; i += kRowThreads) low = fminf(low, ord_score((uint32_t)(sh.list[i] >> 32)));
+    low = -wave_max_f32(-low);
+    if (lane == 0) sc.part[wv] = __float_as_uint(low);
     __syncthreads();
-    auto bin_of = [&](uint64_t x) { return sample_bin(ord_score((uint32_t)(x >> 32)), top); };
+#pragma unroll
+    for (int i = 0; i < kRowWaves; i++) low = fminf(low, __uint_as_float((uint32_t)sc.part[i]));
+    // equal bins from the largest to the smallest; logits too far apart or equal fall into one
+    const float per_bin = fminf((float)(kSampleBins - 1) / (top - low), 3e38f);
+    auto bin_of = [&](uint64_t x) {
+      return (int)fminf(fmaxf((top - ord_score((uint32_t)(x >> 32))) * per_bin, 0.f), (float)(kSampleBins - 1));
+    };
     for (int i = tid; i < n; i += kRowThreads) atomicAdd(&sh.bin_end[bin_of(sh.list[i])], 1u);
     __syncthreads();
     uint32_t count[Q], sum = 0;
