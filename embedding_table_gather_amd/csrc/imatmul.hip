@@ -512,9 +512,78 @@ __global__ void __launch_bounds__(64 * kTileWaves, 1) tile_i8_kernel(MatmulI8 p,
 }
 
 // ---------------------------------------------------------------------------
+// Small products, bound by latency: a workgroup per 16 T x 16 T tile of the output, its
+// four waves a quarter of K each (their integer sums add up in LDS in any order to the same
+// value).  Both operands come straight from memory, four K steps of 64 bytes in flight.
+// ---------------------------------------------------------------------------
+static constexpr int kSplitWaves = 4;
+
+template <int DT, int T>
+__global__ void __launch_bounds__(64 * kSplitWaves) split_i8_kernel(MatmulI8 p) {
+  constexpr int E = 16 * T, U = T == 4 ? 2 : 4;
+  __shared__ int sums[E][E + 1];  // [a row][w row]
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), K = (int)p.k;
+  const int64_t n0 = (int64_t)blockIdx.x * E, m0 = (int64_t)blockIdx.y * E;
+  const int steps = (K + 63) / 64;
+  const int c0 = steps * wv / kSplitWaves, c1 = steps * (wv + 1) / kSplitWaves;
+  const int8_t *wr[T], *ar[T];
+#pragma unroll
+  for (int t = 0; t < T; t++) {
+    wr[t] = p.w + min(n0 + 16 * t + (lane & 15), p.n - 1) * p.w_stride;
+    ar[t] = p.a + min(m0 + 16 * t + (lane & 15), p.m - 1) * p.a_stride;
+  }
+  for (int i = threadIdx.x; i < E * (E + 1); i += 64 * kSplitWaves) ((int*)sums)[i] = 0;
+  i32x4 acc[T][T];
+#pragma unroll
+  for (int t = 0; t < T; t++)
+#pragma unroll
+    for (int j = 0; j < T; j++) acc[t][j] = i32x4{0, 0, 0, 0};
+  for (int c = c0; c < c1; c += U) {
+    i32x4 w[U][T], a[U][T];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int off = min(64 * min(c + u, c1 - 1) + 16 * (lane >> 4), K - 16);
+#pragma unroll
+      for (int t = 0; t < T; t++) {
+        w[u][t] = *(const i32x4u*)(wr[t] + off);
+        a[u][t] = *(const i32x4u*)(ar[t] + off);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      if (c + u >= c1) break;  // uniform
+      if (64 * (c + u) + 64 > K) {  // the row's end: bytes of the slot before and past the row count nothing
+        const int j = 4 * (c + u) + (lane >> 4);
+#pragma unroll
+        for (int t = 0; t < T; t++) a[u][t] = image_slot(ar[t], j, K);
+      }
+#pragma unroll
+      for (int t = 0; t < T; t++)
+#pragma unroll
+        for (int j = 0; j < T; j++)
+          acc[t][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][t], a[u][j], acc[t][j], 0, 0, 0);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < T; t++)
+#pragma unroll
+    for (int j = 0; j < T; j++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) atomicAdd(&sums[16 * j + (lane & 15)][16 * t + 4 * (lane >> 4) + i], acc[t][j][i]);
+  __syncthreads();
+  for (int i = threadIdx.x; i < E * E; i += 64 * kSplitWaves) {
+    const int64_t m = m0 + i / E, n = n0 + i % E;
+    if (m < p.m && n < p.n)
+      store_out<DT>(p.out, m * p.out_stride + n,
+                    (float)sums[i / E][i % E] * p.a_scale[m * p.a_scale_stride] * p.w_scale[n * p.w_scale_stride]);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Dispatch
 // ---------------------------------------------------------------------------
-enum { I8_SIMPLE, I8_STREAM, I8_WIDE, I8_TILE };
+enum { I8_SIMPLE, I8_SPLIT, I8_STREAM, I8_WIDE, I8_TILE };
 struct I8Plan {
   int kind, nt, steps;  // steps of 256 (wide, tile: an even number)
   int64_t passes;
@@ -526,6 +595,11 @@ static I8Plan i8_plan(int64_t m, int64_t n, int64_t k) {
   p.steps = (int)cdiv(k, 256);
   if (k < 16) {
     p.kind = I8_SIMPLE;
+  } else if (cdiv(n, 64) * cdiv(m, 64) <= (m <= 16 ? 128 : 512)) {
+    // Few tiles of 64 x 64.  Measured, split against the others (us): 512 tiles m = 128,
+    // n = 16,384, k = 5,120 45.9 / 52.4, k = 256 10.9 / 13.5; 1,024 tiles m = 256, k = 5,120
+    // 85 / 71.  m = 16: 64 tiles, k = 1,024 4.5 / 6.2, 256 tiles 7.9 / 6.6.
+    p.kind = I8_SPLIT;
   } else if (m <= 16 && (size_t)p.steps * 4096 <= kMaxLds) {
     p.kind = I8_STREAM;
   } else {
@@ -565,12 +639,19 @@ static hipError_t launch_wide_i8(const MatmulI8& p, const I8Plan& pl, const void
 template <int DT>
 static hipError_t launch_matmul_dt(const MatmulI8& p, void* ws, hipStream_t stream) {
   const I8Plan pl = i8_plan(p.m, p.n, p.k);
-  // the block kernels' row offsets are 32-bit (256 rows and K of at most 2^16 bytes)
-  const bool far = (pl.kind == I8_WIDE || pl.kind == I8_TILE) && p.w_stride > (1 << 22);
-  if (pl.kind == I8_SIMPLE || far) {
+  if (pl.kind == I8_SIMPLE) {
     hipLaunchKernelGGL((matmul_i8_kernel<DT>), dim3((unsigned)cdiv(p.n, 64), (unsigned)cdiv(p.m, 16)), dim3(256), 0,
                        stream, p.a, p.a_stride, p.a_scale, p.a_scale_stride, p.w, p.w_stride, p.w_scale,
                        p.w_scale_stride, p.m, p.n, (int)p.k, p.out, p.out_stride);
+    return hipGetLastError();
+  }
+  // the block kernels' row offsets are 32-bit (256 rows and K of at most 2^16 bytes)
+  const bool far = (pl.kind == I8_WIDE || pl.kind == I8_TILE) && p.w_stride > (1 << 22);
+  if (pl.kind == I8_SPLIT || far) {
+    const bool small = cdiv(p.n, 64) * cdiv(p.m, 64) < kTargetBlocks;
+    const int e = small ? 32 : 64;
+    hipLaunchKernelGGL((small ? split_i8_kernel<DT, 2> : split_i8_kernel<DT, 4>),
+                       dim3((unsigned)cdiv(p.n, e), (unsigned)cdiv(p.m, e)), dim3(64 * kSplitWaves), 0, stream, p);
     return hipGetLastError();
   }
   if (pl.kind == I8_STREAM) {
@@ -600,9 +681,20 @@ static hipError_t launch_matmul_dt(const MatmulI8& p, void* ws, hipStream_t stre
 }
 
 hipError_t launch_matmul_i8(const MatmulI8& p, void* ws, hipStream_t stream) {
-  if (p.out_dtype == DT_F32) return launch_matmul_dt<DT_F32>(p, ws, stream);
-  if (p.out_dtype == DT_BF16) return launch_matmul_dt<DT_BF16>(p, ws, stream);
-  return launch_matmul_dt<DT_F16>(p, ws, stream);
+  // grids stay below 2^32 threads
+  constexpr int64_t kMost = (int64_t)1 << 28;
+  for (int64_t n0 = 0; n0 < p.n; n0 += kMost) {
+    MatmulI8 q = p;
+    q.n = std::min(kMost, p.n - n0);
+    q.w += n0 * p.w_stride;
+    q.w_scale += n0 * p.w_scale_stride;
+    q.out = (uint8_t*)p.out + n0 * (p.out_dtype == DT_F32 ? 4 : 2);
+    const hipError_t e = p.out_dtype == DT_F32    ? launch_matmul_dt<DT_F32>(q, ws, stream)
+                         : p.out_dtype == DT_BF16 ? launch_matmul_dt<DT_BF16>(q, ws, stream)
+                                                  : launch_matmul_dt<DT_F16>(q, ws, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace etg
