@@ -334,7 +334,7 @@ struct I8Block {
   // store: a load after it would wait for it.
   static constexpr int ROWS = WAVES * MT * 16;  // w rows of the workgroup
   template <int DT>
-  static constexpr int JT = DT == DT_F32 ? (NT < 4 ? NT : 4) : (NT < 8 ? NT : 8);
+  static constexpr int JT = DT == DT_F32 ? (NT < 4 ? NT : NT == 6 ? 3 : 4) : (NT < 8 ? NT : 8);
   template <int DT>
   static constexpr int PITCH = ROWS * (DT == DT_F32 ? 4 : 2) + 16;  // bytes of an LDS row
   template <int DT>
@@ -604,7 +604,7 @@ static I8Plan i8_plan(int64_t m, int64_t n, int64_t k) {
     p.kind = I8_STREAM;
   } else {
     p.kind = m <= 128 ? I8_WIDE : I8_TILE;
-    p.nt = m <= 32 ? 2 : m <= 64 ? 4 : m <= 128 ? 8 : kTileNT;
+    p.nt = m <= 32 ? 2 : m <= 64 ? 4 : m <= 96 ? 6 : m <= 128 ? 8 : kTileNT;
     p.steps = (p.steps + 1) / 2 * 2;
     p.passes = cdiv(m, 16 * p.nt);
     p.img_bytes = (size_t)p.passes * p.nt * p.steps * 4096;
@@ -677,6 +677,7 @@ static hipError_t launch_matmul_dt(const MatmulI8& p, void* ws, hipStream_t stre
   }
   if (pl.nt == 2) return launch_wide_i8<DT, 2, 1, 16, 4>(p, pl, ws, stream);
   if (pl.nt == 4) return launch_wide_i8<DT, 4, 1, 16, 4>(p, pl, ws, stream);
+  if (pl.nt == 6) return launch_wide_i8<DT, 6, 1, 16, 4>(p, pl, ws, stream);
   return launch_wide_i8<DT, 8, 2, 8, 2>(p, pl, ws, stream);
 }
 

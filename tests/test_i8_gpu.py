@@ -164,6 +164,34 @@ def test_product_bit_exact(M, N, K, dtype):
     _check_product(out, a, sa, w, sw)
 
 
+# outputs of more tiles than the small products' kernel takes: streaming (up to 16 rows), passes
+# of up to 128 rows, tiles of 256 rows; K of one step and of several, odd and even
+LARGE = [(1, 40001, 77), (7, 33000, 1040), (16, 20003, 513), (17, 33000, 127), (33, 32900, 300), (40, 33001, 272),
+         (64, 33001, 1001), (65, 17003, 896), (77, 20011, 1001), (96, 17000, 16), (100, 20011, 16), (128, 16500, 513),
+         (129, 12001, 333), (256, 9001, 256), (300, 8200, 1040), (513, 5003, 192), (1024, 2200, 640)]
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+def test_large_product_bit_exact(M, N, K, dtype):
+    test_product_bit_exact(M, N, K, dtype)
+
+
+def test_product_rows_far_apart():
+    # more than 2^22 bytes between the rows of w, past the 32-bit offsets of the block kernels
+    M, N, K, apart = 200, 8300, 80, (1 << 22) + 272
+    g = np.random.default_rng(12)
+    a, w = _codes(g, M, K), _codes(g, N, K)
+    sa, sw = g.random(M).astype(np.float32), g.random(N).astype(np.float32)
+    big = torch.empty((N - 1) * apart + K, dtype=torch.int8, device="cuda")
+    wv = torch.as_strided(big, (N, K), (apart, 1))
+    wv.copy_(to_dev(w))
+    note("product rows far apart")
+    out = etg.matmul_i8(to_dev(a), to_dev(sa), wv, to_dev(sw))
+    torch.cuda.synchronize()
+    _check_product(out, a, sa, w, sw)
+
+
 @pytest.mark.parametrize("M", [1, 20, 300])
 def test_product_extreme_codes_and_scales(M):
     # the largest sum, 65536 * 128 * 128 = 2^30; scales of zero, a subnormal, huge, NaN
@@ -188,7 +216,8 @@ def test_product_extreme_codes_and_scales(M):
 
 @pytest.mark.parametrize("M,N,K,pad,shift", [(1, 200, 100, 1, 0), (6, 333, 256, 16, 0), (6, 333, 256, 3, 5),
                                              (40, 150, 512, 8, 8), (70, 300, 320, 16, 0), (300, 290, 448, 4, 1),
-                                             (300, 513, 448, 16, 16)])
+                                             (300, 513, 448, 16, 16), (9, 20005, 144, 5, 3), (40, 33003, 144, 8, 8),
+                                             (80, 20001, 400, 1, 2), (300, 8301, 272, 3, 1), (300, 8301, 272, 48, 16)])
 def test_product_strides_leave_the_rest(M, N, K, pad, shift):
     g = np.random.default_rng(M + N + K)
     a, w = _codes(g, M, K), _codes(g, N, K)
@@ -213,6 +242,22 @@ def test_product_strides_leave_the_rest(M, N, K, pad, shift):
     torch.cuda.synchronize()
     _check_product(out16[:, 1:N + 1].contiguous(), a, sa, w, sw)
     assert (out16[:, 0] == -7.0).all() and (out16[:, N + 1:] == -7.0).all()
+
+
+@pytest.mark.parametrize("M", [20, 300])
+def test_output_offsets_past_32_bits(M):
+    # output rows far enough apart that the last begins past 2^32 bytes
+    N, K = 33000 if M == 20 else 8300, 64
+    g = np.random.default_rng(M)
+    a, w = _codes(g, M, K), _codes(g, N, K)
+    sa, sw = g.random(M).astype(np.float32), g.random(N).astype(np.float32)
+    apart = (1 << 32) // (2 * (M - 1)) + 8
+    big = torch.empty((M - 1) * apart + N, dtype=torch.bfloat16, device="cuda")
+    out = torch.as_strided(big, (M, N), (apart, 1))
+    note(f"output offsets past 32 bits M={M}")
+    etg.matmul_i8(to_dev(a), to_dev(sa), to_dev(w), to_dev(sw), out=out)
+    torch.cuda.synchronize()
+    _check_product(out.contiguous(), a, sa, w, sw)
 
 
 def test_product_offsets_past_32_bits():
