@@ -405,9 +405,14 @@ def _float_dtype(dtype) -> torch.dtype:
     return dtype
 
 
+# the current stream's handle without a Stream object around it (0.1 us instead of 1.9)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) \
+    or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(fn, device: torch.device, *args) -> None:
     """fn(*args, current stream of the device), with the device current; raises on an error."""
-    stream = torch.cuda.current_stream(device).cuda_stream
+    stream = _raw_stream(device.index)
     if torch.cuda.current_device() == device.index:
         status = fn(*args, stream)
     else:
