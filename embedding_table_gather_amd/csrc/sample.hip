@@ -530,18 +530,26 @@ __device__ __forceinline__ void sample_each(const SampleSource<DT>& src, F f) {
 template <int NT, int DT>
 struct SampleRange {
   const SampleSource<DT>& src;
+  const SampleWeight& w;
   uint64_t* list;  // key << 32 | id, in no order
+  uint64_t* mass;  // of the list's tokens
   uint32_t* size;
   int n = -1;      // entries of the list; -1: the row
-  __device__ __forceinline__ SampleRange(const SampleSource<DT>& s_, uint64_t* l_, uint32_t* n_)
-      : src(s_), list(l_), size(n_) {}
+  __device__ __forceinline__ SampleRange(const SampleSource<DT>& s_, const SampleWeight& w_, uint64_t* l_, uint64_t* m_,
+                                         uint32_t* n_)
+      : src(s_), w(w_), list(l_), mass(m_), size(n_) {}
+  // f(key, id, mass()) for its tokens
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     if (n >= 0) {
-      for (int i = threadIdx.x; i < n; i += NT) f((uint32_t)(list[i] >> 32), (uint32_t)list[i]);
+      for (int i = threadIdx.x; i < n; i += NT) f((uint32_t)(list[i] >> 32), (uint32_t)list[i], [&] { return mass[i]; });
     } else {
-      sample_each<NT>(src, f);
+      sample_each<NT>(src, [&](uint32_t key, uint32_t id) { f(key, id, [&] { return w.fixed(ord_score(key)); }); });
     }
+  }
+  // after the list was filled: weighs it (each thread the entries that it visits)
+  __device__ __forceinline__ void weigh() {
+    for (int i = threadIdx.x; i < n; i += NT) mass[i] = w.fixed(ord_score((uint32_t)(list[i] >> 32)));
   }
   // lists the row's candidates with keys in [klo, khi] if they fit
   __device__ __forceinline__ void gather(uint32_t klo, uint32_t khi) {
@@ -555,6 +563,7 @@ struct SampleRange {
     });
     __syncthreads();
     n = *size <= kHeavyList ? (int)*size : -1;
+    weigh();
     __syncthreads();
   }
 };
@@ -577,11 +586,11 @@ __device__ __forceinline__ uint64_t sample_find(SampleRange<kSampleThreads, DT>&
     h.count[tid] = 0;
     h.mass[tid] = 0;
     __syncthreads();
-    range.each([&](uint32_t key, uint32_t id) {
+    range.each([&](uint32_t key, uint32_t id, auto mass_of) {
       if (key >= klo && key <= khi && old.keeps(key, id)) {
         const int b = (int)((key - klo) >> sh);
         atomicAdd(&h.count[b], 1u);
-        atomicAdd((unsigned long long*)&h.mass[b], (unsigned long long)w.fixed(ord_score(key)));
+        atomicAdd((unsigned long long*)&h.mass[b], (unsigned long long)mass_of());
       }
     });
     __syncthreads();
@@ -608,7 +617,7 @@ __device__ __forceinline__ uint64_t sample_find(SampleRange<kSampleThreads, DT>&
     const int sh = max(0, 22 - __clz((int)(ihi - ilo)));
     h.count[tid] = 0;
     __syncthreads();
-    range.each([&](uint32_t key, uint32_t id) {
+    range.each([&](uint32_t key, uint32_t id, auto) {
       if (key == klo && id >= ilo && id <= ihi && old.keeps(key, id)) atomicAdd(&h.count[(id - ilo) >> sh], 1u);
     });
     __syncthreads();
@@ -1107,7 +1116,8 @@ __global__ void __launch_bounds__(kSampleThreads, 4) sample_bin_kernel(Sample s,
 template <int DT>
 __global__ void __launch_bounds__(kSampleThreads) sample_gather_kernel(Sample s, SamplePtrs ws) {
   constexpr int N = SampleSource<DT>::N, U = kSlice / (kSampleThreads * N);
-  const int tid = threadIdx.x, lane = tid & 63, count = (int)min(*ws.nheavy, (uint32_t)ws.slots);
+  __shared__ SampleScratch<kSampleWaves> sc;
+  const int tid = threadIdx.x, count = (int)min(*ws.nheavy, (uint32_t)ws.slots);
   for (int slot = blockIdx.y; slot < count; slot += gridDim.y) {
     const int64_t row = ws.heavy[slot];
     const int b = ws.hstate[slot].listed ? ws.hstate[slot].bin : -1;
@@ -1121,16 +1131,13 @@ __global__ void __launch_bounds__(kSampleThreads) sample_gather_kernel(Sample s,
     for (int u = 0; u < U; u++)
 #pragma unroll
       for (int j = 0; j < N; j++) n += l[u][j] > -__builtin_inff() && sample_bin(l[u][j], top) == b;
-    // places by wave: the order of the list does not matter
-    uint32_t upto = n;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const uint32_t o = __shfl_up(upto, off, 64);
-      if (lane >= off) upto += o;
-    }
-    uint32_t place = 0;
-    if (lane == 63 && upto != 0) place = atomicAdd(&ws.hlisted[slot], upto);
-    place = __builtin_amdgcn_readlane(place, 63) + upto - n;
+    // the order of the list does not matter: one addition per workgroup places its tokens
+    uint64_t all, base = 0, unused;
+    const uint64_t upto = block_scan((uint64_t)n, &all, sc);
+    if (all == 0) continue;  // whole workgroup
+    if (tid == 0) base = atomicAdd(&ws.hlisted[slot], (uint32_t)all);
+    block_first(tid == 0, base, 0, &base, &unused, sc);
+    uint32_t place = (uint32_t)(base + upto - n);
     uint64_t* list = ws.hlist + (size_t)slot * kHeavyList;
 #pragma unroll
     for (int u = 0; u < U; u++)
@@ -1146,6 +1153,7 @@ struct SampleHeavyShared {
   SampleScratch<kSampleWaves> sc;
   SampleHist h;
   uint64_t list[kHeavyList];
+  uint64_t mass[kHeavyList];
   uint64_t slice[kMaxSlices];
   uint32_t n;
 };
@@ -1167,7 +1175,7 @@ __device__ __forceinline__ void sample_heavy_row(const Sample& s, const SamplePt
   const SampleState st = hist ? ws.hstate[slot] : SampleState{};
 
   // the tokens of one bin
-  SampleRange<kSampleThreads, DT> range(src, sh.list, &sh.n);
+  SampleRange<kSampleThreads, DT> range(src, w, sh.list, sh.mass, &sh.n);
   int listed = -1;
   uint32_t klo = 1, khi = top_key;
   auto bin_open = [&](int b) {
@@ -1178,6 +1186,7 @@ __device__ __forceinline__ void sample_heavy_row(const Sample& s, const SamplePt
     if (b == st.bin && st.listed) {  // the gather kernel has listed them
       range.n = (int)ws.hlisted[slot];
       for (int i = tid; i < range.n; i += kSampleThreads) sh.list[i] = ws.hlist[(size_t)slot * kHeavyList + i];
+      range.weigh();
       __syncthreads();
     } else {
       range.gather(klo, khi);
@@ -1239,9 +1248,9 @@ __device__ __forceinline__ void sample_heavy_row(const Sample& s, const SamplePt
       z = wave_scan_u64(z);
       if (lane == 63) atomicAdd((unsigned long long*)&sh.slice[i], (unsigned long long)z);
     }
-    range.each([&](uint32_t key, uint32_t id) {
+    range.each([&](uint32_t key, uint32_t id, auto mass_of) {
       if (key >= klo && key <= khi && cut.keeps(key, id))
-        atomicAdd((unsigned long long*)&sh.slice[id / kSlice], (unsigned long long)w.fixed(ord_score(key)));
+        atomicAdd((unsigned long long*)&sh.slice[id / kSlice], (unsigned long long)mass_of());
     });
     __syncthreads();
     const uint64_t z = tid < ws.slices ? sh.slice[tid] : 0;
