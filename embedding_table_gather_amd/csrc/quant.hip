@@ -13,12 +13,15 @@ namespace etg {
 // that holds a NaN or an infinity has scale NaN and codes 0 (whatever is computed
 // from it is then NaN instead of silently wrong).
 //
-// A row is read once, by WPR waves with up to R 16-byte loads per lane at any alignment,
-// and stays in registers until its maximum is known.  Bound by the bytes.  A division
+// A row of up to 2,048 loads of 16 bytes, at any alignment, is read once and stays in
+// registers until its maximum is known; a longer one is read again for its codes, from the
+// caches as a rule.  Bound by the bytes, which needs the arithmetic to be short: a division
 // costs about ten operations, so codes come from x * (1 / scale) instead, added to
 // 1.5 * 2^23, which leaves the rounded integer in the low byte.  x * (1 / scale) is
 // within 127 * 2^-22 of the quotient: where it is that near to a half step (0.02% of the
-// values) the vector is divided out.
+// values) the vector is divided out.  262,144 rows x 5,376 of bf16 take 745 us, 5.7 TB/s of
+// reads and writes (dividing every value 2,758 us, with loads that waited for each other); 64
+// rows of 1,024 take 2.7 us.
 typedef u32x4 u32x4u __attribute__((aligned(1)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2u __attribute__((aligned(1)));
@@ -47,7 +50,9 @@ struct QuantVec {
   }
 };
 
-template <int DT, int WPR, int R>
+// WPR waves per row with R loads per lane; LONG: rows of any length by pieces of that size,
+// read for the maximum and again for the codes.
+template <int DT, int WPR, int R, bool LONG>
 __global__ void __launch_bounds__(WPR == 16 ? 1024 : 256) quantize_i8_kernel(
     const uint8_t* __restrict__ x, int64_t rows, int64_t x_stride, int cols, int8_t* __restrict__ codes,
     int64_t code_stride, float* __restrict__ scale, int64_t scale_stride) {
@@ -59,24 +64,30 @@ __global__ void __launch_bounds__(WPR == 16 ? 1024 : 256) quantize_i8_kernel(
        row += (int64_t)gridDim.x * RPB) {
     const uint8_t* src = x + row * x_stride;
     u32x4 w[R];
-    uint32_t m = 0;
+    auto load = [&](int from) {
 #pragma unroll
-    for (int r = 0; r < R; r++) {
-      const int c = (r * T + t) * N;
-      w[r] = u32x4{0, 0, 0, 0};
-      if (c + N <= cols) {
-        w[r] = __builtin_nontemporal_load((const u32x4u*)(src + (int64_t)c * Q::SIZE));
-      } else if (c < cols) {
+      for (int r = 0; r < R; r++) {
+        const int c = from + (r * T + t) * N;
+        w[r] = u32x4{0, 0, 0, 0};
+        if (c + N <= cols) {
+          const u32x4u* at = (const u32x4u*)(src + (int64_t)c * Q::SIZE);
+          w[r] = LONG ? *at : __builtin_nontemporal_load(at);
+        } else if (c < cols) {
 #pragma unroll
-        for (int j = 0; j < N; j++)
-          if (c + j < cols) {
-            if constexpr (DT == DT_F32) w[r][j] = ((const uint32_t*)src)[c + j];
-            else w[r][j >> 1] |= (uint32_t)((const uint16_t*)src)[c + j] << (16 * (j & 1));
-          }
+          for (int j = 0; j < N; j++)
+            if (c + j < cols) {
+              if constexpr (DT == DT_F32) w[r][j] = ((const uint32_t*)src)[c + j];
+              else w[r][j >> 1] |= (uint32_t)((const uint16_t*)src)[c + j] << (16 * (j & 1));
+            }
+        }
       }
-    }
+    };
+    uint32_t m = 0;
+    for (int from = 0; from < (LONG ? cols : 1); from += R * T * N) {
+      load(from);
 #pragma unroll
-    for (int r = 0; r < R; r++) m = Q::top(w[r], m);
+      for (int r = 0; r < R; r++) m = Q::top(w[r], m);
+    }
     m = wave_minmax_u32<true>(m);
     if constexpr (WPR > 1) {
       __syncthreads();
@@ -92,38 +103,42 @@ __global__ void __launch_bounds__(WPR == 16 ? 1024 : 256) quantize_i8_kernel(
     const float inv = some ? 1.0f / sc : 0.f;
     const bool rough = some && sc < 1.17549435e-38f;  // a subnormal scale: its reciprocal may be infinite
     int8_t* dst = codes + row * code_stride;
+    for (int from = 0; from < (LONG ? cols : 1); from += R * T * N) {
+      if constexpr (LONG) load(from);
 #pragma unroll
-    for (int r = 0; r < R; r++) {
-      const int c = (r * T + t) * N;
-      if (c >= cols) continue;
-      float q[N];
-      float far = 0.f;
+      for (int r = 0; r < R; r++) {
+        const int c = from + (r * T + t) * N;
+        if (c >= cols) continue;
+        float q[N];
+        float far = 0.f;
 #pragma unroll
-      for (int j = 0; j < N; j++) {
-        const float v = some ? Q::value(w[r], j) : 0.f;
-        q[j] = fmaf(v, inv, 12582912.f);
-        far = fmaxf(far, fabsf(fmaf(v, inv, 12582912.f - q[j])));
-      }
-      if (far > 0.4999f || rough) {
+        for (int j = 0; j < N; j++) {
+          const float v = some ? Q::value(w[r], j) : 0.f;
+          q[j] = fmaf(v, inv, 12582912.f);
+          far = fmaxf(far, fabsf(fmaf(v, inv, 12582912.f - q[j])));
+        }
+        if (far > 0.4999f || rough) {
 #pragma unroll
-        for (int j = 0; j < N; j++)
-          q[j] = 12582912.f + fminf(fmaxf(rintf(Q::value(w[r], j) / sc), -127.f), 127.f);
-      }
-      uint32_t out[N / 4];
+          for (int j = 0; j < N; j++)
+            q[j] = 12582912.f + fminf(fmaxf(rintf(Q::value(w[r], j) / sc), -127.f), 127.f);
+        }
+        uint32_t out[N / 4];
 #pragma unroll
-      for (int j = 0; j < N / 4; j++) {
-        // the low bytes of four words
-        const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(q[4 * j + 1]), __float_as_uint(q[4 * j]), 0x0c0c0400u);
-        const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(q[4 * j + 3]), __float_as_uint(q[4 * j + 2]), 0x04000c0cu);
-        out[j] = lo | hi;
-      }
-      if (c + N <= cols) {
-        if constexpr (N == 4) *(u32u*)(dst + c) = out[0];
-        else *(u32x2u*)(dst + c) = u32x2{out[0], out[N / 4 - 1]};
-      } else {
+        for (int j = 0; j < N / 4; j++) {
+          // the low bytes of four words
+          const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(q[4 * j + 1]), __float_as_uint(q[4 * j]), 0x0c0c0400u);
+          const uint32_t hi =
+              __builtin_amdgcn_perm(__float_as_uint(q[4 * j + 3]), __float_as_uint(q[4 * j + 2]), 0x04000c0cu);
+          out[j] = lo | hi;
+        }
+        if (c + N <= cols) {
+          if constexpr (N == 4) *(u32u*)(dst + c) = out[0];
+          else *(u32x2u*)(dst + c) = u32x2{out[0], out[N / 4 - 1]};
+        } else {
 #pragma unroll
-        for (int j = 0; j < N; j++)
-          if (c + j < cols) dst[c + j] = (int8_t)(out[j >> 2] >> (8 * (j & 3)));
+          for (int j = 0; j < N; j++)
+            if (c + j < cols) dst[c + j] = (int8_t)(out[j >> 2] >> (8 * (j & 3)));
+        }
       }
     }
   }
@@ -133,23 +148,24 @@ __global__ void __launch_bounds__(WPR == 16 ? 1024 : 256) quantize_i8_kernel(
 hipError_t launch_quantize_i8(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t x_stride,
                               int8_t* codes, int64_t code_stride, float* scale, int64_t scale_stride,
                               hipStream_t stream) {
-#define ETG_QUANT(DT, WPR, R)                                                                                      \
-  hipLaunchKernelGGL((quantize_i8_kernel<DT, WPR, R>),                                                             \
+#define ETG_QUANT(DT, WPR, R, LONG)                                                                                \
+  hipLaunchKernelGGL((quantize_i8_kernel<DT, WPR, R, LONG>),                                                       \
                      dim3((unsigned)std::min<int64_t>(cdiv(rows, WPR == 1 ? 4 : 1), 1 << 20)),                     \
                      dim3(WPR == 16 ? 1024 : 256), 0, stream, (const uint8_t*)x, rows, x_stride, (int)cols, codes, \
                      code_stride, scale, scale_stride)
-  // A wave per row up to 128 loads; for many rows four waves (they keep every CU busy), for
-  // few rows or long ones sixteen (the fewest loads per lane).
-#define ETG_QUANT_DT(DT)                                                          \
-  {                                                                               \
-    const int64_t loads = cdiv(cols, QuantVec<DT>::N);                            \
-    if (loads <= 128 && rows >= 64) ETG_QUANT(DT, 1, 2);                          \
-    else if (rows >= 1024 && loads <= 512) ETG_QUANT(DT, 4, 2);                   \
-    else if (rows >= 1024 && loads <= 1024) ETG_QUANT(DT, 4, 4);                  \
-    else if (rows >= 1024 && loads <= 2048) ETG_QUANT(DT, 4, 8);                  \
-    else if (loads <= 1024) ETG_QUANT(DT, 16, 1);                                 \
-    else if (loads <= 4096) ETG_QUANT(DT, 16, 4);                                 \
-    else ETG_QUANT(DT, 16, 16);                                                   \
+  // Measured (us, bf16): a wave per row against four, 262,144 x 1,024 153 / 295, 64 x 1,024
+  // 3.0 / 2.7.  Four waves with 2, 4 or 8 loads per lane, as few as hold the row: 262,144 x
+  // 4,096 562 / 671 / 922.  Sixteen waves and pieces against four waves with 8 loads:
+  // 65,536 x 16,384 686 / 568; of rows of 65,536, pieces of sixteen against four waves, 1 row
+  // 10.4 / 18.0, 16,384 rows 739 / 872.
+#define ETG_QUANT_DT(DT)                                                 \
+  {                                                                      \
+    const int64_t loads = cdiv(cols, QuantVec<DT>::N);                   \
+    if (loads <= 128 && rows >= 512) ETG_QUANT(DT, 1, 2, false);         \
+    else if (loads <= 512) ETG_QUANT(DT, 4, 2, false);                   \
+    else if (loads <= 1024) ETG_QUANT(DT, 4, 4, false);                  \
+    else if (loads <= 2048) ETG_QUANT(DT, 4, 8, false);                  \
+    else ETG_QUANT(DT, 16, 2, true);                                     \
   }
   if (dtype == DT_F32) ETG_QUANT_DT(DT_F32)
   else if (dtype == DT_BF16) ETG_QUANT_DT(DT_BF16)

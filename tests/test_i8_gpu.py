@@ -107,6 +107,22 @@ def test_quantize_strides_leave_the_rest(dtype, cols, x_pad, q_pad, offset):
     assert (rest == 55).all() and (q[:offset] == 55).all() and (sbuf[:, 0] == -1).all() and (sbuf[:, 2] == -1).all()
 
 
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("rows,cols", [(3, 8191), (2, 16385), (1500, 16400), (3, 20001), (2, 65535)])
+def test_quantize_long_rows(dtype, rows, cols):
+    # rows past what stays in registers, the largest value and NaNs in any piece
+    x = np.random.default_rng(cols).standard_normal((rows, cols)).astype(np.float32)
+    x[0, cols - 1] = 40.0
+    x[1, 1] = -40.0
+    if rows > 2:
+        x[2, cols - 2] = np.nan
+    note(f"quantize long rows {dtype} {rows} x {cols}")
+    d = torch.from_numpy(x).to(DTYPES[dtype]).cuda()
+    codes, scale = etg.quantize_i8(d)
+    torch.cuda.synchronize()
+    _check_quantized(codes, scale, d)
+
+
 def test_quantize_is_the_wire_encoding():
     V, d, n = 500, 896, 33
     host = synth.make_table(synth.BF16, V, d, seed=9)
