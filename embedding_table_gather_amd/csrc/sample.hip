@@ -77,7 +77,7 @@ static constexpr int kMaxSlices = (1 << 20) / kSlice;
 static constexpr int kList = 2048;               // tokens sorted in LDS by the row kernel
 static constexpr int kHeavyList = 8192;          // tokens of one bin in the heavy kernel
 static constexpr int kMaxGroups = 4096;          // groups per row
-static constexpr size_t kHeavyBytes = 128 << 20;  // most workspace for heavy rows (one slot each)
+static constexpr size_t kHeavyBytes = 256 << 20;  // most workspace for heavy rows (one slot each)
 
 // Where the first cut of a heavy row lies.
 struct SampleState {

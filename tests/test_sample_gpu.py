@@ -207,15 +207,15 @@ def test_logits_of_any_scale(spread):
 
 
 def test_more_flat_rows_than_histograms():
-    # 1,800 rows that keep nearly all of their 2,100 tokens: more than the workspace has
+    # 3,600 rows that keep nearly all of their 2,100 tokens: more than the workspace has
     # histograms for, the rest go by passes over their logits
-    rows, V = 1800, 2100
+    rows, V = 3600, 2100
     logits, u = _logits(rows, V, "bf16", seed=6, spread=0.05)
     g = np.random.default_rng(6)
 
     def pick(vals, t):
         return torch.tensor(g.choice(vals, rows).tolist(), dtype=t, device="cuda")
-    note("sample 1,800 flat rows")
+    note("sample 3,600 flat rows")
     _check(logits, u, temperature=pick([0.5, 1.0], torch.float32), top_k=pick([0, 0, 2090], torch.int32),
            top_p=pick([1.0, 0.995, 0.999], torch.float32), min_p=pick([0.0, 0.01], torch.float32))
 
