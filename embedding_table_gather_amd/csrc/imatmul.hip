@@ -39,6 +39,8 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float x) {
   }
 }
 
+// K below 16, where a row has no whole 16-byte load: bound by the loads of single bytes and by
+// the stores (K = 8, 262,144 w rows: 1 row 10 us, 256 rows 197 us).
 // One wave per tile of 16 w rows x 16 a rows (v_mfma_i32_16x16x64_i8, the w rows as
 // the A operand: lane l holds bytes 16 (l / 16) .. + 15 of row l % 16, and result
 // register i is w row 4 (l / 16) + i of a row l % 16).  Rows past the end are read
@@ -83,10 +85,10 @@ __global__ void __launch_bounds__(256) matmul_i8_kernel(
 // w rows go straight from memory to registers, in four loads per 16 rows and step: lane l of
 // load q reads slot 4 (l / 16) + l % 4 of row 4 (l / 4 % 4) + q, so the four lanes of a quad
 // read 64 contiguous bytes and an instruction four rows of 256.  (With lane l at row l % 16
-// every lane of a quad is in another line, and the address unit takes four times as long: it
-// was what bound the kernels, at 16 bytes a clock per CU.)  A 4 x 4 transposition over the
-// quad's lanes and the four loads, two DPP selects per register, then leaves row l % 16 and
-// slot 4 (l / 16) + i in register set i.
+// every lane of a quad is in another line: 77 x 50,001 x 1,001 took 40 us against 30.)  A 4 x 4
+// transposition over the quad's lanes and the four loads, two DPP selects per register, then
+// leaves row l % 16 and slot 4 (l / 16) + i in register set i.  Rows at odd addresses cost a
+// third more than aligned ones (K = 1,001 against 1,024), as their lines are read twice.
 // ---------------------------------------------------------------------------
 typedef i32x4 i32x4u __attribute__((aligned(1)));
 typedef u32x4 u32x4u __attribute__((aligned(1)));
@@ -174,7 +176,8 @@ __device__ __forceinline__ void store_tile4(void* out, int64_t out_stride, int64
 // Up to 16 a rows, bound by reading w once: the whole image in LDS, a persistent grid, each
 // wave a contiguous run of tiles of 16 w rows.  Two steps (8 KiB a wave) are always in
 // flight, in two register sets used in turn, across tiles too; a tile's scales are loaded
-// with its steps.
+// with its steps.  262,144 w rows x 5,376, 1 row: 217 us, 6.5 TB/s, where a plain read stream
+// reaches 6.8 (a tile at a time, without the second set: 274 us per call against 221).
 // ---------------------------------------------------------------------------
 template <int DT>
 __global__ void __launch_bounds__(1024) stream_i8_kernel(MatmulI8 p, int64_t ntiles, int steps) {
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(1024) stream_i8_kernel(MatmulI8 p, int64_t nti
   }
 }
 
-// Image of all a rows for the kernels below: [pass][step][i][tile of the pass][64 lanes].
+// Image of all a rows for the kernels below (5 us): [pass][step][i][tile of the pass][64 lanes].
 __global__ void __launch_bounds__(256) i8_image_kernel(MatmulI8 p, int nt, int steps, i32x4* __restrict__ img,
                                                        uint32_t total) {
   const uint32_t x = blockIdx.x * 256 + threadIdx.x;
@@ -393,7 +396,10 @@ struct I8Block {
 // Passes of up to 16 NT a rows, bound by reading w: WAVES x MT tiles of 16 w rows per
 // workgroup.  The image passes through three LDS buffers of one step each, copied by
 // global_load_lds two steps ahead; the w rows are loaded up to two steps ahead into two
-// register sets used in turn.  One barrier per step.
+// register sets used in turn.  One barrier per step.  262,144 w rows x 5,376, 64 rows to f32:
+// 233 us, 6.3 TB/s of w rows and outputs.  The least NT that holds the rows, as the image's
+// copies and reads grow with it (K = 16,384, 48 rows 700 us, 128 rows 784); at 128 rows two
+// tiles of w rows per wave share an image fragment, which halves the reads from LDS.
 // ---------------------------------------------------------------------------
 template <int DT, int NT, int MT, int WAVES, int MINW>
 __global__ void __launch_bounds__(64 * WAVES, MINW) wide_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
@@ -445,7 +451,11 @@ __global__ void __launch_bounds__(64 * WAVES, MINW) wide_i8_kernel(MatmulI8 p, c
 // the full MFMA rate.  The image passes through two LDS buffers of one step, each refilled
 // one step ahead.  The next step's copies and w loads are issued one at a time between the
 // MFMAs of this one (32 in a row would hold up the wave, whose MFMAs wait behind them), and its
-// w rows are transposed there too.
+// w rows are transposed there too.  1,024 x 262,144 x 5,120 to bf16: 1,300 us, 2.1 POP/s (the
+// copies in a row before the MFMAs: 1,454).  The MFMAs alone run 777 us; the L2 reads of the
+// image and the w rows by 256 x 256 tiles, and the stores at the end of a tile, with one
+// workgroup per CU and nothing else to run meanwhile, are the rest.  Past 128 rows: 160 rows
+// of it 388 us, two passes of the kernel above 2 x 253.
 // ---------------------------------------------------------------------------
 static constexpr int kTileWaves = 4, kTileMT = 4, kTileNT = 16;
 
@@ -514,7 +524,9 @@ __global__ void __launch_bounds__(64 * kTileWaves, 1) tile_i8_kernel(MatmulI8 p,
 // ---------------------------------------------------------------------------
 // Small products, bound by latency: a workgroup per 16 T x 16 T tile of the output, its
 // four waves a quarter of K each (their integer sums add up in LDS in any order to the same
-// value).  Both operands come straight from memory, four K steps of 64 bytes in flight.
+// value).  Both operands come straight from memory, two or four K steps of 64 bytes in flight.
+// 256 x 1,024 x 5,120: 13 us (by passes of 256 rows 69: 4 workgroups).  Four waves: sixteen
+// took 17.6 us against 13.3 there, as their sums meet in LDS, and won at K = 16,384 (31 / 35).
 // ---------------------------------------------------------------------------
 static constexpr int kSplitWaves = 4;
 
@@ -648,6 +660,7 @@ static hipError_t launch_matmul_dt(const MatmulI8& p, void* ws, hipStream_t stre
   // the block kernels' row offsets are 32-bit (256 rows and K of at most 2^16 bytes)
   const bool far = (pl.kind == I8_WIDE || pl.kind == I8_TILE) && p.w_stride > (1 << 22);
   if (pl.kind == I8_SPLIT || far) {
+    // 32 x 32 where 64 x 64 would leave CUs without a workgroup
     const bool small = cdiv(p.n, 64) * cdiv(p.m, 64) < kTargetBlocks;
     const int e = small ? 32 : 64;
     hipLaunchKernelGGL((small ? split_i8_kernel<DT, 2> : split_i8_kernel<DT, 4>),

@@ -74,10 +74,14 @@ static constexpr int kChunk = 2048;              // tokens of a chunk (a wave's)
 static constexpr int kChunkThreads = 256;
 static constexpr int kSlice = 16384;             // tokens of a histogram slice
 static constexpr int kMaxSlices = (1 << 20) / kSlice;
-static constexpr int kList = 2048;               // tokens sorted in LDS by the row kernel
+// Tokens sorted in LDS by the row kernel.  1,024 x 151,936 bf16 rows of mixed settings: 2,048
+// 250 us, 1,024 357 (more heavy rows), 4,096 276 (one workgroup less per CU).
+static constexpr int kList = 2048;
 static constexpr int kHeavyList = 8192;          // tokens of one bin in the heavy kernel
 static constexpr int kMaxGroups = 4096;          // groups per row
-static constexpr size_t kHeavyBytes = 256 << 20;  // most workspace for heavy rows (one slot each)
+// Most workspace for heavy rows, a slot each; the rest go by passes over their logits (1,024
+// x 262,144 f32 rows, all heavy: 256 MiB 1,490 us, 128 MiB 2,358).
+static constexpr size_t kHeavyBytes = 256 << 20;
 
 // Where the first cut of a heavy row lies.
 struct SampleState {
@@ -454,7 +458,9 @@ __device__ __forceinline__ float group_max(float m, int steps) {
 
 // A wave per chunk, no workgroup synchronisation: bound by the logits' bytes (8 or 4
 // 16-byte loads in flight per lane) where no mass is needed, else by about 25 f64
-// operations per token.
+// operations per token.  64 x 262,144 f32 of mixed settings: 19 us; 1,024 x 151,936
+// bf16: 82 us, 3.8 TB/s; 1 row 4.5 us.  (Each token weighed against its chunk's maximum: the
+// row's is not known yet, and the row kernel rescales one sum per chunk.)
 template <int DT>
 __global__ void __launch_bounds__(kChunkThreads) sample_chunk_kernel(Sample s, SamplePtrs ws) {
   using Src = SampleSource<DT>;
@@ -666,8 +672,11 @@ struct SampleRowShared {
   uint32_t bin_end[kSampleBins];
 };
 
-// A row is a chain of short dependent steps: 512 threads, as more waves synchronise
-// more slowly and fewer read a long list's groups more slowly.
+// A row is a chain of short dependent steps (1 row 17 us, 64 rows 40 us, 1,024 rows 78 us):
+// bound by latency, its barriers and LDS searches.  512 threads: 1,024 synchronise more
+// slowly (one row, top-k of 50: 27.6 us per call against 23.7), 256 read a long list's
+// groups more slowly (64 rows, top-k of 1,000: 73.9 against 57.7, while the short lists of
+// 1,024 rows gain a little, 89.3 against 97.0).
 template <int DT>
 __global__ void __launch_bounds__(kRowThreads) sample_row_kernel(Sample s, SamplePtrs ws) {
   __shared__ SampleRowShared sh;
@@ -1026,6 +1035,8 @@ __device__ __forceinline__ float sample_top(const SamplePtrs& ws, int64_t row) {
   return wave_max_f32(m);
 }
 
+// A workgroup per slice of a heavy row, few of them as there are few heavy rows as a rule:
+// bound by the f64 weights and the LDS additions (64 rows of 262,144 of mixed settings 10 us).
 template <int DT>
 __global__ void __launch_bounds__(kSampleThreads, 4) sample_hist_kernel(Sample s, SamplePtrs ws) {
   constexpr int N = SampleSource<DT>::N;
@@ -1078,6 +1089,7 @@ struct SampleRowHist {
   }
 };
 
+// A workgroup per heavy row, so that many slices do not each search the histogram (10 us).
 // Where the first cut of each heavy row lies: the bin in which the first k end, else that in
 // which the nucleus ends, or that of min-p's bound if it comes first.
 __global__ void __launch_bounds__(kSampleThreads, 4) sample_bin_kernel(Sample s, SamplePtrs ws) {
@@ -1112,7 +1124,9 @@ __global__ void __launch_bounds__(kSampleThreads, 4) sample_bin_kernel(Sample s,
   }
 }
 
-// Lists the tokens of those bins.
+// Lists the tokens of those bins: one workgroup per slice (64 rows of 262,144 of mixed
+// settings 8 us; with an addition per wave to the list's size, instead of one per
+// workgroup, 14).
 template <int DT>
 __global__ void __launch_bounds__(kSampleThreads) sample_gather_kernel(Sample s, SamplePtrs ws) {
   constexpr int N = SampleSource<DT>::N, U = kSlice / (kSampleThreads * N);
@@ -1158,6 +1172,8 @@ struct SampleHeavyShared {
   uint32_t n;
 };
 
+// A workgroup per heavy row, bound by latency as the row kernel is (64 rows of 262,144 of
+// mixed settings 38 us; 4 us where there is none).
 // Heavy row `row`, with the histograms and the list of `slot`, or (slot -1) by passes over it.
 template <int DT>
 __device__ __forceinline__ void sample_heavy_row(const Sample& s, const SamplePtrs& ws, int64_t row, int slot,

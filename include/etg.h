@@ -422,7 +422,8 @@ int32_t etg_logits_topk_noalloc(const etg_table* lm_head, const float* d_residua
  *   d_scale       f32, scale_stride floats apart
  *   rows          0 <= rows <= 2^31 - 1; 0 enqueues nothing;  1 <= cols <= 65536
  * Strides are at least cols (1 for scales) and at most 2^40.  Bytes between rows are
- * left as they were.  Bit-exact to the definition.
+ * left as they were.  The outputs must not overlap the input.  Bit-exact to the
+ * definition.
  * Errors: EDTYPE, ESHAPE (sizes, strides), EINVAL (null), EALIGN.
  */
 int32_t etg_quantize_i8(const void* d_x, int32_t dtype, int64_t rows, int64_t cols, int64_t x_stride,

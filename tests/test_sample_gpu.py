@@ -325,6 +325,25 @@ def test_two_captured_loops_replay_on_two_streams():
             assert all(torch.equal(x, y) for x, y in zip(out, w))
 
 
+def test_workspaces_and_settings_past_the_c_types():
+    logits, u = _logits(2, 300, "f32", seed=3)
+    want = etg.sample(logits, u)
+    note("sample top_k 2^32 + 5")
+    ids, probs = etg.sample(logits, u, top_k=2 ** 32 + 5)  # more than any vocabulary, not 5
+    torch.cuda.synchronize()
+    assert torch.equal(ids, want[0]) and torch.equal(probs, want[1])
+    codes, scale = torch.zeros((2, 64), dtype=torch.int8, device="cuda"), torch.ones(2, device="cuda")
+    head = etg.I8Table(codes, scale)
+    for space in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, dtype=torch.float32, device="cuda"),
+                  torch.empty(1 << 20, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            etg.sample(logits, u, workspace=space)
+        with pytest.raises(ValueError, match="workspace"):
+            etg.matmul_i8(codes, scale, codes, scale, workspace=space)
+        with pytest.raises(ValueError, match="workspace"):
+            head.logits_raw(torch.ones((1, 64), device="cuda"), workspace=space)
+
+
 def test_calls_on_two_streams_at_once():
     V, d, B = 20011, 768, 16
     t = table(synth.make_table(synth.BF16, V, d, seed=51, std=0.05), synth.BF16, V, d)
