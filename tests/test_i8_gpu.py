@@ -291,7 +291,7 @@ def test_product_offsets_past_32_bits():
     out = torch.as_strided(big.view(torch.float32), (M, N), (apart // 4, 1), 512)
     note("product offsets past 32 bits")
     etg.matmul_i8(av, to_dev(sa), wv, to_dev(sw), out=out)
-    q = torch.as_strided(big, (M, N), (apart, 1), 3072)
+    q = torch.as_strided(big, (M, N), (apart, 1), 2560)
     codes, scale = etg.quantize_i8(out, codes=q)
     torch.cuda.synchronize()
     _check_product(out.contiguous(), a, sa, w, sw)
