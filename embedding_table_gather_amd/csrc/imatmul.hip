@@ -337,7 +337,7 @@ struct I8Block {
   // store: a load after it would wait for it.
   static constexpr int ROWS = WAVES * MT * 16;  // w rows of the workgroup
   template <int DT>
-  static constexpr int JT = DT == DT_F32 ? (NT < 4 ? NT : NT == 6 ? 3 : 4) : (NT < 8 ? NT : 8);
+  static constexpr int JT = DT == DT_F32 ? (NT < 4 ? NT : NT == 6 ? 3 : 4) : (NT < 8 ? NT : NT == 12 ? 6 : 8);
   template <int DT>
   static constexpr int PITCH = ROWS * (DT == DT_F32 ? 4 : 2) + 16;  // bytes of an LDS row
   template <int DT>
@@ -399,7 +399,8 @@ struct I8Block {
 // register sets used in turn.  One barrier per step.  262,144 w rows x 5,376, 64 rows to f32:
 // 233 us, 6.3 TB/s of w rows and outputs.  The least NT that holds the rows, as the image's
 // copies and reads grow with it (K = 16,384, 48 rows 700 us, 128 rows 784); at 128 rows two
-// tiles of w rows per wave share an image fragment, which halves the reads from LDS.
+// tiles of w rows per wave share an image fragment, which halves the reads from LDS.  At 192
+// rows two no longer fit the registers (spills: 683 us against 294 at 160 rows, K = 5,120).
 // ---------------------------------------------------------------------------
 template <int DT, int NT, int MT, int WAVES, int MINW>
 __global__ void __launch_bounds__(64 * WAVES, MINW) wide_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
@@ -454,8 +455,8 @@ __global__ void __launch_bounds__(64 * WAVES, MINW) wide_i8_kernel(MatmulI8 p, c
 // w rows are transposed there too.  1,024 x 262,144 x 5,120 to bf16: 1,300 us, 2.1 POP/s (the
 // copies in a row before the MFMAs: 1,454).  The MFMAs alone run 777 us; the L2 reads of the
 // image and the w rows by 256 x 256 tiles, and the stores at the end of a tile, with one
-// workgroup per CU and nothing else to run meanwhile, are the rest.  Past 128 rows: 160 rows
-// of it 388 us, two passes of the kernel above 2 x 253.
+// workgroup per CU and nothing else to run meanwhile, are the rest.  160 rows of it take 402
+// us, the kernel above 294 (K = 1,001: 113 / 124; 32,000 w rows x 5,120: 68 / 62).
 // ---------------------------------------------------------------------------
 static constexpr int kTileWaves = 4, kTileMT = 4, kTileNT = 16;
 
@@ -615,8 +616,8 @@ static I8Plan i8_plan(int64_t m, int64_t n, int64_t k) {
   } else if (m <= 16 && (size_t)p.steps * 4096 <= kMaxLds) {
     p.kind = I8_STREAM;
   } else {
-    p.kind = m <= 128 ? I8_WIDE : I8_TILE;
-    p.nt = m <= 32 ? 2 : m <= 64 ? 4 : m <= 96 ? 6 : m <= 128 ? 8 : kTileNT;
+    p.kind = m <= 192 ? I8_WIDE : I8_TILE;
+    p.nt = m <= 32 ? 2 : m <= 64 ? 4 : m <= 96 ? 6 : m <= 128 ? 8 : m <= 192 ? 12 : kTileNT;
     p.steps = (p.steps + 1) / 2 * 2;
     p.passes = cdiv(m, 16 * p.nt);
     p.img_bytes = (size_t)p.passes * p.nt * p.steps * 4096;
@@ -691,7 +692,8 @@ static hipError_t launch_matmul_dt(const MatmulI8& p, void* ws, hipStream_t stre
   if (pl.nt == 2) return launch_wide_i8<DT, 2, 1, 16, 4>(p, pl, ws, stream);
   if (pl.nt == 4) return launch_wide_i8<DT, 4, 1, 16, 4>(p, pl, ws, stream);
   if (pl.nt == 6) return launch_wide_i8<DT, 6, 1, 16, 4>(p, pl, ws, stream);
-  return launch_wide_i8<DT, 8, 2, 8, 2>(p, pl, ws, stream);
+  if (pl.nt == 8) return launch_wide_i8<DT, 8, 2, 8, 2>(p, pl, ws, stream);
+  return launch_wide_i8<DT, 12, 1, 16, 4>(p, pl, ws, stream);
 }
 
 hipError_t launch_matmul_i8(const MatmulI8& p, void* ws, hipStream_t stream) {

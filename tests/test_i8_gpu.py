@@ -181,10 +181,10 @@ def test_product_bit_exact(M, N, K, dtype):
 
 
 # outputs of more tiles than the small products' kernel takes: streaming (up to 16 rows), passes
-# of up to 128 rows, tiles of 256 rows; K of one step and of several, odd and even
+# of up to 192 rows, tiles of 256 rows; K of one step and of several, odd and even
 LARGE = [(1, 40001, 77), (7, 33000, 1040), (16, 20003, 513), (17, 33000, 127), (33, 32900, 300), (40, 33001, 272),
          (64, 33001, 1001), (65, 17003, 896), (77, 20011, 1001), (96, 17000, 16), (100, 20011, 16), (128, 16500, 513),
-         (129, 12001, 333), (256, 9001, 256), (300, 8200, 1040), (513, 5003, 192), (1024, 2200, 640)]
+         (129, 16411, 1001), (150, 12001, 256), (192, 11000, 896), (200, 8300, 1001), (129, 12001, 333), (256, 9001, 256), (300, 8200, 1040), (513, 5003, 192), (1024, 2200, 640)]
 
 
 @pytest.mark.parametrize("M,N,K", LARGE)
