@@ -184,7 +184,8 @@ def test_product_bit_exact(M, N, K, dtype):
 # of up to 192 rows, tiles of 256 rows; K of one step and of several, odd and even
 LARGE = [(1, 40001, 77), (7, 33000, 1040), (16, 20003, 513), (17, 33000, 127), (33, 32900, 300), (40, 33001, 272),
          (64, 33001, 1001), (65, 17003, 896), (77, 20011, 1001), (96, 17000, 16), (100, 20011, 16), (128, 16500, 513),
-         (129, 16411, 1001), (150, 12001, 256), (192, 11000, 896), (200, 8300, 1001), (129, 12001, 333), (256, 9001, 256), (300, 8200, 1040), (513, 5003, 192), (1024, 2200, 640)]
+         (129, 16411, 1001), (150, 12001, 256), (192, 11000, 896), (200, 8300, 1001), (129, 12001, 333),
+         (256, 9001, 256), (300, 8200, 1040), (513, 5003, 192), (1024, 2200, 640), (5, 8300, 10500), (40, 16450, 10300)]
 
 
 @pytest.mark.parametrize("M,N,K", LARGE)
@@ -296,6 +297,23 @@ def test_product_offsets_past_32_bits():
     torch.cuda.synchronize()
     _check_product(out.contiguous(), a, sa, w, sw)
     _check_quantized(codes, scale, out)
+
+
+@pytest.mark.parametrize("M,K", [(1, 8), (1, 16), (17, 32)])
+def test_more_rows_of_w_than_one_launch_takes(M, K):
+    # sums below 2^24: a float32 matrix product is exact, and scales of 1 leave one rounding
+    N = (1 << 28) + 100
+    w = torch.randint(-128, 128, (N, K), dtype=torch.int8, device="cuda")
+    a = torch.randint(-128, 128, (M, K), dtype=torch.int8, device="cuda")
+    one = torch.ones(1, device="cuda")
+    sw = torch.ones(N, device="cuda")
+    note(f"product {M} x {N} x {K}")
+    out = etg.matmul_i8(a, one.repeat(M), w, sw, out_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    step = 1 << 24
+    for n in range(0, N, step):
+        want = torch.matmul(a.float(), w[n:n + step].float().t().contiguous())
+        assert torch.equal(out[:, n:n + step], want.to(torch.bfloat16)), n
 
 
 def test_empty_calls_write_nothing():
