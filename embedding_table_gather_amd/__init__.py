@@ -447,17 +447,20 @@ def _scales(t: torch.Tensor, n: int, what: str, device: torch.device) -> int:
     return s
 
 
-def _workspace_for(need: int, device: torch.device, given: torch.Tensor | None = None) -> torch.Tensor:
-    """A workspace of one call: the given one checked (its size by the call itself), or a
-    fresh one, as calls on other streams and captured graphs keep their own (the caching
-    allocator makes that cheap)."""
+def _workspace_for(need: int, device: torch.device, given: torch.Tensor | None = None):
+    """(tensor, pointer, bytes) of a call's workspace: the given tensor checked (its size by
+    the call itself), or a fresh one, as calls on other streams and captured graphs keep their
+    own (the caching allocator makes that cheap); no tensor where none is needed."""
     if given is not None:
         if given.dtype != torch.uint8 or given.device != device or not given.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 tensor on the operands' device")
-        return given
+        return given, given.data_ptr(), given.numel()
+    if need == 0:
+        return None, None, 0
     if need < 0:
         _check(need)
-    return torch.empty(need, dtype=torch.uint8, device=device)
+    space = torch.empty(need, dtype=torch.uint8, device=device)
+    return space, space.data_ptr(), need
 
 
 def quantize_i8(x: torch.Tensor, codes: torch.Tensor | None = None, scale: torch.Tensor | None = None):
@@ -511,10 +514,9 @@ def matmul_i8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     sa, sw = _scales(a_scale, m, "a_scale", dev), _scales(w_scale, n, "w_scale", dev)
     out, out_stride = _out(out, out_dtype, m, n, dev)
     L = lib()
-    workspace = _workspace_for(L.etg_matmul_i8_workspace(m, n, k), dev, workspace)
+    workspace, ws_ptr, ws_bytes = _workspace_for(L.etg_matmul_i8_workspace(m, n, k), dev, workspace)
     _call(L.etg_matmul_i8, dev, a.data_ptr(), a_stride, a_scale.data_ptr(), sa, w.data_ptr(), w_stride,
-          w_scale.data_ptr(), sw, m, n, k, out.data_ptr(), _FLOATS[out.dtype], out_stride, workspace.data_ptr(),
-          workspace.numel())
+          w_scale.data_ptr(), sw, m, n, k, out.data_ptr(), _FLOATS[out.dtype], out_stride, ws_ptr, ws_bytes)
     return out
 
 
@@ -581,12 +583,12 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0
             or not out_probs.is_contiguous():
         raise ValueError(f"out_probs must be a contiguous float32 tensor of {rows} values on the logits' device")
     L = lib()
-    workspace = _workspace_for(L.etg_sample_workspace(rows, vocab), dev, workspace)
+    workspace, ws_ptr, ws_bytes = _workspace_for(L.etg_sample_workspace(rows, vocab), dev, workspace)
     if d_k is None and k > 0x7fffffff:
         k = 0  # past every vocabulary: off
     how = _Sampling(T, k, p, mp, d_T, d_k, d_p, d_mp, d_allowed, a_stride)
     _call(L.etg_sample, dev, logits.data_ptr(), dtype, rows, vocab, stride, ctypes.addressof(how), uniform.data_ptr(),
-          out_ids.data_ptr(), out_probs.data_ptr(), workspace.data_ptr(), workspace.numel())
+          out_ids.data_ptr(), out_probs.data_ptr(), ws_ptr, ws_bytes)
     return out_ids, out_probs
 
 
@@ -620,10 +622,10 @@ class I8Table:
             raise ValueError(f"residual has {hidden} columns, the table {self.hidden}")
         out, out_stride = _out(out, out_dtype, B, self.vocab, dev)
         L = lib()
-        workspace = _workspace_for(L.etg_logits_i8_workspace(B, self.vocab, hidden), dev, workspace)
+        workspace, ws_ptr, ws_bytes = _workspace_for(L.etg_logits_i8_workspace(B, self.vocab, hidden), dev, workspace)
         _call(L.etg_logits_i8, dev, self.codes.data_ptr(), self._stride, self.scale.data_ptr(), self._scale_stride,
               self.vocab, hidden, residual.data_ptr(), dtype, stride, B, out.data_ptr(), _FLOATS[out.dtype], out_stride,
-              workspace.data_ptr(), workspace.numel())
+              ws_ptr, ws_bytes)
         return out
 
     def logits_raw_wire(self, residual: torch.Tensor, out_dtype=torch.float32,
