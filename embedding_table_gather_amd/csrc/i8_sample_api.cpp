@@ -163,7 +163,7 @@ int32_t etg_logits_i8(const int8_t* d_codes, int64_t code_stride, const float* d
   }
   uint8_t* ws = (uint8_t*)d_workspace;
   int8_t* a = (int8_t*)ws;
-  float* a_scale = (float*)(ws + w.scale_offset);
+  float* a_scale = ws != nullptr ? (float*)(ws + w.scale_offset) : nullptr;
   // the product's own checks, before anything is enqueued
   st = check_matmul(a, w.code_stride, a_scale, 1, d_codes, code_stride, d_scale, scale_stride, batch, vocab, hidden,
                     d_out, out_dtype, out_stride);
