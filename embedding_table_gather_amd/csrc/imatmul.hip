@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(64 * WAVES, MINW) wide_i8_kernel(MatmulI8 p, c
 // the full MFMA rate.  The image passes through two LDS buffers of one step, each refilled
 // one step ahead.  The next step's copies and w loads are issued one at a time between the
 // MFMAs of this one (32 in a row would hold up the wave, whose MFMAs wait behind them), and its
-// w rows are transposed there too.  1,024 x 262,144 x 5,120 to bf16: 1,300 us, 2.1 POP/s (the
+// w rows are transposed there too.  1,024 x 262,144 x 5,120 to bf16: 1,300-1,350 us, 2.0-2.1 POP/s (the
 // copies in a row before the MFMAs: 1,454).  The MFMAs alone run 777 us; the L2 reads of the
 // image and the w rows by 256 x 256 tiles, and the stores at the end of a tile, with one
 // workgroup per CU and nothing else to run meanwhile, are the rest.  160 rows of it take 402
