@@ -441,6 +441,10 @@ __device__ __forceinline__ int block_pick(const SampleSource<DT>& src, int lo, i
 // ---------------------------------------------------------------------------
 // 1. Chunks
 // ---------------------------------------------------------------------------
+// The larger of a maximum and a logit, which may be any NaN.  v_max_f32 passes over a quiet NaN,
+// but makes a signaling one its (quiet) result and so loses m: the logit is quieted first.
+__device__ __forceinline__ float max_logit(float m, float l) { return fmaxf(m, __builtin_canonicalizef(l)); }
+
 // Max over groups of 2^steps lanes (DPP within 16-lane rows), to every lane of the group.
 __device__ __forceinline__ float group_max(float m, int steps) {
   auto dpp = [&](auto ctrl) {
@@ -481,7 +485,7 @@ __global__ void __launch_bounds__(kChunkThreads) sample_chunk_kernel(Sample s, S
   for (int j = 0; j < NV; j++) {
     float g = -__builtin_inff();
 #pragma unroll
-    for (int e = 0; e < N; e++) g = fmaxf(g, l[j][e]);  // passes over NaN
+    for (int e = 0; e < N; e++) g = max_logit(g, l[j][e]);
     g = group_max(g, steps);
     const int v = c * kChunk + (j * 64 + lane) * N;
     if ((lane & ((1 << steps) - 1)) == 0 && v < src.V) ws.gmax[row * ws.groups + (v >> ws.group_log2)] = g;

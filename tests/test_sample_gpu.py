@@ -364,3 +364,26 @@ def test_calls_on_two_streams_at_once():
     for i in range(2):
         for ids, probs in got[i]:
             assert torch.equal(ids, want[i][0]) and torch.equal(probs, want[i][1])
+
+
+@pytest.mark.parametrize("dtype,view,nans", [("f32", torch.int32, (0x7F800001, -0x7FFFFF, 0x7FBFFFFF)),
+                                             ("bf16", torch.int16, (0x7F81, -0x7F, 0x7FBF)),
+                                             ("f16", torch.int16, (0x7C01, -0x3FF, 0x7DFF))])
+@pytest.mark.parametrize("V", [8, 700, 20011])
+def test_signaling_nan_logits(dtype, view, nans, V):
+    # a signaling NaN at every place of a group of tokens after the row's largest logit, in the
+    # first or the last group, alone or with one in every third place beside it
+    logits, u = _logits(56, V, dtype, seed=V)
+    bits = logits.view(view)
+    pairs = [(a, b) for b in range(8) for a in range(b)]
+    for r in range(56):
+        first = 0 if r < 28 else V - 8
+        a, b = pairs[r % 28]
+        if r % 2:
+            bits[r, 2::3] = nans[r % 3]
+        logits[r, first + a] = 30.0
+        bits[r, first + b] = nans[r % 3]
+    for how in (dict(), dict(temperature=0.0), dict(temperature=2.0, top_k=40), dict(temperature=3.0, top_p=0.9),
+                dict(temperature=4.0, min_p=0.01), dict(temperature=1e4, top_p=0.97)):
+        note(f"sample signaling NaN {dtype} V={V} {how}")
+        _check(logits, u, **how)
