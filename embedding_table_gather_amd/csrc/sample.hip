@@ -186,10 +186,10 @@ struct SampleWeight {
   }
 };
 
-// floor or ceil of f * m for a float f in [0, 1] and an integer m, exactly: f is a
-// 24-bit integer times a power of two, the product 88 bits.
+// floor or ceil of f * m for a float f in [0, 1] (-0 included) and an integer m, exactly: f is
+// a 24-bit integer times a power of two, the product 88 bits.
 __device__ __forceinline__ uint64_t scaled(float f, uint64_t m, bool up) {
-  const uint32_t b = __float_as_uint(f);
+  const uint32_t b = __float_as_uint(f) & 0x7fffffffu;
   const int e = max((int)(b >> 23), 1);  // f = mant * 2^(e - 150)
   const uint64_t mant = (b & 0x7fffffu) | (b >> 23 ? 0x800000u : 0u);
   const unsigned __int128 x = (unsigned __int128)mant * m;

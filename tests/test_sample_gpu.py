@@ -387,3 +387,17 @@ def test_signaling_nan_logits(dtype, view, nans, V):
                 dict(temperature=4.0, min_p=0.01), dict(temperature=1e4, top_p=0.97)):
         note(f"sample signaling NaN {dtype} V={V} {how}")
         _check(logits, u, **how)
+
+
+@pytest.mark.parametrize("V,spread", [(1, 1.0), (900, 2.5), (30011, 2.5), (30011, 0.01)])
+def test_negative_zero_settings(V, spread):
+    # -0 is 0: the first kept token for a random number, greedy for a temperature, off for min-p
+    rows = 3
+    logits, _ = _logits(rows, V, "f32", seed=V, spread=spread)
+    zero = torch.zeros(rows, device="cuda")
+    for how in (dict(), dict(temperature=0.7, top_k=20), dict(top_p=0.9), dict(min_p=0.01), dict(top_k=3000, top_p=0.8),
+                dict(temperature=-0.0), dict(temperature=-zero), dict(min_p=-0.0, top_k=5), dict(min_p=-zero)):
+        note(f"sample u = -0.0, V={V} spread={spread} {how}")
+        got = _check(logits, -zero, **how)
+        want = etg.sample(logits, zero, **how)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
