@@ -584,8 +584,8 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, top_k=0
         raise ValueError(f"out_probs must be a contiguous float32 tensor of {rows} values on the logits' device")
     L = lib()
     workspace, ws_ptr, ws_bytes = _workspace_for(L.etg_sample_workspace(rows, vocab), dev, workspace)
-    if d_k is None and k > 0x7fffffff:
-        k = 0  # past every vocabulary: off
+    if d_k is None:  # the C type's range: past every vocabulary is off, a negative one stays negative
+        k = 0 if k > 0x7fffffff else max(k, -0x80000000)
     how = _Sampling(T, k, p, mp, d_T, d_k, d_p, d_mp, d_allowed, a_stride)
     _call(L.etg_sample, dev, logits.data_ptr(), dtype, rows, vocab, stride, ctypes.addressof(how), uniform.data_ptr(),
           out_ids.data_ptr(), out_probs.data_ptr(), ws_ptr, ws_bytes)

@@ -401,3 +401,11 @@ def test_negative_zero_settings(V, spread):
         got = _check(logits, -zero, **how)
         want = etg.sample(logits, zero, **how)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("k", [-1, -2 ** 31, -2 ** 31 - 1, -2 ** 32, -2 ** 32 + 5, -10 ** 30])
+def test_negative_top_k_is_refused(k):
+    logits, u = _logits(2, 300, "f32", seed=3)
+    with pytest.raises(etg.EtgError, match="top_k") as e:
+        etg.sample(logits, u, top_k=k)
+    assert e.value.status == -5
