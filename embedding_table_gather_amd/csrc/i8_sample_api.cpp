@@ -13,17 +13,23 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 constexpr int64_t kMaxCols = 65536;              // |sum of k int8 products| <= 2^30 fits int32
 constexpr int64_t kMaxRows = 2147483647;
-constexpr int64_t kMaxStride = (int64_t)1 << 40;  // row * stride stays far inside 64 bits
+constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxSpan = (int64_t)1 << 57;   // bytes from a first row to a last: more than an address space holds
 constexpr int64_t kMaxTokens = 65536;
 constexpr int64_t kMaxSampleVocab = 1 << 20;      // a total in 64-bit fixed point stays within 2^-24 of itself
 
 // bytes of one f32 / bf16 / f16 value, 0 for any other dtype
 size_t float_bytes(int32_t dtype) { return dtype == ETG_F32 ? 4 : dtype == ETG_BF16 || dtype == ETG_F16 ? 2 : 0; }
 
-int32_t check_stride(const char* what, int64_t stride, int64_t least) {
+// Rows (at least 0 of them) stride values of `size` bytes apart: kernels compute row * stride
+// * size in 64 bits, so it has to stay inside them.
+int32_t check_stride(const char* what, int64_t stride, int64_t least, int64_t rows, size_t size) {
   if (stride < least || stride > kMaxStride)
     return etg::set_error(ETG_ESHAPE, "%s stride %lld outside [%lld, 2^40]", what, (long long)stride,
                           (long long)least);
+  if (rows > 1 && rows - 1 > kMaxSpan / (stride * (int64_t)size))
+    return etg::set_error(ETG_ESHAPE, "%s stride %lld over %lld rows spans more than 2^57 bytes", what,
+                          (long long)stride, (long long)rows);
   return ETG_OK;
 }
 
@@ -43,11 +49,11 @@ int32_t check_matmul(const int8_t* d_a, int64_t a_stride, const float* d_a_scale
   const size_t esize = float_bytes(out_dtype);
   if (esize == 0) return etg::set_error(ETG_EDTYPE, "output dtype %d is not f32, bf16 or f16", out_dtype);
   int32_t st = check_matmul_shape(m, n, k);
-  if (st == ETG_OK) st = check_stride("a", a_stride, k);
-  if (st == ETG_OK) st = check_stride("w", w_stride, k);
-  if (st == ETG_OK) st = check_stride("a scale", a_scale_stride, 1);
-  if (st == ETG_OK) st = check_stride("w scale", w_scale_stride, 1);
-  if (st == ETG_OK) st = check_stride("output", out_stride, n > 1 ? n : 1);
+  if (st == ETG_OK) st = check_stride("a", a_stride, k, m, 1);
+  if (st == ETG_OK) st = check_stride("w", w_stride, k, n, 1);
+  if (st == ETG_OK) st = check_stride("a scale", a_scale_stride, 1, m, 4);
+  if (st == ETG_OK) st = check_stride("w scale", w_scale_stride, 1, n, 4);
+  if (st == ETG_OK) st = check_stride("output", out_stride, n > 1 ? n : 1, m, esize);
   if (st != ETG_OK) return st;
   if (m == 0 || n == 0) return ETG_OK;
   if (d_a == nullptr || d_a_scale == nullptr || d_w == nullptr || d_w_scale == nullptr || d_out == nullptr)
@@ -78,9 +84,9 @@ int32_t etg_quantize_i8(const void* d_x, int32_t dtype, int64_t rows, int64_t co
     return etg::set_error(ETG_ESHAPE, "rows %lld outside [0, 2^31 - 1]", (long long)rows);
   if (cols < 1 || cols > kMaxCols)
     return etg::set_error(ETG_ESHAPE, "cols %lld outside [1, %lld]", (long long)cols, (long long)kMaxCols);
-  int32_t st = check_stride("input", x_stride, cols);
-  if (st == ETG_OK) st = check_stride("code", code_stride, cols);
-  if (st == ETG_OK) st = check_stride("scale", scale_stride, 1);
+  int32_t st = check_stride("input", x_stride, cols, rows, esize);
+  if (st == ETG_OK) st = check_stride("code", code_stride, cols, rows, 1);
+  if (st == ETG_OK) st = check_stride("scale", scale_stride, 1, rows, 4);
   if (st != ETG_OK) return st;
   if (rows == 0) return ETG_OK;
   if (d_x == nullptr || d_codes == nullptr || d_scale == nullptr)
@@ -186,7 +192,7 @@ int32_t etg_sample(const void* d_logits, int32_t dtype, int64_t batch, int64_t v
   const size_t esize = float_bytes(dtype);
   if (esize == 0) return etg::set_error(ETG_EDTYPE, "logits dtype %d is not f32, bf16 or f16", dtype);
   int32_t st = check_sample_shape(batch, vocab);
-  if (st == ETG_OK) st = check_stride("logits", logits_stride, vocab);
+  if (st == ETG_OK) st = check_stride("logits", logits_stride, vocab, batch, esize);
   if (st != ETG_OK) return st;
   if (how == nullptr) return etg::set_error(ETG_EINVAL, "sampling settings are NULL");
   // written so that a NaN fails; a per-row array replaces its scalar
@@ -199,7 +205,7 @@ int32_t etg_sample(const void* d_logits, int32_t dtype, int64_t batch, int64_t v
     return etg::set_error(ETG_ERANGE, "min_p %g outside [0, 1]", (double)how->min_p);
   const int64_t words = (vocab + 31) / 32;
   if (how->d_allowed != nullptr && how->allowed_stride != 0) {
-    st = check_stride("allowed", how->allowed_stride, words);
+    st = check_stride("allowed", how->allowed_stride, words, batch, 4);
     if (st != ETG_OK) return st;
   }
   if (batch == 0) return ETG_OK;

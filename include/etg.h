@@ -421,9 +421,9 @@ int32_t etg_logits_topk_noalloc(const etg_table* lm_head, const float* d_residua
  *   d_codes       int8, rows code_stride bytes apart, any alignment
  *   d_scale       f32, scale_stride floats apart
  *   rows          0 <= rows <= 2^31 - 1; 0 enqueues nothing;  1 <= cols <= 65536
- * Strides are at least cols (1 for scales) and at most 2^40.  Bytes between rows are
- * left as they were.  The outputs must not overlap the input.  Bit-exact to the
- * definition.
+ * Strides are at least cols (1 for scales) and at most 2^40, and the last row begins at
+ * most 2^57 bytes after the first.  Bytes between rows are left as they were.  The
+ * outputs must not overlap the input.  Bit-exact to the definition.
  * Errors: EDTYPE, ESHAPE (sizes, strides), EINVAL (null), EALIGN.
  */
 int32_t etg_quantize_i8(const void* d_x, int32_t dtype, int64_t rows, int64_t cols, int64_t x_stride,
@@ -447,7 +447,8 @@ int32_t etg_quantize_i8(const void* d_x, int32_t dtype, int64_t rows, int64_t co
  *                  as they were
  *   d_workspace    at least etg_matmul_i8_workspace() bytes, 256-byte aligned (may be
  *                  NULL where that is 0)
- * Results are bitwise repeatable and depend on no other row.
+ * Strides are at least k (codes), 1 (scales) and n (output), bounded as in
+ * etg_quantize_i8.  Results are bitwise repeatable and depend on no other row.
  * Errors: EDTYPE, ESHAPE (sizes, strides), EINVAL (null), EALIGN, EWORKSPACE.
  */
 int64_t etg_matmul_i8_workspace(int64_t m, int64_t n, int64_t k);
@@ -507,8 +508,8 @@ typedef struct {
  * A row without candidates, or with a setting or random number outside its range
  * (uniform: [0, 1)), has id -1 and probability 0.
  *   d_logits     `dtype` (ETG_F32, ETG_BF16, ETG_F16) [batch][vocab], rows logits_stride
- *                values apart, aligned to the value; may be rewritten once the call's
- *                work has run
+ *                values apart (at least vocab, bounded as in etg_quantize_i8), aligned to
+ *                the value; may be rewritten once the call's work has run
  *   d_uniform    f32 [batch]
  *   batch        0 <= batch <= 65536 (0 enqueues nothing);  1 <= vocab <= 2^20
  *   d_workspace  at least etg_sample_workspace() bytes, 256-byte aligned (may be NULL

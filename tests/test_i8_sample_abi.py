@@ -155,3 +155,33 @@ def test_python_refusals_on_host_tensors():
         etg.sample(x, torch.zeros(4))
     with pytest.raises(ValueError):
         etg.I8Table(q, torch.ones(4))
+
+
+def test_rows_that_span_more_than_an_address_space(L):
+    # (rows - 1) * stride * size past 2^57 bytes, up to 2^73: the kernels' 64-bit offsets would wrap
+    M, far = 2 ** 31 - 1, 2 ** 40
+    args = dict(x=_p(), dt=etg.F32, rows=M, cols=64, xs=64, q=_p(), qs=64, s=_p(), ss=1)
+    for name, word in (("xs", "input stride"), ("qs", "code stride"), ("ss", "scale stride")):
+        assert L.etg_quantize_i8(*{**args, name: far}.values(), None) == -3 and word in _err(L) and "2^57" in _err(L)
+    # 2^16 rows 2^40 values apart are 2^56 bytes of codes, 2^57 of 16-bit values, 2^58 of f32 ones
+    args = dict(a=_p(), as_=64, sa=_p(), sas=1, w=_p(), ws=64, sw=_p(), sws=1, m=4, n=M, k=64, out=_p(), dt=etg.F32,
+                os_=M, work=_p(16), nbytes=0)
+    for name, word in (("ws", "w stride"), ("sws", "w scale stride")):
+        assert L.etg_matmul_i8(*{**args, name: far}.values(), None) == -3 and word in _err(L) and "2^57" in _err(L)
+    args.update(m=65536, n=33001, os_=33001)
+    for name, word in (("sas", "a scale stride"), ("os_", "output stride")):
+        assert L.etg_matmul_i8(*{**args, name: far}.values(), None) == -3 and word in _err(L) and "2^57" in _err(L)
+    # within it: past the strides' checks, to the workspace's alignment
+    assert L.etg_matmul_i8(*{**args, "as_": far}.values(), None) == -4
+    assert L.etg_matmul_i8(*{**args, "os_": far, "dt": etg.F16}.values(), None) == -4
+    assert L.etg_logits_i8(_p(), far, _p(), 1, M, 64, _p(), etg.F32, 64, 4, _p(), etg.F32, M, _p(), 1 << 40, None) == -3
+    assert "w stride" in _err(L) and "2^57" in _err(L)
+    assert L.etg_logits_i8(_p(), 64, _p(), 1, 100, 64, _p(), etg.F32, far, 65536, _p(), etg.F32, 100, _p(), 1 << 50,
+                           None) == -3
+    assert "input stride" in _err(L) and "2^57" in _err(L)
+
+    def sampled(how, dt=etg.F32, stride=100):
+        return L.etg_sample(_p(), dt, 65536, 100, stride, ctypes.addressof(how), _p(), _p(), _p(), _p(16), 0, None)
+    assert sampled(_how(), stride=far) == -3 and "logits stride" in _err(L) and "2^57" in _err(L)
+    assert sampled(_how(), etg.BF16, far) == -4
+    assert sampled(_how(allowed=FAKE, stride=far)) == -3 and "allowed stride" in _err(L) and "2^57" in _err(L)
