@@ -185,3 +185,31 @@ def test_rows_that_span_more_than_an_address_space(L):
     assert sampled(_how(), stride=far) == -3 and "logits stride" in _err(L) and "2^57" in _err(L)
     assert sampled(_how(), etg.BF16, far) == -4
     assert sampled(_how(allowed=FAKE, stride=far)) == -3 and "allowed stride" in _err(L) and "2^57" in _err(L)
+
+
+@pytest.mark.parametrize("m,n,k", [(64, 33001, 256), (300, 33001, 1001), (17, 2 ** 20, 16)])
+def test_matmul_workspace_refusals(L, m, n, k):
+    # shapes of the kernels that read the a rows' image from the workspace
+    need = L.etg_matmul_i8_workspace(m, n, k)
+    assert need > 0
+
+    def call(work=_p(), nbytes=need):
+        return L.etg_matmul_i8(_p(), k, _p(), 1, _p(), k, _p(), 1, m, n, k, _p(), etg.F32, n, work, nbytes, None)
+    assert call(work=None) == -1 and "workspace" in _err(L)
+    assert call(work=_p(16)) == -4 and "256-byte aligned" in _err(L)
+    assert call(nbytes=need - 1) == -6 and str(need) in _err(L)
+    assert call(nbytes=0) == -6
+
+
+@pytest.mark.parametrize("batch,vocab", [(1, 1), (4, 100), (64, 262144)])
+def test_sample_workspace_refusals(L, batch, vocab):
+    need = L.etg_sample_workspace(batch, vocab)
+    assert need > 0
+    how = _how()
+
+    def call(work=_p(), nbytes=need):
+        return L.etg_sample(_p(), etg.BF16, batch, vocab, vocab, ctypes.addressof(how), _p(), _p(), _p(), work, nbytes,
+                            None)
+    assert call(work=None) == -1 and "workspace" in _err(L)
+    assert call(work=_p(16)) == -4 and "256-byte aligned" in _err(L)
+    assert call(nbytes=need - 1) == -6 and str(need) in _err(L)
