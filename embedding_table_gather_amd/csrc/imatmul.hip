@@ -236,7 +236,6 @@ __global__ void __launch_bounds__(1024) stream_i8_kernel(MatmulI8 p, int64_t nti
   for (int64_t g = 0; g < total; g += 2) {  // an odd number: the last half has no tile to store
     compute(set[0]);
     load(set[0]);
-    if (st == steps) st = 0;
     compute(set[1]);
     load(set[1]);
   }
