@@ -302,11 +302,7 @@ __device__ __forceinline__ uint32_t first_key(uint32_t hi, F reaches) {
   while (hi - lo > 1) {
     const uint32_t step = (hi - lo - 1) / 64 + 1;  // lane i: lo + (i + 1) step, at most hi
     const uint32_t mine = step <= (hi - lo) / (lane + 1) ? lo + (lane + 1) * step : hi;
-    const uint64_t m = __ballot(reaches(ord_score(mine)));  // hi is among the tried or beyond the last
-    if (m == 0) {
-      lo += 64 * step;
-      continue;
-    }
+    const uint64_t m = __ballot(reaches(ord_score(mine)));  // never 0: the last lane's is hi, as 64 step >= hi - lo
     const uint32_t i = (uint32_t)__ffsll((unsigned long long)m) - 1;
     const uint32_t to = step <= (hi - lo) / (i + 1) ? lo + (i + 1) * step : hi;
     lo += i * step;
