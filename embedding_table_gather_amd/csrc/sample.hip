@@ -1084,8 +1084,7 @@ __global__ void __launch_bounds__(kSampleThreads, 4) sample_hist_kernel(Sample s
 struct SampleRowHist {
   uint64_t c, m, tc, tm, ic, im;
   __device__ __forceinline__ SampleRowHist(const SamplePtrs& ws, int slot, SampleScratch<kSampleWaves>& sc)
-      : c(0), m(0), tc(0), tm(0), ic(0), im(0) {
-    if (slot < 0) return;
+      : c(0), m(0) {
     const size_t at = (size_t)slot * ws.slices * kSampleBins + threadIdx.x;
 #pragma unroll 4
     for (int i = 0; i < ws.slices; i++) {
