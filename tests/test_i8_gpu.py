@@ -351,3 +351,20 @@ def test_i8_table_logits(dtype):
     assert (np.abs(got.cpu().numpy() - L) <= bound * (1 + 1e-6) + 1e-6).all()
     wire = oracle.wire_encode(R, etg.WIRE_I8)
     assert np.array_equal(bits(q.logits_raw_wire(torch.from_numpy(wire).cuda())), bits(got))
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 70, 1), (1, 130, 15), (3, 129, 7), (33, 64, 15), (65, 1000, 9), (16, 16, 4)])
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+def test_short_rows_bit_exact(M, N, K, dtype):
+    # rows without a whole 16-byte load, one byte apart as well
+    g = np.random.default_rng(M + N + K)
+    a, w = _codes(g, M, K), _codes(g, N, K)
+    sa, sw = g.random(M).astype(np.float32), g.random(N).astype(np.float32)
+    note(f"product of short rows {M} x {N} x {K} -> {dtype}")
+    out = etg.matmul_i8(to_dev(a), to_dev(sa), to_dev(w), to_dev(sw), out_dtype=DTYPES[dtype])
+    wide = torch.full((N, K + 1), -128, dtype=torch.int8, device="cuda")
+    wide[:, 1:] = to_dev(w)
+    again = etg.matmul_i8(to_dev(a), to_dev(sa), wide[:, 1:], to_dev(sw), out_dtype=DTYPES[dtype])
+    torch.cuda.synchronize()
+    _check_product(out, a, sa, w, sw)
+    assert torch.equal(again, out)
