@@ -409,3 +409,20 @@ def test_negative_top_k_is_refused(k):
     with pytest.raises(etg.EtgError, match="top_k") as e:
         etg.sample(logits, u, top_k=k)
     assert e.value.status == -5
+
+
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
+@pytest.mark.parametrize("V", [9000, 70001])
+def test_top_tokens_side_by_side(dtype, V):
+    # sorted logits, both ways, and a block of large ones: the first k lie in few groups of tokens,
+    # all of whose other tokens are near them
+    x = np.sort(np.random.default_rng(V).standard_normal((4, V), dtype=np.float32) * np.float32(2.5), axis=1)
+    x[0] = x[0, ::-1]
+    x[2] = np.roll(x[2], V // 3)
+    x[3] = np.where((np.arange(V) > 4000) & (np.arange(V) < 8000), x[3] + 20, x[3])
+    logits = torch.from_numpy(np.ascontiguousarray(x)).to(DTYPES[dtype]).cuda()
+    u = torch.tensor([0.1, 0.5, 0.9, 0.999], device="cuda")
+    for how in (dict(top_k=50), dict(top_k=1000, top_p=0.9), dict(temperature=0.5, top_k=700, min_p=0.3),
+                dict(temperature=0.0), dict(top_p=0.6)):
+        note(f"sample top tokens side by side {dtype} V={V} {how}")
+        _check(logits, u, **how)
