@@ -396,6 +396,7 @@ struct I8Block {
 // copies and reads grow with it (K = 16,384, 48 rows 700 us, 128 rows 784); at 128 rows two
 // tiles of w rows per wave share an image fragment, which halves the reads from LDS.  At 192
 // rows two no longer fit the registers (spills: 683 us against 294 at 160 rows, K = 5,120).
+// w is read by one pass only (non-temporal loads): two passes of 128 rows would read it twice.
 // ---------------------------------------------------------------------------
 template <int DT, int NT, int MT, int WAVES, int MINW>
 __global__ void __launch_bounds__(64 * WAVES, MINW) wide_i8_kernel(MatmulI8 p, const unsigned char* __restrict__ img,
@@ -606,7 +607,9 @@ static I8Plan i8_plan(int64_t m, int64_t n, int64_t k) {
   } else if (cdiv(n, 64) * cdiv(m, 64) <= (m <= 16 ? 128 : 512)) {
     // Few tiles of 64 x 64.  Measured, split against the others (us): 512 tiles m = 128,
     // n = 16,384, k = 5,120 45.9 / 52.4, k = 256 10.9 / 13.5; 1,024 tiles m = 256, k = 5,120
-    // 85 / 71.  m = 16: 64 tiles, k = 1,024 4.5 / 6.2, 256 tiles 7.9 / 6.6.
+    // 85 / 71.  m = 16: 64 tiles, k = 1,024 4.5 / 6.2, 256 tiles 7.9 / 6.6.  Around the border
+    // both are two to four times the bytes' time (128 x 16,384 x 5,120 13 us): split tiles read
+    // their operands once per tile, and the others have a workgroup per 256 w rows, too few.
     p.kind = I8_SPLIT;
   } else if (m <= 16 && (size_t)p.steps * 4096 <= kMaxLds) {
     p.kind = I8_STREAM;

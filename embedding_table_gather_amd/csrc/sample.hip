@@ -20,11 +20,15 @@ namespace etg {
 // exceeds u times the kept mass.
 //
 // Masses are sums of weights in unsigned fixed point, 2^-shift each: integer sums do
-// not depend on the order in which threads add, so a call repeats bitwise, and tokens
-// with equal logits weigh exactly the same.  With vocab <= 2^b the sum is at most
-// 2^(b + shift) <= 2^63: shift = min(45, 63 - b).  A weight is off by at most half a
-// unit, a total (at least 2^shift) by 2^(b - shift - 1) of itself: 2^-28 at 2^18 tokens
-// and 2^-24 at the largest vocabulary, 2^20.
+// not depend on the order in which threads add, so a call repeats bitwise, and the kept
+// tokens of a row with filters weigh exactly the same where their logits are equal.  With
+// vocab <= 2^b the sum is at most 2^(b + shift) <= 2^63: shift = min(45, 63 - b).  A weight
+// is off by at most half a unit, a total (at least 2^shift) by 2^(b - shift - 1) of itself:
+// 2^-28 at 2^18 tokens and 2^-24 at the largest vocabulary, 2^20.  The chunk masses of kernel
+// 1 are relative to each chunk's own largest logit and are rounded again when they are
+// brought to the row's, by half a unit and about 2^-47 of themselves (the exponent of what
+// they are multiplied with, below 46 where it counts, carries roundings of 2^-53): a draw
+// without filters, and the total that top-p alone goes by, are that near.
 //
 // Kernels:
 //  1. sample_chunk_kernel streams the logits once, a wave per 2,048 tokens: the
@@ -36,10 +40,12 @@ namespace etg {
 //     maxima above a value weigh p times the total, so does the nucleus.  Only the groups
 //     that reach the bound are read again, and their tokens at or above it (a few more
 //     than are kept) are sorted in LDS.
-//  3. Rows that keep more than the list holds (flat distributions) go on to
-//     sample_hist_kernel, which counts and weighs every token in 1,024 bins per slice
-//     of 16,384 tokens, sample_gather_kernel, which lists the tokens of the bin that holds
-//     the cut, and sample_heavy_kernel, which narrows the list to the cut.
+//  3. Rows with more tokens at the bound than the list holds (flat distributions, and close
+//     logits: bin 0 of the bound's bins is all that lies within 1/8 of the largest logit,
+//     whatever the temperature) go on to sample_hist_kernel, which counts and weighs every
+//     token in 1,024 bins per slice of 16,384 tokens, sample_gather_kernel, which lists the
+//     tokens of the bin that holds the cut, and sample_heavy_kernel, which narrows the list
+//     to the cut.
 
 struct SampleRow {
   float T, p, minp, u;
@@ -1043,8 +1049,10 @@ __device__ __forceinline__ float sample_top(const SamplePtrs& ws, int64_t row) {
   return wave_max_f32(m);
 }
 
-// A workgroup per slice of a heavy row, few of them as there are few heavy rows as a rule:
-// bound by the f64 weights and the LDS additions (64 rows of 262,144 of mixed settings 10 us).
+// A workgroup per slice of a heavy row, few of them as calls of mixed settings have few heavy
+// rows: bound by the f64 weights and the LDS additions (64 rows of 262,144 of mixed settings
+// 10 us).  Whole batches of heavy rows (1,024 x 151,936 bf16, T = 1.5, top-p 0.95: the call
+// 1,211 us) read and weigh every token here a second time.
 template <int DT>
 __global__ void __launch_bounds__(kSampleThreads, 4) sample_hist_kernel(Sample s, SamplePtrs ws) {
   constexpr int N = SampleSource<DT>::N;
@@ -1349,9 +1357,13 @@ hipError_t launch_sample(const Sample& s, void* space, hipStream_t stream) {
   int bits = 0;
   while ((1ll << bits) < s.vocab) bits++;
   p.shift = std::min(45, 63 - bits);
-  // Rows that keep more than the list holds are left to the heavy kernel, with the
-  // histograms where their settings may ask for it: with one small k for all rows only
-  // ties overflow the list, and the heavy kernel does without (no slots).
+  // Rows with more tokens at the bound than the list holds are left to the heavy kernel, with
+  // the histograms where their settings may ask for it.  With one small k for all rows the list
+  // overflows where thousands of tokens are equal to or within 1/8 of the largest, or where the
+  // first k lie in few groups of large tokens (sorted logits): the heavy kernel does without
+  // histograms then (no slots), by passes of one workgroup.  262,144 f32 tokens, top-k of 50, 1
+  // row / 64: spread 0.01 232 / 351 us, sorted 537 / 554, integers from 0 to 3 848 / 883; a
+  // Gaussian of spread 2.5 22 / 32.
   const bool greedy = s.d_temperature == nullptr && s.temperature == 0.f;
   const bool small_k = greedy || (s.d_top_k == nullptr && s.top_k > 0 && s.top_k <= kList / 2);
   const bool no_filter = s.temperature > 0.f && s.d_temperature == nullptr && s.d_top_k == nullptr && s.top_k == 0 &&

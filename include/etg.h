@@ -515,8 +515,11 @@ typedef struct {
  *   d_workspace  at least etg_sample_workspace() bytes, 256-byte aligned (may be NULL
  *                where that is 0)
  * Weights are added in 64-bit fixed point (rounded to 2^-45 of the largest one at vocab
- * 2^18, coarser by one bit per doubling), so results do not depend on timing: they
- * repeat bitwise, and tokens of equal logits weigh the same.
+ * 2^18, coarser by one bit per doubling; a weight below half a unit counts as 0), so
+ * results do not depend on timing: they repeat bitwise.  Tokens of equal logits weigh the
+ * same; in a row without filters nearly so, as each 2,048 tokens are weighed by the largest
+ * of their own logits and their sum is then brought to the row's (off by at most a unit and
+ * 2^-47 of itself).
  * Errors: EDTYPE, ESHAPE, ERANGE (a scalar setting), EINVAL (null), EALIGN, EWORKSPACE.
  */
 int64_t etg_sample_workspace(int64_t batch, int64_t vocab);
