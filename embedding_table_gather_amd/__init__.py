@@ -16,6 +16,9 @@ fallback: if the library is missing, every call raises.
     q = t.quantize_i8()                           # int8 rows, a scale each: an I8Table
     logits = q.logits_raw(residual)               # int8 product, f32 [B, vocab]
     ids, probs = sample(logits, uniform, top_k=50, min_p=0.05)
+    loss, lse = t.cross_entropy(residual, labels)              # training and evaluation
+    dx, dt = t.cross_entropy_grad(residual, labels, lse, 1 / count)
+    t.embed_gather_grad(dx0, ids, scale="sqrt_d", out=dt, accumulate=True)   # the tied table's gradient
 """
 from __future__ import annotations
 
@@ -80,6 +83,13 @@ SIGNATURES = {
                              ctypes.c_size_t, _VP]),
     "etg_sample_workspace": (_I64, [_I64, _I64]),
     "etg_sample": (_I32, [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+    "etg_cross_entropy_workspace": (_I64, [_VP, _I64]),
+    "etg_cross_entropy": (_I32, [_VP, _VP, _I64, _I64, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+    "etg_cross_entropy_grad_workspace": (_I64, [_VP, _I64]),
+    "etg_cross_entropy_grad": (_I32, [_VP, _VP, _I64, _I64, _VP, _VP, _F, _VP, _VP, _VP, _I64, _VP, _I32, _VP,
+                                      ctypes.c_size_t, _VP]),
+    "etg_embed_gather_grad_workspace": (_I64, [_VP, _I64]),
+    "etg_embed_gather_grad": (_I32, [_VP, _VP, _I64, _VP, _I32, _I64, _F, _VP, _I32, _I32, _VP, ctypes.c_size_t, _VP]),
     "etg_last_error": (ctypes.c_char_p, []),
 }
 
@@ -391,6 +401,127 @@ class Table:
         rows = self.rows.view(-1).view(torch.uint8).view(_TORCH_FLOATS[self.dtype]).view(self.vocab, self.hidden)
         return I8Table(*quantize_i8(rows))
 
+    # ---------------------------------------------------------------- training
+    def _float_type(self) -> torch.dtype:
+        if self.dtype not in _TORCH_FLOATS:
+            raise ValueError("a Q8_0 table has no gradients: the table must be f32, bf16 or f16")
+        return _TORCH_FLOATS[self.dtype]
+
+    def _train_rows(self, residual: torch.Tensor, labels: torch.Tensor):
+        """(row stride, batch) of residual rows of the table's type with a label each, checked."""
+        dtype = self._float_type()
+        if residual.dtype != dtype:
+            raise ValueError(f"residual must be a {dtype} tensor, the table's type")
+        stride = _rows(residual, "residual", self.device)
+        batch, hidden = residual.shape
+        if hidden != self.hidden:
+            raise ValueError(f"residual has {hidden} columns, the table {self.hidden}")
+        if labels.dtype != torch.int32 or labels.device != self.device or labels.shape != (batch,) \
+                or not labels.is_contiguous():
+            raise ValueError(f"labels must be a contiguous int32 tensor of {batch} values on the table's device")
+        return stride, batch
+
+    def cross_entropy(self, residual: torch.Tensor, labels: torch.Tensor, out_loss: torch.Tensor | None = None,
+                      out_lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+        """(loss, lse) float32 [B] of residual rows [B, hidden] of the table's type against int32
+        labels [B]: lse = ln sum_v exp(residual @ table.T), loss = lse - the label's logit, 0
+        where the label is not in [0, vocab).  The logits are never in memory."""
+        stride, batch = self._train_rows(residual, labels)
+        dev = self.device
+        loss = torch.empty(batch, dtype=torch.float32, device=dev) if out_loss is None \
+            else _floats(out_loss, batch, "out_loss", dev)
+        lse = torch.empty(batch, dtype=torch.float32, device=dev) if out_lse is None \
+            else _floats(out_lse, batch, "out_lse", dev)
+        L = lib()
+        workspace, ws_ptr, ws_bytes = _workspace_for(L.etg_cross_entropy_workspace(self._h, batch), dev, workspace)
+        _call(L.etg_cross_entropy, dev, self._h, residual.data_ptr(), stride, batch, labels.data_ptr(),
+              loss.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes)
+        return loss, lse
+
+    def cross_entropy_grad(self, residual: torch.Tensor, labels: torch.Tensor, lse: torch.Tensor, grad_loss=1.0,
+                           grad_lse: torch.Tensor | None = None, residual_grad: bool = True, table_grad: bool = True,
+                           out_residual: torch.Tensor | None = None, out_table: torch.Tensor | None = None,
+                           accumulate: bool = False, workspace: torch.Tensor | None = None):
+        """Gradients of ``cross_entropy`` in the table's type: (residual's [B, hidden], table's
+        [vocab, hidden]), None in the place of one that is not wanted.
+
+        lse: as cross_entropy gave it.  grad_loss: the gradient of each loss, a number or a
+        float32 tensor [B]; grad_lse: that of each lse, a float32 tensor [B] or None.
+        accumulate: add the table's gradient to ``out_table``.  The logits are computed again,
+        by pieces of the vocabulary.
+        """
+        stride, batch = self._train_rows(residual, labels)
+        dev, dtype = self.device, residual.dtype
+        _floats(lse, batch, "lse", dev)
+        d_gl = None
+        if isinstance(grad_loss, torch.Tensor):
+            d_gl, grad_loss = _floats(grad_loss, batch, "grad_loss", dev).data_ptr(), 0.0
+        d_gz = None if grad_lse is None else _floats(grad_lse, batch, "grad_lse", dev).data_ptr()
+        dx_ptr, dx_stride = None, self.hidden
+        if residual_grad:
+            if out_residual is None:
+                out_residual = torch.empty((batch, self.hidden), dtype=dtype, device=dev)
+            elif out_residual.dtype != dtype or out_residual.shape != residual.shape:
+                raise ValueError("out_residual must be a tensor of the residual's type and shape")
+            dx_ptr, dx_stride = out_residual.data_ptr(), _rows(out_residual, "out_residual", dev)
+        elif out_residual is not None:
+            raise ValueError("out_residual is given, but residual_grad is not wanted")
+        if table_grad:
+            out_table = self._table_grad(out_table, (dtype,), dtype, accumulate)
+        elif out_table is not None or accumulate:
+            raise ValueError("out_table or accumulate is given, but table_grad is not wanted")
+        L = lib()
+        workspace, ws_ptr, ws_bytes = _workspace_for(L.etg_cross_entropy_grad_workspace(self._h, batch), dev, workspace)
+        _call(L.etg_cross_entropy_grad, dev, self._h, residual.data_ptr(), stride, batch, labels.data_ptr(),
+              lse.data_ptr(), grad_loss, d_gl, d_gz, dx_ptr, dx_stride,
+              out_table.data_ptr() if table_grad else None, int(accumulate), ws_ptr, ws_bytes)
+        return out_residual, out_table
+
+    def _table_grad(self, out, types, dtype, accumulate) -> torch.Tensor:
+        """The gradient [vocab, hidden] given as ``out``, checked, or a new one."""
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate needs the tensor to add to")
+            return torch.empty((self.vocab, self.hidden), dtype=dtype, device=self.device)
+        if out.dtype not in types or out.device != self.device or out.shape != (self.vocab, self.hidden) \
+                or not out.is_contiguous():
+            raise ValueError(f"the table's gradient must be a contiguous {' or '.join(map(str, types))} tensor "
+                             f"[{self.vocab}, {self.hidden}] on the table's device")
+        return out
+
+    def embed_gather_grad(self, grad: torch.Tensor, ids: torch.Tensor, scale=None, out: torch.Tensor | None = None,
+                          out_dtype=None, accumulate: bool = False, workspace: torch.Tensor | None = None):
+        """Gradient of ``embed_gather`` with respect to the table, [vocab, hidden] in the table's
+        type (or float32: out_dtype or the type of ``out``): out[v] = scale * the sum of grad's
+        rows [n, hidden] (float32, bfloat16 or float16) whose id is v, added to what ``out``
+        holds with accumulate.  Bad ids add nothing.  Sums are in the positions' order, without
+        atomics.  scale: as in embed_gather."""
+        dtype = self._float_type()
+        if ids.dtype != torch.int32 or ids.device != self.device:
+            raise ValueError("ids must be an int32 tensor on the table's device")
+        ids = ids.contiguous().view(-1)
+        n = ids.numel()
+        gtype = _FLOATS.get(grad.dtype)
+        if gtype is None:
+            raise ValueError("grad must be a float32, bfloat16 or float16 tensor")
+        stride = _rows(grad, "grad", self.device)
+        if grad.shape != (n, self.hidden):
+            raise ValueError(f"grad must have {n} rows of {self.hidden} values")
+        sc = 1.0 if scale is None else (sqrt_d(self.hidden) if scale == "sqrt_d" else float(scale))
+        want = dtype if out_dtype is None else _float_dtype(out_dtype)
+        if want not in (dtype, torch.float32):
+            raise ValueError(f"out_dtype must be {dtype} or float32")
+        if out is not None and out_dtype is not None and out.dtype != want:
+            raise ValueError(f"out is not a {want} tensor")
+        types = (dtype,) if dtype == torch.float32 else (dtype, torch.float32)
+        out = self._table_grad(out, types, want, accumulate)
+        L = lib()
+        workspace, ws_ptr, ws_bytes = _workspace_for(L.etg_embed_gather_grad_workspace(self._h, n), self.device,
+                                                     workspace)
+        _call(L.etg_embed_gather_grad, self.device, self._h, ids.data_ptr(), n, grad.data_ptr(), gtype, stride, sc,
+              out.data_ptr(), _FLOATS[out.dtype], int(accumulate), ws_ptr, ws_bytes)
+        return out
+
 
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _TORCH_FLOATS = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
@@ -445,6 +576,13 @@ def _scales(t: torch.Tensor, n: int, what: str, device: torch.device) -> int:
     if s < 1:
         raise ValueError(f"{what} must have a positive stride")
     return s
+
+
+def _floats(t: torch.Tensor, n: int, what: str, device: torch.device) -> torch.Tensor:
+    """A contiguous vector of n f32 values, checked."""
+    if t.dtype != torch.float32 or t.device != device or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 tensor of {n} values on the table's device")
+    return t
 
 
 def _workspace_for(need: int, device: torch.device, given: torch.Tensor | None = None):

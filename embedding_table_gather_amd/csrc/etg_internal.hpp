@@ -226,6 +226,41 @@ struct Sample {
 size_t sample_workspace(int64_t rows, int64_t vocab);
 hipError_t launch_sample(const Sample& p, void* ws, hipStream_t stream);
 
+// One etg_cross_entropy or etg_cross_entropy_grad call (xent.hip): residual rows of the
+// table's type, pitches in bytes.
+struct XentCall {
+  const void* x;
+  int64_t x_pitch;
+  int64_t n;
+  const int32_t* labels;
+  float *loss, *lse_out;   // forward
+  const float* lse;        // gradients
+  float grad_loss_all;     // where grad_loss is null
+  const float *grad_loss, *grad_lse;
+  void* d_x;
+  int64_t d_x_pitch;
+  void* d_rows;
+  int32_t add;
+};
+size_t xent_workspace(const TableDesc& t, int64_t n);
+size_t xent_grad_workspace(const TableDesc& t, int64_t n);
+hipError_t launch_xent(const TableDesc& t, const XentCall& c, void* ws, hipStream_t stream);
+hipError_t launch_xent_grad(const TableDesc& t, const XentCall& c, void* ws, hipStream_t stream);
+
+// One etg_embed_gather_grad call (rowgrad.hip); pitch in bytes.
+struct RowGrad {
+  const int32_t* ids;
+  int64_t n, V, hidden;
+  const void* grad;
+  int32_t grad_dtype;
+  int64_t pitch;
+  float scale;
+  void* out;
+  int32_t out_dtype, add;
+};
+size_t rowgrad_workspace(int64_t n, int64_t V, int64_t hidden);
+hipError_t launch_rowgrad(const RowGrad& g, void* ws, hipStream_t stream);
+
 }  // namespace etg
 
 // The opaque handle of etg.h: host metadata of a table in device memory.

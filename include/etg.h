@@ -527,6 +527,92 @@ int32_t etg_sample(const void* d_logits, int32_t dtype, int64_t batch, int64_t v
                    const etg_sampling* how, const float* d_uniform, int32_t* d_ids, float* d_probs,
                    void* d_workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Training and evaluation of a tied table (f32, bf16 and f16 tables): the softmax cross
+ * entropy of residual rows against their next tokens over the whole vocabulary, its
+ * gradients, and the gradient of the row gather.  The V-wide logits are never in memory.
+ *
+ *   L[b][v]  = sum_i residual[b][i] * row v[i]        (f32 accumulation)
+ *   lse[b]   = ln sum_v exp(L[b][v])
+ *   loss[b]  = lse[b] - L[b][labels[b]];  0 where the label, as uint32, is not below vocab
+ *              (so every negative one): a position without a target
+ *
+ *   d_residual       [batch][hidden] of the TABLE's dtype (ETG_F32, ETG_BF16, ETG_F16; the
+ *                    products' operands are of one type), rows residual_stride values apart
+ *                    (at least hidden, bounded as in etg_quantize_i8), aligned to the value;
+ *                    rows that are not 16-byte aligned are first copied
+ *   batch            0 <= batch <= 65536; 0 enqueues nothing
+ *   d_labels         int32 [batch]
+ *   d_loss, d_lse    f32 [batch]
+ *   d_workspace      at least etg_cross_entropy_workspace() bytes, 256-byte aligned (may be
+ *                    NULL where that is 0)
+ * Accuracy: |lse - exact| <= max_v of the logits' error (f32 accumulation of hidden
+ * products) + about 1e-6 * max(1, |lse|); the loss twice that.  A NaN among a row's logits,
+ * or +inf, makes its lse and loss NaN; logits of -inf weigh nothing.  Results are bitwise
+ * repeatable.
+ * Errors: EINVAL (null), EDTYPE (a Q8_0 table), ESHAPE, EALIGN, EWORKSPACE.
+ */
+int64_t etg_cross_entropy_workspace(const etg_table* lm_head, int64_t batch);
+int32_t etg_cross_entropy(const etg_table* lm_head, const void* d_residual, int64_t residual_stride, int64_t batch,
+                          const int32_t* d_labels, float* d_loss, float* d_lse, void* d_workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of etg_cross_entropy, from its lse and the gradients g that reach loss and h that
+ * reach lse (for a penalty on it, for instance):
+ *   D[b][v]          = (g_b + h_b) exp(L[b][v] - lse[b]) - g_b [v == labels[b]],
+ *                      g_b = 0 where the label is outside the vocabulary
+ *   residual_grad[b] = sum_v D[b][v] row v
+ *   table_grad[v]    = sum_b D[b][v] residual[b]   (+ table_grad[v] with accumulate)
+ * The logits are computed again, by pieces of the vocabulary.  D is rounded once to the
+ * table's dtype (f16: times a power of two that keeps it in range), the sums are f32, each
+ * result is rounded once.  A row with g_b + h_b = 0 and g_b = 0 has D = 0 whatever its logits
+ * are (its residual still enters table_grad as 0 * residual).
+ *   d_lse               f32 [batch], as etg_cross_entropy wrote it
+ *   grad_loss           g for all rows, or d_grad_loss f32 [batch] where that is not NULL
+ *   d_grad_lse          NULLABLE f32 [batch]: h (NULL: 0)
+ *   d_residual_grad     NULLABLE (not wanted) [batch][hidden] of the table's dtype, rows
+ *                       residual_grad_stride values apart, aligned to the value
+ *   d_table_grad        NULLABLE (not wanted; a frozen lm_head) [vocab][hidden] of the table's
+ *                       dtype, 16-byte aligned; with batch 0 it is set to 0 (accumulate: left)
+ *   accumulate          0: table_grad is overwritten; else the sum is added to it
+ * Nothing written may overlap what is read (table_grad with accumulate aside) or the
+ * workspace of etg_cross_entropy_grad_workspace() bytes.  Results are bitwise repeatable.
+ * Errors: as etg_cross_entropy.
+ */
+int64_t etg_cross_entropy_grad_workspace(const etg_table* lm_head, int64_t batch);
+int32_t etg_cross_entropy_grad(const etg_table* lm_head, const void* d_residual, int64_t residual_stride,
+                               int64_t batch, const int32_t* d_labels, const float* d_lse, float grad_loss,
+                               const float* d_grad_loss, const float* d_grad_lse, void* d_residual_grad,
+                               int64_t residual_grad_stride, void* d_table_grad, int32_t accumulate,
+                               void* d_workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of etg_embed_gather with respect to the table:
+ *   out[v] = [out[v] +] scale * sum over the positions i with ids[i] == v, in their order, of grad[i]
+ * (sums, product and addition in f32, one rounding to the output type).  A bad id (>= vocab as
+ * uint32), whose gathered row is zero, adds nothing.
+ *   table        its vocab, hidden and dtype (not Q8_0) alone
+ *   d_ids        int32 [seq_len]
+ *   seq_len      0 <= seq_len <= 2^24; 0 writes zeros (accumulate: nothing)
+ *   d_grad       `grad_dtype` (ETG_F32, ETG_BF16, ETG_F16) [seq_len][hidden], rows grad_stride
+ *                values apart (at least hidden, bounded as in etg_quantize_i8), aligned to the
+ *                value
+ *   scale        as in the gather
+ *   d_out        `out_dtype` (the table's or ETG_F32) [vocab][hidden], 16-byte aligned
+ *   accumulate   0: every row is written (zeros where no id is); else only rows of given ids
+ *                change
+ *   d_workspace  at least etg_embed_gather_grad_workspace() bytes, 256-byte aligned (may be NULL
+ *                where that is 0)
+ * The sums are formed over the positions sorted by token, without atomics: results are bitwise
+ * repeatable.
+ * Errors: EINVAL (null), EDTYPE, ESHAPE, EALIGN, EWORKSPACE.
+ */
+int64_t etg_embed_gather_grad_workspace(const etg_table* table, int64_t seq_len);
+int32_t etg_embed_gather_grad(const etg_table* table, const int32_t* d_ids, int64_t seq_len, const void* d_grad,
+                              int32_t grad_dtype, int64_t grad_stride, float scale, void* d_out, int32_t out_dtype,
+                              int32_t accumulate, void* d_workspace, size_t workspace_bytes, void* stream);
+
 /* Message of the calling thread's last failed call ("" if none). */
 const char* etg_last_error(void);
 
