@@ -8,6 +8,7 @@
 // vocabulary in pieces: the product again, with D (rounded to the table's type, the operand
 // of the two other products) as its result, then the piece's share of dx and its rows of dE.
 #include <algorithm>
+#include <type_traits>
 
 #include "etg_device.hpp"
 #include "etg_internal.hpp"
@@ -22,6 +23,7 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kXWaves = 8;
+constexpr int kGroup = 4;  // tiles along n that neighbouring workgroups share
 constexpr uint32_t kOutside = 0x80000000u;  // a copy's offset past its descriptor: zeros arrive
 
 template <int DT>
@@ -108,32 +110,38 @@ struct Operand {
     }
 #pragma unroll
     for (int j = 0; j < COPIES; j++) {
-      const int q = wv * COPIES + j;
+      const int q = place(wv, j);
       if constexpr (TR) {
         const int at = q % 16 * 1024 + lane * 16, k = at / LINE, piece = at % LINE / 16 ^ swizzle(k);
         const int row = q / 16 * 128 + piece * (16 / ES);  // rows are whole pieces: the pitch and their number are
         k_of[j] = k;
         off[j] = row < left ? (uint32_t)(k * pitch) + (uint32_t)(row * ES) : kOutside;
       } else {
-        const int row = 8 * q + (lane >> 3), piece = (lane & 7) ^ ((row >> 1) & 7);
+        const int row = 8 * q + (lane >> 3);
+        const int piece = (lane & 7) ^ (4 * (COPIES == 1 ? q & 1 : j & 1) + (lane >> 4));  // (row / 2) % 8
         k_of[j] = 16 * piece;
         off[j] = row < left ? (uint32_t)(row * pitch) + (uint32_t)(16 * piece) : kOutside;
       }
     }
   }
-  // the wave's j-th copy of stage s to the image at lds
+  // the wave's j-th copy of stage s to the image at lds (copies of 128 rows of a tile are
+  // side by side: j of R / 64)
   __device__ __forceinline__ void copy(int s, int j, int wv, uint32_t lds) const {
     const int step = TR ? s * KS : s * 128;
     // a lane outside stays outside: 2^31 plus at most 2^30 bytes of K values
     const uint32_t at = k_of[j] + step < k_end ? off[j] + (TR ? 0u : (uint32_t)step) : kOutside;
-    copy_1k(TR ? base + (uint64_t)step * (uint64_t)pitch : base, at, lds + (uint32_t)(wv * COPIES + j) * 1024);
+    copy_1k(TR ? base + (uint64_t)step * (uint64_t)pitch : base, at, lds + (uint32_t)place(wv, j) * 1024);
+  }
+  // which KiB of the image a copy fills: with 256 rows, the wave's first half of copies lies in
+  // rows 0 .. 127 and the second in the others
+  static __device__ __forceinline__ int place(int wv, int j) {
+    return COPIES == 4 ? j / 2 * 16 + wv * 2 + j % 2 : wv * COPIES + j;
   }
   // Fragment of rows [row, row + 16) (row a multiple of 16) and K half kk of the stage at img.
   static __device__ __forceinline__ u32x4 read(const unsigned char* img, int row, int kk, int lane) {
     const int g = lane >> 4;
     if constexpr (!TR) {
-      const int r = row + (lane & 15);
-      return *(const u32x4*)(img + r * 128 + 16 * ((4 * kk + g) ^ ((r >> 1) & 7)));
+      return *(const u32x4*)(img + row * 128 + (lane & 15) * 128 + 16 * ((4 * kk + g) ^ ((lane >> 1) & 7)));
     } else if constexpr (ES == 2) {
       // ds_read_b64_tr_b16: 16 lanes read a 4 x 16 block, lane i K value i / 4 of it and rows
       // 4 (i % 4) .. + 3, and receive row i's four K values
@@ -166,7 +174,6 @@ struct XentProduct {
   int32_t mt, nt;            // tiles
   int32_t splits;            // K slices of kslice values (a multiple of a stage)
   int32_t kslice;
-  bool m_first;              // consecutive workgroups: tiles along m (else along n)
   // X_STATS: part [n][mt], target [n]; X_DLOGIT: D [n][out_pitch bytes]
   // X_PART: f32 [splits][n][m]; X_OUT: values of the type, [n][m]
   void* out;
@@ -211,24 +218,27 @@ __device__ __forceinline__ float2 stats_join(float2 a, float2 b) {
 }
 
 // What a wave does with its MT x NT tiles of 16 x 16: registers i of tile (a, t) are rows
-// mw + 16 a + 4 (lane / 16) + i and column nw + 16 t + lane % 16 of the product.
+// m0 + row(a) + 4 (lane / 16) + i and column n0 + col(t) + lane % 16 of the product, where the
+// first AH (TH) tiles along a direction are neighbours and the others lie 128 further.
 // smem: the LDS of the finished K loop, all of it free.
-template <int DT, int MODE, int MT, int NT, int WM, int BN>
-__device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT], int64_t mw, int64_t nw, int mtile,
-                                       int64_t n0, int split, int wm, int lane, unsigned char* smem) {
+template <int DT, int MODE, int MT, int NT, int AH, int TH, int WM, int BN>
+__device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT], int64_t m0, int64_t n0, int mrow,
+                                       int ncol, int mtile, int split, int wm, int lane, unsigned char* smem) {
   const int g = lane >> 4;
+  auto row_of = [&](int a) { return m0 + mrow + a / AH * 128 + a % AH * 16 + 4 * g; };
+  auto col_of = [&](int t) { return n0 + ncol + t / TH * 128 + t % TH * 16 + (lane & 15); };
   if constexpr (MODE == X_STATS) {
     float2* red = (float2*)smem;  // [WM][BN]
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-      const int64_t n = nw + 16 * t + (lane & 15);
+      const int64_t n = col_of(t);
       const int64_t label = n < p.n ? (int64_t)(uint32_t)p.labels[n] - p.v0 : -1;  // its row in the piece
       float m = -__builtin_inff(), s = 0.f;
 #pragma unroll
       for (int a = 0; a < MT; a++)
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          const int64_t v = mw + 16 * a + 4 * g + i;
+          const int64_t v = row_of(a) + i;
           if (v < p.m) m = fmaxf(m, acc[a][t][i]);
           if (v == label && v < p.m) p.target[n] = acc[a][t][i];
         }
@@ -240,7 +250,7 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
       for (int a = 0; a < MT; a++)
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          const int64_t v = mw + 16 * a + 4 * g + i;
+          const int64_t v = row_of(a) + i;
           if (v < p.m) s += __builtin_amdgcn_exp2f((acc[a][t][i] - at) * kLog2e);
         }
       s += __shfl_xor(s, 16, 64);
@@ -257,7 +267,7 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
     const float scale = p.scale != nullptr ? p.scale[0] : 1.f;
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-      const int64_t n = nw + 16 * t + (lane & 15);
+      const int64_t n = col_of(t);
       if (n >= p.n) continue;
       const uint32_t token = (uint32_t)p.labels[n];
       const float gl = token < (uint64_t)p.vocab ? (p.grad_loss != nullptr ? p.grad_loss[n] : p.grad_loss_all) : 0.f;
@@ -267,7 +277,7 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
       unsigned char* row = (unsigned char*)p.out + n * p.out_pitch;
 #pragma unroll
       for (int a = 0; a < MT; a++) {
-        const int64_t v = mw + 16 * a + 4 * g;
+        const int64_t v = row_of(a);
         f32x4 d;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
@@ -284,12 +294,12 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
     constexpr int ODT = MODE == X_PART ? DT_F32 : DT;
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-      const int64_t n = nw + 16 * t + (lane & 15);
+      const int64_t n = col_of(t);
       if (n >= p.n) continue;
       unsigned char* row = (unsigned char*)p.out + ((int64_t)split * p.n + n) * p.m * kValue<ODT>;
 #pragma unroll
       for (int a = 0; a < MT; a++) {
-        const int64_t m = mw + 16 * a + 4 * g;
+        const int64_t m = row_of(a);
         if (m >= p.m) continue;  // m is a multiple of 4
         f32x4 x = acc[a][t] * scale;
         if (p.add) x += load4<ODT>(row + m * kValue<ODT>);
@@ -300,7 +310,8 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
 }
 
 // Tile and K slice of a workgroup.  Ids {x, x + 8, ...} run on XCD x: each XCD takes a
-// contiguous share of the tiles, so that neighbours find their common operand in its L2.
+// contiguous share of the tiles, in blocks of kGroup tiles along n by all along m: its 32
+// CUs work on about kGroup x 32 / kGroup tiles, which share their operands' slices in its L2.
 struct XentPlace {
   int mtile, ntile, split;
   bool some;
@@ -311,11 +322,11 @@ struct XentPlace {
     some = tile < each * p.splits;
     split = __builtin_amdgcn_readfirstlane(tile / each);
     tile -= split * each;
-    const int fast = p.m_first ? p.mt : p.nt;
-    const int slow = __builtin_amdgcn_readfirstlane(tile / fast);
-    tile -= slow * fast;
-    mtile = p.m_first ? tile : slow;
-    ntile = p.m_first ? slow : tile;
+    const int block = __builtin_amdgcn_readfirstlane(tile / (kGroup * p.mt));
+    tile -= block * kGroup * p.mt;
+    const int wide = min(kGroup, p.nt - block * kGroup);
+    mtile = __builtin_amdgcn_readfirstlane(tile / wide);
+    ntile = block * kGroup + tile - mtile * wide;
   }
 };
 
@@ -371,8 +382,113 @@ __global__ void __launch_bounds__(64 * kXWaves) ring_kernel(XentProduct p) {
   }
   load_wait<0>();
   bare_barrier();
-  finish<DT, MODE, MT, NT, WM, BN>(p, acc, m0 + wm * (BM / WM), n0 + wn * (BN / WN), at.mtile, n0, at.split, wm, lane,
-                                   smem);
+  finish<DT, MODE, MT, NT, MT, NT, WM, BN>(p, acc, m0, n0, wm * (BM / WM), wn * (BN / WN), at.mtile, at.split, wm, lane,
+                                           smem);
+}
+
+// Tiles of 256 x 256, bound by the matrix cores.  Two LDS images of a stage; 2 x 4 waves, two
+// per SIMD, each with 64 rows of either half of A's tile and 32 of either half of B's.  A
+// stage is four steps, one for each pair of halves: a step reads one half's fragments, issues
+// two copies, then runs its 16 fragment products.  The waves of the second row of waves are
+// one barrier behind the first, so that on every SIMD one wave's products run while the
+// other reads.  B's halves are taken in turn, so that the one a stage begins with is read in
+// the last step before it.  A half of an image is free once the second row of waves has read
+// it, a step after the first, and is refilled in that step: every copy has six steps, one
+// and a half stages, until it is waited for.
+template <int DT, bool TA, bool TB, int MODE>
+__global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
+  using A = Operand<DT, TA, 256>;
+  using B = Operand<DT, TB, 256>;
+  constexpr int IMG = A::BYTES + B::BYTES;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [2][IMG]
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wv / 4, wn = wv % 4;
+  const XentPlace at(p);
+  if (!at.some) return;  // whole workgroup
+  const int64_t m0 = (int64_t)at.mtile * 256, n0 = (int64_t)at.ntile * 256, k0 = (int64_t)at.split * p.kslice;
+  const int kn = (int)min((int64_t)p.kslice, p.k - k0), stages = (kn + A::KS - 1) / A::KS;
+  const A oa(p.a, p.a_pitch, m0, p.m, k0, kn, wv, lane);
+  const B ob(p.b, p.b_pitch, n0, p.n, k0, kn, wv, lane);
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem;
+  // half h of stage s (past the last stage: zeros that nothing reads)
+  auto copy_a = [&](int s, int h) {
+    oa.copy(s, 2 * h, wv, lds + (uint32_t)(s & 1) * IMG);
+    oa.copy(s, 2 * h + 1, wv, lds + (uint32_t)(s & 1) * IMG);
+  };
+  auto copy_b = [&](int s, int h) {
+    ob.copy(s, 2 * h, wv, lds + (uint32_t)(s & 1) * IMG + A::BYTES);
+    ob.copy(s, 2 * h + 1, wv, lds + (uint32_t)(s & 1) * IMG + A::BYTES);
+  };
+  f32x4 acc[8][4];
+#pragma unroll
+  for (int a = 0; a < 8; a++)
+#pragma unroll
+    for (int t = 0; t < 4; t++) acc[a][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 fa[4][2], fb[2][2][2];
+  auto read_a = [&](int s, int h) {
+#pragma unroll
+    for (int a = 0; a < 4; a++)
+#pragma unroll
+      for (int kk = 0; kk < 2; kk++) fa[a][kk] = A::read(smem + (s & 1) * IMG, 128 * h + 64 * wm + 16 * a, kk, lane);
+  };
+  auto read_b = [&](int s, int h) {
+#pragma unroll
+    for (int t = 0; t < 2; t++)
+#pragma unroll
+      for (int kk = 0; kk < 2; kk++)
+        fb[h][t][kk] = B::read(smem + (s & 1) * IMG + A::BYTES, 128 * h + 32 * wn + 16 * t, kk, lane);
+  };
+  auto products = [&](int ha, int hb) {
+    load_wait<12>();  // the fragments are read; the half that the next step reads has landed
+    __builtin_amdgcn_sched_barrier(0);
+    bare_barrier();
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int kk = 0; kk < 2; kk++)
+#pragma unroll
+      for (int a = 0; a < 4; a++)
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+          acc[4 * ha + a][2 * hb + t] = mma<DT>(fa[a][kk], fb[hb][t][kk], acc[4 * ha + a][2 * hb + t]);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    bare_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Stage s, half F of B first (its fragments are there).
+  auto stage = [&](int s, auto first) {
+    constexpr int F = decltype(first)::value, L = 1 - F;
+    copy_b(s + 2, F);
+    read_a(s, 0);
+    products(0, F);
+    copy_a(s + 2, 0);
+    read_b(s, L);
+    products(0, L);
+    copy_b(s + 2, L);
+    read_a(s, 1);
+    products(1, L);
+    copy_a(s + 2, 1);
+    read_b(s + 1, L);
+    products(1, F);
+  };
+  copy_b(0, 0), copy_a(0, 0), copy_b(0, 1), copy_a(0, 1);
+  copy_b(1, 1), copy_a(1, 0), copy_b(1, 0), copy_a(1, 1);
+  load_wait<12>();
+  bare_barrier();
+  read_b(0, 0);
+  load_wait<12>();
+  bare_barrier();  // the first step refills what was read here
+  if (wm == 1) bare_barrier();
+  int s = 0;
+  for (; s + 1 < stages; s += 2) {
+    stage(s, std::integral_constant<int, 0>{});
+    stage(s + 1, std::integral_constant<int, 1>{});
+  }
+  if (s < stages) stage(s, std::integral_constant<int, 0>{});
+  if (wm == 0) bare_barrier();
+  load_wait<0>();
+  bare_barrier();
+  finish<DT, MODE, 8, 4, 4, 2, 2, 256>(p, acc, m0, n0, 64 * wm, 32 * wn, at.mtile, at.split, wm, lane, smem);
 }
 
 // Joins a piece's statistics [n][mt] into run [n]; the last piece writes lse and loss.  One
@@ -475,34 +591,54 @@ hipError_t launch_ring(const XentProduct& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int DT, bool TA, bool TB, int MODE>
+hipError_t launch_tile(const XentProduct& p, hipStream_t stream) {
+  const void* fn = (const void*)tile_kernel<DT, TA, TB, MODE>;
+  const size_t lds = 2 * 512 * 128;
+  hipError_t e = set_dynamic_lds(fn, lds);
+  if (e != hipSuccess) return e;
+  const int64_t tiles = (int64_t)p.mt * p.nt * p.splits;
+  hipLaunchKernelGGL((tile_kernel<DT, TA, TB, MODE>), dim3((unsigned)(cdiv(tiles, kXcdCount) * kXcdCount)),
+                     dim3(64 * kXWaves), lds, stream, p);
+  return hipGetLastError();
+}
+
 // A product whose columns are residual rows.
 template <int DT, bool TA, int MODE>
 hipError_t launch_by_rows(const XentProduct& p, int bn, hipStream_t stream) {
   if (bn == 64) return launch_ring<DT, TA, false, MODE, 256, 64, 8, 4>(p, stream);
   if (bn == 128) return launch_ring<DT, TA, false, MODE, 256, 128, 4, 3>(p, stream);
-  return launch_ring<DT, TA, false, MODE, 256, 256, 2, 2>(p, stream);
+  return launch_tile<DT, TA, false, MODE>(p, stream);
 }
 
 constexpr int64_t kMaxTiles = 1 << 20;             // of one launch
 constexpr int64_t kPartBytes = (int64_t)256 << 20;  // statistics, or D, of one piece
 
-// Forward: vocabulary rows per piece (a multiple of 256).
+// Pieces of at most `most` tiles of 256 table rows, as even as they get; in rows.
+int64_t even_piece(int64_t vocab, int64_t most) {
+  const int64_t tiles = cdiv(vocab, 256);
+  return cdiv(tiles, cdiv(tiles, std::max<int64_t>(1, most))) * 256;
+}
+// Forward: the piece's statistics stay within kPartBytes.
 int64_t forward_piece(int64_t vocab, int64_t n) {
-  const int64_t nt = cdiv(n, rows_tile(n));
-  const int64_t mt = std::max<int64_t>(1, std::min(kMaxTiles / nt, kPartBytes / (n * 8)));
-  return std::min(mt, cdiv(vocab, 256)) * 256;
+  return even_piece(vocab, std::min(kMaxTiles / cdiv(n, rows_tile(n)), kPartBytes / (n * 8)));
 }
 // Backward: D of a piece stays within kPartBytes and its rows within 4 MiB.
 int64_t backward_piece(int64_t vocab, int64_t n, int size) {
-  const int64_t nt = cdiv(n, rows_tile(n));
-  const int64_t mt =
-      std::max<int64_t>(1, std::min(std::min(kMaxTiles / nt, (int64_t)4096), kPartBytes / (n * size * 256)));
-  return std::min(mt, cdiv(vocab, 256)) * 256;
+  return even_piece(vocab, std::min(std::min(kMaxTiles / cdiv(n, rows_tile(n)), (int64_t)4096),
+                                    kPartBytes / (n * size * 256)));
 }
-// K slices of dx = D E: enough workgroups to fill the card, at least 512 table rows each.
+// K slices of dx = D E: the fewest rounds of one workgroup per CU, times the stages of one and
+// what its start and end cost (about 24 stages); at least 512 table rows each.
 int64_t backward_splits(int64_t piece, int64_t n, int64_t hidden) {
   const int64_t tiles = cdiv(hidden, 256) * cdiv(n, rows_tile(n));
-  return std::max<int64_t>(1, std::min(cdiv(2 * kTargetBlocks, tiles), piece / 512));
+  int64_t best = 1, least = INT64_MAX;
+  for (int64_t s = 1; s <= std::max<int64_t>(1, piece / 512) && s <= 2 * kTargetBlocks; s++) {
+    const int64_t cost = cdiv(tiles * s, kTargetBlocks) * (cdiv(piece, 64 * s) + 24);
+    if (cost < least) least = cost, best = s;
+    if (tiles * s >= 8 * kTargetBlocks) break;
+  }
+  return best;
 }
 int64_t backward_slice(int64_t piece, int64_t splits) { return (int64_t)align_up(cdiv(piece, splits), 64); }
 
@@ -608,9 +744,8 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
       p.a = x, p.a_pitch = x_pitch, p.b = d, p.b_pitch = w.piece * kValue<DT>;
       p.mt = (int32_t)cdiv(t.hidden, 256), p.nt = (int32_t)cdiv(rows, 256);
       p.splits = 1, p.kslice = (int32_t)align_up((size_t)c.n, 64);
-      p.m_first = true;
       p.out = (uint8_t*)c.d_rows + v0 * t.row_bytes, p.add = c.add, p.scale = scale;
-      if ((e = launch_ring<DT, true, true, X_OUT, 256, 256, 2, 2>(p, stream)) != hipSuccess) return e;
+      if ((e = launch_tile<DT, true, true, X_OUT>(p, stream)) != hipSuccess) return e;
     }
   }
   if (c.d_x != nullptr) {
