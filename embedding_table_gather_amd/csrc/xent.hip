@@ -7,6 +7,11 @@
 // tiles leave a (maximum, sum of exponentials) per residual row.  The backward pass takes the
 // vocabulary in pieces: the product again, with D (rounded to the table's type, the operand
 // of the two other products) as its result, then the piece's share of dx and its rows of dE.
+//
+// D's entry at a label, g (p - 1) + h p, is most of what a row contributes, and is p - 1
+// near 0 in a trained model: it is computed with expm1, and what its rounding to 16 bits takes
+// away is added to dx from a list.  Up to 64 residual rows the products are bound by memory,
+// and D is kept as the sum of two 16-bit values; up to 8, in f32.
 #include <algorithm>
 #include <type_traits>
 
@@ -166,7 +171,7 @@ struct Operand {
 };
 
 // One product C[m][n] = sum_k A[m][k] B[n][k].
-enum { X_STATS, X_DLOGIT, X_PART, X_OUT };
+enum { X_STATS, X_DLOGIT, X_DLOGIT32, X_PART, X_OUT };
 struct XentProduct {
   const uint8_t *a, *b;
   int64_t a_pitch, b_pitch;  // bytes
@@ -174,10 +179,12 @@ struct XentProduct {
   int32_t mt, nt;            // tiles
   int32_t splits;            // K slices of kslice values (a multiple of a stage)
   int32_t kslice;
-  // X_STATS: part [n][mt], target [n]; X_DLOGIT: D [n][out_pitch bytes]
+  // X_STATS: part [n][mt], target [n]; X_DLOGIT: D [n][out_pitch bytes]; X_DLOGIT32: f32 D [m][8]
   // X_PART: f32 [splits][n][m]; X_OUT: values of the type, [n][m]
   void* out;
   int64_t out_pitch;
+  void* out_low;             // X_DLOGIT: what the rounding took away, rounded too, laid out as D (NULL: none)
+  float* rest;               // X_DLOGIT: [n], what it took away from the label's entry (NULL: not wanted)
   int32_t add;               // X_PART, X_OUT: to what is there
   const int32_t* labels;     // [n]
   int64_t v0, vocab;         // the piece's first table row
@@ -195,8 +202,10 @@ __device__ __forceinline__ auto round4(f32x4 x) {
   else return __builtin_convertvector(x, f16x4);
 }
 template <int DT>
-__device__ __forceinline__ void store4(void* at, f32x4 x) {
-  *(decltype(round4<DT>(x))*)at = round4<DT>(x);
+__device__ __forceinline__ auto round1(float x) {
+  if constexpr (DT == DT_F32) return x;
+  else if constexpr (DT == DT_BF16) return (__bf16)x;
+  else return (_Float16)x;
 }
 template <int DT>
 __device__ __forceinline__ f32x4 load4(const void* at) {
@@ -209,6 +218,65 @@ __device__ __forceinline__ f32x4 load4(const void* at) {
   }
 }
 
+// Stores `most` of the 16 AH values that the lanes {l, l + 16, l + 32, l + 48} hold of one row
+// (x[a][i] of lane row g is value 16 a + 4 g + i) at `at`, where `some`.  16-bit types exchange
+// them between the lanes first, so that a lane stores 4 AH values side by side (16-byte stores,
+// whole 128-byte lines per row for AH = 4, instead of 8 bytes in every 32).
+template <int DT, int AH>
+__device__ __forceinline__ void store_rows(unsigned char* at, const f32x4 (&x)[AH], int g, bool some, int most) {
+  if constexpr (DT == DT_F32) {
+#pragma unroll
+    for (int a = 0; a < AH; a++)
+      if (some && 16 * a + 4 * g < most) *(f32x4*)(at + (16 * a + 4 * g) * 4) = x[a];
+  } else {
+    static_assert(AH == 4, "four tiles are exchanged");
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    u32x2 r[4];
+#pragma unroll
+    for (int a = 0; a < 4; a++) r[a] = __builtin_bit_cast(u32x2, round4<DT>(x[a]));
+#pragma unroll
+    for (int w = 0; w < 2; w++) {
+#pragma unroll
+      for (int a = 0; a < 2; a++) {
+        const u32x2 s = __builtin_amdgcn_permlane32_swap(r[a][w], r[a + 2][w], false, false);
+        r[a][w] = s[0], r[a + 2][w] = s[1];
+      }
+#pragma unroll
+      for (int a = 0; a < 4; a += 2) {
+        const u32x2 s = __builtin_amdgcn_permlane16_swap(r[a][w], r[a + 1][w], false, false);
+        r[a][w] = s[0], r[a + 1][w] = s[1];
+      }
+    }
+    // lane row g: values 16 g .. 16 g + 15
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+      if (some && 16 * g + 8 * h < most)
+        *(u32x4*)(at + (16 * g + 8 * h) * 2) = u32x4{r[2 * h][0], r[2 * h][1], r[2 * h + 1][0], r[2 * h + 1][1]};
+  }
+}
+
+// What D's entries of one residual row need.
+struct DRow {
+  float g, h, both, lse;
+  int64_t label;  // the label's row in the piece; negative where there is none
+  __device__ __forceinline__ DRow(const XentProduct& p, int64_t n) {
+    const uint32_t token = (uint32_t)p.labels[n];
+    g = token < (uint64_t)p.vocab ? (p.grad_loss != nullptr ? p.grad_loss[n] : p.grad_loss_all) : 0.f;
+    h = p.grad_lse != nullptr ? p.grad_lse[n] : 0.f;
+    both = g + h;
+    label = token < (uint64_t)p.vocab ? (int64_t)token - p.v0 : -1;
+    lse = p.lse[n];
+  }
+  // A row that nothing reaches has no gradient, whatever its logits are.
+  __device__ __forceinline__ float other(float l) const {
+    return both == 0.f ? 0.f : both * __builtin_amdgcn_exp2f((l - lse) * kLog2e);
+  }
+  // (g + h) p - g without the cancellation near p = 1
+  __device__ __forceinline__ float at_label(float l) const {
+    return g == 0.f && h == 0.f ? 0.f : g * expm1f(l - lse) + h * __builtin_amdgcn_exp2f((l - lse) * kLog2e);
+  }
+};
+
 // (maximum, sum of exp relative to it) of the union of two sets; (-inf, 0) is the empty one.
 // A NaN in either sum stays.
 __device__ __forceinline__ float2 stats_join(float2 a, float2 b) {
@@ -218,30 +286,42 @@ __device__ __forceinline__ float2 stats_join(float2 a, float2 b) {
 }
 
 // What a wave does with its MT x NT tiles of 16 x 16: registers i of tile (a, t) are rows
-// m0 + row(a) + 4 (lane / 16) + i and column n0 + col(t) + lane % 16 of the product, where the
-// first AH (TH) tiles along a direction are neighbours and the others lie 128 further.
+// m0 + mrow + off(a) + 4 (lane / 16) + i and column n0 + ncol + off(t) + lane % 16 of the product,
+// where the first AH (TH) tiles along a direction are neighbours and the others lie 128 further.
 // smem: the LDS of the finished K loop, all of it free.
 template <int DT, int MODE, int MT, int NT, int AH, int TH, int WM, int BN>
 __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT], int64_t m0, int64_t n0, int mrow,
                                        int ncol, int mtile, int split, int wm, int lane, unsigned char* smem) {
   const int g = lane >> 4;
-  auto row_of = [&](int a) { return m0 + mrow + a / AH * 128 + a % AH * 16 + 4 * g; };
+  // rows in 32 bits, from this lane's first one
+  auto off = [](int a) { return a / AH * 128 + a % AH * 16; };
   auto col_of = [&](int t) { return n0 + ncol + t / TH * 128 + t % TH * 16 + (lane & 15); };
+  const int first = mrow + 4 * g, rows = (int)min(p.m - m0, (int64_t)256) - first;
+  auto place = [&](int64_t row) {  // of a row of the piece; negative where the tile lacks it
+    return row >= m0 && row < m0 + 256 && row < p.m ? (int)(row - m0) - first : -1024;
+  };
   if constexpr (MODE == X_STATS) {
     float2* red = (float2*)smem;  // [WM][BN]
 #pragma unroll
     for (int t = 0; t < NT; t++) {
       const int64_t n = col_of(t);
-      const int64_t label = n < p.n ? (int64_t)(uint32_t)p.labels[n] - p.v0 : -1;  // its row in the piece
+      const int label = n < p.n ? place((int64_t)(uint32_t)p.labels[n] - p.v0) : -1024;
       float m = -__builtin_inff(), s = 0.f;
 #pragma unroll
       for (int a = 0; a < MT; a++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int64_t v = row_of(a) + i;
-          if (v < p.m) m = fmaxf(m, acc[a][t][i]);
-          if (v == label && v < p.m) p.target[n] = acc[a][t][i];
-        }
+        for (int i = 0; i < 4; i++)
+          if (off(a) + i < rows) m = fmaxf(m, acc[a][t][i]);
+      if (__ballot(label >= 0) != 0) {
+        float l = 0.f;
+        bool here = false;
+#pragma unroll
+        for (int a = 0; a < MT; a++)
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            if (off(a) + i == label) l = acc[a][t][i], here = true;
+        if (here) p.target[n] = l;
+      }
       m = fmaxf(m, __shfl_xor(m, 16, 64));
       m = fmaxf(m, __shfl_xor(m, 32, 64));
       // all -inf (or no row): exp2(-inf) = 0 for each, a NaN stays one
@@ -249,10 +329,8 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
 #pragma unroll
       for (int a = 0; a < MT; a++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int64_t v = row_of(a) + i;
-          if (v < p.m) s += __builtin_amdgcn_exp2f((acc[a][t][i] - at) * kLog2e);
-        }
+        for (int i = 0; i < 4; i++)
+          if (off(a) + i < rows) s += __builtin_amdgcn_exp2f((acc[a][t][i] - at) * kLog2e);
       s += __shfl_xor(s, 16, 64);
       s += __shfl_xor(s, 32, 64);
       if (g == 0) red[wm * BN + (int)(n - n0)] = make_float2(m, s);
@@ -263,30 +341,57 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
       for (int w = 1; w < WM; w++) r = stats_join(r, red[w * BN + c]);
       if (n0 + c < p.n) ((float2*)p.out)[(n0 + c) * p.mt + mtile] = r;
     }
-  } else if constexpr (MODE == X_DLOGIT) {
+  } else if constexpr (MODE == X_DLOGIT || MODE == X_DLOGIT32) {
     const float scale = p.scale != nullptr ? p.scale[0] : 1.f;
 #pragma unroll
     for (int t = 0; t < NT; t++) {
       const int64_t n = col_of(t);
-      if (n >= p.n) continue;
-      const uint32_t token = (uint32_t)p.labels[n];
-      const float gl = token < (uint64_t)p.vocab ? (p.grad_loss != nullptr ? p.grad_loss[n] : p.grad_loss_all) : 0.f;
-      const float both = p.grad_lse != nullptr ? gl + p.grad_lse[n] : gl;
-      const int64_t label = (int64_t)token - p.v0;
-      const float lse = p.lse[n];
-      unsigned char* row = (unsigned char*)p.out + n * p.out_pitch;
+      if (MODE == X_DLOGIT32 && n >= p.n) continue;
+      const DRow row(p, min(n, p.n - 1));
+      const int label = n < p.n ? place(row.label) : -1024;
 #pragma unroll
-      for (int a = 0; a < MT; a++) {
-        const int64_t v = row_of(a);
-        f32x4 d;
+      for (int a0 = 0; a0 < MT; a0 += AH) {
+        f32x4 d[AH];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const float e = __builtin_amdgcn_exp2f((acc[a][t][i] - lse) * kLog2e);
-          // a row that nothing reaches has no gradient, whatever its logits are
-          const float x = both == 0.f ? 0.f : both * e;
-          d[i] = v + i < p.m ? (x - (v + i == label ? gl : 0.f)) * scale : 0.f;
+        for (int a = 0; a < AH; a++)
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            d[a][i] = off(a0 + a) + i < rows ? row.other(acc[a0 + a][t][i]) * scale : 0.f;
+        const bool hit = label >= off(a0) && label < off(a0) + 16 * AH;
+        if (__ballot(hit) != 0) {
+          float l = 0.f;
+#pragma unroll
+          for (int a = 0; a < AH; a++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+              if (off(a0 + a) + i == label) l = acc[a0 + a][t][i];
+          const float x = row.at_label(l) * scale;
+          bool here = false;
+#pragma unroll
+          for (int a = 0; a < AH; a++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+              if (off(a0 + a) + i == label) d[a][i] = x, here = true;
+          if constexpr (DT != DT_F32 && MODE == X_DLOGIT)
+            if (here && p.rest != nullptr) p.rest[n] = x - (float)round1<DT>(x);
         }
-        store4<DT>(row + v * kValue<DT>, d);
+        if constexpr (MODE == X_DLOGIT32) {
+#pragma unroll
+          for (int a = 0; a < AH; a++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+              if (off(a0 + a) + i < rows) ((float*)p.out)[(m0 + first + off(a0 + a) + i) * 8 + n] = d[a][i];
+        } else {
+          const int64_t at = n * p.out_pitch + (m0 + mrow + a0 / AH * 128) * kValue<DT>;
+          store_rows<DT, AH>((unsigned char*)p.out + at, d, g, n < p.n, 16 * AH);
+          if constexpr (DT != DT_F32) {
+            if (p.out_low != nullptr) {
+#pragma unroll
+              for (int a = 0; a < AH; a++) d[a] -= __builtin_convertvector(round4<DT>(d[a]), f32x4);
+              store_rows<DT, AH>((unsigned char*)p.out_low + at, d, g, n < p.n, 16 * AH);
+            }
+          }
+        }
       }
     }
   } else {
@@ -295,15 +400,18 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
 #pragma unroll
     for (int t = 0; t < NT; t++) {
       const int64_t n = col_of(t);
-      if (n >= p.n) continue;
-      unsigned char* row = (unsigned char*)p.out + ((int64_t)split * p.n + n) * p.m * kValue<ODT>;
+      unsigned char* row =
+          (unsigned char*)p.out + (((int64_t)split * p.n + min(n, p.n - 1)) * p.m + m0 + mrow) * kValue<ODT>;
 #pragma unroll
-      for (int a = 0; a < MT; a++) {
-        const int64_t m = row_of(a);
-        if (m >= p.m) continue;  // m is a multiple of 4
-        f32x4 x = acc[a][t] * scale;
-        if (p.add) x += load4<ODT>(row + m * kValue<ODT>);
-        store4<ODT>(row + m * kValue<ODT>, x);
+      for (int a0 = 0; a0 < MT; a0 += AH) {
+        f32x4 x[AH];
+#pragma unroll
+        for (int a = 0; a < AH; a++) {
+          x[a] = acc[a0 + a][t] * scale;
+          // the number of rows is a multiple of 4
+          if (p.add && n < p.n && off(a0 + a) < rows) x[a] += load4<ODT>(row + (off(a0 + a) + 4 * g) * kValue<ODT>);
+        }
+        store_rows<ODT, AH>(row + off(a0) * kValue<ODT>, x, g, n < p.n, rows + 4 * g - off(a0));
       }
     }
   }
@@ -491,6 +599,167 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
   finish<DT, MODE, 8, 4, 4, 2, 2, 256>(p, acc, m0, n0, 64 * wm, 32 * wn, at.mtile, at.split, wm, lane, smem);
 }
 
+// Few table rows for few residual rows, bound by latency: a workgroup per 16 x 16 logits, its
+// four waves a quarter of K each, straight from memory.
+template <int DT, int MODE>
+__global__ void __launch_bounds__(256) direct_kernel(XentProduct p) {
+  static_assert(MODE == X_STATS || MODE == X_DLOGIT32, "what few residual rows need");
+  constexpr int U = 4;
+  __shared__ float sums[4][16][17];  // [wave][residual row][table row]
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+  const int64_t m0 = (int64_t)(blockIdx.x % p.mt) * 16, n0 = (int64_t)(blockIdx.x / p.mt) * 16;
+  const int bytes = (int)p.k * kValue<DT>, steps = (bytes + 63) / 64;
+  const int c0 = steps * wv / 4, c1 = steps * (wv + 1) / 4;
+  const uint8_t* ar = p.a + min(m0 + (lane & 15), p.m - 1) * p.a_pitch;
+  const uint8_t* br = p.b + min(n0 + (lane & 15), p.n - 1) * p.b_pitch;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int c = c0; c < c1; c += U) {
+    u32x4 a[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int at = 64 * (c + u) + 16 * g;
+      const bool in = c + u < c1 && at < bytes;  // rows are whole 16-byte pieces
+      a[u] = in ? *(const u32x4*)(ar + at) : u32x4{0, 0, 0, 0};
+      b[u] = in ? *(const u32x4*)(br + at) : u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) acc = mma<DT>(a[u], b[u], acc);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) sums[wv][lane & 15][4 * g + i] = acc[i];
+  __syncthreads();
+  // thread: residual row threadIdx / 16, table row threadIdx % 16
+  const int r = threadIdx.x & 15, c = threadIdx.x >> 4;
+  const float l = (sums[0][c][r] + sums[1][c][r]) + (sums[2][c][r] + sums[3][c][r]);
+  const int64_t v = m0 + r, n = n0 + c;
+  if constexpr (MODE == X_STATS) {
+    const bool some = v < p.m;
+    float m = some ? l : -__builtin_inff();
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+    const float at = m == -__builtin_inff() ? 0.f : m;
+    float s = some ? __builtin_amdgcn_exp2f((l - at) * kLog2e) : 0.f;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) s += __shfl_xor(s, o, 64);
+    if (n >= p.n) return;
+    if (some && v == (int64_t)(uint32_t)p.labels[n] - p.v0) p.target[n] = l;
+    if (r == 0) ((float2*)p.out)[n * p.mt + blockIdx.x % p.mt] = make_float2(m, s);
+  } else {
+    if (n >= p.n || v >= p.m) return;
+    const DRow row(p, n);
+    ((float*)p.out)[v * 8 + n] = v == row.label ? row.at_label(l) : row.other(l);
+  }
+}
+
+// Up to 8 residual rows: both gradients in one pass over the table, with vector FMAs and D in
+// f32.  A wave takes 64 pieces of 16 bytes of some consecutive table rows: their share of
+// dx stays in its registers, their rows of dE are written as they come.
+struct XentRows {
+  const uint8_t *table, *x;
+  int64_t row_bytes, x_pitch, m, per;  // per: table rows of a wave
+  int hidden, n, chunks, slices;
+  const float* d;                      // [m][8]
+  uint8_t* rows;                       // dE of the first table row, or NULL
+  int32_t add;
+  float* part;                         // [slices][n][hidden], or NULL
+  bool part_add;                       // to what is there (a later piece)
+};
+
+// The 16 bytes' values.
+template <int DT>
+__device__ __forceinline__ void unpack(u32x4 w, float (&x)[16 / kValue<DT>]) {
+#pragma unroll
+  for (int i = 0; i < 16 / kValue<DT>; i++) {
+    if constexpr (DT == DT_F32) x[i] = __uint_as_float(w[i]);
+    else if constexpr (DT == DT_BF16) x[i] = i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    else x[i] = f16_bits_to_f32(w[i / 2] >> 16 * (i % 2) & 0xffffu);
+  }
+}
+
+template <int DT, int NB>
+__global__ void __launch_bounds__(256) xent_rows_kernel(XentRows p) {
+  constexpr int E = 16 / kValue<DT>, U = 4;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = (int)blockIdx.x * 4 + wv, chunk = w % p.chunks, slice = w / p.chunks;
+  if (slice >= p.slices) return;  // whole wave
+  const int c = (chunk * 64 + lane) * E;
+  const bool live = c < p.hidden;
+  const int64_t at = (int64_t)(live ? c : 0) * kValue<DT>;
+  const int64_t begin = slice * p.per, end = min(begin + p.per, p.m);
+  float x[NB][E], acc[NB][E];
+#pragma unroll
+  for (int b = 0; b < NB; b++) {
+    unpack<DT>(b < p.n ? *(const u32x4*)(p.x + b * p.x_pitch + at) : u32x4{0, 0, 0, 0}, x[b]);
+#pragma unroll
+    for (int i = 0; i < E; i++) acc[b][i] = 0.f;
+  }
+  if (p.part_add && live) {
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+      if (b >= p.n) break;
+      const f32x4* was = (const f32x4*)(p.part + ((int64_t)slice * p.n + b) * p.hidden + c);
+#pragma unroll
+      for (int i = 0; i < E; i++) acc[b][i] = was[i / 4][i % 4];
+    }
+  }
+  for (int64_t v = begin; v < end; v += U) {
+    u32x4 row[U], old[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int64_t r = min(v + u, end - 1) * p.row_bytes + at;
+      row[u] = *(const u32x4*)(p.table + r);
+      if (p.rows != nullptr && p.add) old[u] = *(const u32x4*)(p.rows + r);
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      if (v + u >= end) break;
+      float d[NB];
+#pragma unroll
+      for (int b = 0; b < NB; b++) d[b] = b < p.n ? p.d[(v + u) * 8 + b] : 0.f;
+      if (p.part != nullptr) {
+        float e[E];
+        unpack<DT>(row[u], e);
+#pragma unroll
+        for (int b = 0; b < NB; b++)
+#pragma unroll
+          for (int i = 0; i < E; i++) acc[b][i] = fmaf(d[b], e[i], acc[b][i]);
+      }
+      if (p.rows != nullptr) {
+        float o[E], was[E];
+        if (p.add) unpack<DT>(old[u], was);
+#pragma unroll
+        for (int i = 0; i < E; i++) {
+          o[i] = 0.f;
+#pragma unroll
+          for (int b = 0; b < NB; b++) o[i] = fmaf(d[b], x[b][i], o[i]);
+          if (p.add) o[i] += was[i];
+        }
+        u32x4 out;
+#pragma unroll
+        for (int q = 0; q < E / 4; q++) {
+          const f32x4 four = {o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]};
+          if constexpr (DT == DT_F32) {
+            out = __builtin_bit_cast(u32x4, four);
+          } else {
+            const uint2 two = __builtin_bit_cast(uint2, round4<DT>(four));
+            out[2 * q] = two.x, out[2 * q + 1] = two.y;
+          }
+        }
+        if (live) *(u32x4*)(p.rows + (v + u) * p.row_bytes + at) = out;
+      }
+    }
+  }
+  if (p.part == nullptr || !live) return;
+#pragma unroll
+  for (int b = 0; b < NB; b++) {
+    if (b >= p.n) break;
+    float* to = p.part + ((int64_t)slice * p.n + b) * p.hidden + c;
+#pragma unroll
+    for (int q = 0; q < E / 4; q++)
+      ((f32x4*)to)[q] = f32x4{acc[b][4 * q], acc[b][4 * q + 1], acc[b][4 * q + 2], acc[b][4 * q + 3]};
+  }
+}
+
 // Joins a piece's statistics [n][mt] into run [n]; the last piece writes lse and loss.  One
 // wave per residual row.
 __global__ void __launch_bounds__(256) xent_join_kernel(const float2* __restrict__ part, int mt, int64_t n, bool first,
@@ -543,16 +812,35 @@ __global__ void __launch_bounds__(1024) xent_scale_kernel(const int32_t* __restr
   scale[1] = ldexpf(1.f, -min(max(e, -126), 126));
 }
 
-// out = type(sum of the K slices' partial sums, times the factor)
-template <int DT>
-__global__ void __launch_bounds__(256) xent_sum_kernel(const float* __restrict__ part, int splits, int64_t n,
-                                                       int64_t hidden, void* __restrict__ out, int64_t out_pitch,
-                                                       const float* __restrict__ scale) {
-  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x, each = hidden / 4;
-  if (q >= n * each) return;
-  const int64_t b = q / each, c = q % each * 4;
+// dx row b = type(scale * (sum of the slices' partial sums of rows b, n + b, .. + rest[b] * the
+// label's table row)).  SG slices at a time, joined in LDS.
+template <int DT, int SG>
+__global__ void __launch_bounds__(256) xent_sum_kernel(const float* __restrict__ part, int splits, int planes,
+                                                       int64_t n, int64_t hidden, void* __restrict__ out,
+                                                       int64_t out_pitch, const float* __restrict__ scale,
+                                                       const float* __restrict__ rest,
+                                                       const int32_t* __restrict__ labels, int64_t vocab,
+                                                       const uint8_t* __restrict__ table) {
+  __shared__ f32x4 sums[SG][256 / SG];
+  const int64_t each = hidden / 4, q = (int64_t)blockIdx.x * (256 / SG) + threadIdx.x % (256 / SG);
+  const int sg = threadIdx.x / (256 / SG);
+  const bool live = q < n * each;
+  const int64_t b = live ? q / each : 0, c = live ? q % each * 4 : 0;
   f32x4 x = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < splits; s++) x += *(const f32x4*)(part + ((int64_t)s * n + b) * hidden + c);
+  if (live) {
+#pragma unroll 4
+    for (int s = sg; s < splits * planes; s += SG) x += *(const f32x4*)(part + ((int64_t)s * n + b) * hidden + c);
+  }
+  if constexpr (SG > 1) {
+    sums[sg][threadIdx.x % (256 / SG)] = x;
+    __syncthreads();
+    if (sg != 0) return;
+#pragma unroll
+    for (int i = 1; i < SG; i++) x += sums[i][threadIdx.x];
+  }
+  if (!live) return;
+  if (rest != nullptr && (uint32_t)labels[b] < (uint64_t)vocab)
+    x += rest[b] * load4<DT>(table + ((int64_t)labels[b] * hidden + c) * kValue<DT>);
   x *= scale != nullptr ? scale[1] : 1.f;
   // rows at any address of the type
   typedef decltype(round4<DT>(x)) V;
@@ -560,13 +848,15 @@ __global__ void __launch_bounds__(256) xent_sum_kernel(const float* __restrict__
   *(Vu*)((unsigned char*)out + b * out_pitch + c * kValue<DT>) = round4<DT>(x);
 }
 
-// Rows of `bytes` (a multiple of 16) bytes, pitch bytes apart at any alignment, side by side.
+// Rows of `bytes` (a multiple of 16) bytes, pitch bytes apart at any alignment, side by side;
+// all of them `copies` times.
 __global__ void __launch_bounds__(256) xent_pack_kernel(const uint8_t* __restrict__ src, int64_t pitch, int64_t n,
-                                                        int64_t bytes, uint8_t* __restrict__ dst) {
+                                                        int64_t bytes, int copies, uint8_t* __restrict__ dst) {
   typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
   const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x, each = bytes / 16;
   if (q >= n * each) return;
-  *(u32x4*)(dst + q * 16) = *(const u32x4u*)(src + q / each * pitch + q % each * 16);
+  const u32x4 w = *(const u32x4u*)(src + q / each * pitch + q % each * 16);
+  for (int c = 0; c < copies; c++) *(u32x4*)(dst + (c * n * each + q) * 16) = w;
 }
 
 // ---------------------------------------------------------------------------
@@ -603,16 +893,32 @@ hipError_t launch_tile(const XentProduct& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// A product whose columns are residual rows.
+// A product whose columns are p.n residual rows (or planes of them).
 template <int DT, bool TA, int MODE>
-hipError_t launch_by_rows(const XentProduct& p, int bn, hipStream_t stream) {
-  if (bn == 64) return launch_ring<DT, TA, false, MODE, 256, 64, 8, 4>(p, stream);
-  if (bn == 128) return launch_ring<DT, TA, false, MODE, 256, 128, 4, 3>(p, stream);
-  return launch_tile<DT, TA, false, MODE>(p, stream);
+hipError_t launch_by_rows(XentProduct p, hipStream_t stream) {
+  const int bn = rows_tile(p.n);
+  p.mt = (int32_t)cdiv(p.m, 256), p.nt = (int32_t)cdiv(p.n, bn);
+  if (bn == 64) return launch_ring<DT, TA, false, MODE, 256, 64, 4, 4>(p, stream);
+  if constexpr (MODE != X_DLOGIT32) {
+    if (bn == 128) return launch_ring<DT, TA, false, MODE, 256, 128, 4, 3>(p, stream);
+    return launch_tile<DT, TA, false, MODE>(p, stream);
+  }
+  return hipErrorInvalidValue;  // X_DLOGIT32: up to 8 rows
 }
 
-constexpr int64_t kMaxTiles = 1 << 20;             // of one launch
+constexpr int64_t kMaxTiles = 1 << 20;              // of one launch
 constexpr int64_t kPartBytes = (int64_t)256 << 20;  // statistics, or D, of one piece
+
+// The 16 x 16 kernel instead of tiles of 256 table rows.
+constexpr int64_t kDirectTiles = 2048;
+bool direct_tiles(int64_t vocab, int64_t n) { return n <= 64 && cdiv(vocab, 16) * cdiv(n, 16) <= kDirectTiles; }
+
+template <int DT, int MODE>
+hipError_t launch_direct(XentProduct p, hipStream_t stream) {
+  p.mt = (int32_t)cdiv(p.m, 16), p.nt = (int32_t)cdiv(p.n, 16);
+  hipLaunchKernelGGL((direct_kernel<DT, MODE>), dim3((unsigned)(p.mt * p.nt)), dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
 
 // Pieces of at most `most` tiles of 256 table rows, as even as they get; in rows.
 int64_t even_piece(int64_t vocab, int64_t most) {
@@ -623,15 +929,39 @@ int64_t even_piece(int64_t vocab, int64_t most) {
 int64_t forward_piece(int64_t vocab, int64_t n) {
   return even_piece(vocab, std::min(kMaxTiles / cdiv(n, rows_tile(n)), kPartBytes / (n * 8)));
 }
-// Backward: D of a piece stays within kPartBytes and its rows within 4 MiB.
-int64_t backward_piece(int64_t vocab, int64_t n, int size) {
-  return even_piece(vocab, std::min(std::min(kMaxTiles / cdiv(n, rows_tile(n)), (int64_t)4096),
-                                    kPartBytes / (n * size * 256)));
+
+struct ForwardWs {
+  int64_t piece;
+  int32_t mt;        // statistics per residual row of a whole piece
+  bool direct;
+  size_t target, x, part, bytes;
+};
+ForwardWs forward_ws(const TableDesc& t, int64_t n) {
+  ForwardWs w;
+  w.direct = direct_tiles(t.V, n);
+  w.piece = forward_piece(t.V, n);
+  w.mt = (int32_t)(w.direct ? cdiv(t.V, 16) : w.piece / 256);
+  w.target = align_up((size_t)n * 8, 256);  // after the running statistics
+  w.x = w.target + align_up((size_t)n * 4, 256);
+  w.part = w.x + align_up((size_t)(n * t.row_bytes), 256);
+  w.bytes = w.part + align_up((size_t)(n * w.mt * 8), 256);
+  return w;
 }
+
+// Backward, by the number of residual rows: up to 8 D in f32 and vector FMAs; 16-bit types up
+// to 64 D as two 16-bit values, up to 128 columns of dx's product; else D once.
+constexpr int64_t kVectorRows = 8, kTwoPlaneRows = 64;
+
+struct BackwardWs {
+  int64_t piece, splits, slice, rows;  // rows: of D's planes together
+  int planes, chunks;
+  size_t rest, x, d, sums, bytes;
+  size_t pitch;                        // bytes of a row of D
+};
 // K slices of dx = D E: the fewest rounds of one workgroup per CU, times the stages of one and
 // what its start and end cost (about 24 stages); at least 512 table rows each.
-int64_t backward_splits(int64_t piece, int64_t n, int64_t hidden) {
-  const int64_t tiles = cdiv(hidden, 256) * cdiv(n, rows_tile(n));
+int64_t backward_splits(int64_t piece, int64_t rows, int64_t hidden) {
+  const int64_t tiles = cdiv(hidden, 256) * cdiv(rows, rows_tile(rows));
   int64_t best = 1, least = INT64_MAX;
   for (int64_t s = 1; s <= std::max<int64_t>(1, piece / 512) && s <= 2 * kTargetBlocks; s++) {
     const int64_t cost = cdiv(tiles * s, kTargetBlocks) * (cdiv(piece, 64 * s) + 24);
@@ -640,61 +970,92 @@ int64_t backward_splits(int64_t piece, int64_t n, int64_t hidden) {
   }
   return best;
 }
-int64_t backward_slice(int64_t piece, int64_t splits) { return (int64_t)align_up(cdiv(piece, splits), 64); }
-
-// The residual rows as the copies need them: 16-byte aligned, rows less than 8 MiB apart.
-bool rows_direct(const void* x, int64_t pitch) { return ((uintptr_t)x | (uint64_t)pitch) % 16 == 0 && pitch < (8 << 20); }
-
-struct BackwardWs {
-  int64_t piece, splits, slice;
-  size_t x, d, sums, bytes;
-};
 BackwardWs backward_ws(const TableDesc& t, int64_t n) {
   const int size = t.dtype == DT_F32 ? 4 : 2;
-  BackwardWs w;
-  w.piece = backward_piece(t.V, n, size);
-  w.splits = backward_splits(w.piece, n, t.hidden);
-  w.slice = backward_slice(w.piece, w.splits);
-  w.splits = cdiv(w.piece, w.slice);
-  w.x = 256;  // the two factors before it
-  w.d = w.x + align_up((size_t)(n * t.row_bytes), 256);
-  w.sums = w.d + align_up((size_t)(n * w.piece * size), 256);
-  w.bytes = w.sums + align_up((size_t)(w.splits * n * t.hidden * 4), 256);
+  BackwardWs w = {};
+  size_t x_bytes, d_bytes;
+  if (n <= kVectorRows) {
+    // about eight waves per CU, each with 32 table rows at least
+    w.chunks = (int)cdiv(t.row_bytes, 1024);
+    w.piece = even_piece(t.V, kPartBytes / (256 * 32)), w.rows = n, w.planes = 1;
+    w.slice = std::max<int64_t>(32, cdiv(w.piece, std::max<int64_t>(1, 8 * kTargetBlocks / w.chunks)));
+    w.splits = cdiv(std::min(w.piece, t.V), w.slice);  // of the first piece, the fullest
+    d_bytes = (size_t)w.piece * 32;
+    x_bytes = n * t.row_bytes;
+  } else {
+    w.planes = t.dtype != DT_F32 && n <= kTwoPlaneRows ? 2 : 1;
+    w.rows = n * w.planes;
+    // D of a piece stays within kPartBytes and its rows within 4 MiB
+    w.piece = even_piece(t.V, std::min(std::min(kMaxTiles / cdiv(n, rows_tile(n)), (int64_t)4096),
+                                       kPartBytes / (w.rows * size * 256)));
+    w.slice = (int64_t)align_up(cdiv(w.piece, backward_splits(w.piece, w.rows, t.hidden)), 64);
+    w.splits = cdiv(std::min(w.piece, t.V), w.slice);  // of the first piece, the fullest
+    w.pitch = (size_t)(w.piece * size);
+    d_bytes = (size_t)w.rows * w.pitch;
+    x_bytes = w.rows * t.row_bytes;
+  }
+  w.rest = 256;  // after the two factors
+  w.x = w.rest + align_up((size_t)n * 4, 256);
+  w.d = w.x + align_up(x_bytes, 256);
+  w.sums = w.d + align_up(d_bytes, 256);
+  w.bytes = w.sums + align_up((size_t)(w.splits * w.rows * t.hidden * 4), 256);
   return w;
 }
 
-hipError_t pack_rows(const XentCall& c, const TableDesc& t, uint8_t* to, hipStream_t stream) {
+// The residual rows as the kernels read them: 16-byte aligned, rows less than 8 MiB apart.
+bool rows_direct(const void* x, int64_t pitch) { return ((uintptr_t)x | (uint64_t)pitch) % 16 == 0 && pitch < (8 << 20); }
+
+hipError_t pack_rows(const XentCall& c, const TableDesc& t, int copies, uint8_t* to, hipStream_t stream) {
   const int64_t pieces = c.n * (t.row_bytes / 16);
   hipLaunchKernelGGL(xent_pack_kernel, dim3((unsigned)cdiv(pieces, 256)), dim3(256), 0, stream, (const uint8_t*)c.x,
-                     c.x_pitch, c.n, t.row_bytes, to);
+                     c.x_pitch, c.n, t.row_bytes, copies, to);
   return hipGetLastError();
 }
 
 template <int DT>
 hipError_t forward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStream_t stream) {
-  const int64_t piece = forward_piece(t.V, c.n);
+  if (c.n == 0) return hipSuccess;
+  const ForwardWs w = forward_ws(t, c.n);
   hipError_t e;
-  // workspace: running statistics, targets, packed residual rows, the piece's statistics
-  float2* run = (float2*)ws;
-  float* target = (float*)(ws + align_up((size_t)c.n * 8, 256));
-  uint8_t* packed = (uint8_t*)target + align_up((size_t)c.n * 4, 256);
-  float2* part = (float2*)(packed + align_up((size_t)(c.n * t.row_bytes), 256));
+  float2 *run = (float2*)ws, *part = (float2*)(ws + w.part);
+  float* target = (float*)(ws + w.target);
   const bool direct = rows_direct(c.x, c.x_pitch);
-  if (!direct && (e = pack_rows(c, t, packed, stream)) != hipSuccess) return e;
-  const int bn = rows_tile(c.n);
+  if (!direct && (e = pack_rows(c, t, 1, ws + w.x, stream)) != hipSuccess) return e;
+  const int64_t piece = w.direct ? t.V : w.piece;
   for (int64_t v0 = 0; v0 < t.V; v0 += piece) {
     XentProduct p = {};
     p.m = std::min(piece, t.V - v0), p.n = c.n, p.k = t.hidden;
     p.a = t.rows + v0 * t.row_bytes, p.a_pitch = t.row_bytes;
-    p.b = direct ? (const uint8_t*)c.x : packed, p.b_pitch = direct ? c.x_pitch : t.row_bytes;
-    p.mt = (int32_t)cdiv(p.m, 256), p.nt = (int32_t)cdiv(p.n, bn), p.splits = 1, p.kslice = (int32_t)t.hidden;
+    p.b = direct ? (const uint8_t*)c.x : ws + w.x, p.b_pitch = direct ? c.x_pitch : t.row_bytes;
+    p.splits = 1, p.kslice = (int32_t)t.hidden;
     p.out = part, p.labels = c.labels, p.v0 = v0, p.target = target;
-    if ((e = launch_by_rows<DT, false, X_STATS>(p, bn, stream)) != hipSuccess) return e;
-    hipLaunchKernelGGL(xent_join_kernel, dim3((unsigned)cdiv(c.n, 4)), dim3(256), 0, stream, part, p.mt, c.n, v0 == 0,
+    e = w.direct ? launch_direct<DT, X_STATS>(p, stream) : launch_by_rows<DT, false, X_STATS>(p, stream);
+    if (e != hipSuccess) return e;
+    const int mt = (int)(w.direct ? w.mt : cdiv(p.m, 256));
+    hipLaunchKernelGGL(xent_join_kernel, dim3((unsigned)cdiv(c.n, 4)), dim3(256), 0, stream, part, mt, c.n, v0 == 0,
                        v0 + piece >= t.V, run, target, c.labels, t.V, c.loss, c.lse_out);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+template <int DT, int NB>
+hipError_t launch_rows(const XentRows& p, hipStream_t stream) {
+  hipLaunchKernelGGL((xent_rows_kernel<DT, NB>), dim3((unsigned)cdiv((int64_t)p.chunks * p.slices, 4)), dim3(256), 0,
+                     stream, p);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t sum_slices(const TableDesc& t, const XentCall& c, const BackwardWs& w, const float* sums,
+                      const float* scale, const float* rest, hipStream_t stream) {
+  const int64_t quads = c.n * (t.hidden / 4);
+  // few values of many slices: 16 threads to a value's slices
+  const auto kernel = w.splits * w.planes >= 16 ? xent_sum_kernel<DT, 16> : xent_sum_kernel<DT, 1>;
+  const int each = w.splits * w.planes >= 16 ? 16 : 256;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv(quads, each)), dim3(256), 0, stream, sums, (int)w.splits, w.planes,
+                     c.n, t.hidden, c.d_x, c.d_x_pitch, scale, rest, c.labels, t.V, t.rows);
+  return hipGetLastError();
 }
 
 template <int DT>
@@ -703,68 +1064,80 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
     return c.d_rows == nullptr || c.add ? hipSuccess : launch_write_probe(c.d_rows, t.V * t.row_bytes, 0, stream);
   const BackwardWs w = backward_ws(t, c.n);
   hipError_t e;
-  float* scale = DT == DT_F16 ? (float*)ws : nullptr;
   uint8_t *packed = ws + w.x, *d = ws + w.d;
   float* sums = (float*)(ws + w.sums);
+  const bool direct = w.planes == 1 && rows_direct(c.x, c.x_pitch);
+  if (!direct && (e = pack_rows(c, t, w.planes, packed, stream)) != hipSuccess) return e;
+  XentProduct logits = {};  // of a piece, to D
+  logits.n = c.n, logits.k = t.hidden, logits.a_pitch = t.row_bytes;
+  logits.b = direct ? (const uint8_t*)c.x : packed, logits.b_pitch = direct ? c.x_pitch : t.row_bytes;
+  logits.splits = 1, logits.kslice = (int32_t)t.hidden;
+  logits.out = d, logits.out_pitch = (int64_t)w.pitch;
+  logits.labels = c.labels, logits.vocab = t.V, logits.lse = c.lse, logits.grad_loss = c.grad_loss;
+  logits.grad_loss_all = c.grad_loss_all, logits.grad_lse = c.grad_lse;
+  if (c.n <= kVectorRows) {
+    XentRows p = {};
+    p.x = logits.b, p.row_bytes = t.row_bytes, p.x_pitch = logits.b_pitch, p.per = w.slice;
+    p.hidden = (int)t.hidden, p.n = (int)c.n, p.chunks = w.chunks;
+    p.d = (const float*)d, p.add = c.add, p.part = c.d_x != nullptr ? sums : nullptr;
+    for (int64_t v0 = 0; v0 < t.V; v0 += w.piece) {
+      logits.a = p.table = t.rows + v0 * t.row_bytes, logits.m = p.m = std::min(w.piece, t.V - v0), logits.v0 = v0;
+      p.rows = c.d_rows != nullptr ? (uint8_t*)c.d_rows + v0 * t.row_bytes : nullptr;
+      p.slices = (int)cdiv(p.m, w.slice), p.part_add = p.part != nullptr && v0 != 0;
+      e = direct_tiles(t.V, c.n) ? launch_direct<DT, X_DLOGIT32>(logits, stream)
+                                 : launch_by_rows<DT, false, X_DLOGIT32>(logits, stream);
+      if (e != hipSuccess) return e;
+      e = c.n <= 2   ? launch_rows<DT, 2>(p, stream)
+          : c.n <= 4 ? launch_rows<DT, 4>(p, stream)
+                     : launch_rows<DT, 8>(p, stream);
+      if (e != hipSuccess) return e;
+    }
+    if (c.d_x == nullptr) return hipSuccess;
+    return sum_slices<DT>(t, c, w, sums, nullptr, nullptr, stream);
+  }
+  float* scale = DT == DT_F16 ? (float*)ws : nullptr;
+  float* rest = DT != DT_F32 && w.planes == 1 && c.d_x != nullptr ? (float*)(ws + w.rest) : nullptr;
   if (scale != nullptr) {
     hipLaunchKernelGGL(xent_scale_kernel, dim3(1), dim3(1024), 0, stream, c.labels, c.n, t.V, c.grad_loss,
                        c.grad_loss_all, c.grad_lse, scale);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const bool direct = rows_direct(c.x, c.x_pitch);
-  if (!direct && (e = pack_rows(c, t, packed, stream)) != hipSuccess) return e;
-  const uint8_t* x = direct ? (const uint8_t*)c.x : packed;
-  const int64_t x_pitch = direct ? c.x_pitch : t.row_bytes;
-  const int bn = rows_tile(c.n);
+  logits.scale = scale, logits.rest = rest;
+  logits.out_low = w.planes == 2 ? d + c.n * w.pitch : nullptr;
   for (int64_t v0 = 0; v0 < t.V; v0 += w.piece) {
     const int64_t rows = std::min(w.piece, t.V - v0);
-    const uint8_t* E = t.rows + v0 * t.row_bytes;
-    {
-      XentProduct p = {};
-      p.m = rows, p.n = c.n, p.k = t.hidden;
-      p.a = E, p.a_pitch = t.row_bytes, p.b = x, p.b_pitch = x_pitch;
-      p.mt = (int32_t)cdiv(rows, 256), p.nt = (int32_t)cdiv(c.n, bn), p.splits = 1, p.kslice = (int32_t)t.hidden;
-      p.out = d, p.out_pitch = w.piece * kValue<DT>;
-      p.labels = c.labels, p.v0 = v0, p.vocab = t.V, p.lse = c.lse, p.grad_loss = c.grad_loss;
-      p.grad_loss_all = c.grad_loss_all, p.grad_lse = c.grad_lse, p.scale = scale;
-      if ((e = launch_by_rows<DT, false, X_DLOGIT>(p, bn, stream)) != hipSuccess) return e;
-    }
+    logits.a = t.rows + v0 * t.row_bytes, logits.m = rows, logits.v0 = v0;
+    if ((e = launch_by_rows<DT, false, X_DLOGIT>(logits, stream)) != hipSuccess) return e;
     if (c.d_x != nullptr) {
       XentProduct p = {};
-      p.m = t.hidden, p.n = c.n, p.k = rows;
-      p.a = E, p.a_pitch = t.row_bytes, p.b = d, p.b_pitch = w.piece * kValue<DT>;
-      p.mt = (int32_t)cdiv(t.hidden, 256), p.nt = (int32_t)cdiv(c.n, bn);
+      p.m = t.hidden, p.n = w.rows, p.k = rows;
+      p.a = logits.a, p.a_pitch = t.row_bytes, p.b = d, p.b_pitch = (int64_t)w.pitch;
       p.splits = (int32_t)cdiv(rows, w.slice), p.kslice = (int32_t)w.slice;
       p.out = sums, p.add = v0 != 0;
-      if ((e = launch_by_rows<DT, true, X_PART>(p, bn, stream)) != hipSuccess) return e;
+      if ((e = launch_by_rows<DT, true, X_PART>(p, stream)) != hipSuccess) return e;
     }
     if (c.d_rows != nullptr) {
       XentProduct p = {};
-      p.m = t.hidden, p.n = rows, p.k = c.n;
-      p.a = x, p.a_pitch = x_pitch, p.b = d, p.b_pitch = w.piece * kValue<DT>;
-      p.mt = (int32_t)cdiv(t.hidden, 256), p.nt = (int32_t)cdiv(rows, 256);
-      p.splits = 1, p.kslice = (int32_t)align_up((size_t)c.n, 64);
+      p.m = t.hidden, p.n = rows, p.k = w.rows;
+      p.a = logits.b, p.a_pitch = logits.b_pitch, p.b = d, p.b_pitch = (int64_t)w.pitch;
+      p.splits = 1, p.kslice = (int32_t)align_up((size_t)w.rows, 64);
       p.out = (uint8_t*)c.d_rows + v0 * t.row_bytes, p.add = c.add, p.scale = scale;
-      if ((e = launch_tile<DT, true, true, X_OUT>(p, stream)) != hipSuccess) return e;
+      if (w.rows <= 128) {  // two stages at most: bound by its stores, two workgroups per CU
+        p.mt = (int32_t)cdiv(p.m, 128), p.nt = (int32_t)cdiv(p.n, 128);
+        e = launch_ring<DT, true, true, X_OUT, 128, 128, 2, 2>(p, stream);
+      } else {
+        p.mt = (int32_t)cdiv(p.m, 256), p.nt = (int32_t)cdiv(p.n, 256);
+        e = launch_tile<DT, true, true, X_OUT>(p, stream);
+      }
+      if (e != hipSuccess) return e;
     }
   }
-  if (c.d_x != nullptr) {
-    const int splits = (int)cdiv(std::min(w.piece, t.V), w.slice);  // of the first piece, the fullest
-    hipLaunchKernelGGL(xent_sum_kernel<DT>, dim3((unsigned)cdiv(c.n * (t.hidden / 4), 256)), dim3(256), 0, stream,
-                       sums, splits, c.n, t.hidden, c.d_x, c.d_x_pitch, scale);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  return hipSuccess;
+  return c.d_x == nullptr ? hipSuccess : sum_slices<DT>(t, c, w, sums, scale, rest, stream);
 }
 
 }  // namespace
 
-size_t xent_workspace(const TableDesc& t, int64_t n) {
-  if (n == 0) return 0;
-  const int64_t piece = forward_piece(t.V, n);
-  return align_up((size_t)n * 8, 256) + align_up((size_t)n * 4, 256) + align_up((size_t)(n * t.row_bytes), 256) +
-         align_up((size_t)(n * (piece / 256) * 8), 256);
-}
+size_t xent_workspace(const TableDesc& t, int64_t n) { return n == 0 ? 0 : forward_ws(t, n).bytes; }
 
 size_t xent_grad_workspace(const TableDesc& t, int64_t n) { return n == 0 ? 0 : backward_ws(t, n).bytes; }
 
