@@ -8,10 +8,9 @@
 // vocabulary in pieces: the product again, with D (rounded to the table's type, the operand
 // of the two other products) as its result, then the piece's share of dx and its rows of dE.
 //
-// D's entry at a label, g (p - 1) + h p, is most of what a row contributes, and is p - 1
-// near 0 in a trained model: it is computed with expm1, and what its rounding to 16 bits takes
-// away is added to dx from a list.  Up to 64 residual rows the products are bound by memory,
-// and D is kept as the sum of two 16-bit values; up to 8, in f32.
+// D's entry at a label, g (p - 1) + h p, is most of what a row contributes, and is near 0 where
+// p is near 1: it is computed with expm1, and what its rounding to 16 bits takes away (its
+// "rest") is added to dx, and up to 128 residual rows to dE.  Up to 8 residual rows D is f32.
 #include <algorithm>
 #include <type_traits>
 
@@ -183,8 +182,7 @@ struct XentProduct {
   // X_PART: f32 [splits][n][m]; X_OUT: values of the type, [n][m]
   void* out;
   int64_t out_pitch;
-  void* out_low;             // X_DLOGIT: what the rounding took away, rounded too, laid out as D (NULL: none)
-  float* rest;               // X_DLOGIT: [n], what it took away from the label's entry (NULL: not wanted)
+  float* rest;               // 16-bit types: [n], what D's rounding takes away from a label's entry
   int32_t add;               // X_PART, X_OUT: to what is there
   const int32_t* labels;     // [n]
   int64_t v0, vocab;         // the piece's first table row
@@ -218,40 +216,58 @@ __device__ __forceinline__ f32x4 load4(const void* at) {
   }
 }
 
-// Stores `most` of the 16 AH values that the lanes {l, l + 16, l + 32, l + 48} hold of one row
-// (x[a][i] of lane row g is value 16 a + 4 g + i) at `at`, where `some`.  16-bit types exchange
-// them between the lanes first, so that a lane stores 4 AH values side by side (16-byte stores,
-// whole 128-byte lines per row for AH = 4, instead of 8 bytes in every 32).
+// Stores a wave's 16 rows of 16 AH values: x[a][i] of lane l is value 16 a + 4 (l / 16) + i of row
+// l % 16.  The first value of row 0 goes to `at`, rows are pitch bytes apart; `rows` of them
+// and `most` values (a multiple of 4, 8 for 16-bit types) are stored.  16-bit types exchange
+// them between the lanes first, so that a store writes whole lines (128 bytes of each of
+// eight rows); stores of 8 bytes in every 32 took 1,076 us for 2.8 GB, of half lines 631, of
+// whole ones WHOLE.
 template <int DT, int AH>
-__device__ __forceinline__ void store_rows(unsigned char* at, const f32x4 (&x)[AH], int g, bool some, int most) {
+__device__ __forceinline__ void store_rows(unsigned char* at, int64_t pitch, const f32x4 (&x)[AH], int lane,
+                                           int64_t rows, int most) {
+  const int g = lane >> 4, r = lane & 15;
   if constexpr (DT == DT_F32) {
 #pragma unroll
     for (int a = 0; a < AH; a++)
-      if (some && 16 * a + 4 * g < most) *(f32x4*)(at + (16 * a + 4 * g) * 4) = x[a];
+      if (r < rows && 16 * a + 4 * g < most) *(f32x4*)(at + r * pitch + (16 * a + 4 * g) * 4) = x[a];
   } else {
     static_assert(AH == 4, "four tiles are exchanged");
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    u32x2 r[4];
+    u32x4 w[2];  // of tiles (0, 1) and (2, 3): lane row g has values 8 g .. 8 g + 7 of 32
 #pragma unroll
-    for (int a = 0; a < 4; a++) r[a] = __builtin_bit_cast(u32x2, round4<DT>(x[a]));
+    for (int q = 0; q < 2; q++) {
+      const u32x2 lo = __builtin_bit_cast(u32x2, round4<DT>(x[2 * q]));
+      const u32x2 hi = __builtin_bit_cast(u32x2, round4<DT>(x[2 * q + 1]));
 #pragma unroll
-    for (int w = 0; w < 2; w++) {
-#pragma unroll
-      for (int a = 0; a < 2; a++) {
-        const u32x2 s = __builtin_amdgcn_permlane32_swap(r[a][w], r[a + 2][w], false, false);
-        r[a][w] = s[0], r[a + 2][w] = s[1];
-      }
-#pragma unroll
-      for (int a = 0; a < 4; a += 2) {
-        const u32x2 s = __builtin_amdgcn_permlane16_swap(r[a][w], r[a + 1][w], false, false);
-        r[a][w] = s[0], r[a + 1][w] = s[1];
+      for (int i = 0; i < 2; i++) {
+        // lane rows (0, 1, 2, 3) of tiles a, b -> (a0, a1, b0, b1), (a2, a3, b2, b3)
+        const u32x2 s = __builtin_amdgcn_permlane32_swap(lo[i], hi[i], false, false);
+        // -> (a0, a2, b0, b2), (a1, a3, b1, b3)
+        const u32x2 t = __builtin_amdgcn_permlane16_swap(s[0], s[1], false, false);
+        w[q][i] = t[0], w[q][2 + i] = t[1];
       }
     }
-    // lane row g: values 16 g .. 16 g + 15
+    // lanes r and r ^ 8 exchange a half: the lower eight keep values 0 .. 31, of rows r and
+    // r + 8, the upper eight values 32 .. 63 of rows r - 8 and r
+    const bool upper = r >= 8;
+    u32x4 first, second;
 #pragma unroll
-    for (int h = 0; h < 2; h++)
-      if (some && 16 * g + 8 * h < most)
-        *(u32x4*)(at + (16 * g + 8 * h) * 2) = u32x4{r[2 * h][0], r[2 * h][1], r[2 * h + 1][0], r[2 * h + 1][1]};
+    for (int i = 0; i < 4; i++) {
+      const uint32_t got = __builtin_amdgcn_update_dpp(0u, upper ? w[0][i] : w[1][i], 0x128, 0xf, 0xf, false);  // row_ror:8
+      first[i] = upper ? got : w[0][i];
+      second[i] = upper ? w[1][i] : got;
+    }
+    // a uniform address and 32 bits of the lane's own
+    const int value = (upper ? 32 : 0) + 8 * g;
+    const uint32_t mine = (uint32_t)((r & 7) * (int)pitch) + (uint32_t)(value * 2);
+    unsigned char* at8 = at + 8 * pitch;
+    if (rows >= 16 && most >= 64) {  // uniform
+      *(u32x4*)(at + mine) = first;
+      *(u32x4*)(at8 + mine) = second;
+    } else {
+      if ((r & 7) < rows && value < most) *(u32x4*)(at + mine) = first;
+      if ((r & 7) + 8 < rows && value < most) *(u32x4*)(at8 + mine) = second;
+    }
   }
 }
 
@@ -295,7 +311,8 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
   const int g = lane >> 4;
   // rows in 32 bits, from this lane's first one
   auto off = [](int a) { return a / AH * 128 + a % AH * 16; };
-  auto col_of = [&](int t) { return n0 + ncol + t / TH * 128 + t % TH * 16 + (lane & 15); };
+  auto col0 = [&](int t) { return n0 + ncol + t / TH * 128 + t % TH * 16; };
+  auto col_of = [&](int t) { return col0(t) + (lane & 15); };
   const int first = mrow + 4 * g, rows = (int)min(p.m - m0, (int64_t)256) - first;
   auto place = [&](int64_t row) {  // of a row of the piece; negative where the tile lacks it
     return row >= m0 && row < m0 + 256 && row < p.m ? (int)(row - m0) - first : -1024;
@@ -373,7 +390,7 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
             for (int i = 0; i < 4; i++)
               if (off(a0 + a) + i == label) d[a][i] = x, here = true;
           if constexpr (DT != DT_F32 && MODE == X_DLOGIT)
-            if (here && p.rest != nullptr) p.rest[n] = x - (float)round1<DT>(x);
+            if (here) p.rest[n] = x - (float)round1<DT>(x);
         }
         if constexpr (MODE == X_DLOGIT32) {
 #pragma unroll
@@ -382,36 +399,33 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
             for (int i = 0; i < 4; i++)
               if (off(a0 + a) + i < rows) ((float*)p.out)[(m0 + first + off(a0 + a) + i) * 8 + n] = d[a][i];
         } else {
-          const int64_t at = n * p.out_pitch + (m0 + mrow + a0 / AH * 128) * kValue<DT>;
-          store_rows<DT, AH>((unsigned char*)p.out + at, d, g, n < p.n, 16 * AH);
-          if constexpr (DT != DT_F32) {
-            if (p.out_low != nullptr) {
-#pragma unroll
-              for (int a = 0; a < AH; a++) d[a] -= __builtin_convertvector(round4<DT>(d[a]), f32x4);
-              store_rows<DT, AH>((unsigned char*)p.out_low + at, d, g, n < p.n, 16 * AH);
-            }
-          }
+          const int64_t at = col0(t) * p.out_pitch + (m0 + mrow + off(a0)) * kValue<DT>;
+          store_rows<DT, AH>((unsigned char*)p.out + at, p.out_pitch, d, lane, p.n - col0(t), 16 * AH);
         }
       }
     }
   } else {
-    const float scale = MODE == X_OUT && p.scale != nullptr ? p.scale[1] : 1.f;
+    const float scale = MODE == X_OUT && DT == DT_F16 && p.scale != nullptr ? p.scale[1] : 1.f;
     constexpr int ODT = MODE == X_PART ? DT_F32 : DT;
+    const int64_t pitch = p.m * kValue<ODT>;
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-      const int64_t n = col_of(t);
-      unsigned char* row =
-          (unsigned char*)p.out + (((int64_t)split * p.n + min(n, p.n - 1)) * p.m + m0 + mrow) * kValue<ODT>;
+      unsigned char* row = (unsigned char*)p.out + ((int64_t)split * p.n + col0(t)) * pitch + (m0 + mrow) * kValue<ODT>;
 #pragma unroll
       for (int a0 = 0; a0 < MT; a0 += AH) {
         f32x4 x[AH];
 #pragma unroll
         for (int a = 0; a < AH; a++) {
-          x[a] = acc[a0 + a][t] * scale;
-          // the number of rows is a multiple of 4
-          if (p.add && n < p.n && off(a0 + a) < rows) x[a] += load4<ODT>(row + (off(a0 + a) + 4 * g) * kValue<ODT>);
+          x[a] = acc[a0 + a][t];
+          if constexpr (DT == DT_F16 && MODE == X_OUT) x[a] *= scale;
         }
-        store_rows<ODT, AH>(row + off(a0) * kValue<ODT>, x, g, n < p.n, rows + 4 * g - off(a0));
+        if (p.add) {  // the number of rows is a multiple of 4
+#pragma unroll
+          for (int a = 0; a < AH; a++)
+            if (col_of(t) < p.n && off(a0 + a) < rows)
+              x[a] += load4<ODT>(row + (lane & 15) * pitch + (off(a0 + a) + 4 * g) * kValue<ODT>);
+        }
+        store_rows<ODT, AH>(row + off(a0) * kValue<ODT>, pitch, x, lane, p.n - col0(t), (int)min(p.m - m0, (int64_t)256) - mrow - off(a0));
       }
     }
   }
@@ -597,6 +611,120 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
   load_wait<0>();
   bare_barrier();
   finish<DT, MODE, 8, 4, 4, 2, 2, 256>(p, acc, m0, n0, 64 * wm, 32 * wn, at.mtile, at.split, wm, lane, smem);
+}
+
+// dE = D^T x for up to 128 residual rows (f32: 64), bound by its stores: a workgroup keeps 256
+// columns of x as fragments in registers (64 for each of 4 waves, twice) and walks a range of
+// table rows, 128 at a time (64 for each half of the waves), D's tiles two or three steps ahead
+// in a ring of LDS images.  A tile that holds a label has the rest of its entry of D added,
+// as a second operand built in registers.
+template <int DT, int KT>  // KT: stages of K
+__global__ void __launch_bounds__(64 * kXWaves, 2) outer_kernel(XentProduct p) {
+  using A = Operand<DT, true, 256>;
+  using B = Operand<DT, true, 128>;
+  constexpr int RING = KT == 1 ? 4 : 3, IMG = KT * B::BYTES, COPIES = KT * B::COPIES;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // first A's images, then [RING][IMG]
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wv & 3, wn = wv >> 2;
+  const XentPlace at(p);  // ntile: a range of kslice table rows (a multiple of 128)
+  if (!at.some) return;   // whole workgroup
+  const int64_t m0 = (int64_t)at.mtile * 256, n0 = (int64_t)at.ntile * p.kslice, n1 = min(n0 + p.kslice, p.n);
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem;
+  u32x4 fa[KT][4][2];
+  {
+    const A oa(p.a, p.a_pitch, m0, p.m, 0, (int)p.k, wv, lane);
+#pragma unroll
+    for (int s = 0; s < KT; s++) {
+#pragma unroll
+      for (int j = 0; j < A::COPIES; j++) oa.copy(s, j, wv, lds + s * A::BYTES);
+    }
+    load_wait<0>();
+    bare_barrier();
+#pragma unroll
+    for (int s = 0; s < KT; s++)
+#pragma unroll
+      for (int a = 0; a < 4; a++)
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) fa[s][a][kk] = A::read(smem + s * A::BYTES, 64 * wm + 16 * a, kk, lane);
+    load_wait<0>();
+    bare_barrier();  // the images are free
+  }
+  // this lane's labels, as rows of the piece
+  int64_t label[KT];
+#pragma unroll
+  for (int s = 0; s < KT; s++) {
+    const int b = 64 * s + lane;
+    label[s] = DT != DT_F32 && b < p.k ? (int64_t)(uint32_t)p.labels[b] - p.v0 : -1;
+  }
+  const int steps = (int)((n1 - n0 + 127) / 128);
+  auto copy = [&](int i) {  // D's tile of step i (past the last: zeros that nothing reads)
+    const int64_t first = n0 + (int64_t)i * 128;
+    const B ob(p.b, p.b_pitch, i < steps ? first : n0, i < steps ? p.n : n0, 0, (int)p.k, wv, lane);
+#pragma unroll
+    for (int s = 0; s < KT; s++)
+#pragma unroll
+      for (int j = 0; j < B::COPIES; j++) ob.copy(s, j, wv, lds + (uint32_t)(i % RING) * IMG + s * B::BYTES);
+  };
+  // Copies and stores complete in order: behind a step's copies are those of the RING - 2 steps
+  // after it and the stores of RING - 1 steps, whose number is known where none is left out.
+  constexpr int STORES = DT == DT_F32 ? 16 : 8;
+  const bool whole = m0 + 256 <= p.m && !p.add;
+  for (int i = 0; i < RING - 1; i++) copy(i);
+  for (int i = 0; i < steps; i++) {
+    if (whole && i >= RING - 1) load_wait<(RING - 2) * COPIES + (RING - 1) * STORES>();
+    else load_wait<(RING - 2) * COPIES>();
+    bare_barrier();
+    copy(i + RING - 1);
+    const unsigned char* img = smem + i % RING * IMG;
+    const int64_t first = n0 + (int64_t)i * 128;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      f32x4 acc[4][2];
+#pragma unroll
+      for (int a = 0; a < 4; a++)
+#pragma unroll
+        for (int t = 0; t < 2; t++) acc[a][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < KT; s++)
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) {
+          u32x4 fb[2];
+#pragma unroll
+          for (int t = 0; t < 2; t++) fb[t] = B::read(img + s * B::BYTES, 64 * wn + 32 * h + 16 * t, kk, lane);
+#pragma unroll
+          for (int a = 0; a < 4; a++)
+#pragma unroll
+            for (int t = 0; t < 2; t++) acc[a][t] = mma<DT>(fa[s][a][kk], fb[t], acc[a][t]);
+        }
+      if constexpr (DT != DT_F32) {
+        bool hit = false;
+#pragma unroll
+        for (int s = 0; s < KT; s++) hit |= label[s] >= first && label[s] < first + 128;
+        if (__ballot(hit) != 0) {  // few tiles
+#pragma unroll
+          for (int s = 0; s < KT; s++)
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++)
+#pragma unroll
+              for (int t = 0; t < 2; t++) {
+                const int64_t v = first + 64 * wn + 32 * h + 16 * t + (lane & 15);
+                uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                  const int b = 64 * s + 32 * kk + 8 * (lane >> 4) + j;
+                  if (b < p.k && (int64_t)(uint32_t)p.labels[b] - p.v0 == v)
+                    w[j / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, round1<DT>(p.rest[b])) << 16 * (j % 2);
+                }
+                const u32x4 f = {w[0], w[1], w[2], w[3]};
+#pragma unroll
+                for (int a = 0; a < 4; a++) acc[a][t] = mma<DT>(fa[s][a][kk], f, acc[a][t]);
+              }
+        }
+      }
+      finish<DT, X_OUT, 4, 2, 4, 2, 1, 128>(p, acc, m0, first, 64 * wm, 64 * wn + 32 * h, 0, 0, 0, lane, smem);
+    }
+  }
+  load_wait<0>();  // nothing of this workgroup is in flight when its LDS is given away
 }
 
 // Few table rows for few residual rows, bound by latency: a workgroup per 16 x 16 logits, its
@@ -812,11 +940,11 @@ __global__ void __launch_bounds__(1024) xent_scale_kernel(const int32_t* __restr
   scale[1] = ldexpf(1.f, -min(max(e, -126), 126));
 }
 
-// dx row b = type(scale * (sum of the slices' partial sums of rows b, n + b, .. + rest[b] * the
-// label's table row)).  SG slices at a time, joined in LDS.
+// dx row b = type(scale * (sum of the slices' partial sums + rest[b] * the label's table row)).
+// SG slices at a time, joined in LDS.
 template <int DT, int SG>
-__global__ void __launch_bounds__(256) xent_sum_kernel(const float* __restrict__ part, int splits, int planes,
-                                                       int64_t n, int64_t hidden, void* __restrict__ out,
+__global__ void __launch_bounds__(256) xent_sum_kernel(const float* __restrict__ part, int splits, int64_t n,
+                                                       int64_t hidden, void* __restrict__ out,
                                                        int64_t out_pitch, const float* __restrict__ scale,
                                                        const float* __restrict__ rest,
                                                        const int32_t* __restrict__ labels, int64_t vocab,
@@ -829,7 +957,7 @@ __global__ void __launch_bounds__(256) xent_sum_kernel(const float* __restrict__
   f32x4 x = {0.f, 0.f, 0.f, 0.f};
   if (live) {
 #pragma unroll 4
-    for (int s = sg; s < splits * planes; s += SG) x += *(const f32x4*)(part + ((int64_t)s * n + b) * hidden + c);
+    for (int s = sg; s < splits; s += SG) x += *(const f32x4*)(part + ((int64_t)s * n + b) * hidden + c);
   }
   if constexpr (SG > 1) {
     sums[sg][threadIdx.x % (256 / SG)] = x;
@@ -848,15 +976,13 @@ __global__ void __launch_bounds__(256) xent_sum_kernel(const float* __restrict__
   *(Vu*)((unsigned char*)out + b * out_pitch + c * kValue<DT>) = round4<DT>(x);
 }
 
-// Rows of `bytes` (a multiple of 16) bytes, pitch bytes apart at any alignment, side by side;
-// all of them `copies` times.
+// Rows of `bytes` (a multiple of 16) bytes, pitch bytes apart at any alignment, side by side.
 __global__ void __launch_bounds__(256) xent_pack_kernel(const uint8_t* __restrict__ src, int64_t pitch, int64_t n,
-                                                        int64_t bytes, int copies, uint8_t* __restrict__ dst) {
+                                                        int64_t bytes, uint8_t* __restrict__ dst) {
   typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
   const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x, each = bytes / 16;
   if (q >= n * each) return;
-  const u32x4 w = *(const u32x4u*)(src + q / each * pitch + q % each * 16);
-  for (int c = 0; c < copies; c++) *(u32x4*)(dst + (c * n * each + q) * 16) = w;
+  *(u32x4*)(dst + q * 16) = *(const u32x4u*)(src + q / each * pitch + q % each * 16);
 }
 
 // ---------------------------------------------------------------------------
@@ -893,7 +1019,26 @@ hipError_t launch_tile(const XentProduct& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// A product whose columns are p.n residual rows (or planes of them).
+// A product with at most two stages of K.
+template <int DT>
+hipError_t launch_outer(XentProduct p, hipStream_t stream) {
+  const bool two = p.k > 128 / kValue<DT>;
+  const void* fn = two ? (const void*)outer_kernel<DT, 2> : (const void*)outer_kernel<DT, 1>;
+  const size_t lds = two ? 3 * 32768 : 4 * 16384;
+  hipError_t e = set_dynamic_lds(fn, lds);
+  if (e != hipSuccess) return e;
+  // one workgroup per CU
+  p.mt = (int32_t)cdiv(p.m, 256);
+  const int64_t ranges = std::max<int64_t>(1, kTargetBlocks / p.mt);
+  p.kslice = (int32_t)align_up(cdiv(p.n, ranges), 128);
+  p.nt = (int32_t)cdiv(p.n, p.kslice);
+  const dim3 grid((unsigned)(cdiv((int64_t)p.mt * p.nt, kXcdCount) * kXcdCount));
+  if (two) hipLaunchKernelGGL((outer_kernel<DT, 2>), grid, dim3(64 * kXWaves), lds, stream, p);
+  else hipLaunchKernelGGL((outer_kernel<DT, 1>), grid, dim3(64 * kXWaves), lds, stream, p);
+  return hipGetLastError();
+}
+
+// A product whose columns are p.n residual rows.
 template <int DT, bool TA, int MODE>
 hipError_t launch_by_rows(XentProduct p, hipStream_t stream) {
   const int bn = rows_tile(p.n);
@@ -948,20 +1093,19 @@ ForwardWs forward_ws(const TableDesc& t, int64_t n) {
   return w;
 }
 
-// Backward, by the number of residual rows: up to 8 D in f32 and vector FMAs; 16-bit types up
-// to 64 D as two 16-bit values, up to 128 columns of dx's product; else D once.
-constexpr int64_t kVectorRows = 8, kTwoPlaneRows = 64;
+// Backward: up to this many residual rows D is f32, and vector FMAs read it.
+constexpr int64_t kVectorRows = 8;
 
 struct BackwardWs {
-  int64_t piece, splits, slice, rows;  // rows: of D's planes together
-  int planes, chunks;
+  int64_t piece, splits, slice;
+  int chunks;
   size_t rest, x, d, sums, bytes;
-  size_t pitch;                        // bytes of a row of D
+  size_t pitch;  // bytes of a row of D
 };
 // K slices of dx = D E: the fewest rounds of one workgroup per CU, times the stages of one and
 // what its start and end cost (about 24 stages); at least 512 table rows each.
-int64_t backward_splits(int64_t piece, int64_t rows, int64_t hidden) {
-  const int64_t tiles = cdiv(hidden, 256) * cdiv(rows, rows_tile(rows));
+int64_t backward_splits(int64_t piece, int64_t n, int64_t hidden) {
+  const int64_t tiles = cdiv(hidden, 256) * cdiv(n, rows_tile(n));
   int64_t best = 1, least = INT64_MAX;
   for (int64_t s = 1; s <= std::max<int64_t>(1, piece / 512) && s <= 2 * kTargetBlocks; s++) {
     const int64_t cost = cdiv(tiles * s, kTargetBlocks) * (cdiv(piece, 64 * s) + 24);
@@ -973,42 +1117,38 @@ int64_t backward_splits(int64_t piece, int64_t rows, int64_t hidden) {
 BackwardWs backward_ws(const TableDesc& t, int64_t n) {
   const int size = t.dtype == DT_F32 ? 4 : 2;
   BackwardWs w = {};
-  size_t x_bytes, d_bytes;
+  size_t d_bytes;
   if (n <= kVectorRows) {
     // about eight waves per CU, each with 32 table rows at least
     w.chunks = (int)cdiv(t.row_bytes, 1024);
-    w.piece = even_piece(t.V, kPartBytes / (256 * 32)), w.rows = n, w.planes = 1;
+    w.piece = even_piece(t.V, kPartBytes / (256 * 32));
     w.slice = std::max<int64_t>(32, cdiv(w.piece, std::max<int64_t>(1, 8 * kTargetBlocks / w.chunks)));
     w.splits = cdiv(std::min(w.piece, t.V), w.slice);  // of the first piece, the fullest
     d_bytes = (size_t)w.piece * 32;
-    x_bytes = n * t.row_bytes;
   } else {
-    w.planes = t.dtype != DT_F32 && n <= kTwoPlaneRows ? 2 : 1;
-    w.rows = n * w.planes;
     // D of a piece stays within kPartBytes and its rows within 4 MiB
     w.piece = even_piece(t.V, std::min(std::min(kMaxTiles / cdiv(n, rows_tile(n)), (int64_t)4096),
-                                       kPartBytes / (w.rows * size * 256)));
-    w.slice = (int64_t)align_up(cdiv(w.piece, backward_splits(w.piece, w.rows, t.hidden)), 64);
+                                       kPartBytes / (n * size * 256)));
+    w.slice = (int64_t)align_up(cdiv(w.piece, backward_splits(w.piece, n, t.hidden)), 64);
     w.splits = cdiv(std::min(w.piece, t.V), w.slice);  // of the first piece, the fullest
     w.pitch = (size_t)(w.piece * size);
-    d_bytes = (size_t)w.rows * w.pitch;
-    x_bytes = w.rows * t.row_bytes;
+    d_bytes = (size_t)n * w.pitch;
   }
   w.rest = 256;  // after the two factors
   w.x = w.rest + align_up((size_t)n * 4, 256);
-  w.d = w.x + align_up(x_bytes, 256);
+  w.d = w.x + align_up((size_t)(n * t.row_bytes), 256);
   w.sums = w.d + align_up(d_bytes, 256);
-  w.bytes = w.sums + align_up((size_t)(w.splits * w.rows * t.hidden * 4), 256);
+  w.bytes = w.sums + align_up((size_t)(w.splits * n * t.hidden * 4), 256);
   return w;
 }
 
 // The residual rows as the kernels read them: 16-byte aligned, rows less than 8 MiB apart.
 bool rows_direct(const void* x, int64_t pitch) { return ((uintptr_t)x | (uint64_t)pitch) % 16 == 0 && pitch < (8 << 20); }
 
-hipError_t pack_rows(const XentCall& c, const TableDesc& t, int copies, uint8_t* to, hipStream_t stream) {
+hipError_t pack_rows(const XentCall& c, const TableDesc& t, uint8_t* to, hipStream_t stream) {
   const int64_t pieces = c.n * (t.row_bytes / 16);
   hipLaunchKernelGGL(xent_pack_kernel, dim3((unsigned)cdiv(pieces, 256)), dim3(256), 0, stream, (const uint8_t*)c.x,
-                     c.x_pitch, c.n, t.row_bytes, copies, to);
+                     c.x_pitch, c.n, t.row_bytes, to);
   return hipGetLastError();
 }
 
@@ -1020,7 +1160,7 @@ hipError_t forward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStream
   float2 *run = (float2*)ws, *part = (float2*)(ws + w.part);
   float* target = (float*)(ws + w.target);
   const bool direct = rows_direct(c.x, c.x_pitch);
-  if (!direct && (e = pack_rows(c, t, 1, ws + w.x, stream)) != hipSuccess) return e;
+  if (!direct && (e = pack_rows(c, t, ws + w.x, stream)) != hipSuccess) return e;
   const int64_t piece = w.direct ? t.V : w.piece;
   for (int64_t v0 = 0; v0 < t.V; v0 += piece) {
     XentProduct p = {};
@@ -1051,10 +1191,9 @@ hipError_t sum_slices(const TableDesc& t, const XentCall& c, const BackwardWs& w
                       const float* scale, const float* rest, hipStream_t stream) {
   const int64_t quads = c.n * (t.hidden / 4);
   // few values of many slices: 16 threads to a value's slices
-  const auto kernel = w.splits * w.planes >= 16 ? xent_sum_kernel<DT, 16> : xent_sum_kernel<DT, 1>;
-  const int each = w.splits * w.planes >= 16 ? 16 : 256;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv(quads, each)), dim3(256), 0, stream, sums, (int)w.splits, w.planes,
-                     c.n, t.hidden, c.d_x, c.d_x_pitch, scale, rest, c.labels, t.V, t.rows);
+  const auto kernel = w.splits >= 16 ? xent_sum_kernel<DT, 16> : xent_sum_kernel<DT, 1>;
+  const int each = w.splits >= 16 ? 16 : 256;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv(quads, each)), dim3(256), 0, stream, sums, (int)w.splits, c.n, t.hidden, c.d_x, c.d_x_pitch, scale, rest, c.labels, t.V, t.rows);
   return hipGetLastError();
 }
 
@@ -1066,8 +1205,8 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
   hipError_t e;
   uint8_t *packed = ws + w.x, *d = ws + w.d;
   float* sums = (float*)(ws + w.sums);
-  const bool direct = w.planes == 1 && rows_direct(c.x, c.x_pitch);
-  if (!direct && (e = pack_rows(c, t, w.planes, packed, stream)) != hipSuccess) return e;
+  const bool direct = rows_direct(c.x, c.x_pitch);
+  if (!direct && (e = pack_rows(c, t, packed, stream)) != hipSuccess) return e;
   XentProduct logits = {};  // of a piece, to D
   logits.n = c.n, logits.k = t.hidden, logits.a_pitch = t.row_bytes;
   logits.b = direct ? (const uint8_t*)c.x : packed, logits.b_pitch = direct ? c.x_pitch : t.row_bytes;
@@ -1096,21 +1235,20 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
     return sum_slices<DT>(t, c, w, sums, nullptr, nullptr, stream);
   }
   float* scale = DT == DT_F16 ? (float*)ws : nullptr;
-  float* rest = DT != DT_F32 && w.planes == 1 && c.d_x != nullptr ? (float*)(ws + w.rest) : nullptr;
+  float* rest = DT != DT_F32 ? (float*)(ws + w.rest) : nullptr;
   if (scale != nullptr) {
     hipLaunchKernelGGL(xent_scale_kernel, dim3(1), dim3(1024), 0, stream, c.labels, c.n, t.V, c.grad_loss,
                        c.grad_loss_all, c.grad_lse, scale);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   logits.scale = scale, logits.rest = rest;
-  logits.out_low = w.planes == 2 ? d + c.n * w.pitch : nullptr;
   for (int64_t v0 = 0; v0 < t.V; v0 += w.piece) {
     const int64_t rows = std::min(w.piece, t.V - v0);
     logits.a = t.rows + v0 * t.row_bytes, logits.m = rows, logits.v0 = v0;
     if ((e = launch_by_rows<DT, false, X_DLOGIT>(logits, stream)) != hipSuccess) return e;
     if (c.d_x != nullptr) {
       XentProduct p = {};
-      p.m = t.hidden, p.n = w.rows, p.k = rows;
+      p.m = t.hidden, p.n = c.n, p.k = rows;
       p.a = logits.a, p.a_pitch = t.row_bytes, p.b = d, p.b_pitch = (int64_t)w.pitch;
       p.splits = (int32_t)cdiv(rows, w.slice), p.kslice = (int32_t)w.slice;
       p.out = sums, p.add = v0 != 0;
@@ -1118,13 +1256,12 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
     }
     if (c.d_rows != nullptr) {
       XentProduct p = {};
-      p.m = t.hidden, p.n = rows, p.k = w.rows;
+      p.m = t.hidden, p.n = rows, p.k = c.n;
       p.a = logits.b, p.a_pitch = logits.b_pitch, p.b = d, p.b_pitch = (int64_t)w.pitch;
-      p.splits = 1, p.kslice = (int32_t)align_up((size_t)w.rows, 64);
-      p.out = (uint8_t*)c.d_rows + v0 * t.row_bytes, p.add = c.add, p.scale = scale;
-      if (w.rows <= 128) {  // two stages at most: bound by its stores, two workgroups per CU
-        p.mt = (int32_t)cdiv(p.m, 128), p.nt = (int32_t)cdiv(p.n, 128);
-        e = launch_ring<DT, true, true, X_OUT, 128, 128, 2, 2>(p, stream);
+      p.splits = 1, p.kslice = (int32_t)align_up((size_t)c.n, 64);
+      p.out = (uint8_t*)c.d_rows + v0 * t.row_bytes, p.add = c.add, p.scale = scale, p.labels = c.labels, p.v0 = v0, p.rest = rest;
+      if (c.n <= 2 * (128 / kValue<DT>)) {
+        e = launch_outer<DT>(p, stream);
       } else {
         p.mt = (int32_t)cdiv(p.m, 256), p.nt = (int32_t)cdiv(p.n, 256);
         e = launch_tile<DT, true, true, X_OUT>(p, stream);
