@@ -13,9 +13,27 @@
 
 namespace etg {
 
-constexpr int kTileKeys = 4096;   // keys of one workgroup of the radix sort
 constexpr int kSortWaves = 4;
-constexpr int kMaxDigits = 512;   // 9 bits
+constexpr int kMaxDigits = 1024;  // 10 bits
+
+// Zeros for the output, written by the workgroups behind those that sort: the sort's short
+// kernels leave the chip idle, and the fill has to be over before the sums are written anyway.
+// 16,384 ids into 262,144 x 768 f32 rows: FILLED.
+struct Fill {
+  u32x4* at;
+  int64_t n16;  // 16-byte pieces
+  static constexpr int kPieces = 8192;  // of one workgroup: 128 KiB
+  int64_t workgroups() const { return cdiv(n16, kPieces); }
+  // the g-th workgroup's part
+  __device__ __forceinline__ void run(int64_t g, int threads) const {
+    const u32x4 zero = {0, 0, 0, 0};
+    const int64_t end = min((g + 1) * kPieces, n16);
+#pragma unroll 4
+    for (int64_t i = g * kPieces + threadIdx.x; i < end; i += threads) at[i] = zero;
+  }
+};
+
+__global__ void __launch_bounds__(256) rowgrad_fill_kernel(Fill fill) { fill.run(blockIdx.x, 256); }
 
 // Bad ids sort behind every token.
 __device__ __forceinline__ uint32_t token_key(int32_t id, uint32_t V) { return min((uint32_t)id, V); }
@@ -27,19 +45,30 @@ __device__ __forceinline__ uint32_t token_key(int32_t id, uint32_t V) { return m
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024) rowgrad_rank_kernel(const int32_t* __restrict__ ids, int n, uint32_t V,
                                                             uint32_t* __restrict__ keys,
-                                                            uint32_t* __restrict__ order) {
+                                                            uint32_t* __restrict__ order, int work, Fill fill) {
   __shared__ uint32_t count[16][64];
+  if ((int)blockIdx.x >= work) {  // whole workgroup
+    fill.run((int)blockIdx.x - work, 1024);
+    return;
+  }
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i0 = blockIdx.x * 64, i = i0 + lane;
   const uint32_t key = i < n ? token_key(ids[i], V) : 0xffffffffu;
   const int each = (n + 16 * 64 - 1) / (16 * 64) * 64;  // whole blocks of 64
   uint32_t before = 0;
   for (int j0 = wv * each; j0 < min((wv + 1) * each, n); j0 += 64) {
-    const int m = min(64, n - j0);
+    // past the last id: larger than every key
     const uint32_t other = j0 + lane < n ? token_key(ids[j0 + lane], V) : 0xffffffffu;
-    for (int j = 0; j < m; j++) {  // equal ids keep their order
-      const uint32_t o = __builtin_amdgcn_readlane(other, j);
-      before += o < key || (o == key && j0 + j < i) ? 1u : 0u;
+    if (j0 != i0) {  // equal ids keep their order: those of an earlier block come before
+      const uint32_t limit = key + (j0 < i0 && i < n ? 1u : 0u);
+#pragma unroll 16
+      for (int j = 0; j < 64; j++) before += (uint32_t)__builtin_amdgcn_readlane(other, j) < limit ? 1u : 0u;
+    } else {
+#pragma unroll 16
+      for (int j = 0; j < 64; j++) {
+        const uint32_t o = __builtin_amdgcn_readlane(other, j);
+        before += o < key || (o == key && j < lane) ? 1u : 0u;
+      }
     }
   }
   count[wv][lane] = before;
@@ -53,96 +82,139 @@ __global__ void __launch_bounds__(1024) rowgrad_rank_kernel(const int32_t* __res
 
 // ---------------------------------------------------------------------------
 // More ids: a stable radix sort, least significant digit first.  Per pass: the digits'
-// counts of every tile of 4,096 keys, their running sum over (digit, tile), and the keys' move.
+// counts of every tile of keys, their running sum over (digit, tile), and the keys' move.
+// Up to kFewTiles tiles a workgroup of the move adds up what it needs of the counts itself;
+// more have a kernel for it.
 // ---------------------------------------------------------------------------
+constexpr int kFewTiles = 64;
+
 struct SortPass {
   const int32_t* ids;        // the first pass: the ids themselves, positions 0, 1, ..
   const uint32_t *key, *pos;
   int64_t n;
   uint32_t V;
-  int shift, bits, tiles;
+  int shift, bits, tiles, tile;  // tile: keys of one, a multiple of 256
   __device__ __forceinline__ uint32_t load_key(int64_t i) const { return ids != nullptr ? token_key(ids[i], V) : key[i]; }
   __device__ __forceinline__ uint32_t digit(uint32_t k) const { return (k >> shift) & ((1u << bits) - 1); }
 };
 
-__global__ void __launch_bounds__(64 * kSortWaves) rowgrad_count_kernel(SortPass p, uint32_t* __restrict__ counts) {
+// counts [tiles][kMaxDigits]
+__global__ void __launch_bounds__(64 * kSortWaves) rowgrad_count_kernel(SortPass p, uint32_t* __restrict__ counts,
+                                                                        Fill fill) {
   __shared__ uint32_t hist[kMaxDigits];
-  const int digits = 1 << p.bits;
-  for (int d = threadIdx.x; d < digits; d += 64 * kSortWaves) hist[d] = 0;
+  if ((int)blockIdx.x >= p.tiles) {  // whole workgroup
+    fill.run((int)blockIdx.x - p.tiles, 64 * kSortWaves);
+    return;
+  }
+  for (int d = threadIdx.x; d < kMaxDigits; d += 64 * kSortWaves) hist[d] = 0;
   __syncthreads();
-  const int64_t i0 = (int64_t)blockIdx.x * kTileKeys;
-  for (int j = threadIdx.x; j < kTileKeys && i0 + j < p.n; j += 64 * kSortWaves)
-    atomicAdd(&hist[p.digit(p.load_key(i0 + j))], 1u);
+  const int64_t i0 = (int64_t)blockIdx.x * p.tile;
+#pragma unroll 4
+  for (int j = threadIdx.x; j < p.tile; j += 64 * kSortWaves)
+    if (i0 + j < p.n) atomicAdd(&hist[p.digit(p.load_key(i0 + j))], 1u);
   __syncthreads();
-  for (int d = threadIdx.x; d < digits; d += 64 * kSortWaves) counts[(int64_t)d * p.tiles + blockIdx.x] = hist[d];
+  for (int d = threadIdx.x; d < kMaxDigits; d += 64 * kSortWaves) counts[(int64_t)blockIdx.x * kMaxDigits + d] = hist[d];
 }
 
-// counts -> their exclusive running sum, in place.  One workgroup, a contiguous share per thread.
-__global__ void __launch_bounds__(1024) rowgrad_scan_kernel(uint32_t* __restrict__ counts, int64_t n) {
-  __shared__ uint32_t sums[16];
+// Exclusive running sum of one value per thread over a workgroup of 64 W threads; the total too.
+template <int W>
+__device__ __forceinline__ uint32_t workgroup_scan(uint32_t v, uint32_t (&sums)[W], uint32_t* total) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  uint32_t base = 0;
-  for (int64_t c0 = 0; c0 < n; c0 += 8 * 1024) {
-    const int64_t at = c0 + 8 * (int64_t)threadIdx.x;
-    uint32_t v[8], total = 0;
+  uint32_t incl = v;
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-      v[j] = at + j < n ? counts[at + j] : 0u;
-      total += v[j];
-    }
-    uint32_t incl = total;
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t up = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 63) sums[wv] = incl;
+  __syncthreads();
+  uint32_t run = incl - v, all = 0;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t up = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += up;
-    }
-    if (lane == 63) sums[wv] = incl;
-    __syncthreads();
-    uint32_t run = base + incl - total, all = 0;
-#pragma unroll
-    for (int w = 0; w < 16; w++) {
-      if (w < wv) run += sums[w];
-      all += sums[w];
-    }
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-      if (at + j < n) counts[at + j] = run;
-      run += v[j];
-    }
-    base += all;
-    __syncthreads();
+  for (int w = 0; w < W; w++) {
+    if (w < wv) run += sums[w];
+    all += sums[w];
+  }
+  __syncthreads();
+  *total = all;
+  return run;
+}
+
+// counts -> where a tile's first key of each digit goes, in place.  One workgroup, a thread per
+// digit.
+__global__ void __launch_bounds__(kMaxDigits) rowgrad_scan_kernel(uint32_t* __restrict__ counts, int tiles, Fill fill) {
+  __shared__ uint32_t sums[kMaxDigits / 64];
+  if (blockIdx.x > 0) {  // whole workgroup
+    fill.run((int)blockIdx.x - 1, kMaxDigits);
+    return;
+  }
+  uint32_t own = 0, total;
+#pragma unroll 8
+  for (int t = 0; t < tiles; t++) own += counts[(int64_t)t * kMaxDigits + threadIdx.x];
+  uint32_t run = workgroup_scan(own, sums, &total);
+#pragma unroll 8
+  for (int t = 0; t < tiles; t++) {
+    const uint32_t c = counts[(int64_t)t * kMaxDigits + threadIdx.x];
+    counts[(int64_t)t * kMaxDigits + threadIdx.x] = run;
+    run += c;
   }
 }
 
-__global__ void __launch_bounds__(64 * kSortWaves) rowgrad_move_kernel(SortPass p,
-                                                                       const uint32_t* __restrict__ offsets,
+// FEW: counts as the count kernel left them, else as the scan kernel did.
+template <bool FEW>
+__global__ void __launch_bounds__(64 * kSortWaves) rowgrad_move_kernel(SortPass p, const uint32_t* __restrict__ counts,
                                                                        uint32_t* __restrict__ key_out,
-                                                                       uint32_t* __restrict__ pos_out) {
+                                                                       uint32_t* __restrict__ pos_out, Fill fill) {
   __shared__ uint32_t next[kSortWaves][kMaxDigits];  // where a wave's next key of a digit goes
-  constexpr int SHARE = kTileKeys / kSortWaves;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int digits = 1 << p.bits;
+  __shared__ uint32_t sums[kSortWaves];
+  constexpr int DPT = kMaxDigits / (64 * kSortWaves);  // digits of a thread, side by side
+  static_assert(DPT == 4, "16-byte loads of the counts");
+  if ((int)blockIdx.x >= p.tiles) {  // whole workgroup
+    fill.run((int)blockIdx.x - p.tiles, 64 * kSortWaves);
+    return;
+  }
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, share = p.tile / kSortWaves;
   for (int d = threadIdx.x; d < kSortWaves * kMaxDigits; d += 64 * kSortWaves) ((uint32_t*)next)[d] = 0;
   __syncthreads();
-  const int64_t i0 = (int64_t)blockIdx.x * kTileKeys + wv * SHARE;
-  for (int j = lane; j < SHARE && i0 + j < p.n; j += 64) atomicAdd(&next[wv][p.digit(p.load_key(i0 + j))], 1u);
+  const int64_t i0 = (int64_t)blockIdx.x * p.tile + wv * share;
+#pragma unroll 4
+  for (int j = lane; j < share; j += 64)
+    if (i0 + j < p.n) atomicAdd(&next[wv][p.digit(p.load_key(i0 + j))], 1u);
+  u32x4 at = {0, 0, 0, 0};
+  const int d0 = DPT * threadIdx.x;
+  if constexpr (FEW) {
+    u32x4 all = {0, 0, 0, 0};
+#pragma unroll 8
+    for (int t = 0; t < p.tiles; t++) {
+      const u32x4 c = *(const u32x4*)(counts + (int64_t)t * kMaxDigits + d0);
+      all += c;
+      if (t < (int)blockIdx.x) at += c;
+    }
+    uint32_t total, run = workgroup_scan(all[0] + all[1] + all[2] + all[3], sums, &total);
+#pragma unroll
+    for (int q = 0; q < DPT; q++) {
+      at[q] += run;
+      run += all[q];
+    }
+  } else {
+    at = *(const u32x4*)(counts + (int64_t)blockIdx.x * kMaxDigits + d0);
+  }
   __syncthreads();
-  for (int d = threadIdx.x; d < digits; d += 64 * kSortWaves) {
-    uint32_t at = offsets[(int64_t)d * p.tiles + blockIdx.x];
+#pragma unroll
+  for (int q = 0; q < DPT; q++)
 #pragma unroll
     for (int w = 0; w < kSortWaves; w++) {
-      const uint32_t c = next[w][d];
-      next[w][d] = at;
-      at += c;
+      const uint32_t c = next[w][d0 + q];
+      next[w][d0 + q] = at[q];
+      at[q] += c;
     }
-  }
   __syncthreads();
   // the wave's keys in order, 64 at a time: a key's place among them is the number of lanes
   // below with its digit
-  for (int j = 0; j < SHARE && i0 + j < p.n; j += 64) {
+  for (int j = 0; j < share && i0 + j < p.n; j += 64) {
     const int64_t i = i0 + j + lane;
     const bool some = i < p.n;
     const uint32_t k = some ? p.load_key(i) : 0u;
+    const uint32_t pos = some && p.ids == nullptr ? p.pos[i] : (uint32_t)i;
     const uint32_t d = p.digit(k);
     uint64_t same = __ballot(some);
     for (int b = 0; b < p.bits; b++) {
@@ -150,13 +222,13 @@ __global__ void __launch_bounds__(64 * kSortWaves) rowgrad_move_kernel(SortPass 
       same &= (d >> b) & 1 ? ones : ~ones;
     }
     const uint32_t below = (uint32_t)__builtin_popcountll(same & ((1ull << lane) - 1));
-    const uint32_t at = some ? next[wv][d] + below : 0u;
+    const uint32_t to = some ? next[wv][d] + below : 0u;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // every lane has read its counter before it moves on
-    if (some && below == 0) next[wv][d] = at + (uint32_t)__builtin_popcountll(same);
+    if (some && below == 0) next[wv][d] = to + (uint32_t)__builtin_popcountll(same);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (some) {
-      key_out[at] = k;
-      pos_out[at] = p.ids != nullptr ? (uint32_t)i : p.pos[i];
+      key_out[to] = k;
+      pos_out[to] = pos;
     }
   }
 }
@@ -203,19 +275,18 @@ __device__ __forceinline__ Vec<E> load_vec(const uint8_t* at) {
   return v;
 }
 
-// out row = type([out row +] scale * sum): the product and the sum rounded to f32, then to the type
+template <int DT>
+__device__ __forceinline__ uint8_t* out_row(const RowSums& p, uint32_t v, int c) {
+  return (uint8_t*)p.out + ((int64_t)v * p.hidden + c) * (DT == DT_F32 ? 4 : 2);
+}
+
+// out row = type([old +] scale * sum): the product and the sum rounded to f32, then to the type
 template <int DT, int E>
-__device__ __forceinline__ void write_row(const RowSums& p, uint32_t v, int c, const Vec<E>& sum) {
-  constexpr int ES = DT == DT_F32 ? 4 : 2;
-  uint8_t* at = (uint8_t*)p.out + ((int64_t)v * p.hidden + c) * ES;
+__device__ __forceinline__ void write_row(const RowSums& p, uint32_t v, int c, const Vec<E>& sum, const Vec<E>& old) {
+  uint8_t* at = out_row<DT>(p, v, c);
   Vec<E> x;
 #pragma unroll
-  for (int i = 0; i < E; i++) x.x[i] = sum.x[i] * p.scale;
-  if (p.add) {
-    const Vec<E> old = load_vec<DT, E>(at);
-#pragma unroll
-    for (int i = 0; i < E; i++) x.x[i] += old.x[i];
-  }
+  for (int i = 0; i < E; i++) x.x[i] = p.add ? old.x[i] + sum.x[i] * p.scale : sum.x[i] * p.scale;
 #pragma unroll
   for (int q = 0; q < E / 4; q++) {
     const f32x4 w = {x.x[4 * q], x.x[4 * q + 1], x.x[4 * q + 2], x.x[4 * q + 3]};
@@ -238,7 +309,8 @@ __device__ __forceinline__ void write_part(float* at, const Vec<E>& sum) {
     ((f32x4*)at)[q] = f32x4{sum.x[4 * q], sum.x[4 * q + 1], sum.x[4 * q + 2], sum.x[4 * q + 3]};
 }
 
-// A wave per piece and 64 E columns; U rows are loaded before the first is added.
+// A wave per piece and 64 E columns; U rows, and the output rows that their runs' ends are added
+// to, are loaded before the first is used.
 template <int GDT, int ODT, int E>
 __global__ void __launch_bounds__(256) rowgrad_sum_kernel(RowSums p) {
   constexpr int U = 8, ES = GDT == DT_F32 ? 4 : 2;
@@ -248,42 +320,43 @@ __global__ void __launch_bounds__(256) rowgrad_sum_kernel(RowSums p) {
   const bool live = c < p.hidden;
   const int cl = live ? c : 0;
   const int64_t q = blockIdx.x, begin = q * p.piece, end = min(begin + p.piece, p.n);
-  uint32_t cur = p.keys[begin];
-  bool entered = begin > 0 && p.keys[begin - 1] == cur;
+  bool entered = begin > 0 && p.keys[begin - 1] == p.keys[begin];
   Vec<E> acc = {};
-  auto flush = [&](bool leaves) {
-    if (cur >= p.V || !live) return;
-    if (entered || leaves) write_part<E>(p.part + (2 * q + (entered ? 0 : 1)) * p.hidden + c, acc);
-    else write_row<ODT, E>(p, cur, c, acc);
-  };
-  for (int64_t b = begin; b < end && cur < p.V; b += 64) {
+  for (int64_t b = begin; b < end; b += 64) {
     const int m = (int)min((int64_t)64, end - b);
+    // the key behind the last one ends its run there; none: 0xffffffff
     const uint32_t key64 = lane < m ? p.keys[b + lane] : 0xffffffffu, pos64 = lane < m ? p.order[b + lane] : 0u;
-    for (int j = 0; j < m && cur < p.V; j += U) {
-      Vec<E> row[U];
+    const uint32_t behind = b + m < p.n ? p.keys[b + m] : 0xffffffffu;
+    for (int j = 0; j < m; j += U) {
+      Vec<E> row[U], old[U];
+      uint32_t key[U + 1];
+#pragma unroll
+      for (int u = 0; u <= U; u++) key[u] = j + u < m ? __builtin_amdgcn_readlane(key64, (j + u) & 63) : behind;
+      if (key[0] >= p.V) return;  // bad ids from here on; the run before them has been written
 #pragma unroll
       for (int u = 0; u < U; u++) {
         const uint32_t pos = __builtin_amdgcn_readlane(pos64, min(j + u, m - 1));
         row[u] = load_vec<GDT, E>(p.grad + (int64_t)pos * p.pitch + (int64_t)cl * ES);
+        old[u] = {};
+        if (p.add && j + u < m && key[u] != key[u + 1] && key[u] < p.V) old[u] = load_vec<ODT, E>(out_row<ODT>(p, key[u], cl));
       }
 #pragma unroll
       for (int u = 0; u < U; u++) {
-        if (j + u >= m || cur >= p.V) break;  // uniform
-        const uint32_t k = __builtin_amdgcn_readlane(key64, j + u);
-        if (k != cur) {
-          flush(false);
-          cur = k;
-          entered = false;
-          if (k >= p.V) break;
-#pragma unroll
-          for (int i = 0; i < E; i++) acc.x[i] = 0.f;
-        }
+        if (j + u >= m || key[u] >= p.V) break;  // uniform
 #pragma unroll
         for (int i = 0; i < E; i++) acc.x[i] += row[u].x[i];
+        const bool last = b + j + u + 1 == end, leaves = last && key[u] == key[u + 1];
+        if (!last && key[u] == key[u + 1]) continue;
+        if (live) {
+          if (entered || leaves) write_part<E>(p.part + (2 * q + (entered ? 0 : 1)) * p.hidden + c, acc);
+          else write_row<ODT, E>(p, key[u], c, acc, old[u]);
+        }
+        entered = false;
+#pragma unroll
+        for (int i = 0; i < E; i++) acc.x[i] = 0.f;
       }
     }
   }
-  flush(end < p.n && p.keys[end] == cur);
 }
 
 // A workgroup per piece and 256 columns.  If a run begins in the piece and leaves it: its
@@ -320,17 +393,17 @@ __global__ void __launch_bounds__(256) rowgrad_join_kernel(RowSums p) {
 #pragma unroll
   for (int w = 1; w < 4; w++) acc += sums[w][lane];
   const Vec<4> x = {{acc[0], acc[1], acc[2], acc[3]}};
-  write_row<ODT, 4>(p, cur, c, x);
+  write_row<ODT, 4>(p, cur, c, x, p.add ? load_vec<ODT, 4>(out_row<ODT>(p, cur, c)) : Vec<4>{});
 }
 
 namespace {
 
-constexpr int64_t kRankIds = 8192;                 // most ids placed by comparison
+constexpr int64_t kRankIds = 4096;                 // most ids placed by comparison
 constexpr int64_t kPartialBytes = (int64_t)256 << 20;
 
 struct RowGradWs {
   int64_t piece;
-  int passes, bits, tiles;
+  int passes, bits, tiles, tile;
   size_t keys[2], pos[2], counts, part, bytes;
 };
 RowGradWs rowgrad_ws(int64_t n, int64_t V, int64_t hidden) {
@@ -342,9 +415,10 @@ RowGradWs rowgrad_ws(int64_t n, int64_t V, int64_t hidden) {
   if (!ranked) {
     int bits = 1;
     while (((uint64_t)V >> bits) != 0) bits++;  // keys 0 .. V
-    w.passes = (bits + 8) / 9;
+    w.passes = (bits + 9) / 10;
     w.bits = (bits + w.passes - 1) / w.passes;
-    w.tiles = (int)cdiv(n, kTileKeys);
+    w.tile = n <= 1024 * kFewTiles ? 1024 : 4096;
+    w.tiles = (int)cdiv(n, w.tile);
   }
   size_t at = 0;
   for (int i = 0; i < (ranked ? 1 : 2); i++) {
@@ -359,6 +433,19 @@ RowGradWs rowgrad_ws(int64_t n, int64_t V, int64_t hidden) {
   w.bytes = at + align_up((size_t)(cdiv(n, w.piece) * 2 * hidden * 4), 256);
   return w;
 }
+
+// Hands out the output's zeros over the launches of the sort.
+struct FillShares {
+  Fill rest;
+  int launches;
+  // the next launch's share, a launch with `work` workgroups of its own
+  Fill next() {
+    Fill f = rest;
+    f.n16 = std::min(rest.n16, cdiv(cdiv(rest.n16, Fill::kPieces), std::max(launches, 1)) * Fill::kPieces);
+    rest.at += f.n16, rest.n16 -= f.n16, launches--;
+    return f;
+  }
+};
 
 template <int GDT, int ODT>
 hipError_t launch_sums(const RowSums& p, hipStream_t stream) {
@@ -393,32 +480,48 @@ size_t rowgrad_workspace(int64_t n, int64_t V, int64_t hidden) { return n == 0 ?
 
 hipError_t launch_rowgrad(const RowGrad& g, void* ws, hipStream_t stream) {
   hipError_t e;
-  if (!g.add) {
-    const int64_t bytes = g.V * g.hidden * (g.out_dtype == DT_F32 ? 4 : 2);  // whole rows of 16 bytes
-    if ((e = launch_write_probe(g.out, bytes, 0, stream)) != hipSuccess) return e;
+  // whole rows of 16 bytes
+  Fill all = {(u32x4*)g.out, g.add ? 0 : g.V * g.hidden * (g.out_dtype == DT_F32 ? 4 : 2) / 16};
+  // one launch writes at most 2^20 workgroups' zeros; what the sort's launches cannot take goes first
+  while (all.n16 > ((int64_t)1 << 20) * Fill::kPieces || (g.n == 0 && all.n16 > 0)) {
+    const Fill f = {all.at, std::min(all.n16, ((int64_t)1 << 20) * Fill::kPieces)};
+    hipLaunchKernelGGL(rowgrad_fill_kernel, dim3((unsigned)f.workgroups()), dim3(256), 0, stream, f);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    all.at += f.n16, all.n16 -= f.n16;
   }
   if (g.n == 0) return hipSuccess;
   const RowGradWs w = rowgrad_ws(g.n, g.V, g.hidden);
   uint8_t* base = (uint8_t*)ws;
   uint32_t *keys = (uint32_t*)(base + w.keys[0]), *order = (uint32_t*)(base + w.pos[0]);
   if (w.passes == 0) {
-    hipLaunchKernelGGL(rowgrad_rank_kernel, dim3((unsigned)cdiv(g.n, 64)), dim3(1024), 0, stream, g.ids, (int)g.n,
-                       (uint32_t)g.V, keys, order);
+    const int work = (int)cdiv(g.n, 64);
+    hipLaunchKernelGGL(rowgrad_rank_kernel, dim3((unsigned)(work + all.workgroups())), dim3(1024), 0, stream, g.ids,
+                       (int)g.n, (uint32_t)g.V, keys, order, work, all);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
+  const bool few = w.tiles <= kFewTiles;
+  FillShares shares = {all, w.passes * (few ? 2 : 3)};
   for (int i = 0; i < w.passes; i++) {
     SortPass p = {};
     p.ids = i == 0 ? g.ids : nullptr;
     p.key = (uint32_t*)(base + w.keys[(i + 1) % 2]), p.pos = (uint32_t*)(base + w.pos[(i + 1) % 2]);
-    p.n = g.n, p.V = (uint32_t)g.V, p.shift = i * w.bits, p.bits = w.bits, p.tiles = w.tiles;
+    p.n = g.n, p.V = (uint32_t)g.V, p.shift = i * w.bits, p.bits = w.bits, p.tiles = w.tiles, p.tile = w.tile;
     keys = (uint32_t*)(base + w.keys[i % 2]), order = (uint32_t*)(base + w.pos[i % 2]);
     uint32_t* counts = (uint32_t*)(base + w.counts);
-    hipLaunchKernelGGL(rowgrad_count_kernel, dim3((unsigned)w.tiles), dim3(64 * kSortWaves), 0, stream, p, counts);
+    Fill f = shares.next();
+    hipLaunchKernelGGL(rowgrad_count_kernel, dim3((unsigned)(w.tiles + f.workgroups())), dim3(64 * kSortWaves), 0,
+                       stream, p, counts, f);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(rowgrad_scan_kernel, dim3(1), dim3(1024), 0, stream, counts, (int64_t)w.tiles << w.bits);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(rowgrad_move_kernel, dim3((unsigned)w.tiles), dim3(64 * kSortWaves), 0, stream, p, counts, keys,
-                       order);
+    if (!few) {
+      f = shares.next();
+      hipLaunchKernelGGL(rowgrad_scan_kernel, dim3((unsigned)(1 + f.workgroups())), dim3(kMaxDigits), 0, stream,
+                         counts, w.tiles, f);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    f = shares.next();
+    hipLaunchKernelGGL(few ? rowgrad_move_kernel<true> : rowgrad_move_kernel<false>,
+                       dim3((unsigned)(w.tiles + f.workgroups())), dim3(64 * kSortWaves), 0, stream, p, counts, keys,
+                       order, f);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   RowSums p = {};

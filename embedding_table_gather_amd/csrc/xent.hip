@@ -740,7 +740,9 @@ __global__ void __launch_bounds__(256) direct_kernel(XentProduct p) {
   const int c0 = steps * wv / 4, c1 = steps * (wv + 1) / 4;
   const uint8_t* ar = p.a + min(m0 + (lane & 15), p.m - 1) * p.a_pitch;
   const uint8_t* br = p.b + min(n0 + (lane & 15), p.n - 1) * p.b_pitch;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  f32x4 part[U];  // short sums: logits near their log-partition lose little
+#pragma unroll
+  for (int u = 0; u < U; u++) part[u] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int c = c0; c < c1; c += U) {
     u32x4 a[U], b[U];
 #pragma unroll
@@ -751,8 +753,9 @@ __global__ void __launch_bounds__(256) direct_kernel(XentProduct p) {
       b[u] = in ? *(const u32x4*)(br + at) : u32x4{0, 0, 0, 0};
     }
 #pragma unroll
-    for (int u = 0; u < U; u++) acc = mma<DT>(a[u], b[u], acc);
+    for (int u = 0; u < U; u++) part[u] = mma<DT>(a[u], b[u], part[u]);
   }
+  const f32x4 acc = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
   for (int i = 0; i < 4; i++) sums[wv][lane & 15][4 * g + i] = acc[i];
   __syncthreads();
