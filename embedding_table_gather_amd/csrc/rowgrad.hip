@@ -245,7 +245,6 @@ struct RowSums {
   int hidden, piece;
   float scale;
   void* out;
-  int32_t add;
   float* part;     // [pieces][2][hidden]: the run that enters a piece, the one that only leaves it
 };
 
@@ -254,26 +253,33 @@ struct Vec {
   float x[E];
 };
 
+// E values as they are stored, at any address of the type, and their values.
 template <int DT, int E>
-__device__ __forceinline__ Vec<E> load_vec(const uint8_t* at) {
-  Vec<E> v;
-  if constexpr (DT == DT_F32) {
-    typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+struct Raw {
+  static constexpr int WORDS = E * (DT == DT_F32 ? 4 : 2) / 4;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void load(const uint8_t* at) {
+    if constexpr (WORDS % 4 == 0) {
+      typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
 #pragma unroll
-    for (int q = 0; q < E / 4; q++) {
-      const f32x4u w = ((const f32x4u*)at)[q];
+      for (int q = 0; q < WORDS / 4; q++) {
+        const u32x4u v = ((const u32x4u*)at)[q];
 #pragma unroll
-      for (int i = 0; i < 4; i++) v.x[4 * q + i] = w[i];
+        for (int i = 0; i < 4; i++) w[4 * q + i] = v[i];
+      }
+    } else {
+      static_assert(WORDS == 2, "four 16-bit values");
+      typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(2)));
+      const u32x2u v = *(const u32x2u*)at;
+      w[0] = v[0], w[1] = v[1];
     }
-  } else {
-    typedef uint16_t u16xEu __attribute__((ext_vector_type(E), aligned(2)));
-    const u16xEu w = *(const u16xEu*)at;
-#pragma unroll
-    for (int i = 0; i < E; i++)
-      v.x[i] = DT == DT_BF16 ? __uint_as_float((uint32_t)w[i] << 16) : f16_bits_to_f32(w[i]);
   }
-  return v;
-}
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (DT == DT_F32) return __uint_as_float(w[i]);
+    else if constexpr (DT == DT_BF16) return i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    else return f16_bits_to_f32(w[i / 2] >> 16 * (i % 2) & 0xffffu);
+  }
+};
 
 template <int DT>
 __device__ __forceinline__ uint8_t* out_row(const RowSums& p, uint32_t v, int c) {
@@ -281,12 +287,13 @@ __device__ __forceinline__ uint8_t* out_row(const RowSums& p, uint32_t v, int c)
 }
 
 // out row = type([old +] scale * sum): the product and the sum rounded to f32, then to the type
-template <int DT, int E>
-__device__ __forceinline__ void write_row(const RowSums& p, uint32_t v, int c, const Vec<E>& sum, const Vec<E>& old) {
+template <int DT, int E, bool ADD>
+__device__ __forceinline__ void write_row(const RowSums& p, uint32_t v, int c, const Vec<E>& sum,
+                                          const Raw<DT, E>& old) {
   uint8_t* at = out_row<DT>(p, v, c);
   Vec<E> x;
 #pragma unroll
-  for (int i = 0; i < E; i++) x.x[i] = p.add ? old.x[i] + sum.x[i] * p.scale : sum.x[i] * p.scale;
+  for (int i = 0; i < E; i++) x.x[i] = ADD ? old.value(i) + sum.x[i] * p.scale : sum.x[i] * p.scale;
 #pragma unroll
   for (int q = 0; q < E / 4; q++) {
     const f32x4 w = {x.x[4 * q], x.x[4 * q + 1], x.x[4 * q + 2], x.x[4 * q + 3]};
@@ -309,9 +316,9 @@ __device__ __forceinline__ void write_part(float* at, const Vec<E>& sum) {
     ((f32x4*)at)[q] = f32x4{sum.x[4 * q], sum.x[4 * q + 1], sum.x[4 * q + 2], sum.x[4 * q + 3]};
 }
 
-// A wave per piece and 64 E columns; U rows, and the output rows that their runs' ends are added
+// A wave per piece and 64 E columns; U rows, and the output rows that their runs' sums are added
 // to, are loaded before the first is used.
-template <int GDT, int ODT, int E>
+template <int GDT, int ODT, int E, bool ADD>
 __global__ void __launch_bounds__(256) rowgrad_sum_kernel(RowSums p) {
   constexpr int U = 8, ES = GDT == DT_F32 ? 4 : 2;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -327,29 +334,45 @@ __global__ void __launch_bounds__(256) rowgrad_sum_kernel(RowSums p) {
     // the key behind the last one ends its run there; none: 0xffffffff
     const uint32_t key64 = lane < m ? p.keys[b + lane] : 0xffffffffu, pos64 = lane < m ? p.order[b + lane] : 0u;
     const uint32_t behind = b + m < p.n ? p.keys[b + m] : 0xffffffffu;
+    auto load = [&](int j, Raw<GDT, E> (&row)[U]) {  // past the last: the last again
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        const uint32_t pos = __builtin_amdgcn_readlane(pos64, min(j + u, m - 1));
+        row[u].load(p.grad + (int64_t)pos * p.pitch + (int64_t)cl * ES);
+      }
+    };
+    Raw<GDT, E> ahead[U];
+    load(0, ahead);
     for (int j = 0; j < m; j += U) {
-      Vec<E> row[U], old[U];
+      Raw<GDT, E> row[U];
+      Raw<ODT, E> old[U];
       uint32_t key[U + 1];
 #pragma unroll
       for (int u = 0; u <= U; u++) key[u] = j + u < m ? __builtin_amdgcn_readlane(key64, (j + u) & 63) : behind;
       if (key[0] >= p.V) return;  // bad ids from here on; the run before them has been written
 #pragma unroll
       for (int u = 0; u < U; u++) {
-        const uint32_t pos = __builtin_amdgcn_readlane(pos64, min(j + u, m - 1));
-        row[u] = load_vec<GDT, E>(p.grad + (int64_t)pos * p.pitch + (int64_t)cl * ES);
-        old[u] = {};
-        if (p.add && j + u < m && key[u] != key[u + 1] && key[u] < p.V) old[u] = load_vec<ODT, E>(out_row<ODT>(p, key[u], cl));
+        row[u] = ahead[u];
+        // all of them here: the compiler would move each load to its use
+#pragma unroll
+        for (int i = 0; i < Raw<GDT, E>::WORDS; i++) asm volatile("" : "+v"(row[u].w[i]));
+      }
+      if (j + U < m) load(j + U, ahead);
+      if constexpr (ADD) {
+#pragma unroll
+        for (int u = 0; u < U; u++)  // (a row within the table where no run ends: not used)
+          old[u].load(out_row<ODT>(p, key[u] != key[u + 1] && key[u] < p.V ? key[u] : key[0], cl));
       }
 #pragma unroll
       for (int u = 0; u < U; u++) {
         if (j + u >= m || key[u] >= p.V) break;  // uniform
 #pragma unroll
-        for (int i = 0; i < E; i++) acc.x[i] += row[u].x[i];
+        for (int i = 0; i < E; i++) acc.x[i] += row[u].value(i);
         const bool last = b + j + u + 1 == end, leaves = last && key[u] == key[u + 1];
         if (!last && key[u] == key[u + 1]) continue;
         if (live) {
           if (entered || leaves) write_part<E>(p.part + (2 * q + (entered ? 0 : 1)) * p.hidden + c, acc);
-          else write_row<ODT, E>(p, key[u], c, acc, old[u]);
+          else write_row<ODT, E, ADD>(p, key[u], c, acc, old[u]);
         }
         entered = false;
 #pragma unroll
@@ -359,17 +382,19 @@ __global__ void __launch_bounds__(256) rowgrad_sum_kernel(RowSums p) {
   }
 }
 
-// A workgroup per piece and 256 columns.  If a run begins in the piece and leaves it: its
-// partial sums, a contiguous share of them per wave.
-template <int ODT>
+// A wave per piece and 256 columns, four of them to a workgroup.  If a run begins in the piece and
+// leaves it: its partial sums, in order.
+template <int ODT, bool ADD>
 __global__ void __launch_bounds__(256) rowgrad_join_kernel(RowSums p) {
-  __shared__ f32x4 sums[4][64];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t q = blockIdx.x, begin = q * p.piece, end = begin + p.piece;
   if (end >= p.n) return;
-  const uint32_t cur = p.keys[end - 1];
-  if (cur >= p.V || p.keys[end] != cur) return;                                        // nothing leaves
-  if (p.keys[begin] == cur && begin > 0 && p.keys[begin - 1] == cur) return;           // it began before
+  const uint32_t before = begin > 0 ? p.keys[begin - 1] : 0xffffffffu;
+  const uint32_t first = p.keys[begin], cur = p.keys[end - 1], after = p.keys[end];
+  if (cur >= p.V || after != cur) return;        // nothing leaves
+  if (first == cur && before == cur) return;     // it began before
+  const int c = (((int)blockIdx.y * 4 + wv) * 64 + lane) * 4;
+  if (c >= p.hidden) return;
   int64_t lo = end, hi = p.n;  // the first position behind the run
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
@@ -377,23 +402,23 @@ __global__ void __launch_bounds__(256) rowgrad_join_kernel(RowSums p) {
     else hi = mid;
   }
   const int64_t pieces = (lo - 1) / p.piece - q;  // after this one
-  const int c = ((int)blockIdx.y * 64 + lane) * 4;
-  const bool live = c < p.hidden;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  if (live) {
-    const int64_t each = (pieces + 3) / 4;
-    const float* at = p.part + 2 * (q + 1) * p.hidden + c;
-    if (wv == 0) acc = *(const f32x4*)(p.part + (2 * q + 1) * p.hidden + c);
-#pragma unroll 8
-    for (int64_t i = wv * each; i < min((wv + 1) * each, pieces); i++) acc += *(const f32x4*)(at + 2 * i * p.hidden);
-  }
-  sums[wv][lane] = acc;
-  __syncthreads();
-  if (wv != 0 || !live) return;
+  Raw<ODT, 4> old;
+  if constexpr (ADD) old.load(out_row<ODT>(p, cur, c));
+  f32x4 acc = *(const f32x4*)(p.part + (2 * q + 1) * p.hidden + c);
+  const float* at = p.part + 2 * (q + 1) * p.hidden + c;
+  int64_t i = 0;
+  for (; i + 16 <= pieces; i += 16) {
+    f32x4 x[16];
 #pragma unroll
-  for (int w = 1; w < 4; w++) acc += sums[w][lane];
-  const Vec<4> x = {{acc[0], acc[1], acc[2], acc[3]}};
-  write_row<ODT, 4>(p, cur, c, x, p.add ? load_vec<ODT, 4>(out_row<ODT>(p, cur, c)) : Vec<4>{});
+    for (int u = 0; u < 16; u++) x[u] = *(const f32x4*)(at + 2 * (i + u) * p.hidden);
+#pragma unroll
+    for (int o = 1; o < 16; o *= 2)
+#pragma unroll
+      for (int u = 0; u < 16; u += 2 * o) x[u] += x[u + o];
+    acc += x[0];
+  }
+  for (; i < pieces; i++) acc += *(const f32x4*)(at + 2 * i * p.hidden);
+  write_row<ODT, 4, ADD>(p, cur, c, Vec<4>{{acc[0], acc[1], acc[2], acc[3]}}, old);
 }
 
 namespace {
@@ -408,8 +433,8 @@ struct RowGradWs {
 };
 RowGradWs rowgrad_ws(int64_t n, int64_t V, int64_t hidden) {
   RowGradWs w = {};
-  // 32 positions to a piece, 8 where there are few; more where the partial sums would not fit
-  w.piece = n <= 4096 ? 8 : 32;
+  // 8 positions to a piece where there are few, up to 64; more where the partial sums would not fit
+  w.piece = n <= 4096 ? 8 : n <= 32768 ? 32 : 64;
   w.piece = std::max<int64_t>(w.piece, (int64_t)align_up(cdiv(n * hidden * 8, kPartialBytes), 32));
   const bool ranked = n <= kRankIds;
   if (!ranked) {
@@ -447,30 +472,30 @@ struct FillShares {
   }
 };
 
-template <int GDT, int ODT>
+template <int GDT, int ODT, bool ADD>
 hipError_t launch_sums(const RowSums& p, hipStream_t stream) {
   const int64_t pieces = cdiv(p.n, p.piece);
   // 16-byte loads of the gradient rows
-  if (GDT != DT_F32 && p.hidden % 8 == 0) {
-    hipLaunchKernelGGL((rowgrad_sum_kernel<GDT, ODT, GDT == DT_F32 ? 4 : 8>),
-                       dim3((unsigned)pieces, (unsigned)cdiv(p.hidden, 4 * 64 * 8)), dim3(256), 0, stream, p);
-  } else {
-    hipLaunchKernelGGL((rowgrad_sum_kernel<GDT, ODT, 4>), dim3((unsigned)pieces, (unsigned)cdiv(p.hidden, 4 * 64 * 4)),
-                       dim3(256), 0, stream, p);
-  }
+  constexpr int E = GDT == DT_F32 ? 4 : 8;
+  if (p.hidden % E == 0)
+    hipLaunchKernelGGL((rowgrad_sum_kernel<GDT, ODT, E, ADD>),
+                       dim3((unsigned)pieces, (unsigned)cdiv(p.hidden, 4 * 64 * E)), dim3(256), 0, stream, p);
+  else  // 16-bit gradients of a f32 table
+    hipLaunchKernelGGL((rowgrad_sum_kernel<GDT, ODT, 4, ADD>),
+                       dim3((unsigned)pieces, (unsigned)cdiv(p.hidden, 4 * 64 * 4)), dim3(256), 0, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pieces == 1) return e;
-  hipLaunchKernelGGL(rowgrad_join_kernel<ODT>, dim3((unsigned)(pieces - 1), (unsigned)cdiv(p.hidden, 256)), dim3(256),
-                     0, stream, p);
+  hipLaunchKernelGGL((rowgrad_join_kernel<ODT, ADD>), dim3((unsigned)(pieces - 1), (unsigned)cdiv(p.hidden, 1024)),
+                     dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 
 template <int GDT>
-hipError_t launch_sums_to(const RowSums& p, int32_t out_dtype, hipStream_t stream) {
+hipError_t launch_sums_to(const RowSums& p, int32_t out_dtype, bool add, hipStream_t stream) {
   switch (out_dtype) {
-    case DT_F32: return launch_sums<GDT, DT_F32>(p, stream);
-    case DT_BF16: return launch_sums<GDT, DT_BF16>(p, stream);
-    default: return launch_sums<GDT, DT_F16>(p, stream);
+    case DT_F32: return add ? launch_sums<GDT, DT_F32, true>(p, stream) : launch_sums<GDT, DT_F32, false>(p, stream);
+    case DT_BF16: return add ? launch_sums<GDT, DT_BF16, true>(p, stream) : launch_sums<GDT, DT_BF16, false>(p, stream);
+    default: return add ? launch_sums<GDT, DT_F16, true>(p, stream) : launch_sums<GDT, DT_F16, false>(p, stream);
   }
 }
 
@@ -527,11 +552,11 @@ hipError_t launch_rowgrad(const RowGrad& g, void* ws, hipStream_t stream) {
   RowSums p = {};
   p.keys = keys, p.order = order, p.n = g.n, p.V = (uint32_t)g.V;
   p.grad = (const uint8_t*)g.grad, p.pitch = g.pitch, p.hidden = (int)g.hidden, p.piece = (int)w.piece;
-  p.scale = g.scale, p.out = g.out, p.add = g.add, p.part = (float*)(base + w.part);
+  p.scale = g.scale, p.out = g.out, p.part = (float*)(base + w.part);
   switch (g.grad_dtype) {
-    case DT_F32: return launch_sums_to<DT_F32>(p, g.out_dtype, stream);
-    case DT_BF16: return launch_sums_to<DT_BF16>(p, g.out_dtype, stream);
-    default: return launch_sums_to<DT_F16>(p, g.out_dtype, stream);
+    case DT_F32: return launch_sums_to<DT_F32>(p, g.out_dtype, g.add, stream);
+    case DT_BF16: return launch_sums_to<DT_BF16>(p, g.out_dtype, g.add, stream);
+    default: return launch_sums_to<DT_F16>(p, g.out_dtype, g.add, stream);
   }
 }
 
