@@ -271,12 +271,18 @@ __device__ __forceinline__ void store_rows(unsigned char* at, int64_t pitch, con
   }
 }
 
-// What D's entries of one residual row need.
+// What D's entries (and the loss: the label alone) of one residual row need.
 struct DRow {
   float g, h, both, lse;
   int64_t label;  // the label's row in the piece; negative where there is none
-  __device__ __forceinline__ DRow(const XentProduct& p, int64_t n) {
+  DRow() = default;
+  template <int MODE>
+  __device__ __forceinline__ void load(const XentProduct& p, int64_t n) {
     const uint32_t token = (uint32_t)p.labels[n];
+    if constexpr (MODE == X_STATS) {
+      label = (int64_t)token - p.v0;
+      return;
+    }
     g = token < (uint64_t)p.vocab ? (p.grad_loss != nullptr ? p.grad_loss[n] : p.grad_loss_all) : 0.f;
     h = p.grad_lse != nullptr ? p.grad_lse[n] : 0.f;
     both = g + h;
@@ -305,9 +311,11 @@ __device__ __forceinline__ float2 stats_join(float2 a, float2 b) {
 // m0 + mrow + off(a) + 4 (lane / 16) + i and column n0 + ncol + off(t) + lane % 16 of the product,
 // where the first AH (TH) tiles along a direction are neighbours and the others lie 128 further.
 // smem: the LDS of the finished K loop, all of it free.
+// row: of the columns, loaded (X_STATS, X_DLOGIT, X_DLOGIT32)
 template <int DT, int MODE, int MT, int NT, int AH, int TH, int WM, int BN>
 __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT], int64_t m0, int64_t n0, int mrow,
-                                       int ncol, int mtile, int split, int wm, int lane, unsigned char* smem) {
+                                       int ncol, int mtile, int split, int wm, int lane, const DRow (&drow)[NT],
+                                       unsigned char* smem) {
   const int g = lane >> 4;
   // rows in 32 bits, from this lane's first one
   auto off = [](int a) { return a / AH * 128 + a % AH * 16; };
@@ -322,7 +330,7 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
 #pragma unroll
     for (int t = 0; t < NT; t++) {
       const int64_t n = col_of(t);
-      const int label = n < p.n ? place((int64_t)(uint32_t)p.labels[n] - p.v0) : -1024;
+      const int label = n < p.n ? place(drow[t].label) : -1024;
       float m = -__builtin_inff(), s = 0.f;
 #pragma unroll
       for (int a = 0; a < MT; a++)
@@ -364,7 +372,7 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
     for (int t = 0; t < NT; t++) {
       const int64_t n = col_of(t);
       if (MODE == X_DLOGIT32 && n >= p.n) continue;
-      const DRow row(p, min(n, p.n - 1));
+      const DRow& row = drow[t];
       const int label = n < p.n ? place(row.label) : -1024;
 #pragma unroll
       for (int a0 = 0; a0 < MT; a0 += AH) {
@@ -483,6 +491,17 @@ __global__ void __launch_bounds__(64 * kXWaves) ring_kernel(XentProduct p) {
 #pragma unroll
     for (int t = 0; t < NT; t++) acc[a][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < RING - 1; s++) copy(s);
+  // the end's few values now, beside the first copies
+  DRow drow[NT];
+  if constexpr (MODE == X_STATS || MODE == X_DLOGIT || MODE == X_DLOGIT32) {
+#pragma unroll
+    for (int t = 0; t < NT; t++) drow[t].template load<MODE>(p, min(n0 + wn * (BN / WN) + 16 * t + (lane & 15), p.n - 1));
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+      asm volatile("" : "+v"(drow[t].label));
+      if constexpr (MODE != X_STATS) asm volatile("" : "+v"(drow[t].g), "+v"(drow[t].h), "+v"(drow[t].lse));
+    }
+  }
   for (int s = 0; s < stages; s++) {
     // stage s has landed, and every wave has read the image that the next copies refill
     load_wait<(RING - 2) * (A::COPIES + B::COPIES)>();
@@ -505,7 +524,7 @@ __global__ void __launch_bounds__(64 * kXWaves) ring_kernel(XentProduct p) {
   load_wait<0>();
   bare_barrier();
   finish<DT, MODE, MT, NT, MT, NT, WM, BN>(p, acc, m0, n0, wm * (BM / WM), wn * (BN / WN), at.mtile, at.split, wm, lane,
-                                           smem);
+                                           drow, smem);
 }
 
 // Tiles of 256 x 256, bound by the matrix cores.  Two LDS images of a stage; 2 x 4 waves, two
@@ -610,7 +629,13 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
   if (wm == 0) bare_barrier();
   load_wait<0>();
   bare_barrier();
-  finish<DT, MODE, 8, 4, 4, 2, 2, 256>(p, acc, m0, n0, 64 * wm, 32 * wn, at.mtile, at.split, wm, lane, smem);
+  DRow drow[4];
+  if constexpr (MODE == X_STATS || MODE == X_DLOGIT) {
+#pragma unroll
+    for (int t = 0; t < 4; t++)
+      drow[t].template load<MODE>(p, min(n0 + 32 * wn + t / 2 * 128 + t % 2 * 16 + (lane & 15), p.n - 1));
+  }
+  finish<DT, MODE, 8, 4, 4, 2, 2, 256>(p, acc, m0, n0, 64 * wm, 32 * wn, at.mtile, at.split, wm, lane, drow, smem);
 }
 
 // dE = D^T x for up to 128 residual rows (f32: 64), bound by its stores: a workgroup keeps 256
@@ -618,11 +643,14 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
 // table rows, 128 at a time (64 for each half of the waves), D's tiles two or three steps ahead
 // in a ring of LDS images.  A tile that holds a label has the rest of its entry of D added,
 // as a second operand built in registers.
+template <int DT, int KT>
+constexpr int kOuterRing = DT == DT_F32 ? 4 : KT == 1 ? 7 : 5;  // as deep as the count of a wait and LDS allow
+
 template <int DT, int KT>  // KT: stages of K
 __global__ void __launch_bounds__(64 * kXWaves, 2) outer_kernel(XentProduct p) {
   using A = Operand<DT, true, 256>;
   using B = Operand<DT, true, 128>;
-  constexpr int RING = KT == 1 ? 4 : 3, IMG = KT * B::BYTES, COPIES = KT * B::COPIES;
+  constexpr int RING = kOuterRing<DT, KT>, IMG = KT * B::BYTES, COPIES = KT * B::COPIES;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // first A's images, then [RING][IMG]
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv & 3, wn = wv >> 2;
@@ -649,12 +677,16 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) outer_kernel(XentProduct p) {
     load_wait<0>();
     bare_barrier();  // the images are free
   }
-  // this lane's labels, as rows of the piece
-  int64_t label[KT];
+  // this lane's residual rows' labels (no token: none) and what D lacks there
+  uint32_t token[KT];
+  float rest[KT];
 #pragma unroll
   for (int s = 0; s < KT; s++) {
     const int b = 64 * s + lane;
-    label[s] = DT != DT_F32 && b < p.k ? (int64_t)(uint32_t)p.labels[b] - p.v0 : -1;
+    const bool some = DT != DT_F32 && b < p.k;
+    token[s] = some ? (uint32_t)p.labels[b] : 0xffffffffu;
+    rest[s] = some && token[s] < (uint64_t)p.vocab ? p.rest[b] : 0.f;
+    asm volatile("" : "+v"(token[s]), "+v"(rest[s]));  // here, not where a copy would be waited for
   }
   const int steps = (int)((n1 - n0 + 127) / 128);
   auto copy = [&](int i) {  // D's tile of step i (past the last: zeros that nothing reads)
@@ -697,31 +729,35 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) outer_kernel(XentProduct p) {
             for (int t = 0; t < 2; t++) acc[a][t] = mma<DT>(fa[s][a][kk], fb[t], acc[a][t]);
         }
       if constexpr (DT != DT_F32) {
+        const uint32_t token0 = (uint32_t)(p.v0 + first);
         bool hit = false;
 #pragma unroll
-        for (int s = 0; s < KT; s++) hit |= label[s] >= first && label[s] < first + 128;
+        for (int s = 0; s < KT; s++) hit |= token[s] - token0 < 128u;
         if (__ballot(hit) != 0) {  // few tiles
 #pragma unroll
           for (int s = 0; s < KT; s++)
 #pragma unroll
-            for (int kk = 0; kk < 2; kk++)
+            for (int kk = 0; kk < 2; kk++) {
+              uint32_t w[2][4] = {};
 #pragma unroll
-              for (int t = 0; t < 2; t++) {
-                const int64_t v = first + 64 * wn + 32 * h + 16 * t + (lane & 15);
-                uint32_t w[4] = {0, 0, 0, 0};
+              for (int j = 0; j < 8; j++) {
+                const int from = 32 * kk + 8 * (lane >> 4) + j;
+                const uint32_t column = __shfl(token[s], from, 64) - token0 - (64 * wn + 32 * h);
+                const uint32_t value = __builtin_bit_cast(uint16_t, round1<DT>(__shfl(rest[s], from, 64)));
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                  const int b = 64 * s + 32 * kk + 8 * (lane >> 4) + j;
-                  if (b < p.k && (int64_t)(uint32_t)p.labels[b] - p.v0 == v)
-                    w[j / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, round1<DT>(p.rest[b])) << 16 * (j % 2);
-                }
-                const u32x4 f = {w[0], w[1], w[2], w[3]};
-#pragma unroll
-                for (int a = 0; a < 4; a++) acc[a][t] = mma<DT>(fa[s][a][kk], f, acc[a][t]);
+                for (int t = 0; t < 2; t++)
+                  if (column == 16u * t + (lane & 15)) w[t][j / 2] |= value << 16 * (j % 2);
               }
+#pragma unroll
+              for (int t = 0; t < 2; t++)
+#pragma unroll
+                for (int a = 0; a < 4; a++)
+                  acc[a][t] = mma<DT>(fa[s][a][kk], u32x4{w[t][0], w[t][1], w[t][2], w[t][3]}, acc[a][t]);
+            }
         }
       }
-      finish<DT, X_OUT, 4, 2, 4, 2, 1, 128>(p, acc, m0, first, 64 * wm, 64 * wn + 32 * h, 0, 0, 0, lane, smem);
+      const DRow none[2] = {};
+      finish<DT, X_OUT, 4, 2, 4, 2, 1, 128>(p, acc, m0, first, 64 * wm, 64 * wn + 32 * h, 0, 0, 0, lane, none, smem);
     }
   }
   load_wait<0>();  // nothing of this workgroup is in flight when its LDS is given away
@@ -777,7 +813,8 @@ __global__ void __launch_bounds__(256) direct_kernel(XentProduct p) {
     if (r == 0) ((float2*)p.out)[n * p.mt + blockIdx.x % p.mt] = make_float2(m, s);
   } else {
     if (n >= p.n || v >= p.m) return;
-    const DRow row(p, n);
+    DRow row;
+    row.load<MODE>(p, n);
     ((float*)p.out)[v * 8 + n] = v == row.label ? row.at_label(l) : row.other(l);
   }
 }
@@ -793,7 +830,6 @@ struct XentRows {
   uint8_t* rows;                       // dE of the first table row, or NULL
   int32_t add;
   float* part;                         // [slices][n][hidden], or NULL
-  bool part_add;                       // to what is there (a later piece)
 };
 
 // The 16 bytes' values.
@@ -809,7 +845,7 @@ __device__ __forceinline__ void unpack(u32x4 w, float (&x)[16 / kValue<DT>]) {
 
 template <int DT, int NB>
 __global__ void __launch_bounds__(256) xent_rows_kernel(XentRows p) {
-  constexpr int E = 16 / kValue<DT>, U = 4;
+  constexpr int E = 16 / kValue<DT>, U = 8;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w = (int)blockIdx.x * 4 + wv, chunk = w % p.chunks, slice = w / p.chunks;
   if (slice >= p.slices) return;  // whole wave
@@ -824,46 +860,52 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(XentRows p) {
 #pragma unroll
     for (int i = 0; i < E; i++) acc[b][i] = 0.f;
   }
-  if (p.part_add && live) {
-#pragma unroll
-    for (int b = 0; b < NB; b++) {
-      if (b >= p.n) break;
-      const f32x4* was = (const f32x4*)(p.part + ((int64_t)slice * p.n + b) * p.hidden + c);
-#pragma unroll
-      for (int i = 0; i < E; i++) acc[b][i] = was[i / 4][i % 4];
-    }
-  }
-  for (int64_t v = begin; v < end; v += U) {
+  // U table rows, their values of D (lane 8 u + b: residual row b; zeros where there is none) and
+  // what their gradients are added to, one batch ahead; past the last row: the last again
+  struct Batch {
     u32x4 row[U], old[U];
+    float d;
+  };
+  const bool read = p.part != nullptr, add = p.rows != nullptr && p.add;
+  auto load = [&](int64_t v, Batch& t) {
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const int64_t r = min(v + u, end - 1) * p.row_bytes + at;
-      row[u] = *(const u32x4*)(p.table + r);
-      if (p.rows != nullptr && p.add) old[u] = *(const u32x4*)(p.rows + r);
+      if (read) t.row[u] = *(const u32x4*)(p.table + r);
+      if (add) t.old[u] = *(const u32x4*)(p.rows + r);
     }
+    t.d = (lane & 7) < p.n ? p.d[min(v + (lane >> 3), end - 1) * 8 + (lane & 7)] : 0.f;
+  };
+  Batch ahead = {};
+  load(begin, ahead);
+  for (int64_t v = begin; v < end; v += U) {
+    Batch t = ahead;
+#pragma unroll
+    for (int u = 0; u < U; u++) asm volatile("" : "+v"(t.row[u]), "+v"(t.old[u]));  // all of them here
+    if (v + U < end) load(v + U, ahead);
 #pragma unroll
     for (int u = 0; u < U; u++) {
       if (v + u >= end) break;
       float d[NB];
 #pragma unroll
-      for (int b = 0; b < NB; b++) d[b] = b < p.n ? p.d[(v + u) * 8 + b] : 0.f;
-      if (p.part != nullptr) {
+      for (int b = 0; b < NB; b++) d[b] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(t.d), 8 * u + b));
+      if (read) {
         float e[E];
-        unpack<DT>(row[u], e);
+        unpack<DT>(t.row[u], e);
 #pragma unroll
         for (int b = 0; b < NB; b++)
 #pragma unroll
           for (int i = 0; i < E; i++) acc[b][i] = fmaf(d[b], e[i], acc[b][i]);
       }
       if (p.rows != nullptr) {
-        float o[E], was[E];
-        if (p.add) unpack<DT>(old[u], was);
+        float o[E];
+        if (add) unpack<DT>(t.old[u], o);
 #pragma unroll
         for (int i = 0; i < E; i++) {
-          o[i] = 0.f;
+          float sum = d[0] * x[0][i];
 #pragma unroll
-          for (int b = 0; b < NB; b++) o[i] = fmaf(d[b], x[b][i], o[i]);
-          if (p.add) o[i] += was[i];
+          for (int b = 1; b < NB; b++) sum = fmaf(d[b], x[b][i], sum);
+          o[i] = add ? o[i] + sum : sum;
         }
         u32x4 out;
 #pragma unroll
@@ -995,8 +1037,25 @@ namespace {
 
 constexpr int kXcdCount = 8;
 
-// Tile columns for n residual rows.
-int rows_tile(int64_t n) { return n <= 64 ? 64 : n <= 128 ? 128 : 256; }
+// Columns of a product's tiles for n residual rows, and what the product then takes: rounds of
+// one workgroup per CU, times its columns and stages.  16-bit products of 256 columns keep
+// the matrix cores busier than those of 128 (1,024 x 262,144 x 5,120: RATE16); in f32, where
+// they are slow enough for either, the choice is about rounds alone.
+struct Tiling {
+  int columns;
+  int64_t cost;
+};
+Tiling tiling(int64_t m, int64_t n, int64_t k, int64_t splits, int size) {
+  Tiling best = {0, INT64_MAX};
+  for (int c = n <= 64 || size == 4 ? 64 : 128; c <= 256; c *= 2) {
+    const int64_t percent = size == 4 ? 100 : c == 256 ? 100 : 140;  // time of a column
+    const int64_t stages = cdiv(cdiv(k, splits), 128 / size) + 24;    // and what a start and an end cost
+    const int64_t cost = cdiv(cdiv(m, 256) * cdiv(n, c) * splits, kTargetBlocks) * c * percent * stages;
+    if (cost < best.cost) best = {c, cost};
+    if (c >= n) break;
+  }
+  return best;
+}
 
 template <int DT, bool TA, bool TB, int MODE, int BM, int BN, int WM, int RING>
 hipError_t launch_ring(const XentProduct& p, hipStream_t stream) {
@@ -1027,7 +1086,7 @@ template <int DT>
 hipError_t launch_outer(XentProduct p, hipStream_t stream) {
   const bool two = p.k > 128 / kValue<DT>;
   const void* fn = two ? (const void*)outer_kernel<DT, 2> : (const void*)outer_kernel<DT, 1>;
-  const size_t lds = two ? 3 * 32768 : 4 * 16384;
+  const size_t lds = two ? kOuterRing<DT, 2> * 32768 : kOuterRing<DT, 1> * 16384;
   hipError_t e = set_dynamic_lds(fn, lds);
   if (e != hipSuccess) return e;
   // one workgroup per CU
@@ -1044,7 +1103,7 @@ hipError_t launch_outer(XentProduct p, hipStream_t stream) {
 // A product whose columns are p.n residual rows.
 template <int DT, bool TA, int MODE>
 hipError_t launch_by_rows(XentProduct p, hipStream_t stream) {
-  const int bn = rows_tile(p.n);
+  const int bn = tiling(p.m, p.n, p.k, p.splits, kValue<DT>).columns;
   p.mt = (int32_t)cdiv(p.m, 256), p.nt = (int32_t)cdiv(p.n, bn);
   if (bn == 64) return launch_ring<DT, TA, false, MODE, 256, 64, 4, 4>(p, stream);
   if constexpr (MODE != X_DLOGIT32) {
@@ -1075,7 +1134,7 @@ int64_t even_piece(int64_t vocab, int64_t most) {
 }
 // Forward: the piece's statistics stay within kPartBytes.
 int64_t forward_piece(int64_t vocab, int64_t n) {
-  return even_piece(vocab, std::min(kMaxTiles / cdiv(n, rows_tile(n)), kPartBytes / (n * 8)));
+  return even_piece(vocab, std::min(kMaxTiles / cdiv(n, 64), kPartBytes / (n * 8)));
 }
 
 struct ForwardWs {
@@ -1096,8 +1155,11 @@ ForwardWs forward_ws(const TableDesc& t, int64_t n) {
   return w;
 }
 
-// Backward: up to this many residual rows D is f32, and vector FMAs read it.
-constexpr int64_t kVectorRows = 8;
+// Few residual rows and a table that the caches hold: D in f32 and one kernel of vector FMAs
+// for both gradients, fewer launches (VECTOR).  A larger table takes longer that way: its
+// reads and writes alternate (1 x 262,144 x 5,376: 1,668 us, by products 1,554).
+constexpr int64_t kVectorBytes = (int64_t)64 << 20;
+bool vector_rows(const TableDesc& t, int64_t n) { return n <= 8 && t.V * t.row_bytes <= kVectorBytes; }
 
 struct BackwardWs {
   int64_t piece, splits, slice;
@@ -1105,15 +1167,13 @@ struct BackwardWs {
   size_t rest, x, d, sums, bytes;
   size_t pitch;  // bytes of a row of D
 };
-// K slices of dx = D E: the fewest rounds of one workgroup per CU, times the stages of one and
-// what its start and end cost (about 24 stages); at least 512 table rows each.
-int64_t backward_splits(int64_t piece, int64_t n, int64_t hidden) {
-  const int64_t tiles = cdiv(hidden, 256) * cdiv(n, rows_tile(n));
+// K slices of dx = D E, at least 512 table rows each.
+int64_t backward_splits(int64_t piece, int64_t n, int64_t hidden, int size) {
   int64_t best = 1, least = INT64_MAX;
-  for (int64_t s = 1; s <= std::max<int64_t>(1, piece / 512) && s <= 2 * kTargetBlocks; s++) {
-    const int64_t cost = cdiv(tiles * s, kTargetBlocks) * (cdiv(piece, 64 * s) + 24);
+  for (int64_t s = 1; s <= std::max<int64_t>(1, piece / 512) && s <= kTargetBlocks; s++) {
+    const int64_t cost = tiling(hidden, n, piece, s, size).cost;
     if (cost < least) least = cost, best = s;
-    if (tiles * s >= 8 * kTargetBlocks) break;
+    if (cdiv(hidden, 256) * cdiv(n, 256) * s >= 8 * kTargetBlocks) break;
   }
   return best;
 }
@@ -1121,18 +1181,18 @@ BackwardWs backward_ws(const TableDesc& t, int64_t n) {
   const int size = t.dtype == DT_F32 ? 4 : 2;
   BackwardWs w = {};
   size_t d_bytes;
-  if (n <= kVectorRows) {
-    // about eight waves per CU, each with 32 table rows at least
+  if (vector_rows(t, n)) {
+    // about eight waves per CU, each with 16 table rows at least
     w.chunks = (int)cdiv(t.row_bytes, 1024);
-    w.piece = even_piece(t.V, kPartBytes / (256 * 32));
-    w.slice = std::max<int64_t>(32, cdiv(w.piece, std::max<int64_t>(1, 8 * kTargetBlocks / w.chunks)));
-    w.splits = cdiv(std::min(w.piece, t.V), w.slice);  // of the first piece, the fullest
+    w.piece = t.V;
+    w.slice = std::max<int64_t>(16, cdiv(w.piece, std::max<int64_t>(1, 8 * kTargetBlocks / w.chunks)));
+    w.splits = cdiv(w.piece, w.slice);
     d_bytes = (size_t)w.piece * 32;
   } else {
     // D of a piece stays within kPartBytes and its rows within 4 MiB
-    w.piece = even_piece(t.V, std::min(std::min(kMaxTiles / cdiv(n, rows_tile(n)), (int64_t)4096),
+    w.piece = even_piece(t.V, std::min(std::min(kMaxTiles / cdiv(n, 64), (int64_t)4096),
                                        kPartBytes / (n * size * 256)));
-    w.slice = (int64_t)align_up(cdiv(w.piece, backward_splits(w.piece, n, t.hidden)), 64);
+    w.slice = (int64_t)align_up(cdiv(w.piece, backward_splits(w.piece, n, t.hidden, size)), 64);
     w.splits = cdiv(std::min(w.piece, t.V), w.slice);  // of the first piece, the fullest
     w.pitch = (size_t)(w.piece * size);
     d_bytes = (size_t)n * w.pitch;
@@ -1217,23 +1277,19 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
   logits.out = d, logits.out_pitch = (int64_t)w.pitch;
   logits.labels = c.labels, logits.vocab = t.V, logits.lse = c.lse, logits.grad_loss = c.grad_loss;
   logits.grad_loss_all = c.grad_loss_all, logits.grad_lse = c.grad_lse;
-  if (c.n <= kVectorRows) {
+  if (vector_rows(t, c.n)) {
     XentRows p = {};
+    logits.a = p.table = t.rows, logits.m = p.m = t.V;
     p.x = logits.b, p.row_bytes = t.row_bytes, p.x_pitch = logits.b_pitch, p.per = w.slice;
-    p.hidden = (int)t.hidden, p.n = (int)c.n, p.chunks = w.chunks;
-    p.d = (const float*)d, p.add = c.add, p.part = c.d_x != nullptr ? sums : nullptr;
-    for (int64_t v0 = 0; v0 < t.V; v0 += w.piece) {
-      logits.a = p.table = t.rows + v0 * t.row_bytes, logits.m = p.m = std::min(w.piece, t.V - v0), logits.v0 = v0;
-      p.rows = c.d_rows != nullptr ? (uint8_t*)c.d_rows + v0 * t.row_bytes : nullptr;
-      p.slices = (int)cdiv(p.m, w.slice), p.part_add = p.part != nullptr && v0 != 0;
-      e = direct_tiles(t.V, c.n) ? launch_direct<DT, X_DLOGIT32>(logits, stream)
-                                 : launch_by_rows<DT, false, X_DLOGIT32>(logits, stream);
-      if (e != hipSuccess) return e;
-      e = c.n <= 2   ? launch_rows<DT, 2>(p, stream)
-          : c.n <= 4 ? launch_rows<DT, 4>(p, stream)
-                     : launch_rows<DT, 8>(p, stream);
-      if (e != hipSuccess) return e;
-    }
+    p.hidden = (int)t.hidden, p.n = (int)c.n, p.chunks = w.chunks, p.slices = (int)w.splits;
+    p.d = (const float*)d, p.rows = (uint8_t*)c.d_rows, p.add = c.add, p.part = c.d_x != nullptr ? sums : nullptr;
+    e = direct_tiles(t.V, c.n) ? launch_direct<DT, X_DLOGIT32>(logits, stream)
+                               : launch_by_rows<DT, false, X_DLOGIT32>(logits, stream);
+    if (e != hipSuccess) return e;
+    e = c.n <= 2   ? launch_rows<DT, 2>(p, stream)
+        : c.n <= 4 ? launch_rows<DT, 4>(p, stream)
+                   : launch_rows<DT, 8>(p, stream);
+    if (e != hipSuccess) return e;
     if (c.d_x == nullptr) return hipSuccess;
     return sum_slices<DT>(t, c, w, sums, nullptr, nullptr, stream);
   }
@@ -1262,7 +1318,7 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
       p.m = t.hidden, p.n = rows, p.k = c.n;
       p.a = logits.b, p.a_pitch = logits.b_pitch, p.b = d, p.b_pitch = (int64_t)w.pitch;
       p.splits = 1, p.kslice = (int32_t)align_up((size_t)c.n, 64);
-      p.out = (uint8_t*)c.d_rows + v0 * t.row_bytes, p.add = c.add, p.scale = scale, p.labels = c.labels, p.v0 = v0, p.rest = rest;
+      p.out = (uint8_t*)c.d_rows + v0 * t.row_bytes, p.add = c.add, p.scale = scale, p.labels = c.labels, p.v0 = v0, p.vocab = t.V, p.rest = rest;
       if (c.n <= 2 * (128 / kValue<DT>)) {
         e = launch_outer<DT>(p, stream);
       } else {
