@@ -86,13 +86,17 @@ __device__ __forceinline__ void bare_barrier() { asm volatile("s_barrier" ::: "m
 //             piece of lie on 16 different piece columns of the 256-byte bank row.
 //   TR true   blocks of 128 rows (16 KiB); K value k at 128 ES k, piece p at p ^ swizzle(k), so
 //             that the K values that one transposing read takes lie on different banks.
-template <int DT, bool TR, int R>
+//
+// BLK: D, which is kept in blocks of 256 table rows, each [residual row][256]: what a tile writes
+// and reads of it is one range of memory.  Rows as long as a piece took TLB.
+constexpr int kBlock = 256;
+template <int DT, bool TR, int R, bool BLK = false>
 struct Operand {
   static constexpr int ES = kValue<DT>, KS = 128 / ES, BYTES = R * 128, COPIES = BYTES / 1024 / kXWaves;
   static constexpr int LINE = 128 * ES;  // TR: bytes of one K value's 128 rows
   static_assert(COPIES >= 1 && (!TR || R % 128 == 0), "tile rows");
   uint64_t base;            // first byte of the tile: row row0 (TR: K value k0, row row0)
-  int64_t pitch;
+  int64_t pitch, block;     // block: bytes of one (BLK)
   uint32_t off[COPIES];     // this lane's piece of each of the wave's copies, or kOutside
   int k_of[COPIES];         // TR: its K value within the stage; else its first byte within the stage
   int k_end;                // K values (TR) or bytes of K values in the slice
@@ -100,16 +104,18 @@ struct Operand {
   static __device__ __forceinline__ int swizzle(int k) {
     return ES == 2 ? 2 * (((k >> 3) & 1) * 4 + (k & 3)) : 4 * ((k >> 2) & 3);
   }
-  // rows [row0, rows) of the operand, K values [k0, k0 + kn)
+  // rows [row0, rows) of the operand, K values [k0, k0 + kn).  BLK: pitch_ are a block's bytes;
+  // k0 begins a block, and a tile's rows lie in one (TR).
   __device__ __forceinline__ Operand(const uint8_t* p, int64_t pitch_, int64_t row0, int64_t rows, int64_t k0, int kn,
                                      int wv, int lane) {
-    pitch = pitch_;
+    pitch = BLK ? kBlock * ES : pitch_;
+    block = BLK ? pitch_ : 0;
     const int left = (int)min(rows - row0, (int64_t)R);
     if constexpr (TR) {
-      base = (uint64_t)p + (uint64_t)(k0 * pitch + row0 * ES);
+      base = (uint64_t)p + (uint64_t)(BLK ? row0 / kBlock * block + k0 * pitch + row0 % kBlock * ES : k0 * pitch + row0 * ES);
       k_end = kn;
     } else {
-      base = (uint64_t)p + (uint64_t)(row0 * pitch + k0 * ES);
+      base = (uint64_t)p + (uint64_t)(BLK ? k0 / kBlock * block + row0 * pitch : row0 * pitch + k0 * ES);
       k_end = kn * ES;
     }
 #pragma unroll
@@ -133,8 +139,12 @@ struct Operand {
   __device__ __forceinline__ void copy(int s, int j, int wv, uint32_t lds) const {
     const int step = TR ? s * KS : s * 128;
     // a lane outside stays outside: 2^31 plus at most 2^30 bytes of K values
-    const uint32_t at = k_of[j] + step < k_end ? off[j] + (TR ? 0u : (uint32_t)step) : kOutside;
-    copy_1k(TR ? base + (uint64_t)step * (uint64_t)pitch : base, at, lds + (uint32_t)place(wv, j) * 1024);
+    const uint32_t far = TR ? 0u : BLK ? (uint32_t)(step % (kBlock * ES)) : (uint32_t)step;
+    const uint32_t at = k_of[j] + step < k_end ? off[j] + far : kOutside;
+    uint64_t from = base;
+    if constexpr (TR) from += (uint64_t)step * (uint64_t)pitch;
+    else if constexpr (BLK) from += (uint64_t)(step / (kBlock * ES)) * (uint64_t)block;
+    copy_1k(from, at, lds + (uint32_t)place(wv, j) * 1024);
   }
   // which KiB of the image a copy fills: with 256 rows, the wave's first half of copies lies in
   // rows 0 .. 127 and the second in the others
@@ -173,15 +183,14 @@ struct Operand {
 enum { X_STATS, X_DLOGIT, X_DLOGIT32, X_PART, X_OUT };
 struct XentProduct {
   const uint8_t *a, *b;
-  int64_t a_pitch, b_pitch;  // bytes
+  int64_t a_pitch, b_pitch;  // bytes (X_PART, X_OUT: b is D, b_pitch a block's bytes)
   int64_t m, n, k;
   int32_t mt, nt;            // tiles
   int32_t splits;            // K slices of kslice values (a multiple of a stage)
   int32_t kslice;
-  // X_STATS: part [n][mt], target [n]; X_DLOGIT: D [n][out_pitch bytes]; X_DLOGIT32: f32 D [m][8]
+  // X_STATS: part [n][mt], target [n]; X_DLOGIT: D [m / 256][n][256]; X_DLOGIT32: f32 D [m][8]
   // X_PART: f32 [splits][n][m]; X_OUT: values of the type, [n][m]
   void* out;
-  int64_t out_pitch;
   float* rest;               // 16-bit types: [n], what D's rounding takes away from a label's entry
   int32_t add;               // X_PART, X_OUT: to what is there
   const int32_t* labels;     // [n]
@@ -407,8 +416,9 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
             for (int i = 0; i < 4; i++)
               if (off(a0 + a) + i < rows) ((float*)p.out)[(m0 + first + off(a0 + a) + i) * 8 + n] = d[a][i];
         } else {
-          const int64_t at = col0(t) * p.out_pitch + (m0 + mrow + off(a0)) * kValue<DT>;
-          store_rows<DT, AH>((unsigned char*)p.out + at, p.out_pitch, d, lane, p.n - col0(t), 16 * AH);
+          constexpr int64_t pitch = kBlock * kValue<DT>;
+          const int64_t at = (m0 / kBlock * p.n + col0(t)) * pitch + (mrow + off(a0)) * kValue<DT>;
+          store_rows<DT, AH>((unsigned char*)p.out + at, pitch, d, lane, p.n - col0(t), 16 * AH);
         }
       }
     }
@@ -465,7 +475,7 @@ struct XentPlace {
 template <int DT, bool TA, bool TB, int MODE, int BM, int BN, int WM, int RING>
 __global__ void __launch_bounds__(64 * kXWaves) ring_kernel(XentProduct p) {
   using A = Operand<DT, TA, BM>;
-  using B = Operand<DT, TB, BN>;
+  using B = Operand<DT, TB, BN, MODE == X_PART || MODE == X_OUT>;
   constexpr int WN = kXWaves / WM, MT = BM / WM / 16, NT = BN / WN / 16, IMG = A::BYTES + B::BYTES;
   static_assert(RING * IMG <= (int)kMaxLds, "LDS");
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -539,7 +549,7 @@ __global__ void __launch_bounds__(64 * kXWaves) ring_kernel(XentProduct p) {
 template <int DT, bool TA, bool TB, int MODE>
 __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
   using A = Operand<DT, TA, 256>;
-  using B = Operand<DT, TB, 256>;
+  using B = Operand<DT, TB, 256, MODE == X_PART || MODE == X_OUT>;
   constexpr int IMG = A::BYTES + B::BYTES;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [2][IMG]
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -649,7 +659,7 @@ constexpr int kOuterRing = DT == DT_F32 ? 4 : KT == 1 ? 7 : 5;  // as deep as th
 template <int DT, int KT>  // KT: stages of K
 __global__ void __launch_bounds__(64 * kXWaves, 2) outer_kernel(XentProduct p) {
   using A = Operand<DT, true, 256>;
-  using B = Operand<DT, true, 128>;
+  using B = Operand<DT, true, 128, true>;
   constexpr int RING = kOuterRing<DT, KT>, IMG = KT * B::BYTES, COPIES = KT * B::COPIES;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // first A's images, then [RING][IMG]
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1164,8 +1174,8 @@ bool vector_rows(const TableDesc& t, int64_t n) { return n <= 8 && t.V * t.row_b
 struct BackwardWs {
   int64_t piece, splits, slice;
   int chunks;
+  int64_t block;  // bytes of a block of D
   size_t rest, x, d, sums, bytes;
-  size_t pitch;  // bytes of a row of D
 };
 // K slices of dx = D E, at least 512 table rows each.
 int64_t backward_splits(int64_t piece, int64_t n, int64_t hidden, int size) {
@@ -1189,13 +1199,13 @@ BackwardWs backward_ws(const TableDesc& t, int64_t n) {
     w.splits = cdiv(w.piece, w.slice);
     d_bytes = (size_t)w.piece * 32;
   } else {
-    // D of a piece stays within kPartBytes and its rows within 4 MiB
-    w.piece = even_piece(t.V, std::min(std::min(kMaxTiles / cdiv(n, 64), (int64_t)4096),
+    // D of a piece stays within kPartBytes, and a piece's K values within 2^28
+    w.piece = even_piece(t.V, std::min(std::min(kMaxTiles / cdiv(n, 64), (int64_t)1 << 20),
                                        kPartBytes / (n * size * 256)));
-    w.slice = (int64_t)align_up(cdiv(w.piece, backward_splits(w.piece, n, t.hidden, size)), 64);
+    w.slice = (int64_t)align_up(cdiv(w.piece, backward_splits(w.piece, n, t.hidden, size)), kBlock);
     w.splits = cdiv(std::min(w.piece, t.V), w.slice);  // of the first piece, the fullest
-    w.pitch = (size_t)(w.piece * size);
-    d_bytes = (size_t)n * w.pitch;
+    w.block = n * kBlock * size;
+    d_bytes = (size_t)(n * w.piece * size);
   }
   w.rest = 256;  // after the two factors
   w.x = w.rest + align_up((size_t)n * 4, 256);
@@ -1274,7 +1284,7 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
   logits.n = c.n, logits.k = t.hidden, logits.a_pitch = t.row_bytes;
   logits.b = direct ? (const uint8_t*)c.x : packed, logits.b_pitch = direct ? c.x_pitch : t.row_bytes;
   logits.splits = 1, logits.kslice = (int32_t)t.hidden;
-  logits.out = d, logits.out_pitch = (int64_t)w.pitch;
+  logits.out = d;
   logits.labels = c.labels, logits.vocab = t.V, logits.lse = c.lse, logits.grad_loss = c.grad_loss;
   logits.grad_loss_all = c.grad_loss_all, logits.grad_lse = c.grad_lse;
   if (vector_rows(t, c.n)) {
@@ -1308,7 +1318,7 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
     if (c.d_x != nullptr) {
       XentProduct p = {};
       p.m = t.hidden, p.n = c.n, p.k = rows;
-      p.a = logits.a, p.a_pitch = t.row_bytes, p.b = d, p.b_pitch = (int64_t)w.pitch;
+      p.a = logits.a, p.a_pitch = t.row_bytes, p.b = d, p.b_pitch = w.block;
       p.splits = (int32_t)cdiv(rows, w.slice), p.kslice = (int32_t)w.slice;
       p.out = sums, p.add = v0 != 0;
       if ((e = launch_by_rows<DT, true, X_PART>(p, stream)) != hipSuccess) return e;
@@ -1316,7 +1326,7 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
     if (c.d_rows != nullptr) {
       XentProduct p = {};
       p.m = t.hidden, p.n = rows, p.k = c.n;
-      p.a = logits.b, p.a_pitch = logits.b_pitch, p.b = d, p.b_pitch = (int64_t)w.pitch;
+      p.a = logits.b, p.a_pitch = logits.b_pitch, p.b = d, p.b_pitch = w.block;
       p.splits = 1, p.kslice = (int32_t)align_up((size_t)c.n, 64);
       p.out = (uint8_t*)c.d_rows + v0 * t.row_bytes, p.add = c.add, p.scale = scale, p.labels = c.labels, p.v0 = v0, p.vocab = t.V, p.rest = rest;
       if (c.n <= 2 * (128 / kValue<DT>)) {
