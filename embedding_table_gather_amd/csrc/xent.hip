@@ -28,7 +28,7 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kXWaves = 8;
 constexpr int kGroup = 4;  // tiles along n that neighbouring workgroups share
-constexpr uint32_t kOutside = 0x80000000u;  // a copy's offset past its descriptor: zeros arrive
+constexpr uint32_t kOutside = 0x80000000u;  // an offset past every descriptor: zeros arrive
 
 template <int DT>
 constexpr int kValue = DT == DT_F32 ? 4 : 2;  // bytes
@@ -53,12 +53,18 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 acc) {
   }
 }
 
-// 1 KiB from memory to LDS: lane l's 16 bytes at base + offset to lds + 16 l (base and lds
-// uniform).  An offset at or past 2^31 - 1 is outside the descriptor: no memory is read and
-// zeros are written.  In assembly because the compiler would wait for every such copy before
-// any LDS read; load_wait waits for the one that is due.  No register is written.
-__device__ __forceinline__ void copy_1k(uint64_t base, uint32_t offset, uint32_t lds) {
-  const u32x4 rsrc = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, 0x7fffffffu, 0x00020000u};
+// A buffer descriptor of `valid` bytes (at most 2^31) at base, an address below 2^48.
+__device__ __forceinline__ u32x4 descriptor(uint64_t base, int64_t valid) {
+  return u32x4{(uint32_t)base, (uint32_t)(base >> 32), (uint32_t)min(max(valid, (int64_t)0), (int64_t)kOutside),
+               0x00020000u};
+}
+
+// 1 KiB from memory to LDS: lane l's 16 bytes at the descriptor's base + offset to lds + 16 l
+// (descriptor and lds uniform).  A lane whose offset is outside the descriptor reads no
+// memory: zeros are written for it.  In assembly because the compiler would wait for every
+// such copy before any LDS read; load_wait waits for the one that is due.  No register is
+// written.
+__device__ __forceinline__ void copy_1k(u32x4 rsrc, uint32_t offset, uint32_t lds) {
   uint32_t m0;  // the LDS base register, left as it was
   asm volatile(
       "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds\n\ts_mov_b32 m0, %0"
@@ -73,6 +79,8 @@ __device__ __forceinline__ void load_wait() {
   static_assert(N >= 0 && N < 64, "vmcnt field");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
 }
+// Waits for this wave's LDS accesses alone.
+__device__ __forceinline__ void load_wait_lds() { __builtin_amdgcn_s_waitcnt(0xc07f); }
 // A workgroup barrier that no memory access crosses (the compiler's own also waits for copies).
 __device__ __forceinline__ void bare_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
@@ -94,57 +102,79 @@ template <int DT, bool TR, int R, bool BLK = false>
 struct Operand {
   static constexpr int ES = kValue<DT>, KS = 128 / ES, BYTES = R * 128, COPIES = BYTES / 1024 / kXWaves;
   static constexpr int LINE = 128 * ES;  // TR: bytes of one K value's 128 rows
-  static_assert(COPIES >= 1 && (!TR || R % 128 == 0), "tile rows");
-  uint64_t base;            // first byte of the tile: row row0 (TR: K value k0, row row0)
-  int64_t pitch, block;     // block: bytes of one (BLK)
-  uint32_t off[COPIES];     // this lane's piece of each of the wave's copies, or kOutside
-  int k_of[COPIES];         // TR: its K value within the stage; else its first byte within the stage
-  int k_end;                // K values (TR) or bytes of K values in the slice
+  static_assert(COPIES >= 1 && (!TR || (R % 128 == 0 && COPIES >= 2)), "tile rows");
+  // of the stage that is copied from
+  u32x4 rsrc;            // from the tile's first row (TR: and the stage's first K value) to the end of what may be read
+  uint64_t base;         // its address
+  int64_t valid;         // TR: its bytes
+  int32_t k_left, far;   // TR false: bytes of K values left in a row; those before the stage (BLK: in the block)
+  // always
+  int64_t pitch, block;  // block: bytes of one (BLK)
+  uint32_t off[TR ? 1 : 2];  // this lane's piece of the wave's first copy (TR false: and of one an odd number of copies on)
+  uint32_t k_first;          // TR false: the former's first byte within the stage
 
   static __device__ __forceinline__ int swizzle(int k) {
     return ES == 2 ? 2 * (((k >> 3) & 1) * 4 + (k & 3)) : 4 * ((k >> 2) & 3);
   }
-  // rows [row0, rows) of the operand, K values [k0, k0 + kn).  BLK: pitch_ are a block's bytes;
-  // k0 begins a block, and a tile's rows lie in one (TR).
+  // Rows [row0, rows) of the operand, K values [k0, k0 + kn).  BLK: pitch_ are a block's bytes;
+  // k0 begins a block, and a tile's rows lie in one (TR).  TR: rows past the last one of a K value
+  // are the next one's first: the products of such rows are not stored.
   __device__ __forceinline__ Operand(const uint8_t* p, int64_t pitch_, int64_t row0, int64_t rows, int64_t k0, int kn,
                                      int wv, int lane) {
     pitch = BLK ? kBlock * ES : pitch_;
     block = BLK ? pitch_ : 0;
-    const int left = (int)min(rows - row0, (int64_t)R);
+    const int q = place(wv, 0);
     if constexpr (TR) {
-      base = (uint64_t)p + (uint64_t)(BLK ? row0 / kBlock * block + k0 * pitch + row0 % kBlock * ES : k0 * pitch + row0 * ES);
-      k_end = kn;
+      const int64_t first = (BLK ? row0 % kBlock : row0) * ES;
+      base = (uint64_t)p + (uint64_t)((BLK ? row0 / kBlock * block : 0) + k0 * pitch + first);
+      valid = rows > row0 ? (BLK ? (int64_t)kn * pitch - first : (int64_t)(kn - 1) * pitch + (rows - row0) * ES) : 0;
+      const int at = q % 16 * 1024 + lane * 16, k = at / LINE;
+      off[0] = (uint32_t)(k * (int)pitch) + (uint32_t)((at % LINE / 16 ^ swizzle(k)) * 16);
     } else {
       base = (uint64_t)p + (uint64_t)(BLK ? k0 / kBlock * block + row0 * pitch : row0 * pitch + k0 * ES);
-      k_end = kn * ES;
+      valid = min(rows - row0, (int64_t)R) * pitch;
+      k_left = kn * ES, far = 0;
+      k_first = 16u * ((lane & 7) ^ (4 * (q & 1) + (lane >> 4)));  // piece by (row / 2) % 8
+      off[0] = (uint32_t)((8 * q + (lane >> 3)) * (int)pitch) + k_first;
+      off[1] = off[0] - k_first + (k_first ^ 64u) + 8u * (uint32_t)pitch;
     }
-#pragma unroll
-    for (int j = 0; j < COPIES; j++) {
-      const int q = place(wv, j);
-      if constexpr (TR) {
-        const int at = q % 16 * 1024 + lane * 16, k = at / LINE, piece = at % LINE / 16 ^ swizzle(k);
-        const int row = q / 16 * 128 + piece * (16 / ES);  // rows are whole pieces: the pitch and their number are
-        k_of[j] = k;
-        off[j] = row < left ? (uint32_t)(k * pitch) + (uint32_t)(row * ES) : kOutside;
-      } else {
-        const int row = 8 * q + (lane >> 3);
-        const int piece = (lane & 7) ^ (4 * (COPIES == 1 ? q & 1 : j & 1) + (lane >> 4));  // (row / 2) % 8
-        k_of[j] = 16 * piece;
-        off[j] = row < left ? (uint32_t)(row * pitch) + (uint32_t)(16 * piece) : kOutside;
+    rsrc = descriptor(base, valid);
+  }
+  // The wave's j-th copy of the stage to the image at lds.  Its place differs from the first
+  // one's by whole rows (TR: K values of the same swizzle; and 128 rows), and TR false by the
+  // piece's third bit, as rows 8 apart have it.
+  __device__ __forceinline__ void copy(int j, int wv, uint32_t lds) const {
+    const int q = place(wv, j), d = q - place(wv, 0);  // d: 0, 1, 16 or 17
+    uint32_t at;
+    if constexpr (TR) {
+      at = off[0] + (uint32_t)(d % 16 * (1024 / LINE) * (int)pitch + d / 16 * LINE);
+    } else {
+      at = off[d & 1] + (uint32_t)(far + d / 16 * 128 * (int)pitch);
+      at = (int)(k_first ^ (d & 1 ? 64u : 0u)) < k_left ? at : kOutside;
+    }
+    copy_1k(rsrc, at, lds + (uint32_t)q * 1024);
+  }
+  // BLK, TR: to the first stage of the tile of kn K values at row0 (none: zeros)
+  __device__ __forceinline__ void restart(const uint8_t* p, int64_t row0, int kn) {
+    const int first = (int)(row0 % kBlock) * ES;
+    base = (uint64_t)p + (uint64_t)(row0 / kBlock * block + first);
+    valid = kn == 0 ? 0 : kn * pitch - first;
+    rsrc = descriptor(base, valid);
+  }
+  // on to the next stage
+  __device__ __forceinline__ void advance() {
+    if constexpr (TR) {
+      base += (uint64_t)(KS * pitch);
+      valid -= KS * pitch;
+      rsrc = descriptor(base, valid);
+    } else {
+      k_left -= 128, far += 128;
+      if (BLK && far == kBlock * ES) {
+        far = 0;
+        base += (uint64_t)block;
+        rsrc[0] = (uint32_t)base, rsrc[1] = (uint32_t)(base >> 32);
       }
     }
-  }
-  // the wave's j-th copy of stage s to the image at lds (copies of 128 rows of a tile are
-  // side by side: j of R / 64)
-  __device__ __forceinline__ void copy(int s, int j, int wv, uint32_t lds) const {
-    const int step = TR ? s * KS : s * 128;
-    // a lane outside stays outside: 2^31 plus at most 2^30 bytes of K values
-    const uint32_t far = TR ? 0u : BLK ? (uint32_t)(step % (kBlock * ES)) : (uint32_t)step;
-    const uint32_t at = k_of[j] + step < k_end ? off[j] + far : kOutside;
-    uint64_t from = base;
-    if constexpr (TR) from += (uint64_t)step * (uint64_t)pitch;
-    else if constexpr (BLK) from += (uint64_t)(step / (kBlock * ES)) * (uint64_t)block;
-    copy_1k(from, at, lds + (uint32_t)place(wv, j) * 1024);
   }
   // which KiB of the image a copy fills: with 256 rows, the wave's first half of copies lies in
   // rows 0 .. 127 and the second in the others
@@ -308,6 +338,16 @@ struct DRow {
   }
 };
 
+// Waits for what they loaded.
+template <int MODE, int N>
+__device__ __forceinline__ void here(DRow (&r)[N]) {
+#pragma unroll
+  for (int t = 0; t < N; t++) {
+    asm volatile("" : "+v"(r[t].label));
+    if constexpr (MODE != X_STATS) asm volatile("" : "+v"(r[t].g), "+v"(r[t].h), "+v"(r[t].both), "+v"(r[t].lse));
+  }
+}
+
 // (maximum, sum of exp relative to it) of the union of two sets; (-inf, 0) is the empty one.
 // A NaN in either sum stays.
 __device__ __forceinline__ float2 stats_join(float2 a, float2 b) {
@@ -319,11 +359,11 @@ __device__ __forceinline__ float2 stats_join(float2 a, float2 b) {
 // What a wave does with its MT x NT tiles of 16 x 16: registers i of tile (a, t) are rows
 // m0 + mrow + off(a) + 4 (lane / 16) + i and column n0 + ncol + off(t) + lane % 16 of the product,
 // where the first AH (TH) tiles along a direction are neighbours and the others lie 128 further.
-// smem: the LDS of the finished K loop, all of it free.
-// row: of the columns, loaded (X_STATS, X_DLOGIT, X_DLOGIT32)
-template <int DT, int MODE, int MT, int NT, int AH, int TH, int WM, int BN>
+// smem: LDS that is free.
+// drow(t): of column tile t (X_STATS, X_DLOGIT, X_DLOGIT32)
+template <int DT, int MODE, int MT, int NT, int AH, int TH, int WM, int BN, typename Rows>
 __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT], int64_t m0, int64_t n0, int mrow,
-                                       int ncol, int mtile, int split, int wm, int lane, const DRow (&drow)[NT],
+                                       int ncol, int mtile, int split, int wm, int lane, Rows drow,
                                        unsigned char* smem) {
   const int g = lane >> 4;
   // rows in 32 bits, from this lane's first one
@@ -339,7 +379,8 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
 #pragma unroll
     for (int t = 0; t < NT; t++) {
       const int64_t n = col_of(t);
-      const int label = n < p.n ? place(drow[t].label) : -1024;
+      const DRow row = drow(t);
+      const int label = n < p.n ? place(row.label) : -1024;
       float m = -__builtin_inff(), s = 0.f;
 #pragma unroll
       for (int a = 0; a < MT; a++)
@@ -369,7 +410,10 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
       s += __shfl_xor(s, 32, 64);
       if (g == 0) red[wm * BN + (int)(n - n0)] = make_float2(m, s);
     }
-    __syncthreads();
+    // twice: a row of waves may be one barrier behind
+    load_wait_lds();
+    bare_barrier();
+    bare_barrier();
     for (int c = threadIdx.x; c < BN; c += 64 * kXWaves) {
       float2 r = red[c];
       for (int w = 1; w < WM; w++) r = stats_join(r, red[w * BN + c]);
@@ -381,7 +425,7 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
     for (int t = 0; t < NT; t++) {
       const int64_t n = col_of(t);
       if (MODE == X_DLOGIT32 && n >= p.n) continue;
-      const DRow& row = drow[t];
+      const DRow row = drow(t);
       const int label = n < p.n ? place(row.label) : -1024;
 #pragma unroll
       for (int a0 = 0; a0 < MT; a0 += AH) {
@@ -449,22 +493,23 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
   }
 }
 
-// Tile and K slice of a workgroup.  Ids {x, x + 8, ...} run on XCD x: each XCD takes a
-// contiguous share of the tiles, in blocks of kGroup tiles along n by all along m: its 32
-// CUs work on about kGroup x 32 / kGroup tiles, which share their operands' slices in its L2.
+// Tiles and K slices.  Workgroups {x, x + 8, ...} run on XCD x: each XCD takes a contiguous
+// share of the tiles, in blocks of kGroup tiles along n by all along m: its 32 CUs work on about
+// kGroup x 32 / kGroup tiles, which share their operands' slices in its L2 (4,096 x 32,768 x
+// 5,120: 1,004 us, tile rows in turn 1,080).
 struct XentPlace {
   int mtile, ntile, split;
   bool some;
-  __device__ __forceinline__ XentPlace(const XentProduct& p) {
-    const int per = (int)(gridDim.x / 8), id = (int)blockIdx.x;
-    int tile = id % 8 * per + id / 8;
-    const int each = p.mt * p.nt;
-    some = tile < each * p.splits;
+  // the i-th tile of an XCD's share
+  __device__ __forceinline__ XentPlace(const XentProduct& p, int xcd, int i) {
+    const int each = p.mt * p.nt, all = each * p.splits, per = (all + 7) / 8;
+    int tile = xcd * per + i;
+    some = i < per && tile < all;
     split = __builtin_amdgcn_readfirstlane(tile / each);
     tile -= split * each;
     const int block = __builtin_amdgcn_readfirstlane(tile / (kGroup * p.mt));
     tile -= block * kGroup * p.mt;
-    const int wide = min(kGroup, p.nt - block * kGroup);
+    const int wide = max(1, min(kGroup, p.nt - block * kGroup));
     mtile = __builtin_amdgcn_readfirstlane(tile / wide);
     ntile = block * kGroup + tile - mtile * wide;
   }
@@ -481,19 +526,21 @@ __global__ void __launch_bounds__(64 * kXWaves) ring_kernel(XentProduct p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv / WN, wn = wv % WN;
-  const XentPlace at(p);
+  const XentPlace at(p, (int)blockIdx.x % 8, (int)blockIdx.x / 8);
   if (!at.some) return;  // whole workgroup
   const int64_t m0 = (int64_t)at.mtile * BM, n0 = (int64_t)at.ntile * BN, k0 = (int64_t)at.split * p.kslice;
   const int kn = (int)min((int64_t)p.kslice, p.k - k0), stages = (kn + A::KS - 1) / A::KS;
-  const A oa(p.a, p.a_pitch, m0, p.m, k0, kn, wv, lane);
-  const B ob(p.b, p.b_pitch, n0, p.n, k0, kn, wv, lane);
+  A oa(p.a, p.a_pitch, m0, p.m, k0, kn, wv, lane);
+  B ob(p.b, p.b_pitch, n0, p.n, k0, kn, wv, lane);
   const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem;
-  auto copy = [&](int s) {  // past the last stage: zeros that nothing reads
+  auto copy = [&](int s) {  // stage after stage; past the last one: zeros that nothing reads
     const uint32_t to = lds + (uint32_t)(s % RING) * IMG;
 #pragma unroll
-    for (int j = 0; j < A::COPIES; j++) oa.copy(s, j, wv, to);
+    for (int j = 0; j < A::COPIES; j++) oa.copy(j, wv, to);
 #pragma unroll
-    for (int j = 0; j < B::COPIES; j++) ob.copy(s, j, wv, to + A::BYTES);
+    for (int j = 0; j < B::COPIES; j++) ob.copy(j, wv, to + A::BYTES);
+    oa.advance();
+    ob.advance();
   };
   f32x4 acc[MT][NT];
 #pragma unroll
@@ -506,11 +553,7 @@ __global__ void __launch_bounds__(64 * kXWaves) ring_kernel(XentProduct p) {
   if constexpr (MODE == X_STATS || MODE == X_DLOGIT || MODE == X_DLOGIT32) {
 #pragma unroll
     for (int t = 0; t < NT; t++) drow[t].template load<MODE>(p, min(n0 + wn * (BN / WN) + 16 * t + (lane & 15), p.n - 1));
-#pragma unroll
-    for (int t = 0; t < NT; t++) {
-      asm volatile("" : "+v"(drow[t].label));
-      if constexpr (MODE != X_STATS) asm volatile("" : "+v"(drow[t].g), "+v"(drow[t].h), "+v"(drow[t].lse));
-    }
+    here<MODE>(drow);
   }
   for (int s = 0; s < stages; s++) {
     // stage s has landed, and every wave has read the image that the next copies refill
@@ -534,7 +577,7 @@ __global__ void __launch_bounds__(64 * kXWaves) ring_kernel(XentProduct p) {
   load_wait<0>();
   bare_barrier();
   finish<DT, MODE, MT, NT, MT, NT, WM, BN>(p, acc, m0, n0, wm * (BM / WM), wn * (BN / WN), at.mtile, at.split, wm, lane,
-                                           drow, smem);
+                                           [&](int t) { return drow[t]; }, smem);
 }
 
 // Tiles of 256 x 256, bound by the matrix cores.  Two LDS images of a stage; 2 x 4 waves, two
@@ -546,51 +589,70 @@ __global__ void __launch_bounds__(64 * kXWaves) ring_kernel(XentProduct p) {
 // the last step before it.  A half of an image is free once the second row of waves has read
 // it, a step after the first, and is refilled in that step: every copy has six steps, one
 // and a half stages, until it is waited for.
+//
+// One workgroup per CU takes tile after tile: the copies run two stages ahead, into the next
+// tile, whose first stages thus arrive while this one's end is computed and stored.  A tile
+// has an even number of stages (zeros behind an odd one), so that each begins alike.
 template <int DT, bool TA, bool TB, int MODE>
 __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
   using A = Operand<DT, TA, 256>;
   using B = Operand<DT, TB, 256, MODE == X_PART || MODE == X_OUT>;
   constexpr int IMG = A::BYTES + B::BYTES;
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [2][IMG]
+  // what finish stores in a whole tile, for each wave
+  constexpr int STORES = MODE == X_STATS || MODE == X_DLOGIT ? 0 : DT == DT_F32 || MODE == X_PART ? 32 : 16;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [2][IMG], then what finish needs
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv / 4, wn = wv % 4;
-  const XentPlace at(p);
+  const int xcd = (int)blockIdx.x % 8, step = (int)gridDim.x / 8;
+  int i = (int)blockIdx.x / 8;
+  XentPlace at(p, xcd, i);
   if (!at.some) return;  // whole workgroup
-  const int64_t m0 = (int64_t)at.mtile * 256, n0 = (int64_t)at.ntile * 256, k0 = (int64_t)at.split * p.kslice;
-  const int kn = (int)min((int64_t)p.kslice, p.k - k0), stages = (kn + A::KS - 1) / A::KS;
-  const A oa(p.a, p.a_pitch, m0, p.m, k0, kn, wv, lane);
-  const B ob(p.b, p.b_pitch, n0, p.n, k0, kn, wv, lane);
-  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem;
-  // half h of stage s (past the last stage: zeros that nothing reads)
-  auto copy_a = [&](int s, int h) {
-    oa.copy(s, 2 * h, wv, lds + (uint32_t)(s & 1) * IMG);
-    oa.copy(s, 2 * h + 1, wv, lds + (uint32_t)(s & 1) * IMG);
+  auto stages_of = [&](const XentPlace& t) {
+    const int kn = (int)min((int64_t)p.kslice, p.k - (int64_t)t.split * p.kslice);
+    return (kn + 2 * A::KS - 1) / (2 * A::KS) * 2;
   };
-  auto copy_b = [&](int s, int h) {
-    ob.copy(s, 2 * h, wv, lds + (uint32_t)(s & 1) * IMG + A::BYTES);
-    ob.copy(s, 2 * h + 1, wv, lds + (uint32_t)(s & 1) * IMG + A::BYTES);
+  // of the tile that is copied from; past the last tile: no rows, so zeros that nothing reads
+  auto side_a = [&](const XentPlace& t) {
+    const int64_t k0 = (int64_t)t.split * p.kslice, m0 = t.some ? (int64_t)t.mtile * 256 : 0;
+    return A(p.a, p.a_pitch, m0, t.some ? p.m : 0, t.some ? k0 : 0, (int)min((int64_t)p.kslice, p.k - k0), wv, lane);
+  };
+  auto side_b = [&](const XentPlace& t) {
+    const int64_t k0 = (int64_t)t.split * p.kslice, n0 = t.some ? (int64_t)t.ntile * 256 : 0;
+    return B(p.b, p.b_pitch, n0, t.some ? p.n : 0, t.some ? k0 : 0, (int)min((int64_t)p.kslice, p.k - k0), wv, lane);
+  };
+  A oa = side_a(at);
+  B ob = side_b(at);
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem;
+  // half h of the stage, to image img
+  auto copy_a = [&](int img, int h) {
+    oa.copy(2 * h, wv, lds + (uint32_t)img * IMG);
+    oa.copy(2 * h + 1, wv, lds + (uint32_t)img * IMG);
+  };
+  auto copy_b = [&](int img, int h) {
+    ob.copy(2 * h, wv, lds + (uint32_t)img * IMG + A::BYTES);
+    ob.copy(2 * h + 1, wv, lds + (uint32_t)img * IMG + A::BYTES);
   };
   f32x4 acc[8][4];
-#pragma unroll
-  for (int a = 0; a < 8; a++)
-#pragma unroll
-    for (int t = 0; t < 4; t++) acc[a][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   u32x4 fa[4][2], fb[2][2][2];
-  auto read_a = [&](int s, int h) {
+  auto read_a = [&](int img, int h) {
 #pragma unroll
     for (int a = 0; a < 4; a++)
 #pragma unroll
-      for (int kk = 0; kk < 2; kk++) fa[a][kk] = A::read(smem + (s & 1) * IMG, 128 * h + 64 * wm + 16 * a, kk, lane);
+      for (int kk = 0; kk < 2; kk++) fa[a][kk] = A::read(smem + img * IMG, 128 * h + 64 * wm + 16 * a, kk, lane);
   };
-  auto read_b = [&](int s, int h) {
+  auto read_b = [&](int img, int h) {
 #pragma unroll
     for (int t = 0; t < 2; t++)
 #pragma unroll
       for (int kk = 0; kk < 2; kk++)
-        fb[h][t][kk] = B::read(smem + (s & 1) * IMG + A::BYTES, 128 * h + 32 * wn + 16 * t, kk, lane);
+        fb[h][t][kk] = B::read(smem + img * IMG + A::BYTES, 128 * h + 32 * wn + 16 * t, kk, lane);
   };
-  auto products = [&](int ha, int hb) {
-    load_wait<12>();  // the fragments are read; the half that the next step reads has landed
+  // behind: the six steps after a tile's end, in which its stores are newer than the copies that
+  // are waited for
+  auto products = [&](int ha, int hb, bool behind) {
+    // the fragments are read; the half that the next step reads has landed
+    if (STORES > 0 && behind) load_wait<12 + STORES>();
+    else load_wait<12>();
     __builtin_amdgcn_sched_barrier(0);
     bare_barrier();
     __builtin_amdgcn_s_setprio(1);
@@ -606,46 +668,80 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
     bare_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Stage s, half F of B first (its fragments are there).
-  auto stage = [&](int s, auto first) {
+  // The stage in image F, half F of B first (its fragments are there).
+  auto stage = [&](auto first, bool behind) {
     constexpr int F = decltype(first)::value, L = 1 - F;
-    copy_b(s + 2, F);
-    read_a(s, 0);
-    products(0, F);
-    copy_a(s + 2, 0);
-    read_b(s, L);
-    products(0, L);
-    copy_b(s + 2, L);
-    read_a(s, 1);
-    products(1, L);
-    copy_a(s + 2, 1);
-    read_b(s + 1, L);
-    products(1, F);
+    copy_b(F, F);
+    read_a(F, 0);
+    products(0, F, behind);
+    copy_a(F, 0);
+    read_b(F, L);
+    products(0, L, behind);
+    copy_b(F, L);
+    read_a(F, 1);
+    products(1, L, behind && F == 0);
+    copy_a(F, 1);
+    read_b(L, L);
+    oa.advance();
+    ob.advance();
+    products(1, F, behind && F == 0);
   };
   copy_b(0, 0), copy_a(0, 0), copy_b(0, 1), copy_a(0, 1);
+  oa.advance();
+  ob.advance();
   copy_b(1, 1), copy_a(1, 0), copy_b(1, 0), copy_a(1, 1);
+  oa.advance();
+  ob.advance();
   load_wait<12>();
   bare_barrier();
   read_b(0, 0);
   load_wait<12>();
   bare_barrier();  // the first step refills what was read here
   if (wm == 1) bare_barrier();
-  int s = 0;
-  for (; s + 1 < stages; s += 2) {
-    stage(s, std::integral_constant<int, 0>{});
-    stage(s + 1, std::integral_constant<int, 1>{});
-  }
-  if (s < stages) stage(s, std::integral_constant<int, 0>{});
-  if (wm == 0) bare_barrier();
-  load_wait<0>();
-  bare_barrier();
-  DRow drow[4];
-  if constexpr (MODE == X_STATS || MODE == X_DLOGIT) {
+  bool behind = false;
+  for (;;) {
+    const int stages = stages_of(at);
+    const XentPlace next(p, xcd, i + step);
 #pragma unroll
-    for (int t = 0; t < 4; t++)
-      drow[t].template load<MODE>(p, min(n0 + 32 * wn + t / 2 * 128 + t % 2 * 16 + (lane & 15), p.n - 1));
+    for (int a = 0; a < 8; a++)
+#pragma unroll
+      for (int t = 0; t < 4; t++) acc[a][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < stages; s += 2) {
+      if (s + 2 == stages) {  // the copies, two stages ahead, go on to the next tile
+        oa = side_a(next);
+        ob = side_b(next);
+      }
+      stage(std::integral_constant<int, 0>{}, behind && s == 0);
+      stage(std::integral_constant<int, 1>{}, behind && s == 0);
+    }
+    if (wm == 0) bare_barrier();  // both rows of waves at once, or the ends would follow each other
+    const int64_t m0 = (int64_t)at.mtile * 256, n0 = (int64_t)at.ntile * 256;
+    // opaque copies: what the end needs of the arguments, and derives from the lane, is not kept
+    // through the K loop
+    int xl = lane;
+    asm volatile("" : "+v"(xl));
+    const auto* args = (const __attribute__((address_space(4))) XentProduct*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(args));
+    const XentProduct q = *(const XentProduct*)args;
+    // a column tile's as it is its turn: four at once would spill into the K loop
+    auto drow = [&](int t) {
+      DRow r[1];
+      if constexpr (MODE == X_STATS || MODE == X_DLOGIT) {
+        r[0].template load<MODE>(q, min(n0 + 32 * wn + t / 2 * 128 + t % 2 * 16 + (xl & 15), q.n - 1));
+        here<MODE>(r);  // a load that some path leaves unread would be waited for there
+      }
+      return r[0];
+    };
+    finish<DT, MODE, 8, 4, 4, 2, 2, 256>(q, acc, m0, n0, 64 * wm, 32 * wn, at.mtile, at.split, wm, xl, drow,
+                                         smem + 2 * IMG);
+    // every store of a whole tile was issued
+    behind = STORES > 0 && m0 + 256 <= p.m && n0 + 256 <= p.n && !p.add;
+    if (!next.some) break;
+    at = next;
+    i += step;
+    if (wm == 1) bare_barrier();  // one behind again
   }
-  finish<DT, MODE, 8, 4, 4, 2, 2, 256>(p, acc, m0, n0, 64 * wm, 32 * wn, at.mtile, at.split, wm, lane, drow, smem);
+  load_wait<0>();  // nothing of this workgroup is in flight when its LDS is given away
 }
 
 // dE = D^T x for up to 128 residual rows (f32: 64), bound by its stores: a workgroup keeps 256
@@ -664,17 +760,18 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) outer_kernel(XentProduct p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // first A's images, then [RING][IMG]
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv & 3, wn = wv >> 2;
-  const XentPlace at(p);  // ntile: a range of kslice table rows (a multiple of 128)
+  const XentPlace at(p, (int)blockIdx.x % 8, (int)blockIdx.x / 8);  // ntile: a range of kslice table rows (a multiple of 128)
   if (!at.some) return;   // whole workgroup
   const int64_t m0 = (int64_t)at.mtile * 256, n0 = (int64_t)at.ntile * p.kslice, n1 = min(n0 + p.kslice, p.n);
   const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem;
   u32x4 fa[KT][4][2];
   {
-    const A oa(p.a, p.a_pitch, m0, p.m, 0, (int)p.k, wv, lane);
+    A oa(p.a, p.a_pitch, m0, p.m, 0, (int)p.k, wv, lane);
 #pragma unroll
     for (int s = 0; s < KT; s++) {
 #pragma unroll
-      for (int j = 0; j < A::COPIES; j++) oa.copy(s, j, wv, lds + s * A::BYTES);
+      for (int j = 0; j < A::COPIES; j++) oa.copy(j, wv, lds + s * A::BYTES);
+      oa.advance();
     }
     load_wait<0>();
     bare_barrier();
@@ -699,13 +796,15 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) outer_kernel(XentProduct p) {
     asm volatile("" : "+v"(token[s]), "+v"(rest[s]));  // here, not where a copy would be waited for
   }
   const int steps = (int)((n1 - n0 + 127) / 128);
+  B ob(p.b, p.b_pitch, n0, p.n, 0, (int)p.k, wv, lane);
   auto copy = [&](int i) {  // D's tile of step i (past the last: zeros that nothing reads)
-    const int64_t first = n0 + (int64_t)i * 128;
-    const B ob(p.b, p.b_pitch, i < steps ? first : n0, i < steps ? p.n : n0, 0, (int)p.k, wv, lane);
+    ob.restart(p.b, n0 + (int64_t)i * 128, i < steps ? (int)p.k : 0);
 #pragma unroll
-    for (int s = 0; s < KT; s++)
+    for (int s = 0; s < KT; s++) {
 #pragma unroll
-      for (int j = 0; j < B::COPIES; j++) ob.copy(s, j, wv, lds + (uint32_t)(i % RING) * IMG + s * B::BYTES);
+      for (int j = 0; j < B::COPIES; j++) ob.copy(j, wv, lds + (uint32_t)(i % RING) * IMG + s * B::BYTES);
+      ob.advance();
+    }
   };
   // Copies and stores complete in order: behind a step's copies are those of the RING - 2 steps
   // after it and the stores of RING - 1 steps, whose number is known where none is left out.
@@ -766,8 +865,8 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) outer_kernel(XentProduct p) {
             }
         }
       }
-      const DRow none[2] = {};
-      finish<DT, X_OUT, 4, 2, 4, 2, 1, 128>(p, acc, m0, first, 64 * wm, 64 * wn + 32 * h, 0, 0, 0, lane, none, smem);
+      finish<DT, X_OUT, 4, 2, 4, 2, 1, 128>(p, acc, m0, first, 64 * wm, 64 * wn + 32 * h, 0, 0, 0, lane,
+                                            [](int) { return DRow(); }, smem);
     }
   }
   load_wait<0>();  // nothing of this workgroup is in flight when its LDS is given away
@@ -1043,6 +1142,9 @@ __global__ void __launch_bounds__(256) xent_pack_kernel(const uint8_t* __restric
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
+#ifndef TILE_GRID
+#define TILE_GRID kTargetBlocks
+#endif
 namespace {
 
 constexpr int kXcdCount = 8;
@@ -1082,11 +1184,12 @@ hipError_t launch_ring(const XentProduct& p, hipStream_t stream) {
 template <int DT, bool TA, bool TB, int MODE>
 hipError_t launch_tile(const XentProduct& p, hipStream_t stream) {
   const void* fn = (const void*)tile_kernel<DT, TA, TB, MODE>;
-  const size_t lds = 2 * 512 * 128;
+  const size_t lds = 2 * 512 * 128 + (MODE == X_STATS ? 2 * 256 * 8 : 0);
   hipError_t e = set_dynamic_lds(fn, lds);
   if (e != hipSuccess) return e;
   const int64_t tiles = (int64_t)p.mt * p.nt * p.splits;
-  hipLaunchKernelGGL((tile_kernel<DT, TA, TB, MODE>), dim3((unsigned)(cdiv(tiles, kXcdCount) * kXcdCount)),
+  hipLaunchKernelGGL((tile_kernel<DT, TA, TB, MODE>),
+                     dim3((unsigned)std::min<int64_t>(cdiv(tiles, kXcdCount) * kXcdCount, TILE_GRID)),
                      dim3(64 * kXWaves), lds, stream, p);
   return hipGetLastError();
 }
