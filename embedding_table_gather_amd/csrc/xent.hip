@@ -96,7 +96,8 @@ __device__ __forceinline__ void bare_barrier() { asm volatile("s_barrier" ::: "m
 //             that the K values that one transposing read takes lie on different banks.
 //
 // BLK: D, which is kept in blocks of 256 table rows, each [residual row][256]: what a tile writes
-// and reads of it is one range of memory.  Rows as long as a piece took TLB.
+// and reads of it is one range of memory (64 x 262,144 x 5,376: 1,595 us with rows as long as the
+// vocabulary, 1,538 so; 160 rows' table gradient 1,464 and 1,246).
 constexpr int kBlock = 256;
 template <int DT, bool TR, int R, bool BLK = false>
 struct Operand {
@@ -260,7 +261,7 @@ __device__ __forceinline__ f32x4 load4(const void* at) {
 // and `most` values (a multiple of 4, 8 for 16-bit types) are stored.  16-bit types exchange
 // them between the lanes first, so that a store writes whole lines (128 bytes of each of
 // eight rows); stores of 8 bytes in every 32 took 1,076 us for 2.8 GB, of half lines 631, of
-// whole ones WHOLE.
+// whole ones 562.
 template <int DT, int AH>
 __device__ __forceinline__ void store_rows(unsigned char* at, int64_t pitch, const f32x4 (&x)[AH], int lane,
                                            int64_t rows, int most) {
@@ -876,7 +877,6 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) outer_kernel(XentProduct p) {
 // four waves a quarter of K each, straight from memory.
 template <int DT, int MODE>
 __global__ void __launch_bounds__(256) direct_kernel(XentProduct p) {
-  static_assert(MODE == X_STATS || MODE == X_DLOGIT32, "what few residual rows need");
   constexpr int U = 4;
   __shared__ float sums[4][16][17];  // [wave][residual row][table row]
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
@@ -921,10 +921,18 @@ __global__ void __launch_bounds__(256) direct_kernel(XentProduct p) {
     if (some && v == (int64_t)(uint32_t)p.labels[n] - p.v0) p.target[n] = l;
     if (r == 0) ((float2*)p.out)[n * p.mt + blockIdx.x % p.mt] = make_float2(m, s);
   } else {
-    if (n >= p.n || v >= p.m) return;
+    if (n >= p.n || (MODE == X_DLOGIT32 && v >= p.m)) return;
     DRow row;
     row.load<MODE>(p, n);
-    ((float*)p.out)[v * 8 + n] = v == row.label ? row.at_label(l) : row.other(l);
+    const float x = v == row.label ? row.at_label(l) : row.other(l);
+    if constexpr (MODE == X_DLOGIT32) {
+      ((float*)p.out)[v * 8 + n] = x;
+    } else {
+      const float scaled = v < p.m ? x * (p.scale != nullptr ? p.scale[0] : 1.f) : 0.f;
+      const auto d = round1<DT>(scaled);
+      ((decltype(round1<DT>(x))*)p.out)[(v / kBlock * p.n + n) * kBlock + v % kBlock] = d;
+      if (DT != DT_F32 && v == row.label) p.rest[n] = scaled - (float)d;
+    }
   }
 }
 
@@ -1142,17 +1150,15 @@ __global__ void __launch_bounds__(256) xent_pack_kernel(const uint8_t* __restric
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-#ifndef TILE_GRID
-#define TILE_GRID kTargetBlocks
-#endif
 namespace {
 
 constexpr int kXcdCount = 8;
 
 // Columns of a product's tiles for n residual rows, and what the product then takes: rounds of
 // one workgroup per CU, times its columns and stages.  16-bit products of 256 columns keep
-// the matrix cores busier than those of 128 (1,024 x 262,144 x 5,120: RATE16); in f32, where
-// they are slow enough for either, the choice is about rounds alone.
+// the matrix cores busier than those of 128 (1,024 x 262,144 x 5,120: 2,034 us, by 128 columns
+// 2,672); in f32, where they are slow enough for either, the choice is about rounds alone (300
+// x 20,000 x 600: 271 us, 456 by 256 columns throughout).
 struct Tiling {
   int columns;
   int64_t cost;
@@ -1161,7 +1167,7 @@ Tiling tiling(int64_t m, int64_t n, int64_t k, int64_t splits, int size) {
   Tiling best = {0, INT64_MAX};
   for (int c = n <= 64 || size == 4 ? 64 : 128; c <= 256; c *= 2) {
     const int64_t percent = size == 4 ? 100 : c == 256 ? 100 : 140;  // time of a column
-    const int64_t stages = cdiv(cdiv(k, splits), 128 / size) + 24;    // and what a start and an end cost
+    const int64_t stages = cdiv(cdiv(k, splits), 128 / size) + (size == 4 ? 6 : 24);  // and a start and an end
     const int64_t cost = cdiv(cdiv(m, 256) * cdiv(n, c) * splits, kTargetBlocks) * c * percent * stages;
     if (cost < best.cost) best = {c, cost};
     if (c >= n) break;
@@ -1189,7 +1195,7 @@ hipError_t launch_tile(const XentProduct& p, hipStream_t stream) {
   if (e != hipSuccess) return e;
   const int64_t tiles = (int64_t)p.mt * p.nt * p.splits;
   hipLaunchKernelGGL((tile_kernel<DT, TA, TB, MODE>),
-                     dim3((unsigned)std::min<int64_t>(cdiv(tiles, kXcdCount) * kXcdCount, TILE_GRID)),
+                     dim3((unsigned)std::min<int64_t>(cdiv(tiles, kXcdCount) * kXcdCount, kTargetBlocks)),
                      dim3(64 * kXWaves), lds, stream, p);
   return hipGetLastError();
 }
@@ -1229,13 +1235,16 @@ hipError_t launch_by_rows(XentProduct p, hipStream_t stream) {
 constexpr int64_t kMaxTiles = 1 << 20;              // of one launch
 constexpr int64_t kPartBytes = (int64_t)256 << 20;  // statistics, or D, of one piece
 
-// The 16 x 16 kernel instead of tiles of 256 table rows.
-constexpr int64_t kDirectTiles = 2048;
-bool direct_tiles(int64_t vocab, int64_t n) { return n <= 64 && cdiv(vocab, 16) * cdiv(n, 16) <= kDirectTiles; }
+// The 16 x 16 kernel instead of tiles of 256 table rows (1 x 16,384 x 1,024 bf16: 14 us, by the
+// tiles 17; 16 x 32,768 x 1,024 29 / 19; 4 x 4,096 x 256 f32 12 / 24).
+bool direct_tiles(int64_t vocab, int64_t n, int dtype) {
+  return n <= 64 && cdiv(vocab, 16) * cdiv(n, 16) <= (dtype == DT_F32 ? 4096 : 1024);
+}
 
 template <int DT, int MODE>
 hipError_t launch_direct(XentProduct p, hipStream_t stream) {
-  p.mt = (int32_t)cdiv(p.m, 16), p.nt = (int32_t)cdiv(p.n, 16);
+  // D's last block is written whole
+  p.mt = (int32_t)(MODE == X_DLOGIT ? cdiv(p.m, kBlock) * (kBlock / 16) : cdiv(p.m, 16)), p.nt = (int32_t)cdiv(p.n, 16);
   hipLaunchKernelGGL((direct_kernel<DT, MODE>), dim3((unsigned)(p.mt * p.nt)), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
@@ -1258,7 +1267,7 @@ struct ForwardWs {
 };
 ForwardWs forward_ws(const TableDesc& t, int64_t n) {
   ForwardWs w;
-  w.direct = direct_tiles(t.V, n);
+  w.direct = direct_tiles(t.V, n, t.dtype);
   w.piece = forward_piece(t.V, n);
   w.mt = (int32_t)(w.direct ? cdiv(t.V, 16) : w.piece / 256);
   w.target = align_up((size_t)n * 8, 256);  // after the running statistics
@@ -1268,11 +1277,12 @@ ForwardWs forward_ws(const TableDesc& t, int64_t n) {
   return w;
 }
 
-// Few residual rows and a table that the caches hold: D in f32 and one kernel of vector FMAs
-// for both gradients, fewer launches (VECTOR).  A larger table takes longer that way: its
-// reads and writes alternate (1 x 262,144 x 5,376: 1,668 us, by products 1,554).
-constexpr int64_t kVectorBytes = (int64_t)64 << 20;
-bool vector_rows(const TableDesc& t, int64_t n) { return n <= 8 && t.V * t.row_bytes <= kVectorBytes; }
+// Few residual rows and a small table: D in f32 and one kernel of vector FMAs for both
+// gradients, fewer launches (1 x 4,096 x 256 f32: 16 us, by products 70; 4 x 32,768 x 1,024 bf16
+// 46 / 47; 8 x 16,384 x 1,024 45 / 38).  A large one takes longer that way: its reads and writes
+// alternate (1 x 262,144 x 5,376: 1,668 / 1,554).
+constexpr int64_t kVectorBytes = (int64_t)128 << 20;
+bool vector_rows(const TableDesc& t, int64_t n) { return n <= 8 && n * t.V * t.row_bytes <= kVectorBytes; }
 
 struct BackwardWs {
   int64_t piece, splits, slice;
@@ -1280,10 +1290,10 @@ struct BackwardWs {
   int64_t block;  // bytes of a block of D
   size_t rest, x, d, sums, bytes;
 };
-// K slices of dx = D E, at least 512 table rows each.
+// K slices of dx = D E, at least 256 table rows each.
 int64_t backward_splits(int64_t piece, int64_t n, int64_t hidden, int size) {
   int64_t best = 1, least = INT64_MAX;
-  for (int64_t s = 1; s <= std::max<int64_t>(1, piece / 512) && s <= kTargetBlocks; s++) {
+  for (int64_t s = 1; s <= std::max<int64_t>(1, piece / 256) && s <= kTargetBlocks; s++) {
     const int64_t cost = tiling(hidden, n, piece, s, size).cost;
     if (cost < least) least = cost, best = s;
     if (cdiv(hidden, 256) * cdiv(n, 256) * s >= 8 * kTargetBlocks) break;
@@ -1396,8 +1406,8 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
     p.x = logits.b, p.row_bytes = t.row_bytes, p.x_pitch = logits.b_pitch, p.per = w.slice;
     p.hidden = (int)t.hidden, p.n = (int)c.n, p.chunks = w.chunks, p.slices = (int)w.splits;
     p.d = (const float*)d, p.rows = (uint8_t*)c.d_rows, p.add = c.add, p.part = c.d_x != nullptr ? sums : nullptr;
-    e = direct_tiles(t.V, c.n) ? launch_direct<DT, X_DLOGIT32>(logits, stream)
-                               : launch_by_rows<DT, false, X_DLOGIT32>(logits, stream);
+    e = direct_tiles(t.V, c.n, DT) ? launch_direct<DT, X_DLOGIT32>(logits, stream)
+                                   : launch_by_rows<DT, false, X_DLOGIT32>(logits, stream);
     if (e != hipSuccess) return e;
     e = c.n <= 2   ? launch_rows<DT, 2>(p, stream)
         : c.n <= 4 ? launch_rows<DT, 4>(p, stream)
@@ -1417,7 +1427,9 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
   for (int64_t v0 = 0; v0 < t.V; v0 += w.piece) {
     const int64_t rows = std::min(w.piece, t.V - v0);
     logits.a = t.rows + v0 * t.row_bytes, logits.m = rows, logits.v0 = v0;
-    if ((e = launch_by_rows<DT, false, X_DLOGIT>(logits, stream)) != hipSuccess) return e;
+    e = direct_tiles(rows, c.n, DT) ? launch_direct<DT, X_DLOGIT>(logits, stream)
+                                    : launch_by_rows<DT, false, X_DLOGIT>(logits, stream);
+    if (e != hipSuccess) return e;
     if (c.d_x != nullptr) {
       XentProduct p = {};
       p.m = t.hidden, p.n = c.n, p.k = rows;
