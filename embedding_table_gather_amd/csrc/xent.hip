@@ -311,6 +311,19 @@ __device__ __forceinline__ void store_rows(unsigned char* at, int64_t pitch, con
   }
 }
 
+// The gradients that reach a residual row's loss and lse.
+struct RowGrads {
+  const int32_t* labels;
+  int64_t vocab;
+  const float *grad_loss, *grad_lse;
+  float grad_loss_all;  // where grad_loss is NULL
+  // Neither does: the row adds nothing to dE, whatever it holds (0 times a NaN would).
+  __device__ __forceinline__ bool none(int64_t b) const {
+    const float h = grad_lse != nullptr ? grad_lse[b] : 0.f, g = grad_loss != nullptr ? grad_loss[b] : grad_loss_all;
+    return (g == 0.f || (uint32_t)labels[b] >= (uint64_t)vocab) && h == 0.f;
+  }
+};
+
 // What D's entries (and the loss: the label alone) of one residual row need.
 struct DRow {
   float g, h, both, lse;
@@ -517,7 +530,8 @@ struct XentPlace {
 };
 
 // Tiles of BM x BN, K through a ring of RING LDS images, RING - 1 stages ahead: one barrier
-// per stage.
+// per stage.  For few residual rows, where reading the table is the bound: 64 x 262,144 x 5,376
+// statistics 464 us (6.1 TB/s; a kernel that only reads reaches 6.9), dx from D 455 us.
 template <int DT, bool TA, bool TB, int MODE, int BM, int BN, int WM, int RING>
 __global__ void __launch_bounds__(64 * kXWaves) ring_kernel(XentProduct p) {
   using A = Operand<DT, TA, BM>;
@@ -594,6 +608,10 @@ __global__ void __launch_bounds__(64 * kXWaves) ring_kernel(XentProduct p) {
 // One workgroup per CU takes tile after tile: the copies run two stages ahead, into the next
 // tile, whose first stages thus arrive while this one's end is computed and stored.  A tile
 // has an even number of stages (zeros behind an odd one), so that each begins alike.
+//
+// 4,096 x 32,768 x 5,120 bf16, a launch each: D 1,004 us (1.37 PF/s), dx 1,102 us, dE 1,086 us;
+// the library's plain products take 964, 1,410 and 1,184.  What bounds it is the time at which
+// fragments leave LDS: a step reads 8 or 4 KiB per wave for 16 products.
 template <int DT, bool TA, bool TB, int MODE>
 __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
   using A = Operand<DT, TA, 256>;
@@ -747,8 +765,9 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
 
 // dE = D^T x for up to 128 residual rows (f32: 64), bound by its stores: a workgroup keeps 256
 // columns of x as fragments in registers (64 for each of 4 waves, twice) and walks a range of
-// table rows, 128 at a time (64 for each half of the waves), D's tiles two or three steps ahead
-// in a ring of LDS images.  A tile that holds a label has the rest of its entry of D added,
+// table rows, 128 at a time (64 for each half of the waves), D's tiles RING - 1 steps ahead in
+// a ring of LDS images: 64 x 262,144 x 5,376 bf16 640 us (4.4 TB/s), 128 rows 860; tiles as the
+// other products have them keep too few stores in flight.  A tile that holds a label has the rest of its entry of D added,
 // as a second operand built in registers.
 template <int DT, int KT>
 constexpr int kOuterRing = DT == DT_F32 ? 4 : KT == 1 ? 7 : 5;  // as deep as the count of a wait and LDS allow
@@ -938,7 +957,8 @@ __global__ void __launch_bounds__(256) direct_kernel(XentProduct p) {
 
 // Up to 8 residual rows: both gradients in one pass over the table, with vector FMAs and D in
 // f32.  A wave takes 64 pieces of 16 bytes of some consecutive table rows: their share of
-// dx stays in its registers, their rows of dE are written as they come.
+// dx stays in its registers, their rows of dE are written as they come: 1 x 4,096 x 256 f32 14 us
+// with the launches before and after.
 struct XentRows {
   const uint8_t *table, *x;
   int64_t row_bytes, x_pitch, m, per;  // per: table rows of a wave
@@ -946,6 +966,7 @@ struct XentRows {
   const float* d;                      // [m][8]
   uint8_t* rows;                       // dE of the first table row, or NULL
   int32_t add;
+  RowGrads grads;
   float* part;                         // [slices][n][hidden], or NULL
 };
 
@@ -973,7 +994,13 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(XentRows p) {
   float x[NB][E], acc[NB][E];
 #pragma unroll
   for (int b = 0; b < NB; b++) {
-    unpack<DT>(b < p.n ? *(const u32x4*)(p.x + b * p.x_pitch + at) : u32x4{0, 0, 0, 0}, x[b]);
+    // past the last row: the last again, as zeros
+    const int64_t row = min(b, p.n - 1);
+    const uint32_t keep = b < p.n && !p.grads.none(row) ? ~0u : 0u;
+    u32x4 w = *(const u32x4*)(p.x + row * p.x_pitch + at);
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] &= keep;
+    unpack<DT>(w, x[b]);
 #pragma unroll
     for (int i = 0; i < E; i++) acc[b][i] = 0.f;
   }
@@ -1138,13 +1165,18 @@ __global__ void __launch_bounds__(256) xent_sum_kernel(const float* __restrict__
   *(Vu*)((unsigned char*)out + b * out_pitch + c * kValue<DT>) = round4<DT>(x);
 }
 
-// Rows of `bytes` (a multiple of 16) bytes, pitch bytes apart at any alignment, side by side.
+// Rows of `bytes` (a multiple of 16) bytes, pitch bytes apart at any alignment, side by side; for
+// the gradients, zeros in the place of those that nothing reaches.
 __global__ void __launch_bounds__(256) xent_pack_kernel(const uint8_t* __restrict__ src, int64_t pitch, int64_t n,
-                                                        int64_t bytes, uint8_t* __restrict__ dst) {
+                                                        int64_t bytes, uint8_t* __restrict__ dst, RowGrads grads) {
   typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
-  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x, each = bytes / 16;
-  if (q >= n * each) return;
-  *(u32x4*)(dst + q * 16) = *(const u32x4u*)(src + q / each * pitch + q % each * 16);
+  const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x, each = bytes / 16, b = q / each;
+  if (b >= n) return;
+  const uint32_t keep = grads.labels != nullptr && grads.none(b) ? 0u : ~0u;
+  u32x4 w = *(const u32x4u*)(src + b * pitch + q % each * 16);
+#pragma unroll
+  for (int i = 0; i < 4; i++) w[i] &= keep;
+  *(u32x4*)(dst + q * 16) = w;
 }
 
 // ---------------------------------------------------------------------------
@@ -1331,10 +1363,10 @@ BackwardWs backward_ws(const TableDesc& t, int64_t n) {
 // The residual rows as the kernels read them: 16-byte aligned, rows less than 8 MiB apart.
 bool rows_direct(const void* x, int64_t pitch) { return ((uintptr_t)x | (uint64_t)pitch) % 16 == 0 && pitch < (8 << 20); }
 
-hipError_t pack_rows(const XentCall& c, const TableDesc& t, uint8_t* to, hipStream_t stream) {
+hipError_t pack_rows(const XentCall& c, const TableDesc& t, uint8_t* to, const RowGrads& grads, hipStream_t stream) {
   const int64_t pieces = c.n * (t.row_bytes / 16);
   hipLaunchKernelGGL(xent_pack_kernel, dim3((unsigned)cdiv(pieces, 256)), dim3(256), 0, stream, (const uint8_t*)c.x,
-                     c.x_pitch, c.n, t.row_bytes, to);
+                     c.x_pitch, c.n, t.row_bytes, to, grads);
   return hipGetLastError();
 }
 
@@ -1346,7 +1378,7 @@ hipError_t forward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStream
   float2 *run = (float2*)ws, *part = (float2*)(ws + w.part);
   float* target = (float*)(ws + w.target);
   const bool direct = rows_direct(c.x, c.x_pitch);
-  if (!direct && (e = pack_rows(c, t, ws + w.x, stream)) != hipSuccess) return e;
+  if (!direct && (e = pack_rows(c, t, ws + w.x, {}, stream)) != hipSuccess) return e;
   const int64_t piece = w.direct ? t.V : w.piece;
   for (int64_t v0 = 0; v0 < t.V; v0 += piece) {
     XentProduct p = {};
@@ -1391,8 +1423,10 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
   hipError_t e;
   uint8_t *packed = ws + w.x, *d = ws + w.d;
   float* sums = (float*)(ws + w.sums);
-  const bool direct = rows_direct(c.x, c.x_pitch);
-  if (!direct && (e = pack_rows(c, t, packed, stream)) != hipSuccess) return e;
+  const RowGrads grads = {c.labels, t.V, c.grad_loss, c.grad_lse, c.grad_loss_all};
+  // the products of dE take a copy without the rows that nothing reaches
+  const bool direct = rows_direct(c.x, c.x_pitch) && (vector_rows(t, c.n) || c.d_rows == nullptr);
+  if (!direct && (e = pack_rows(c, t, packed, grads, stream)) != hipSuccess) return e;
   XentProduct logits = {};  // of a piece, to D
   logits.n = c.n, logits.k = t.hidden, logits.a_pitch = t.row_bytes;
   logits.b = direct ? (const uint8_t*)c.x : packed, logits.b_pitch = direct ? c.x_pitch : t.row_bytes;
@@ -1405,7 +1439,7 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
     logits.a = p.table = t.rows, logits.m = p.m = t.V;
     p.x = logits.b, p.row_bytes = t.row_bytes, p.x_pitch = logits.b_pitch, p.per = w.slice;
     p.hidden = (int)t.hidden, p.n = (int)c.n, p.chunks = w.chunks, p.slices = (int)w.splits;
-    p.d = (const float*)d, p.rows = (uint8_t*)c.d_rows, p.add = c.add, p.part = c.d_x != nullptr ? sums : nullptr;
+    p.d = (const float*)d, p.rows = (uint8_t*)c.d_rows, p.add = c.add, p.grads = grads, p.part = c.d_x != nullptr ? sums : nullptr;
     e = direct_tiles(t.V, c.n, DT) ? launch_direct<DT, X_DLOGIT32>(logits, stream)
                                    : launch_by_rows<DT, false, X_DLOGIT32>(logits, stream);
     if (e != hipSuccess) return e;

@@ -566,8 +566,8 @@ int32_t etg_cross_entropy(const etg_table* lm_head, const void* d_residual, int6
  *   table_grad[v]    = sum_b D[b][v] residual[b]   (+ table_grad[v] with accumulate)
  * The logits are computed again, by pieces of the vocabulary.  D is rounded once to the
  * table's dtype (f16: times a power of two that keeps it in range), the sums are f32, each
- * result is rounded once.  A row with g_b + h_b = 0 and g_b = 0 has D = 0 whatever its logits
- * are (its residual still enters table_grad as 0 * residual).
+ * result is rounded once.  A row with g_b = 0 and h_b = 0 (padding, for instance) has D = 0 and
+ * adds nothing to table_grad, whatever it holds: a NaN or an infinity in it goes nowhere.
  *   d_lse               f32 [batch], as etg_cross_entropy wrote it
  *   grad_loss           g for all rows, or d_grad_loss f32 [batch] where that is not NULL
  *   d_grad_lse          NULLABLE f32 [batch]: h (NULL: 0)

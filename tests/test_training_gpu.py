@@ -450,3 +450,151 @@ def test_captured_graph_replays():
             torch.cuda.synchronize()
             for a, b in zip(want, list(outs[name]) + [dE]):
                 assert torch.equal(a, b), (rep, name)
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("n,V", [(3, 300), (8, 5000), (40, 700), (100, 2000), (150, 513), (600, 1100)])
+def test_padding_may_hold_anything(dtype, n, V):
+    # rows without a target, or whose gradient is 0, hold NaN and infinities: as if they were 0
+    note(f"padding {dtype} {n} x {V}")
+    d = 72
+    t, E, x, labels = make(n, V, d, TYPES[dtype], seed=51)
+    g = upstream(n, 3)[0]
+    dead = torch.arange(n, device="cuda") % 3 == 1
+    labels[dead] = -100
+    labels[0], g[0], dead[0] = 1, 0.0, True
+    clean = torch.where(dead[:, None], torch.zeros_like(x), x)
+    bad = x.clone()
+    bad[dead] = torch.tensor([float("nan"), float("inf"), float("-inf")], device="cuda").repeat(24).to(x.dtype)
+    want_loss, want_lse = t.cross_entropy(clean, labels)
+    loss, lse = t.cross_entropy(bad, labels)
+    want = t.cross_entropy_grad(clean, labels, want_lse, g)
+    got = t.cross_entropy_grad(bad, labels, lse, g)
+    only_x, _ = t.cross_entropy_grad(bad, labels, lse, g, table_grad=False)
+    torch.cuda.synchronize()
+    live = ~dead
+    assert torch.equal(loss[live], want_loss[live]) and torch.equal(lse[live], want_lse[live])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(only_x, want[0])
+    assert not got[0][dead].any()
+
+
+# more tiles than CUs in each product, odd numbers of stages; many labels in one tile
+@pytest.mark.parametrize("dtype,n,V,d", [("bf16", 700, 40001, 520), ("f16", 700, 40001, 520), ("f32", 600, 24003, 524),
+                                         ("bf16", 128, 40001, 264), ("f16", 65, 30000, 264), ("bf16", 100, 20011, 328),
+                                         ("bf16", 8, 150001, 64), ("f16", 8, 300003, 64), ("f32", 8, 20001, 1000)])
+def test_more_tiles_than_units(dtype, n, V, d):
+    note(f"many tiles {dtype} {n} x {V} x {d}")
+    t, E, x, labels = make(n, V, d, TYPES[dtype], seed=52)
+    labels[n // 2:] = torch.where(labels[n // 2:] % 2 == 0, 17, labels[n // 2:])  # one token many times
+    g, h = upstream(n, 8)
+    loss, lse = t.cross_entropy(x, labels)
+    old = (torch.randn((V, d), generator=torch.Generator().manual_seed(2)) * 0.01).to(x.dtype).cuda()
+    out = old.clone()
+    dx, dE = t.cross_entropy_grad(x, labels, lse, g, h)
+    t.cross_entropy_grad(x, labels, lse, g, h, out_table=out, accumulate=True)
+    torch.cuda.synchronize()
+    want, want_lse, tol, tol_lse = to.loss(x, E, labels)
+    # tiles in turn over 64 lanes: fewer than 100 additions in a row
+    to.check(lse, want_lse, tol_lse, "lse")
+    to.check(loss, want, tol, "loss")
+    wx, wE, tx, tE = to.grads(x, E, labels, lse, g, h)
+    to.check(dx, wx, tx, "residual gradient")
+    to.check(dE, wE, tE, "table gradient")
+    _, wE, _, tE = to.grads(x, E, labels, lse, g, h, old)
+    to.check(out, wE, tE, "table gradient, added")
+
+
+@pytest.mark.parametrize("n", [3, 70, 260])
+def test_table_past_4_gib(n):
+    # 4.5 GB of bf16 rows; labels and ids at both ends
+    V, d = 420001, 5376
+    note(f"4.5 GB table, {n} rows")
+    gen = torch.Generator(device="cuda").manual_seed(61)
+    E = (torch.randn((V, d), generator=gen, device="cuda", dtype=torch.bfloat16) * 0.02)
+    x = torch.randn((n, d), generator=gen, device="cuda", dtype=torch.bfloat16)
+    labels = torch.randint(V, (n,), generator=gen, device="cuda").to(torch.int32)
+    labels[0], labels[1], labels[2] = V - 1, 0, V - 300
+    g, h = upstream(n, 9)
+    t = etg.Table(E, etg.BF16, V, d)
+    loss, lse = t.cross_entropy(x, labels)
+    dx, dE = t.cross_entropy_grad(x, labels, lse, g, h)
+    torch.cuda.synchronize()
+    want, want_lse, tol, tol_lse = to.loss(x, E, labels)
+    # 1,641 tiles in turn over 64 lanes: 26 additions and six exchanges
+    to.check(lse, want_lse, tol_lse, "lse")
+    to.check(loss, want, tol, "loss")
+    del want, want_lse, tol, tol_lse
+    note("  gradients")
+    wx, _, tx, _ = to.grads(x, E, labels, lse, g, h) if n == 3 else (None,) * 4
+    if wx is not None:
+        to.check(dx, wx, tx, "residual gradient")
+    del wx, tx
+    # the table's gradient at rows near the start, the 4 GiB border and the end, and at the labels
+    some = torch.cat([torch.arange(70), torch.arange(399400, 399500), torch.arange(V - 320, V),
+                      labels.long().cpu()]).unique().cuda()
+    ok = torch.isin(some, labels.long())
+    assert ok.sum() >= 3
+    L = x.double() @ E[some].double().t().contiguous()
+    hot = (labels.long()[:, None] == some[None, :]).double()
+    # as the oracle's gradients: the product with D, its rounding to 8 bits and the logits' error
+    cp = torch.exp(L - lse.double()[:, None]) * (g + h).double()[:, None]
+    D = cp - hot * g.double()[:, None]
+    dL = d * 2.0 ** -22 * (x.double().abs() @ E[some].double().abs().t().contiguous())
+    dD = cp.abs() * (torch.expm1(dL) + 4e-6) + 2.0 ** -23 * (cp.abs() + hot * g.double().abs()[:, None])
+    dD = dD + D.abs() * 2.0 ** -8 + to.SUBNORMAL[torch.bfloat16] / 2
+    want = D.t().contiguous() @ x.double()
+    e = dD.t().contiguous() @ x.double().abs() + (n + 1) * 2.0 ** -22 * ((D.abs() + dD).t().contiguous() @ x.double().abs())
+    to.check(dE[some], want, e + to.rounding(want, torch.bfloat16) + e * 2.0 ** -7, "table gradient")
+    note("  gather's gradient")
+    ids = torch.cat([labels, labels, torch.tensor([-1, V], dtype=torch.int32, device="cuda")])
+    grad = torch.randn((len(ids), d), generator=gen, device="cuda", dtype=torch.bfloat16)
+    t.embed_gather_grad(grad, ids, scale=3.0, out=dE)
+    torch.cuda.synchronize()
+    want, tol = to.gather_grad(grad[:, :], torch.searchsorted(some, ids.long()).where((ids >= 0) & (ids < V), -1).to(torch.int32),
+                               len(some), 3.0, torch.bfloat16)
+    to.check(dE[some], want, tol, "gather's gradient")
+    assert int((dE != 0).any(1).sum()) == int(labels.unique().numel())
+
+
+@pytest.mark.parametrize("n,V,d", [(70001, 3000, 32), (140000, 200000, 16), (70000, 20, 1032)])
+def test_gather_grad_of_many_ids(n, V, d):
+    note(f"{n} ids into {V} x {d}")
+    gen = torch.Generator(device="cuda").manual_seed(71)
+    t = etg.Table(torch.zeros((V, d), dtype=torch.bfloat16, device="cuda"), etg.BF16, V, d)
+    ids = torch.randint(-2, V + 2, (n,), generator=gen, device="cuda").to(torch.int32)
+    grad = torch.randn((n, d), generator=gen, device="cuda", dtype=torch.bfloat16)
+    old = torch.randn((V, d), generator=gen, device="cuda")
+    got, added = t.embed_gather_grad(grad, ids, out_dtype=etg.F32), old.clone()
+    t.embed_gather_grad(grad, ids, out=added, accumulate=True)
+    torch.cuda.synchronize()
+    to.check(got, *to.gather_grad(grad, ids, V, 1.0, torch.float32), "rows")
+    to.check(added, *to.gather_grad(grad, ids, V, 1.0, torch.float32, old), "rows, added")
+
+
+def test_two_graphs_share_a_workspace():
+    # replayed one after the other on a stream: each leaves what it leaves when run alone
+    n, V, d = 150, 3000, 136
+    t, E, x, labels = make(n, V, d, torch.bfloat16, seed=81)
+    g = upstream(n, 2)[0]
+    _, lse = t.cross_entropy(x, labels)
+    _, lse2 = t.cross_entropy(x[:20], labels[:20])
+    L = etg.lib()
+    need = max(L.etg_cross_entropy_grad_workspace(t._h, n), L.etg_cross_entropy_grad_workspace(t._h, 20))
+    space = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want = [v.clone() for v in t.cross_entropy_grad(x, labels, lse, g) + t.cross_entropy_grad(x[:20], labels[:20], lse2, 0.5)]
+    side = torch.cuda.Stream()
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graphs[0], stream=side):
+        outs += t.cross_entropy_grad(x, labels, lse, g, workspace=space)
+    with torch.cuda.graph(graphs[1], stream=side):
+        outs += t.cross_entropy_grad(x[:20], labels[:20], lse2, 0.5, workspace=space)
+    for rep in range(3):
+        space.fill_(255)
+        for v in outs:
+            v.fill_(7)
+        graphs[rep % 2].replay()
+        graphs[1 - rep % 2].replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, outs):
+            assert torch.equal(a, b), rep
