@@ -20,15 +20,15 @@ python3 "$REPO/embedding_table_gather_amd/build.py"
 
 # host translation units with the sanitizers; the rest as built above
 CSRC="$REPO/embedding_table_gather_amd/csrc"
-for f in etg_api i8_sample_api step; do
+for f in etg_api i8_sample_api train_api step; do
   /opt/rocm/bin/hipcc -O1 -fPIC -std=c++17 -Xarch_host -fsanitize=address -Xarch_host -fsanitize=undefined \
     -Xarch_host -fno-sanitize-recover=undefined -Xarch_host -fno-omit-frame-pointer -g \
     -c "$CSRC/$f.cpp" -o "$OUT/$f.o"
 done
 objs=""
-for f in gather logits stream wide gemm rank q8 row probe quant imatmul sample noalloc; do objs="$objs $REPO/embedding_table_gather_amd/_build/$f.o"; done
+for f in gather logits stream wide gemm rank q8 row probe quant imatmul sample xent rowgrad noalloc; do objs="$objs $REPO/embedding_table_gather_amd/_build/$f.o"; done
 /opt/rocm/bin/hipcc --offload-arch=gfx950 -shared -fPIC -Xarch_host -fsanitize=address -Xarch_host -fsanitize=undefined \
-  -shared-libsan -o "$OUT/libetg_san.so" "$OUT/etg_api.o" "$OUT/i8_sample_api.o" "$OUT/step.o" $objs
+  -shared-libsan -o "$OUT/libetg_san.so" "$OUT/etg_api.o" "$OUT/i8_sample_api.o" "$OUT/train_api.o" "$OUT/step.o" $objs
 
 RT="$("$LLVM/bin/clang" -print-file-name=libclang_rt.asan-x86_64.so)"
 cd "$REPO"
