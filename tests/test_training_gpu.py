@@ -598,3 +598,29 @@ def test_two_graphs_share_a_workspace():
         torch.cuda.synchronize()
         for a, b in zip(want, outs):
             assert torch.equal(a, b), rep
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n,V,d", [(20, 300, 64), (70, 2000, 136), (128, 700, 72), (200, 3001, 264), (700, 300, 128),
+                                   (5000, 600, 64)])
+def test_label_entries_keep_what_rounding_takes(dtype, n, V, d):
+    # D is rounded to 16 bits, but what that takes from a label's entry is added again, to the table's
+    # gradient up to 128 rows: the bound without that part of it (of a rest that is itself
+    # rounded: eps^2 / 4 of the entry).  Few distinct labels, many of them in one tile
+    note(f"rests {dtype} {n} x {V} x {d}")
+    t, E, x, labels = make(n, V, d, TYPES[dtype], seed=91, size=0.02)
+    labels[n // 2:] = (labels[n // 2:] & 3) * 64 + 5
+    g = upstream(n, 11)[0]
+    _, lse = t.cross_entropy(x, labels)
+    dx, dE = t.cross_entropy_grad(x, labels, lse, g)
+    torch.cuda.synchronize()
+    wx, wE, tx, tE = to.grads(x, E, labels, lse, g)
+    ok = to.has_label(labels, V)
+    at = labels[ok].long()
+    p = torch.exp((x.double() @ E.double().t().contiguous())[ok, at] - lse.double()[ok])
+    entry = (g.double()[ok] * (p - 1)).abs() * (torch.finfo(x.dtype).eps / 2 - torch.finfo(x.dtype).eps ** 2 / 4)
+    less_x, less_E = torch.zeros_like(tx), torch.zeros_like(tE)
+    less_x[ok] = entry[:, None] * E.double().abs()[at]
+    less_E.index_add_(0, at, entry[:, None] * x.double().abs()[ok])
+    to.check(dx, wx, tx - less_x, "residual gradient")
+    to.check(dE, wE, tE - less_E if n <= 128 else tE, "table gradient")
