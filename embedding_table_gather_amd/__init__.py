@@ -494,7 +494,7 @@ class Table:
         """Gradient of ``embed_gather`` with respect to the table, [vocab, hidden] in the table's
         type (or float32: out_dtype or the type of ``out``): out[v] = scale * the sum of grad's
         rows [n, hidden] (float32, bfloat16 or float16) whose id is v, added to what ``out``
-        holds with accumulate.  Bad ids add nothing.  Sums are in the positions' order, without
+        holds with accumulate.  Bad ids add nothing.  Sums are in a fixed order, without
         atomics.  scale: as in embed_gather."""
         dtype = self._float_type()
         if ids.dtype != torch.int32 or ids.device != self.device:

@@ -1,11 +1,12 @@
 // Gradient of the row gather with respect to the table:
 //   out[v][c] = [out[v][c] +] scale * sum over the positions i with ids[i] = v of grad[i][c]
-// The positions are sorted by token (stably), so that a token's gradient rows are added in
-// their order in 32 bits, without atomics: results repeat bitwise.
+// The positions are sorted by token (stably), and a token's gradient rows are added in an order
+// that depends on the sizes and their places alone, in 32 bits, without atomics: results repeat
+// bitwise.
 //
 // A wave takes a piece of consecutive sorted positions and a chunk of columns, and writes the
 // sum of each run of equal tokens that lies inside its piece.  Runs that cross a piece's
-// border leave their partial sums, which rowgrad_join_kernel adds in order.
+// border leave their partial sums, which rowgrad_join_kernel adds, sixteen at a time as a tree.
 #include <algorithm>
 
 #include "etg_device.hpp"
@@ -465,7 +466,7 @@ RowGradWs rowgrad_ws(int64_t n, int64_t V, int64_t hidden) {
 struct FillShares {
   Fill rest;
   int launches;
-  // the next launch's share, a launch with `work` workgroups of its own
+  // the next launch's share
   Fill next() {
     Fill f = rest;
     f.n16 = std::min(rest.n16, cdiv(cdiv(rest.n16, Fill::kPieces), std::max(launches, 1)) * Fill::kPieces);

@@ -501,7 +501,8 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
             if (col_of(t) < p.n && off(a0 + a) < rows)
               x[a] += load4<ODT>(row + (lane & 15) * pitch + (off(a0 + a) + 4 * g) * kValue<ODT>);
         }
-        store_rows<ODT, AH>(row + off(a0) * kValue<ODT>, pitch, x, lane, p.n - col0(t), (int)min(p.m - m0, (int64_t)256) - mrow - off(a0));
+        store_rows<ODT, AH>(row + off(a0) * kValue<ODT>, pitch, x, lane, p.n - col0(t),
+                             (int)min(p.m - m0, (int64_t)256) - mrow - off(a0));
       }
     }
   }
@@ -1276,7 +1277,8 @@ bool direct_tiles(int64_t vocab, int64_t n, int dtype) {
 template <int DT, int MODE>
 hipError_t launch_direct(XentProduct p, hipStream_t stream) {
   // D's last block is written whole
-  p.mt = (int32_t)(MODE == X_DLOGIT ? cdiv(p.m, kBlock) * (kBlock / 16) : cdiv(p.m, 16)), p.nt = (int32_t)cdiv(p.n, 16);
+  p.mt = (int32_t)(MODE == X_DLOGIT ? cdiv(p.m, kBlock) * (kBlock / 16) : cdiv(p.m, 16));
+  p.nt = (int32_t)cdiv(p.n, 16);
   hipLaunchKernelGGL((direct_kernel<DT, MODE>), dim3((unsigned)(p.mt * p.nt)), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
@@ -1411,7 +1413,8 @@ hipError_t sum_slices(const TableDesc& t, const XentCall& c, const BackwardWs& w
   // few values of many slices: 16 threads to a value's slices
   const auto kernel = w.splits >= 16 ? xent_sum_kernel<DT, 16> : xent_sum_kernel<DT, 1>;
   const int each = w.splits >= 16 ? 16 : 256;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv(quads, each)), dim3(256), 0, stream, sums, (int)w.splits, c.n, t.hidden, c.d_x, c.d_x_pitch, scale, rest, c.labels, t.V, t.rows);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)cdiv(quads, each)), dim3(256), 0, stream, sums, (int)w.splits, c.n,
+                     t.hidden, c.d_x, c.d_x_pitch, scale, rest, c.labels, t.V, t.rows);
   return hipGetLastError();
 }
 
@@ -1477,7 +1480,8 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
       p.m = t.hidden, p.n = rows, p.k = c.n;
       p.a = logits.b, p.a_pitch = logits.b_pitch, p.b = d, p.b_pitch = w.block;
       p.splits = 1, p.kslice = (int32_t)align_up((size_t)c.n, 64);
-      p.out = (uint8_t*)c.d_rows + v0 * t.row_bytes, p.add = c.add, p.scale = scale, p.labels = c.labels, p.v0 = v0, p.vocab = t.V, p.rest = rest;
+      p.out = (uint8_t*)c.d_rows + v0 * t.row_bytes, p.add = c.add, p.scale = scale;
+      p.labels = c.labels, p.v0 = v0, p.vocab = t.V, p.rest = rest;
       if (c.n <= 2 * (128 / kValue<DT>)) {
         e = launch_outer<DT>(p, stream);
       } else {

@@ -589,7 +589,7 @@ int32_t etg_cross_entropy_grad(const etg_table* lm_head, const void* d_residual,
 
 /*
  * Gradient of etg_embed_gather with respect to the table:
- *   out[v] = [out[v] +] scale * sum over the positions i with ids[i] == v, in their order, of grad[i]
+ *   out[v] = [out[v] +] scale * sum over the positions i with ids[i] == v of grad[i]
  * (sums, product and addition in f32, one rounding to the output type).  A bad id (>= vocab as
  * uint32), whose gathered row is zero, adds nothing.
  *   table        its vocab, hidden and dtype (not Q8_0) alone
@@ -604,8 +604,8 @@ int32_t etg_cross_entropy_grad(const etg_table* lm_head, const void* d_residual,
  *                change
  *   d_workspace  at least etg_embed_gather_grad_workspace() bytes, 256-byte aligned (may be NULL
  *                where that is 0)
- * The sums are formed over the positions sorted by token, without atomics: results are bitwise
- * repeatable.
+ * The sums are formed over the positions sorted by token, in a fixed order and without atomics:
+ * results are bitwise repeatable.
  * Errors: EINVAL (null), EDTYPE, ESHAPE, EALIGN, EWORKSPACE.
  */
 int64_t etg_embed_gather_grad_workspace(const etg_table* table, int64_t seq_len);
