@@ -9,8 +9,11 @@
 // of the two other products) as its result, then the piece's share of dx and its rows of dE.
 //
 // D's entry at a label, g (p - 1) + h p, is most of what a row contributes, and is near 0 where
-// p is near 1: it is computed with expm1, and what its rounding to 16 bits takes away (its
-// "rest") is added to dx, and up to 128 residual rows to dE.  Up to 8 residual rows D is f32.
+// p is near 1.  There it is about g (L - lse), and an f32 logit of 17 is off by 1e-6: a label's
+// logit is summed again, in 64 bits, for loss and lse (xent_join_kernel) and for the entry, which
+// is formed by expm1 of its distance to lse and so has f32's relative accuracy for the given lse
+// (label_entry).  What its rounding to 16 bits takes away (its "rest") is added to dx, and up to
+// 128 residual rows to dE.  Up to 8 residual rows D is f32.
 #include <algorithm>
 #include <type_traits>
 
@@ -222,7 +225,8 @@ struct XentProduct {
   // X_STATS: part [n][mt], target [n]; X_DLOGIT: D [m / 256][n][256]; X_DLOGIT32: f32 D [m][8]
   // X_PART: f32 [splits][n][m]; X_OUT: values of the type, [n][m]
   void* out;
-  float* rest;               // 16-bit types: [n], what D's rounding takes away from a label's entry
+  const float* entry;        // X_DLOGIT, X_DLOGIT32, but for direct_kernel: [n], D's entries at the labels
+  float* rest;               // 16-bit types: [n], what D's rounding takes away from them
   int32_t add;               // X_PART, X_OUT: to what is there
   const int32_t* labels;     // [n]
   int64_t v0, vocab;         // the piece's first table row
@@ -326,7 +330,7 @@ struct RowGrads {
 
 // What D's entries (and the loss: the label alone) of one residual row need.
 struct DRow {
-  float g, h, both, lse;
+  float both, lse, entry;
   int64_t label;  // the label's row in the piece; negative where there is none
   DRow() = default;
   template <int MODE>
@@ -336,19 +340,15 @@ struct DRow {
       label = (int64_t)token - p.v0;
       return;
     }
-    g = token < (uint64_t)p.vocab ? (p.grad_loss != nullptr ? p.grad_loss[n] : p.grad_loss_all) : 0.f;
-    h = p.grad_lse != nullptr ? p.grad_lse[n] : 0.f;
-    both = g + h;
+    both = token < (uint64_t)p.vocab ? (p.grad_loss != nullptr ? p.grad_loss[n] : p.grad_loss_all) : 0.f;
+    if (p.grad_lse != nullptr) both += p.grad_lse[n];
     label = token < (uint64_t)p.vocab ? (int64_t)token - p.v0 : -1;
     lse = p.lse[n];
+    entry = p.entry != nullptr ? p.entry[n] : 0.f;
   }
   // A row that nothing reaches has no gradient, whatever its logits are.
   __device__ __forceinline__ float other(float l) const {
     return both == 0.f ? 0.f : both * __builtin_amdgcn_exp2f((l - lse) * kLog2e);
-  }
-  // (g + h) p - g without the cancellation near p = 1
-  __device__ __forceinline__ float at_label(float l) const {
-    return g == 0.f && h == 0.f ? 0.f : g * expm1f(l - lse) + h * __builtin_amdgcn_exp2f((l - lse) * kLog2e);
   }
 };
 
@@ -358,8 +358,51 @@ __device__ __forceinline__ void here(DRow (&r)[N]) {
 #pragma unroll
   for (int t = 0; t < N; t++) {
     asm volatile("" : "+v"(r[t].label));
-    if constexpr (MODE != X_STATS) asm volatile("" : "+v"(r[t].g), "+v"(r[t].h), "+v"(r[t].both), "+v"(r[t].lse));
+    if constexpr (MODE != X_STATS) asm volatile("" : "+v"(r[t].both), "+v"(r[t].lse), "+v"(r[t].entry));
   }
+}
+
+// The 16 bytes' values.
+template <int DT>
+__device__ __forceinline__ void unpack(u32x4 w, float (&x)[16 / kValue<DT>]) {
+#pragma unroll
+  for (int i = 0; i < 16 / kValue<DT>; i++) {
+    if constexpr (DT == DT_F32) x[i] = __uint_as_float(w[i]);
+    else if constexpr (DT == DT_BF16) x[i] = i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    else x[i] = f16_bits_to_f32(w[i / 2] >> 16 * (i % 2) & 0xffffu);
+  }
+}
+
+// sum + a b over 16 bytes each; a product of two f32 values is exact in 64 bits
+template <int DT>
+__device__ __forceinline__ double dot64(u32x4 a, u32x4 b, double sum) {
+  float x[16 / kValue<DT>], y[16 / kValue<DT>];
+  unpack<DT>(a, x);
+  unpack<DT>(b, y);
+#pragma unroll
+  for (int i = 0; i < 16 / kValue<DT>; i++) sum = fma((double)x[i], (double)y[i], sum);
+  return sum;
+}
+
+// The logit of a residual row and a table row, in 64 bits, by one wave.
+template <int DT>
+__device__ __forceinline__ double wave_dot64(const uint8_t* x, const uint8_t* row, int64_t row_bytes, int lane) {
+  double sum = 0.;
+#pragma unroll 4
+  for (int64_t at = lane * 16; at < row_bytes; at += 1024)
+    sum = dot64<DT>(*(const u32x4*)(x + at), *(const u32x4*)(row + at), sum);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  return sum;
+}
+
+// (g + h) p - g at the label, from its logit's distance to lse: rounded once to f32, where expm1
+// keeps its relative accuracy near p = 1.  A row that nothing reaches: 0.
+__device__ __forceinline__ float label_entry(const RowGrads& grads, int64_t b, double logit, float lse) {
+  const float g = grads.grad_loss != nullptr ? grads.grad_loss[b] : grads.grad_loss_all;
+  const float h = grads.grad_lse != nullptr ? grads.grad_lse[b] : 0.f;
+  const float t = (float)(logit - (double)lse);
+  return g == 0.f && h == 0.f ? 0.f : g * expm1f(t) + h * __builtin_amdgcn_exp2f(t * kLog2e);
 }
 
 // (maximum, sum of exp relative to it) of the union of two sets; (-inf, 0) is the empty one.
@@ -451,21 +494,11 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
             d[a][i] = off(a0 + a) + i < rows ? row.other(acc[a0 + a][t][i]) * scale : 0.f;
         const bool hit = label >= off(a0) && label < off(a0) + 16 * AH;
         if (__ballot(hit) != 0) {
-          float l = 0.f;
 #pragma unroll
           for (int a = 0; a < AH; a++)
 #pragma unroll
             for (int i = 0; i < 4; i++)
-              if (off(a0 + a) + i == label) l = acc[a0 + a][t][i];
-          const float x = row.at_label(l) * scale;
-          bool here = false;
-#pragma unroll
-          for (int a = 0; a < AH; a++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-              if (off(a0 + a) + i == label) d[a][i] = x, here = true;
-          if constexpr (DT != DT_F32 && MODE == X_DLOGIT)
-            if (here) p.rest[n] = x - (float)round1<DT>(x);
+              if (off(a0 + a) + i == label) d[a][i] = row.entry;
         }
         if constexpr (MODE == X_DLOGIT32) {
 #pragma unroll
@@ -941,10 +974,22 @@ __global__ void __launch_bounds__(256) direct_kernel(XentProduct p) {
     if (some && v == (int64_t)(uint32_t)p.labels[n] - p.v0) p.target[n] = l;
     if (r == 0) ((float2*)p.out)[n * p.mt + blockIdx.x % p.mt] = make_float2(m, s);
   } else {
-    if (n >= p.n || (MODE == X_DLOGIT32 && v >= p.m)) return;
+    // past the last residual row: the last again
+    const int64_t nc = min(n, p.n - 1);
     DRow row;
-    row.load<MODE>(p, n);
-    const float x = v == row.label ? row.at_label(l) : row.other(l);
+    row.load<MODE>(p, nc);
+    float x = row.other(l);
+    const bool hit = row.label >= m0 && row.label < min(m0 + 16, p.m);
+    if (__ballot(hit) != 0) {  // a row's 16 threads sum its label's logit
+      const uint8_t* at = p.a + (hit ? row.label : (int64_t)0) * p.a_pitch;
+      const uint8_t* xr = p.b + nc * p.b_pitch;
+      double sum = 0.;
+      for (int o = 16 * r; o < bytes; o += 256) sum = dot64<DT>(*(const u32x4*)(xr + o), *(const u32x4*)(at + o), sum);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor(sum, o, 64);
+      if (v == row.label) x = label_entry({p.labels, p.vocab, p.grad_loss, p.grad_lse, p.grad_loss_all}, nc, sum, row.lse);
+    }
+    if (n >= p.n || (MODE == X_DLOGIT32 && v >= p.m)) return;
     if constexpr (MODE == X_DLOGIT32) {
       ((float*)p.out)[v * 8 + n] = x;
     } else {
@@ -970,17 +1015,6 @@ struct XentRows {
   RowGrads grads;
   float* part;                         // [slices][n][hidden], or NULL
 };
-
-// The 16 bytes' values.
-template <int DT>
-__device__ __forceinline__ void unpack(u32x4 w, float (&x)[16 / kValue<DT>]) {
-#pragma unroll
-  for (int i = 0; i < 16 / kValue<DT>; i++) {
-    if constexpr (DT == DT_F32) x[i] = __uint_as_float(w[i]);
-    else if constexpr (DT == DT_BF16) x[i] = i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
-    else x[i] = f16_bits_to_f32(w[i / 2] >> 16 * (i % 2) & 0xffffu);
-  }
-}
 
 template <int DT, int NB>
 __global__ void __launch_bounds__(256) xent_rows_kernel(XentRows p) {
@@ -1078,16 +1112,47 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(XentRows p) {
   }
 }
 
+// D's entries at the labels, in 64 bits up to the distance of a label's logit to lse, times scale[0]
+// (NULL: 1), and their rests: one wave per residual row, bound by the latency of its loads.
+template <int DT>
+__global__ void __launch_bounds__(256) xent_label_kernel(const uint8_t* __restrict__ x, int64_t x_pitch,
+                                                         const uint8_t* __restrict__ table, int64_t row_bytes,
+                                                         int64_t n, RowGrads grads, const float* __restrict__ lse,
+                                                         const float* __restrict__ scale, float* __restrict__ entry,
+                                                         float* __restrict__ rest) {
+  const int lane = threadIdx.x & 63;
+  const int64_t b = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (b >= n) return;  // whole wave
+  const uint32_t token = (uint32_t)grads.labels[b];
+  if (token >= (uint64_t)grads.vocab) return;  // no entry
+  const double sum = wave_dot64<DT>(x + b * x_pitch, table + (int64_t)token * row_bytes, row_bytes, lane);
+  if (lane != 0) return;
+  const float d = label_entry(grads, b, sum, lse[b]) * (scale != nullptr ? scale[0] : 1.f);
+  entry[b] = d;
+  if (DT != DT_F32 && rest != nullptr) rest[b] = d - (float)round1<DT>(d);
+}
+
 // Joins a piece's statistics [n][mt] into run [n]; the last piece writes lse and loss.  One
 // wave per residual row.
+//
+// The statistics hold the label's logit as the product left it, off by c.  With that logit in 64
+// bits, exp(lse) grows by p (exp(c) - 1) of itself, and the loss is the distance to the logit that
+// the gradients take: where p is near 1, neither error is left in lse - logit.
+template <int DT>
 __global__ void __launch_bounds__(256) xent_join_kernel(const float2* __restrict__ part, int mt, int64_t n, bool first,
                                                         bool last, float2* __restrict__ run,
                                                         const float* __restrict__ target,
                                                         const int32_t* __restrict__ labels, int64_t vocab,
+                                                        const uint8_t* __restrict__ x, int64_t x_pitch,
+                                                        const uint8_t* __restrict__ table, int64_t row_bytes,
                                                         float* __restrict__ loss, float* __restrict__ lse) {
   const int lane = threadIdx.x & 63;
-  const int64_t b = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t b = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (b >= n) return;  // whole wave
+  const uint32_t token = (uint32_t)labels[b];
+  const bool has = token < (uint64_t)vocab;
+  double logit = 0.;
+  if (last && has) logit = wave_dot64<DT>(x + b * x_pitch, table + (int64_t)token * row_bytes, row_bytes, lane);
   float2 r = make_float2(-__builtin_inff(), 0.f);
   for (int i = lane; i < mt; i += 64) r = stats_join(r, part[b * mt + i]);
 #pragma unroll
@@ -1100,9 +1165,15 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2* __restrict
     return;
   }
   // ln s in 64 bits: one rounding of the sum of both terms
-  const float total = (float)((double)r.x + log((double)r.y));
-  lse[b] = total;
-  loss[b] = (uint32_t)labels[b] < (uint64_t)vocab ? (float)((double)r.x - (double)target[b] + log((double)r.y)) : 0.f;
+  const double s = log((double)r.y);
+  double more = 0., at = has ? (double)target[b] : 0.;
+  if (has && __builtin_isfinite(target[b])) {  // (an infinite or NaN logit stays what it is)
+    const float p = expf((float)(at - (double)r.x - s));
+    more = log1pf(fmaxf(p * expm1f((float)(logit - at)), -0.99999994f));
+    at = logit;
+  }
+  lse[b] = (float)((double)r.x + s + more);
+  loss[b] = has ? (float)((double)r.x - at + s + more) : 0.f;
 }
 
 // scale[0] = 2^e with the largest |g| + |h| times it in [2^13, 2^14), scale[1] = 2^-e: D in f16
@@ -1322,7 +1393,7 @@ struct BackwardWs {
   int64_t piece, splits, slice;
   int chunks;
   int64_t block;  // bytes of a block of D
-  size_t rest, x, d, sums, bytes;
+  size_t rest, entry, x, d, sums, bytes;
 };
 // K slices of dx = D E, at least 256 table rows each.
 int64_t backward_splits(int64_t piece, int64_t n, int64_t hidden, int size) {
@@ -1355,7 +1426,8 @@ BackwardWs backward_ws(const TableDesc& t, int64_t n) {
     d_bytes = (size_t)(n * w.piece * size);
   }
   w.rest = 256;  // after the two factors
-  w.x = w.rest + align_up((size_t)n * 4, 256);
+  w.entry = w.rest + align_up((size_t)n * 4, 256);
+  w.x = w.entry + align_up((size_t)n * 4, 256);
   w.d = w.x + align_up((size_t)(n * t.row_bytes), 256);
   w.sums = w.d + align_up(d_bytes, 256);
   w.bytes = w.sums + align_up((size_t)(w.splits * n * t.hidden * 4), 256);
@@ -1392,8 +1464,9 @@ hipError_t forward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStream
     e = w.direct ? launch_direct<DT, X_STATS>(p, stream) : launch_by_rows<DT, false, X_STATS>(p, stream);
     if (e != hipSuccess) return e;
     const int mt = (int)(w.direct ? w.mt : cdiv(p.m, 256));
-    hipLaunchKernelGGL(xent_join_kernel, dim3((unsigned)cdiv(c.n, 4)), dim3(256), 0, stream, part, mt, c.n, v0 == 0,
-                       v0 + piece >= t.V, run, target, c.labels, t.V, c.loss, c.lse_out);
+    hipLaunchKernelGGL(xent_join_kernel<DT>, dim3((unsigned)cdiv(c.n, 4)), dim3(256), 0, stream, part, mt, c.n,
+                       v0 == 0, v0 + piece >= t.V, run, target, c.labels, t.V, p.b, p.b_pitch, t.rows, t.row_bytes,
+                       c.loss, c.lse_out);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;
@@ -1419,13 +1492,21 @@ hipError_t sum_slices(const TableDesc& t, const XentCall& c, const BackwardWs& w
 }
 
 template <int DT>
+hipError_t launch_labels(const TableDesc& t, const XentProduct& logits, const RowGrads& grads, float* entry,
+                         hipStream_t stream) {
+  hipLaunchKernelGGL(xent_label_kernel<DT>, dim3((unsigned)cdiv(logits.n, 4)), dim3(256), 0, stream, logits.b,
+                     logits.b_pitch, t.rows, t.row_bytes, logits.n, grads, logits.lse, logits.scale, entry, logits.rest);
+  return hipGetLastError();
+}
+
+template <int DT>
 hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStream_t stream) {
   if (c.n == 0)  // a sum of nothing
     return c.d_rows == nullptr || c.add ? hipSuccess : launch_write_probe(c.d_rows, t.V * t.row_bytes, 0, stream);
   const BackwardWs w = backward_ws(t, c.n);
   hipError_t e;
   uint8_t *packed = ws + w.x, *d = ws + w.d;
-  float* sums = (float*)(ws + w.sums);
+  float *sums = (float*)(ws + w.sums), *entry = (float*)(ws + w.entry);
   const RowGrads grads = {c.labels, t.V, c.grad_loss, c.grad_lse, c.grad_loss_all};
   // the products of dE take a copy without the rows that nothing reaches
   const bool direct = rows_direct(c.x, c.x_pitch) && (vector_rows(t, c.n) || c.d_rows == nullptr);
@@ -1443,7 +1524,10 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
     p.x = logits.b, p.row_bytes = t.row_bytes, p.x_pitch = logits.b_pitch, p.per = w.slice;
     p.hidden = (int)t.hidden, p.n = (int)c.n, p.chunks = w.chunks, p.slices = (int)w.splits;
     p.d = (const float*)d, p.rows = (uint8_t*)c.d_rows, p.add = c.add, p.grads = grads, p.part = c.d_x != nullptr ? sums : nullptr;
-    e = direct_tiles(t.V, c.n, DT) ? launch_direct<DT, X_DLOGIT32>(logits, stream)
+    const bool small = direct_tiles(t.V, c.n, DT);
+    logits.entry = entry;
+    if (!small && (e = launch_labels<DT>(t, logits, grads, entry, stream)) != hipSuccess) return e;
+    e = small ? launch_direct<DT, X_DLOGIT32>(logits, stream)
                                    : launch_by_rows<DT, false, X_DLOGIT32>(logits, stream);
     if (e != hipSuccess) return e;
     e = c.n <= 2   ? launch_rows<DT, 2>(p, stream)
@@ -1461,6 +1545,10 @@ hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStrea
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   logits.scale = scale, logits.rest = rest;
+  if (!direct_tiles(std::min(w.piece, t.V), c.n, DT)) {  // (a last, shorter piece may be)
+    logits.entry = entry;
+    if ((e = launch_labels<DT>(t, logits, grads, entry, stream)) != hipSuccess) return e;
+  }
   for (int64_t v0 = 0; v0 < t.V; v0 += w.piece) {
     const int64_t rows = std::min(w.piece, t.V - v0);
     logits.a = t.rows + v0 * t.row_bytes, logits.m = rows, logits.v0 = v0;

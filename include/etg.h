@@ -546,10 +546,12 @@ int32_t etg_sample(const void* d_logits, int32_t dtype, int64_t batch, int64_t v
  *   d_loss, d_lse    f32 [batch]
  *   d_workspace      at least etg_cross_entropy_workspace() bytes, 256-byte aligned (may be
  *                    NULL where that is 0)
- * Accuracy: |lse - exact| <= max_v of the logits' error (f32 accumulation of hidden
- * products) + about 1e-6 * max(1, |lse|); the loss twice that.  A NaN among a row's logits,
- * or +inf, makes its lse and loss NaN; logits of -inf weigh nothing.  Results are bitwise
- * repeatable.
+ * Accuracy: the label's logit is summed in 64 bits, so with p its probability
+ * |lse - exact| <= (1 - p) max_v of the other logits' error (f32 accumulation of hidden
+ * products) + 2^-24 |lse| + e, where e < 1e-5 up to 2^18 table rows covers exponentials and f32
+ * sums (31 * 2^-23 and the longest chain of additions, 64 + vocab / 16384 of 2^-24 each); the
+ * loss as that with its own rounding.  A NaN among a row's logits, or +inf, makes its lse and
+ * loss NaN; logits of -inf weigh nothing.  Results are bitwise repeatable.
  * Errors: EINVAL (null), EDTYPE (a Q8_0 table), ESHAPE, EALIGN, EWORKSPACE.
  */
 int64_t etg_cross_entropy_workspace(const etg_table* lm_head, int64_t batch);
@@ -566,7 +568,9 @@ int32_t etg_cross_entropy(const etg_table* lm_head, const void* d_residual, int6
  *   table_grad[v]    = sum_b D[b][v] residual[b]   (+ table_grad[v] with accumulate)
  * The logits are computed again, by pieces of the vocabulary.  D is rounded once to the
  * table's dtype (f16: times a power of two that keeps it in range), the sums are f32, each
- * result is rounded once.  A row with g_b = 0 and h_b = 0 (padding, for instance) has D = 0 and
+ * result is rounded once.  At a label, D is g expm1(t) + h exp(t) with t = L - lse in 64 bits:
+ * within 2^-21 of these terms for the given lse, also where the probability is near 1.  (lse itself
+ * is rounded to f32: where 1 - p is 1e-4, an lse of 17 is off by up to 1% of that.)  A row with g_b = 0 and h_b = 0 (padding, for instance) has D = 0 and
  * adds nothing to table_grad, whatever it holds: a NaN or an infinity in it goes nowhere.
  *   d_lse               f32 [batch], as etg_cross_entropy wrote it
  *   grad_loss           g for all rows, or d_grad_loss f32 [batch] where that is not NULL
