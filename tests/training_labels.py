@@ -99,10 +99,10 @@ def entries(E, x, labels, lse, g, h=None):
 
 
 def half_step(v, dtype):
-    """Half the distance of the type's values at v."""
+    """Half the distance of the type's values at v (powers of two by frexp: a device's exp2 may round)."""
     smallest = {torch.float32: -126, torch.bfloat16: -126, torch.float16: -14}[dtype]
-    e = torch.floor(torch.log2(v.abs().clamp(min=2.0 ** smallest)))
-    return torch.exp2(e) * (EPS[dtype] / 2)
+    v = v.abs().clamp(min=2.0 ** smallest)
+    return v / torch.frexp(v).mantissa * (EPS[dtype] / 4)
 
 
 def shown(E, x, labels, Y, entry, e_entry, rest_in_table):
