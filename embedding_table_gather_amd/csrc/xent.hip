@@ -27,6 +27,8 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kXWaves = 8;
@@ -187,29 +189,62 @@ struct Operand {
   }
   // Fragment of rows [row, row + 16) (row a multiple of 16) and K half kk of the stage at img.
   static __device__ __forceinline__ u32x4 read(const unsigned char* img, int row, int kk, int lane) {
+    const uint32_t at = (uint32_t)(uintptr_t)(const lds_u32*)img;
+    return TR ? read_at(at + lane_at(row & 127, 0, lane), (row >> 7) * 16384 + kk * HALF)
+              : read_at(at + lane_at(0, kk, lane), row * 128);
+  }
+  // Where the lane's values of rows [row, row + 16) begin in an image, by K half (TR: the second half
+  // lies HALF bytes on, and row < 128; else row r lies 128 r bytes on).
+  static constexpr int HALF = 64 / ES * LINE;
+  static __device__ __forceinline__ uint32_t lane_at(int row, int kk, int lane) {
     const int g = lane >> 4;
     if constexpr (!TR) {
-      return *(const u32x4*)(img + row * 128 + (lane & 15) * 128 + 16 * ((4 * kk + g) ^ ((lane >> 1) & 7)));
+      return row * 128 + (lane & 15) * 128 + 16 * ((4 * kk + g) ^ ((lane >> 1) & 7));
     } else if constexpr (ES == 2) {
       // ds_read_b64_tr_b16: 16 lanes read a 4 x 16 block, lane i K value i / 4 of it and rows
       // 4 (i % 4) .. + 3, and receive row i's four K values
-      const unsigned char* blk = img + (row >> 7) * 16384;
       const int kl = 8 * g + ((lane & 15) >> 2);
-      const int piece = (((row & 127) >> 3) + ((lane & 3) >> 1)) ^ swizzle(kl);
-      const unsigned char* at = blk + (32 * kk + kl) * LINE + 16 * piece + 8 * (lane & 1);
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * LINE));
+      return kl * LINE + 16 * (((row >> 3) + ((lane & 3) >> 1)) ^ swizzle(kl)) + 8 * (lane & 1);
+    } else {
+      const int col = row + (lane & 15);
+      return 4 * g * LINE + 16 * ((col >> 2) ^ swizzle(4 * g)) + 4 * (col & 3);
+    }
+  }
+  // The fragment that begins `more` (a constant) bytes behind a lane_at of the LDS address of an image.
+  static __device__ __forceinline__ u32x4 read_at(uint32_t at, int more) {
+    at += (uint32_t)more;
+    if constexpr (!TR) {
+      return *(const lds_u32x4*)(uintptr_t)at;
+    } else if constexpr (ES == 2) {
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)at);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(at + 4 * LINE));
       const uint2 l2 = __builtin_bit_cast(uint2, lo), h2 = __builtin_bit_cast(uint2, hi);
       return u32x4{l2.x, l2.y, h2.x, h2.y};
     } else {
-      const unsigned char* blk = img + (row >> 7) * 16384;
-      const int col = (row & 127) + (lane & 15);
-      const unsigned char* at = blk + (16 * kk + 4 * g) * LINE + 16 * ((col >> 2) ^ swizzle(4 * g)) + 4 * (col & 3);
       u32x4 v;
 #pragma unroll
-      for (int i = 0; i < 4; i++) v[i] = *(const uint32_t*)(at + i * LINE);
+      for (int i = 0; i < 4; i++) v[i] = *(const lds_u32*)(uintptr_t)(at + i * LINE);
       return v;
     }
+  }
+};
+
+// The lane_at of T neighbouring tiles of 16 rows from `row`, in as many registers as it takes: left to
+// itself the compiler keeps one for nearly every fragment of both images, and spilled in f32.  (In 16
+// bits, too, the products gain: 1,024 x 262,144 x 5,120 bf16 statistics 2,056 us, 1,969 so.  f32 is bound
+// elsewhere: 2,000 x 30,000 x 1,024 dx 2,026 us with 26 spilled registers, 2,077 so, dE 2,044 and 2,035.)
+template <typename Op, bool TR, int T>
+struct LaneAt {
+  uint32_t at[TR ? T : 2];
+  __device__ __forceinline__ LaneAt(uint32_t lds, int row, int lane) {
+#pragma unroll
+    for (int i = 0; i < (TR ? T : 2); i++) {
+      at[i] = lds + (TR ? Op::lane_at(row + 16 * i, 0, lane) : Op::lane_at(row, i, lane));
+      asm volatile("" : "+v"(at[i]));
+    }
+  }
+  __device__ __forceinline__ u32x4 read(int tile, int kk, int more) const {
+    return TR ? Op::read_at(at[tile], more + kk * Op::HALF) : Op::read_at(at[kk], more + tile * 16 * 128);
   }
 };
 
@@ -653,7 +688,8 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
   constexpr int IMG = A::BYTES + B::BYTES;
   // what finish stores in a whole tile, for each wave
   constexpr int STORES = MODE == X_STATS || MODE == X_DLOGIT ? 0 : DT == DT_F32 || MODE == X_PART ? 32 : 16;
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // [2][IMG], then what finish needs
+  // A's two images, B's two (64 KiB either: a lane's address and immediate offsets), then what finish needs
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wv / 4, wn = wv % 4;
   const int xcd = (int)blockIdx.x % 8, step = (int)gridDim.x / 8;
@@ -678,27 +714,28 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
   const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem;
   // half h of the stage, to image img
   auto copy_a = [&](int img, int h) {
-    oa.copy(2 * h, wv, lds + (uint32_t)img * IMG);
-    oa.copy(2 * h + 1, wv, lds + (uint32_t)img * IMG);
+    oa.copy(2 * h, wv, lds + (uint32_t)img * A::BYTES);
+    oa.copy(2 * h + 1, wv, lds + (uint32_t)img * A::BYTES);
   };
   auto copy_b = [&](int img, int h) {
-    ob.copy(2 * h, wv, lds + (uint32_t)img * IMG + A::BYTES);
-    ob.copy(2 * h + 1, wv, lds + (uint32_t)img * IMG + A::BYTES);
+    ob.copy(2 * h, wv, lds + 2 * A::BYTES + (uint32_t)img * B::BYTES);
+    ob.copy(2 * h + 1, wv, lds + 2 * A::BYTES + (uint32_t)img * B::BYTES);
   };
   f32x4 acc[8][4];
   u32x4 fa[4][2], fb[2][2][2];
+  const LaneAt<A, TA, 4> la(lds, 64 * wm, lane);
+  const LaneAt<B, TB, 2> lb(lds + 2 * A::BYTES, 32 * wn, lane);
   auto read_a = [&](int img, int h) {
 #pragma unroll
     for (int a = 0; a < 4; a++)
 #pragma unroll
-      for (int kk = 0; kk < 2; kk++) fa[a][kk] = A::read(smem + img * IMG, 128 * h + 64 * wm + 16 * a, kk, lane);
+      for (int kk = 0; kk < 2; kk++) fa[a][kk] = la.read(a, kk, img * A::BYTES + 16384 * h);
   };
   auto read_b = [&](int img, int h) {
 #pragma unroll
     for (int t = 0; t < 2; t++)
 #pragma unroll
-      for (int kk = 0; kk < 2; kk++)
-        fb[h][t][kk] = B::read(smem + img * IMG + A::BYTES, 128 * h + 32 * wn + 16 * t, kk, lane);
+      for (int kk = 0; kk < 2; kk++) fb[h][t][kk] = lb.read(t, kk, img * B::BYTES + 16384 * h);
   };
   // behind: the six steps after a tile's end, in which its stores are newer than the copies that
   // are waited for
@@ -717,6 +754,12 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
         for (int t = 0; t < 2; t++)
           acc[4 * ha + a][2 * hb + t] = mma<DT>(fa[a][kk], fb[hb][t][kk], acc[4 * ha + a][2 * hb + t]);
     __builtin_amdgcn_s_setprio(0);
+    if constexpr (DT == DT_F32) {  // keeps the accumulators where they are: moved about, some spill
+#pragma unroll
+      for (int a = 0; a < 4; a++)
+#pragma unroll
+        for (int t = 0; t < 2; t++) asm volatile("" : "+v"(acc[4 * ha + a][2 * hb + t]));
+    }
     __builtin_amdgcn_sched_barrier(0);
     bare_barrier();
     __builtin_amdgcn_sched_barrier(0);
