@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -425,7 +426,15 @@ class Table:
                       out_lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
         """(loss, lse) float32 [B] of residual rows [B, hidden] of the table's type against int32
         labels [B]: lse = ln sum_v exp(residual @ table.T), loss = lse - the label's logit, 0
-        where the label is not in [0, vocab).  The logits are never in memory."""
+        where the label is not in [0, vocab).  The logits are never in memory.
+
+        Nothing is recorded for autograd: the caller's backward pass calls ``cross_entropy_grad``,
+        in a torch.autograd.Function for instance (whose forward runs without gradients).  A
+        residual that requires grad where they are recorded gets a warning.  The outputs must not
+        overlap each other or the inputs."""
+        if residual.requires_grad and torch.is_grad_enabled():
+            warnings.warn("residual requires grad, but cross_entropy records nothing for autograd: its gradient is "
+                          "what cross_entropy_grad gives", stacklevel=2)
         stride, batch = self._train_rows(residual, labels)
         dev = self.device
         loss = torch.empty(batch, dtype=torch.float32, device=dev) if out_loss is None \
@@ -448,7 +457,8 @@ class Table:
         lse: as cross_entropy gave it.  grad_loss: the gradient of each loss, a number or a
         float32 tensor [B]; grad_lse: that of each lse, a float32 tensor [B] or None.
         accumulate: add the table's gradient to ``out_table``.  The logits are computed again,
-        by pieces of the vocabulary.
+        by pieces of the vocabulary.  The outputs must not overlap each other or the inputs (the
+        table's rows among them).
         """
         stride, batch = self._train_rows(residual, labels)
         dev, dtype = self.device, residual.dtype
@@ -495,7 +505,8 @@ class Table:
         type (or float32: out_dtype or the type of ``out``): out[v] = scale * the sum of grad's
         rows [n, hidden] (float32, bfloat16 or float16) whose id is v, added to what ``out``
         holds with accumulate.  Bad ids add nothing.  Sums are in a fixed order, without
-        atomics.  scale: as in embed_gather."""
+        atomics.  scale: as in embed_gather.  ``out`` must not overlap grad or ids (it is written
+        while they are read); the table itself is not read."""
         dtype = self._float_type()
         if ids.dtype != torch.int32 or ids.device != self.device:
             raise ValueError("ids must be an int32 tensor on the table's device")
