@@ -13,7 +13,7 @@
 // logit is summed again, in 64 bits, for loss and lse (xent_join_kernel) and for the entry, which
 // is formed by expm1 of its distance to lse and so has f32's relative accuracy for the given lse
 // (label_entry).  What its rounding to 16 bits takes away (its "rest") is added to dx, and up to
-// 128 residual rows to dE.  Up to 8 residual rows D is f32.
+// 128 residual rows to dE.  Up to 8 residual rows of small tables D is f32 (vector_rows).
 #include <algorithm>
 #include <type_traits>
 

@@ -546,6 +546,7 @@ int32_t etg_sample(const void* d_logits, int32_t dtype, int64_t batch, int64_t v
  *   d_loss, d_lse    f32 [batch]
  *   d_workspace      at least etg_cross_entropy_workspace() bytes, 256-byte aligned (may be
  *                    NULL where that is 0)
+ * Loss, lse and workspace must not overlap one another or what is read.
  * Accuracy: the label's logit is summed in 64 bits, so with p its probability
  * |lse - exact| <= (1 - p) max_v of the other logits' error (f32 accumulation of hidden
  * products) + 2^-24 |lse| + e, where e < 1e-5 up to 2^18 table rows covers exponentials and f32
@@ -567,11 +568,18 @@ int32_t etg_cross_entropy(const etg_table* lm_head, const void* d_residual, int6
  *   residual_grad[b] = sum_v D[b][v] row v
  *   table_grad[v]    = sum_b D[b][v] residual[b]   (+ table_grad[v] with accumulate)
  * The logits are computed again, by pieces of the vocabulary.  D is rounded once to the
- * table's dtype (f16: times a power of two that keeps it in range), the sums are f32, each
- * result is rounded once.  At a label, D is g expm1(t) + h exp(t) with t = L - lse in 64 bits:
- * within 2^-21 of these terms for the given lse, also where the probability is near 1.  (lse itself
- * is rounded to f32: where 1 - p is 1e-4, an lse of 17 is off by up to 1% of that.)  A row with g_b = 0 and h_b = 0 (padding, for instance) has D = 0 and
- * adds nothing to table_grad, whatever it holds: a NaN or an infinity in it goes nowhere.
+ * table's dtype, but stays f32 for f32 tables and where batch <= 8 and batch * vocab * row
+ * bytes <= 128 MiB.  In f16 it is kept times one power of two for the whole call, which puts the
+ * largest |g|, |g + h| into [2^13, 2^14): an entry of D keeps 11 bits down to 2^-27 of that largest
+ * one, fewer below, and is 0 below 2^-38 of it; rows whose gradients are that far apart belong
+ * in calls of their own.  The sums are f32, each result is rounded once.
+ * At a label, D is g expm1(t) + h exp(t) with t = L - lse in 64 bits: within 2^-21 of these terms
+ * for the given lse, also where the probability is near 1.  (lse itself is rounded to f32: where
+ * 1 - p is 1e-4, an lse of 17 is off by up to 1% of that.)  What the entry's rounding to 16
+ * bits takes away is added to residual_grad, and up to 128 rows to table_grad; table_grad of
+ * more rows keeps one rounding of D, as it does elsewhere.
+ * A row with g_b = 0 and h_b = 0 (padding, for instance) has D = 0 and adds nothing to
+ * table_grad, whatever it holds: a NaN or an infinity in it goes nowhere.
  *   d_lse               f32 [batch], as etg_cross_entropy wrote it
  *   grad_loss           g for all rows, or d_grad_loss f32 [batch] where that is not NULL
  *   d_grad_lse          NULLABLE f32 [batch]: h (NULL: 0)
@@ -608,6 +616,7 @@ int32_t etg_cross_entropy_grad(const etg_table* lm_head, const void* d_residual,
  *                change
  *   d_workspace  at least etg_embed_gather_grad_workspace() bytes, 256-byte aligned (may be NULL
  *                where that is 0)
+ * d_out must not overlap d_ids, d_grad or the workspace: its rows are written while they are read.
  * The sums are formed over the positions sorted by token, in a fixed order and without atomics:
  * results are bitwise repeatable.
  * Errors: EINVAL (null), EDTYPE, ESHAPE, EALIGN, EWORKSPACE.
