@@ -260,6 +260,8 @@ struct RowGrad {
 };
 size_t rowgrad_workspace(int64_t n, int64_t V, int64_t hidden);
 hipError_t launch_rowgrad(const RowGrad& g, void* ws, hipStream_t stream);
+// Zeros of `bytes` (a multiple of 16) bytes at a 16-byte aligned address.
+hipError_t launch_zeros(void* at, int64_t bytes, hipStream_t stream);
 
 }  // namespace etg
 

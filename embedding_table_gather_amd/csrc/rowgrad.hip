@@ -510,17 +510,28 @@ hipError_t launch_sums_to(const RowSums& p, int32_t out_dtype, bool add, hipStre
 
 size_t rowgrad_workspace(int64_t n, int64_t V, int64_t hidden) { return n == 0 ? 0 : rowgrad_ws(n, V, hidden).bytes; }
 
+// One launch writes at most so many 16-byte pieces of zeros (128 GiB).
+constexpr int64_t kFillMost = ((int64_t)1 << 20) * Fill::kPieces;
+
+hipError_t launch_zeros(void* at, int64_t bytes, hipStream_t stream) {
+  for (Fill all = {(u32x4*)at, bytes / 16}; all.n16 > 0;) {
+    const Fill f = {all.at, std::min(all.n16, kFillMost)};
+    hipLaunchKernelGGL(rowgrad_fill_kernel, dim3((unsigned)f.workgroups()), dim3(256), 0, stream, f);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    all.at += f.n16, all.n16 -= f.n16;
+  }
+  return hipSuccess;
+}
+
 hipError_t launch_rowgrad(const RowGrad& g, void* ws, hipStream_t stream) {
   hipError_t e;
   // whole rows of 16 bytes
   Fill all = {(u32x4*)g.out, g.add ? 0 : g.V * g.hidden * (g.out_dtype == DT_F32 ? 4 : 2) / 16};
-  // one launch writes at most 2^20 workgroups' zeros; what the sort's launches cannot take goes first
-  while (all.n16 > ((int64_t)1 << 20) * Fill::kPieces || (g.n == 0 && all.n16 > 0)) {
-    const Fill f = {all.at, std::min(all.n16, ((int64_t)1 << 20) * Fill::kPieces)};
-    hipLaunchKernelGGL(rowgrad_fill_kernel, dim3((unsigned)f.workgroups()), dim3(256), 0, stream, f);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    all.at += f.n16, all.n16 -= f.n16;
-  }
+  // what the sort's launches cannot take goes first
+  const int64_t ahead = g.n == 0 ? all.n16 : std::max<int64_t>(0, all.n16 - kFillMost);
+  if ((e = launch_zeros(all.at, ahead * 16, stream)) != hipSuccess) return e;
+  all.at += ahead, all.n16 -= ahead;
   if (g.n == 0) return hipSuccess;
   const RowGradWs w = rowgrad_ws(g.n, g.V, g.hidden);
   uint8_t* base = (uint8_t*)ws;

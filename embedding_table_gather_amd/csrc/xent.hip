@@ -1545,7 +1545,7 @@ hipError_t launch_labels(const TableDesc& t, const XentProduct& logits, const Ro
 template <int DT>
 hipError_t backward(const TableDesc& t, const XentCall& c, uint8_t* ws, hipStream_t stream) {
   if (c.n == 0)  // a sum of nothing
-    return c.d_rows == nullptr || c.add ? hipSuccess : launch_write_probe(c.d_rows, t.V * t.row_bytes, 0, stream);
+    return c.d_rows == nullptr || c.add ? hipSuccess : launch_zeros(c.d_rows, t.V * t.row_bytes, stream);
   const BackwardWs w = backward_ws(t, c.n);
   hipError_t e;
   uint8_t *packed = ws + w.x, *d = ws + w.d;
