@@ -136,6 +136,23 @@ __device__ __forceinline__ void heap_replace_root(uint64_t* h, int k, uint64_t k
   h[i] = key;
 }
 
+// Waits until at most N loads or copies of this wave are in flight and its LDS reads are done
+// (expcnt(7) lgkmcnt(0) vmcnt(N)).
+template <int N>
+__device__ __forceinline__ void load_wait() {
+  static_assert(N >= 0 && N < 64, "vmcnt field");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
+}
+
+// A workgroup barrier that no memory access crosses (the compiler's own also waits for copies).
+__device__ __forceinline__ void bare_barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void load_barrier() {
+  load_wait<N>();
+  bare_barrier();
+}
+
 // Butterfly sum: every lane ends with the same (bitwise) value because each
 // pairwise add is commutative.
 __device__ __forceinline__ float wave_sum(float v) {

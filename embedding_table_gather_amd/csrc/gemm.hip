@@ -71,22 +71,14 @@ struct GemmCfg {
 
 __device__ __forceinline__ int gemm_swz(int r, int piece) { return r * 64 + 16 * (piece ^ ((r >> 2) & 3)); }
 
-// vmcnt(n) lgkmcnt(0), then a workgroup barrier that no memory access crosses.
-template <int N>
-__device__ __forceinline__ void gemm_stage_barrier() {
-  static_assert(N >= 0 && N < 64, "vmcnt field");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);  // expcnt(7) lgkmcnt(0) vmcnt(N)
-  asm volatile("s_barrier" ::: "memory");
-}
-
-// gemm_stage_barrier<groups * G> for a run-time number of outstanding load groups.
+// load_barrier<groups * G> for a run-time number of outstanding load groups.
 template <int G>
 __device__ __forceinline__ void gemm_stage_barrier_groups(int groups) {
   switch (groups) {
-    case 0: gemm_stage_barrier<0>(); break;
-    case 1: gemm_stage_barrier<G>(); break;
-    case 2: gemm_stage_barrier<2 * G>(); break;
-    default: gemm_stage_barrier<3 * G>(); break;
+    case 0: load_barrier<0>(); break;
+    case 1: load_barrier<G>(); break;
+    case 2: load_barrier<2 * G>(); break;
+    default: load_barrier<3 * G>(); break;
   }
 }
 
@@ -402,7 +394,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_logits_kernel(
       if (tid < COLS) athr[tid] = ~0u;
       if (tid < 2) aovf[tid] = 0;
       if (thr0) {
-        gemm_stage_barrier<0>();
+        load_barrier<0>();
         // groups each holder vouches for (opaque: its compares below stay here
         // instead of holding scalar registers across the tile loop)
         int q = (k + 3) >> 2;
@@ -440,7 +432,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_logits_kernel(
       for (int round = 0;; round++) {
         if (tid < COLS) acnt[tid] = 0;
         if (tid == 0) aovf[(round + 1) & 1] = 0;
-        gemm_stage_barrier<0>();
+        load_barrier<0>();
 #pragma unroll
         for (int t = 0; t < NTR; t++) {
           const int col = nw * WCR + 32 * t + (xl & 31);
@@ -491,7 +483,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_logits_kernel(
             }
           }
         }
-        gemm_stage_barrier<0>();
+        load_barrier<0>();
         if (tid < COLS) {
           uint32_t n = acnt[tid];
           if (n > (uint32_t)ACAP) {
@@ -528,10 +520,10 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_logits_kernel(
             }
           }
         }
-        gemm_stage_barrier<0>();
+        load_barrier<0>();
         if (aovf[round & 1] == 0) {
           // every wave has read the flag before the next tile's copies refill the rings
-          gemm_stage_barrier<0>();
+          load_barrier<0>();
           break;
         }
       }
@@ -548,13 +540,13 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_logits_kernel(
     run = lse_combine(run, make_float2(__shfl_xor(run.x, 32, 64), __shfl_xor(run.y, 32, 64)), lse_c);
     float2* xl = (float2*)smem;  // [WN][32]
     if (mw == 1 && lane < 32) xl[nw * 32 + lane] = run;
-    gemm_stage_barrier<0>();
+    load_barrier<0>();
     const int64_t b = (int64_t)ct * kGemmCols + nw * (WC / 2) + lane;
     if (mw == 0 && lane < 32 && b < B) lse[b * nvr + vr] = lse_combine(run, xl[nw * 32 + lane], lse_c);
   }
   // heaps -> candidates [B][nvr][k]; the barrier orders the heap writes (also
   // the zeroing, for a range past the table that ran no tile) before the reads
-  gemm_stage_barrier<0>();
+  load_barrier<0>();
   if (tid < COLS) {
     const int64_t b = (int64_t)ct * COLS + tid;
     if (b < B) {

@@ -260,14 +260,6 @@ __device__ __forceinline__ void lds_copy_1k(const void* src, uint32_t offset, ui
                : "memory");
 }
 
-// vmcnt(N) lgkmcnt(0), then a workgroup barrier that no memory access crosses.
-template <int N>
-__device__ __forceinline__ void load_barrier() {
-  static_assert(N >= 0 && N < 64, "vmcnt field");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
-  asm volatile("s_barrier" ::: "memory");
-}
-
 // What the two kernels below share: the place of a workgroup, its w rows and its part of the
 // image.  Workgroup ids {x, x + 8, ...} run on XCD x: the passes of one block of w rows
 // follow each other there, and find its rows in that XCD's L2.

@@ -78,16 +78,8 @@ __device__ __forceinline__ void copy_1k(u32x4 rsrc, uint32_t offset, uint32_t ld
       : "memory");
 }
 
-// Waits until at most N copies of this wave are in flight and its LDS reads are done.
-template <int N>
-__device__ __forceinline__ void load_wait() {
-  static_assert(N >= 0 && N < 64, "vmcnt field");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
-}
 // Waits for this wave's LDS accesses alone.
 __device__ __forceinline__ void load_wait_lds() { __builtin_amdgcn_s_waitcnt(0xc07f); }
-// A workgroup barrier that no memory access crosses (the compiler's own also waits for copies).
-__device__ __forceinline__ void bare_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
 // One operand of a product, R rows of it per tile and 128 bytes of K values per stage (KS of
 // them).  TR false: rows of K values in memory, pitch bytes apart.  TR true: the K values of
