@@ -1038,7 +1038,7 @@ __global__ void __launch_bounds__(256) direct_kernel(XentProduct p) {
 
 // Up to 8 residual rows: both gradients in one pass over the table, with vector FMAs and D in
 // f32.  A wave takes 64 pieces of 16 bytes of some consecutive table rows: their share of
-// dx stays in its registers, their rows of dE are written as they come: 1 x 4,096 x 256 f32 14 us
+// dx stays in its registers, their rows of dE are written as they come: 1 x 4,096 x 256 f32 15.8 us
 // with the launches before and after.
 struct XentRows {
   const uint8_t *table, *x;
@@ -1306,7 +1306,10 @@ Tiling tiling(int64_t m, int64_t n, int64_t k, int64_t splits, int size) {
   Tiling best = {0, INT64_MAX};
   for (int c = n <= 64 || size == 4 ? 64 : 128; c <= 256; c *= 2) {
     const int64_t percent = size == 4 ? 100 : c == 256 ? 100 : 140;  // time of a column
-    const int64_t stages = cdiv(cdiv(k, splits), 128 / size) + (size == 4 ? 6 : 24);  // and a start and an end
+    // and a start and an end (5 to 6 stages' time: statistics of 2,048 x 131,072 take 441, 784 and
+    // 1,421 us at 14, 28 and 56 stages), and in dx the partial sums that one more K slice leaves: with 24
+    // dx of 1,500 x 5,000 x 640 bf16 takes 54 us, with 6 59; most choices are the same
+    const int64_t stages = cdiv(cdiv(k, splits), 128 / size) + (size == 4 ? 6 : 24);
     const int64_t cost = cdiv(cdiv(m, 256) * cdiv(n, c) * splits, kTargetBlocks) * c * percent * stages;
     if (cost < best.cost) best = {c, cost};
     if (c >= n) break;
@@ -1418,8 +1421,12 @@ ForwardWs forward_ws(const TableDesc& t, int64_t n) {
 }
 
 // Few residual rows and a small table: D in f32 and one kernel of vector FMAs for both
-// gradients, fewer launches (1 x 4,096 x 256 f32: 16 us, by products 70; 4 x 32,768 x 1,024 bf16
-// 46 / 47; 8 x 16,384 x 1,024 45 / 38).  A large one takes longer that way: its reads and writes
+// gradients, three launches where the products take five.  In a graph of calls, by it / by
+// products: 1 x 4,096 x 256 f32 15.8 / 40.5 us, 8 x 4,096 x 256 19.8 / 41.2, 1 x 32,768 x 256 38 / 51,
+// 3 x 3,000 x 136 bf16 17.6 / 23.1, 1 x 16,384 x 1,024 34 / 38; from there on they are even (4 x 32,768 x
+// 1,024 56.4 / 55.8, f32 8 x 32,768 x 256 52.9 / 51.8).  dx alone costs it more than the products take
+// in 16 bits (2 x 32,768 x 1,024 44 / 34), the table's gradient alone less (37 / 40); one rule serves
+// all, so that a gradient is the same alone.  A large table takes longer that way: its reads and writes
 // alternate (1 x 262,144 x 5,376: 1,668 / 1,554).
 constexpr int64_t kVectorBytes = (int64_t)128 << 20;
 bool vector_rows(const TableDesc& t, int64_t n) { return n <= 8 && n * t.V * t.row_bytes <= kVectorBytes; }
