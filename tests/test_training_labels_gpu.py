@@ -66,3 +66,29 @@ def test_loss_of_cancelling_label_logits(case):
     want, want_lse, tol, tol_lse = tl.loss_of(E, x, labels)
     _check(lse, want_lse, tol_lse, "lse")
     _check(loss, want, tol, "loss")
+
+
+@pytest.mark.parametrize("dtype", sorted(tl.TYPES))
+@pytest.mark.parametrize("n,V,d", [(1, 1, 8), (5, 1, 64), (40, 700, 128), (100, 20011, 264), (300, 3001, 1024)])
+def test_losses_of_sure_labels_are_never_negative(dtype, n, V, d):
+    # probabilities that round to 1, sums that an f32 accumulator gets wrong by more than 1 - p
+    note(f"sure labels {dtype} {n} x {V} x {d}")
+    T = tl.TYPES[dtype]
+    gen = torch.Generator().manual_seed(n + V)
+    E = torch.randn((V, d), generator=gen).to(T)
+    x = torch.randn((n, d), generator=gen)
+    at = torch.randint(V, (n,), generator=gen, dtype=torch.int32)
+    target = E[at.long()].float()
+    x += target * (60 / target.square().sum(1, keepdim=True))
+    x = x.to(T)
+    t = etg.Table(E.cuda(), CODES[T], V, d)
+    loss, lse = t.cross_entropy(x.cuda(), at.cuda())
+    torch.cuda.synchronize()
+    L = x.double() @ E.double().t().contiguous()
+    want = torch.logsumexp(L, 1)
+    assert (loss >= 0).all()
+    if V == 1:
+        assert (loss <= 1e-9).all()
+    dL = d * 2.0 ** -22 * (x.double().abs() @ E.double().abs().t().contiguous()).max(1).values
+    _check(lse.cpu(), want, dL + 1e-5 + want.abs() * 2.0 ** -24, "lse")
+    _check(loss.cpu(), want - L.gather(1, at.long()[:, None])[:, 0], dL + 1e-5, "loss")
