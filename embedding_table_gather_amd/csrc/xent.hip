@@ -571,7 +571,7 @@ __device__ __forceinline__ void finish(const XentProduct& p, f32x4 (&acc)[MT][NT
 // Tiles and K slices.  Workgroups {x, x + 8, ...} run on XCD x: each XCD takes a contiguous
 // share of the tiles, in blocks of kGroup tiles along n by all along m: its 32 CUs work on about
 // kGroup x 32 / kGroup tiles, which share their operands' slices in its L2 (4,096 x 32,768 x
-// 5,120: 1,004 us, tile rows in turn 1,080).
+// 5,120 D: 1,004 us, tile rows in turn 1,080).
 struct XentPlace {
   int mtile, ntile, split;
   bool some;
@@ -592,7 +592,7 @@ struct XentPlace {
 
 // Tiles of BM x BN, K through a ring of RING LDS images, RING - 1 stages ahead: one barrier
 // per stage.  For few residual rows, where reading the table is the bound: 64 x 262,144 x 5,376
-// statistics 464 us (6.1 TB/s; a kernel that only reads reaches 6.9), dx from D 455 us.
+// statistics 465 us (6.1 TB/s; a kernel that only reads reaches 6.9), dx from D 459 us.
 template <int DT, bool TA, bool TB, int MODE, int BM, int BN, int WM, int RING>
 __global__ void __launch_bounds__(64 * kXWaves) ring_kernel(XentProduct p) {
   using A = Operand<DT, TA, BM>;
@@ -670,9 +670,11 @@ __global__ void __launch_bounds__(64 * kXWaves) ring_kernel(XentProduct p) {
 // tile, whose first stages thus arrive while this one's end is computed and stored.  A tile
 // has an even number of stages (zeros behind an odd one), so that each begins alike.
 //
-// 4,096 x 32,768 x 5,120 bf16, a launch each: D 1,004 us (1.37 PF/s), dx 1,102 us, dE 1,086 us;
-// the library's plain products take 964, 1,410 and 1,184.  What bounds it is the time at which
-// fragments leave LDS: a step reads 8 or 4 KiB per wave for 16 products.
+// 4,096 x 32,768 x 5,120 bf16, a launch each, on two cards: D 1,004 to 1,066 us (1.3 PF/s), dx 1,102 to
+// 1,181, dE 1,070 to 1,154; the library's plain products take 964, 1,410 and 1,184.  What bounds it are
+// the matrix cores at the clock that their load leaves (1.8 GHz): they are busy 72, 62 and 67% of the
+// time, LDS is read in 23 to 27% of it, without bank conflicts.  At 14 stages the end of a tile weighs
+// most: 2,048 x 151,936 x 896 keeps them busy 37% in D, 54% in dx.
 template <int DT, bool TA, bool TB, int MODE>
 __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
   using A = Operand<DT, TA, 256>;
@@ -835,7 +837,7 @@ __global__ void __launch_bounds__(64 * kXWaves, 2) tile_kernel(XentProduct p) {
 // dE = D^T x for up to 128 residual rows (f32: 64), bound by its stores: a workgroup keeps 256
 // columns of x as fragments in registers (64 for each of 4 waves, twice) and walks a range of
 // table rows, 128 at a time (64 for each half of the waves), D's tiles RING - 1 steps ahead in
-// a ring of LDS images: 64 x 262,144 x 5,376 bf16 640 us (4.4 TB/s), 128 rows 860; tiles as the
+// a ring of LDS images: 64 x 262,144 x 5,376 bf16 646 us (4.4 TB/s), 128 rows 836; tiles as the
 // other products have them keep too few stores in flight.  A tile that holds a label has the rest of its entry of D added,
 // as a second operand built in registers.
 template <int DT, int KT>
@@ -1148,7 +1150,8 @@ __global__ void __launch_bounds__(256) xent_rows_kernel(XentRows p) {
 }
 
 // D's entries at the labels, in 64 bits up to the distance of a label's logit to lse, times scale[0]
-// (NULL: 1), and their rests: one wave per residual row, bound by the latency of its loads.
+// (NULL: 1), and their rests: one wave per residual row, bound by the latency of its loads (64 x
+// 262,144 x 5,376 bf16 5 us, 4,096 rows of 5,120 13).
 template <int DT>
 __global__ void __launch_bounds__(256) xent_label_kernel(const uint8_t* __restrict__ x, int64_t x_pitch,
                                                          const uint8_t* __restrict__ table, int64_t row_bytes,
@@ -1304,9 +1307,9 @@ constexpr int kXcdCount = 8;
 
 // Columns of a product's tiles for n residual rows, and what the product then takes: rounds of
 // one workgroup per CU, times its columns and stages.  16-bit products of 256 columns keep
-// the matrix cores busier than those of 128 (1,024 x 262,144 x 5,120: 2,034 us, by 128 columns
-// 2,672); in f32, where they are slow enough for either, the choice is about rounds alone (300
-// x 20,000 x 600: 271 us, 456 by 256 columns throughout).
+// the matrix cores busier than those of 128 (1,024 x 262,144 x 5,120: 1,994 us, by 128 columns
+// 2,893); in f32, where they are slow enough for either, the choice is about rounds alone (300
+// x 20,000 x 600 gradients: 296 us, 425 by 256 columns throughout).
 struct Tiling {
   int columns;
   int64_t cost;
@@ -1386,8 +1389,9 @@ hipError_t launch_by_rows(XentProduct p, hipStream_t stream) {
 constexpr int64_t kMaxTiles = 1 << 20;              // of one launch
 constexpr int64_t kPartBytes = (int64_t)256 << 20;  // statistics, or D, of one piece
 
-// The 16 x 16 kernel instead of tiles of 256 table rows (1 x 16,384 x 1,024 bf16: 14 us, by the
-// tiles 17; 16 x 32,768 x 1,024 29 / 19; 4 x 4,096 x 256 f32 12 / 24).
+// The 16 x 16 kernel instead of tiles of 256 table rows.  Loss by it / by the tiles: 4 x 4,096 x 256 f32
+// 10.3 / 27.0 us, 16 x 32,768 x 256 27.0 / 28.9, 1 x 16,384 x 1,024 bf16 17.4 / 20.1, 64 x 4,096 x 1,024 17.0 /
+// 20.0, 16 x 16,384 x 1,024 21.2 / 21.0, and past the border 16 x 32,768 x 1,024 32.6 / 22.2.
 bool direct_tiles(int64_t vocab, int64_t n, int dtype) {
   return n <= 64 && cdiv(vocab, 16) * cdiv(n, 16) <= (dtype == DT_F32 ? 4096 : 1024);
 }
