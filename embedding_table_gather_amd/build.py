@@ -51,7 +51,7 @@ def _compile(src: str) -> str:
     if remarks:
         if bad := spilled(out):
             raise RuntimeError(f"spilled vector registers in {src}: {'; '.join(bad)}")
-        out = ""
+        out = "\n".join(l for l in out.splitlines() if " warning: " in l)
     if out.strip():
         print(out, file=sys.stderr)
     return obj
