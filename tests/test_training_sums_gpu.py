@@ -84,3 +84,26 @@ def test_lse_near_zero(dtype, n, V, d):
     _check(lse.cpu(), want, e + ts.half_step(want.abs() + e, torch.float32), "lse")
     want = want - L.gather(1, labels.long()[:, None])[:, 0]
     _check(loss.cpu(), want, e + ts.half_step(want.abs() + e, torch.float32), "loss")
+
+
+@pytest.mark.parametrize("n,V,d", [(21, 5000, 64), (42, 20011, 136), (150, 5000, 264), (300, 9001, 72)])
+def test_f16_rows_of_small_gradients(n, V, d):
+    """Row b's gradient is 2^-(b % 21) of the largest: D is kept in f16 times one power of two, which puts the
+    largest coefficient at 2^13 or more, so an entry is off by 2^-11 of itself or half of f16's smallest step,
+    2^-25 / 2^13 of that coefficient, and by 1e-5 of itself before; sums of V terms round by 2^-22 each at most."""
+    note(f"small gradients {n} x {V} x {d}")
+    T = torch.float16
+    E, x, labels, _ = ts.make(n, V, d, T)
+    half = d // 2
+    k = torch.arange(n) % 21
+    h = (1000.0 * (1 + torch.arange(n) / (3.0 * n)) * 0.5 ** k.double()).float()
+    t = etg.Table(E.cuda(), etg.F16, V, d)
+    _, lse = t.cross_entropy(x.cuda(), labels.cuda())
+    dx, _ = t.cross_entropy_grad(x.cuda(), labels.cuda(), lse, 0.0, h.cuda(), table_grad=False)
+    both, _ = t.cross_entropy_grad(x.cuda(), labels.cuda(), lse, 0.0, h.cuda())
+    torch.cuda.synchronize()
+    assert torch.equal(dx, both)
+    D, sums = h.double() / V, E[:, 1:half].double().sum(0)
+    e = D * (1e-5 + 2.0 ** -11 + (V + 64) * 2.0 ** -22) + 2.0 ** -38 * float(h.max())
+    want, bound = D[:, None] * sums[None, :], e[:, None] * sums[None, :]
+    _check(dx[:, 1:half].cpu(), want, bound + ts.half_step(want + bound, T), "residual gradient")
